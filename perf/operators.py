@@ -535,7 +535,7 @@ def _run_turnover(s):
     first = torch.cumsum(need, 0) - need
     come = (col >= have[:, None]) & (col < want[:, None])
     page, free = _free_page(s["refs"], (first[:, None] + col - have[:, None]).clamp(min=0))
-    ok = first + need <= free
+    ok = (need == 0) | (first + need <= free)
     come = come & ok[:, None]
     s["bt"][rows] = torch.where(come, page.int(), table)
     s["refs"].index_add_(0, page.view(-1), come.int().view(-1))
