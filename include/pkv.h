@@ -24,6 +24,15 @@
  *    over an FP8 cache with the query quantised to e4m3 per (row, head), so
  *    that the score MMAs run on 8-bit operands (an opt-in numerics change).
  *
+ *  - pkv_paged_decode_attn_fp8 / pkv_paged_window_attn: GQA decode over an e4m3
+ *    cache with a scale for each (page, kv head) of K and of V, and over a bf16
+ *    cache; a sliding window may keep the first tokens of a request visible.
+ *    pkv_gqa_kv_append_fp8 writes tokens (one each, or whole prompts) into the
+ *    e4m3 cache.
+ *
+ *  - pkv_pages_fork / _release / _reserve / _compact / _copy: the cache's pages,
+ *    kept on the device in block tables, lengths and reference counts.
+ *
  *  - pkv_gqa_kv_append / pkv_mla_kv_append: the step before either call,
  *    writing the current token (or the verify tokens' latent rows) into the
  *    paged cache in place through the same block table (transformers page,
@@ -67,6 +76,10 @@
  *    current token's slot right before the call (pkv_gqa_kv_append) is fine,
  *    as is anything written by copies or by kernels that completed.  q, sinks,
  *    the workspace and all outputs are touched only after the wait.
+ *    pkv_paged_decode_attn_fp8 and pkv_paged_window_attn read nothing before
+ *    the wait.  The pkv_pages_* calls write tables, lengths and pages: the first
+ *    attention call after one on its stream waits for it to end (the library
+ *    launches that call plainly), so no care is needed there.
  *  - The launch shape depends only on the device and the batch size, never on
  *    the sequence lengths or the block table, which the kernels read on the
  *    device: a captured graph stays valid when seq_lens and block_table change.
@@ -104,6 +117,7 @@ extern "C" {
 #define PKV_ERR_CAPTURE -5         /* workspace first needed while the stream is being captured */
 #define PKV_ERR_CUDA -6            /* a CUDA runtime or driver call failed (see pkv_last_error) */
 #define PKV_ERR_BAD_BLOCK_TABLE -7 /* reported by pkv_check_errors for bad block-table data */
+#define PKV_ERR_NO_PAGES -8        /* reported by pkv_check_errors: the page pool ran out */
 
 /* Element types of pkv_tensor. */
 #define PKV_DTYPE_BF16 1
@@ -388,14 +402,197 @@ PKV_API int pkv_mla_kv_append(const pkv_tensor* latent, const pkv_tensor* latent
                               int page_size, const pkv_tensor* k_scale, void* stream);
 
 /*
+ * pkv_paged_decode_attn_fp8 -- GQA paged decode attention over an e4m3 cache
+ * with one fp32 scale for K and one for V per (page, kv head), one query token
+ * per request, an optional sliding window with first tokens that stay visible,
+ * and optional sink logits.
+ *
+ *   x_j = scale * kv_scale[page of j, head, 0] * (q . K_j)
+ *   out = sum_j w_j kv_scale[page of j, head, 1] V_j,
+ *         w_j = e^(x_j - m) / (sum_i e^(x_i - m) + e^(sink - m)),  m = max_i x_i
+ *   lse = m + log sum_j e^(x_j - m)  (natural log, keys alone)
+ *
+ *   q            bf16 [B, Hq, D], D 64 or 128; last dim contiguous; strides
+ *                multiples of 8; 16-byte aligned.
+ *   kv_cache     e4m3 [num_blocks, Hkv, P, 2D]: K in [..., :D], V in [..., D:];
+ *                last dim contiguous, the other strides any multiples of 16
+ *                (so a [num_blocks, P, Hkv, 2D] cache serves as a permuted
+ *                view); 16-byte aligned.  Hq = G * Hkv with G from 1 to 16:
+ *                query head h reads kv head h / G.
+ *   kv_scale     fp32 [num_blocks, Hkv, 2] (K, V): any finite values >= 0;
+ *                pkv_gqa_kv_append_fp8 writes powers of two.  The pairs are
+ *                contiguous and 8-byte aligned.
+ *   block_table  int32 [B, max_blocks], stride(1) == 1.  Entries of pages that
+ *                hold no visible key are never read: with a window, pages
+ *                between the first tokens' and the window's may be given back.
+ *   seq_lens     int32 [B], lengths including the current token.  A length of 0
+ *                writes zeros and lse = -inf.
+ *   sinks        fp32 [Hq] natural-log sink logits (not multiplied by scale),
+ *                or NULL.  They enter only the output's denominator.
+ *   window       > 0: keys [max(L - window, 0), L) are visible; <= 0: all keys.
+ *   first_tokens >= 0: with a window, keys [0, first_tokens) stay visible too.
+ *   scale        softmax scale applied to q.k.
+ *   page_size    P: 16, 32, 64 or 128 (must equal kv_cache.shape[2]).
+ *   out          bf16 [B, Hq, D], alignment as q.
+ *   lse          fp32 [B, Hq] or NULL.
+ *   stream       cudaStream_t.
+ * What masked keys hold (NaN, infinities, stale bytes) reaches no result.
+ * Errors as pkv_paged_decode_attn; a bad block-table entry reads as a page of
+ * zeros and raises bit 1, a seq_len beyond the table is clamped and raises bit
+ * 2 of the device error word.
+ */
+PKV_API int pkv_paged_decode_attn_fp8(const pkv_tensor* q, const pkv_tensor* kv_cache,
+                                      const pkv_tensor* kv_scale, const pkv_tensor* block_table,
+                                      const pkv_tensor* seq_lens, const pkv_tensor* sinks,
+                                      int window, int first_tokens, float scale, int page_size,
+                                      const pkv_tensor* out, const pkv_tensor* lse, void* stream);
+
+/*
+ * pkv_paged_window_attn -- pkv_paged_decode_attn_fp8 over a bf16 cache (no
+ * scales): decode with a sliding window and first tokens that stay visible.
+ * Next to pkv_paged_decode_attn it takes first_tokens, 1 to 16 query heads per
+ * kv head, head_dim 64, pages of 64 and 128 tokens and any token stride.
+ *   kv_cache     bf16 [num_blocks, Hkv, P, 2D]; strides multiples of 8.
+ *   other arguments as pkv_paged_decode_attn_fp8.
+ */
+PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cache,
+                                  const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                                  const pkv_tensor* sinks, int window, int first_tokens, float scale,
+                                  int page_size, const pkv_tensor* out, const pkv_tensor* lse,
+                                  void* stream);
+
+/*
+ * pkv_gqa_kv_append_fp8 -- write new tokens into an e4m3 cache with a scale for
+ * each (page, kv head) of K and of V, in place: one token each (decode), or
+ * whole prompts.
+ *
+ * For each page that receives tokens, each kv head, and K and V apart:
+ *   a     = max |x| over the page's new finite values
+ *   need  = 0 if a == 0, else the smallest power of two >= 2^-100 with a <= 448 need
+ *   s_old = the page's scale if it holds tokens before the new ones, else 0
+ *   s     = max(s_old, need), the page's new scale
+ *   code  = e4m3(x / s) for the new tokens (1 in place of s == 0): round to
+ *           nearest even, saturating at +-448, NaN stays NaN; when s > s_old the
+ *           held tokens become e4m3(code * (s_old / s)).
+ *
+ *   k, v          bf16 [T, Hkv, D], the new tokens of all requests, one request
+ *                 after the other; last dim contiguous, rows 16-byte aligned,
+ *                 the same strides.
+ *   kv_cache, kv_scale  as pkv_paged_decode_attn_fp8, written in place.
+ *   block_table   int32 [B, max_blocks].
+ *   seq_lens      int32 [B], lengths including the new tokens: the n new tokens
+ *                 of request b go to positions seq_lens[b] - n .. seq_lens[b] - 1
+ *                 (those at negative positions are dropped).
+ *   cu_tokens     int32 [B + 1], non-decreasing: request b's tokens are rows
+ *                 [cu_tokens[b], cu_tokens[b + 1]) (none if equal); rows outside
+ *                 [cu_tokens[0], cu_tokens[B]) are padding and are not written.
+ *                 NULL: T / B tokens each (T % B must be 0).
+ *   page_size     P.
+ *   stream        cudaStream_t.
+ * No page may receive tokens of two requests in one call (forked requests share
+ * full pages only).  Bad table entries and error codes as pkv_gqa_kv_append.
+ */
+PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
+                                  const pkv_tensor* kv_cache, const pkv_tensor* kv_scale,
+                                  const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                                  const pkv_tensor* cu_tokens, int page_size, void* stream);
+
+/*
+ * The pages of a cache, on the device.  State, shared by all layers:
+ *   block_table  int32 [rows, W], rows contiguous and apart (rows <= 8192): row
+ *                b's logical page j is block_table[b][j].
+ *   seq_lens     int32 [rows]: row b owns entries [0, ceil(seq_lens[b] / P)).
+ *   page_refs    int32 [num_pages]: how many owned entries name each page; 0 is
+ *                free.  Zeros at the start; the calls below keep it.
+ * Pages are taken lowest index first, in the order of the call's list, so a
+ * call's results depend on its inputs alone.  All lists are contiguous int32 on
+ * the device, read there: the calls are graph-capturable and never synchronise.
+ * Device error word: bit 1 a page index outside the pool, bit 2 a length beyond
+ * the table, bit 32 (PKV_ERR_NO_PAGES) the pool ran out, bit 64
+ * (PKV_ERR_BAD_BLOCK_TABLE) a list entry that was refused (a row outside the
+ * table, a row named twice) or a count that would fall below zero.  An entry
+ * that raises bit 32 or 64 changes nothing.
+ *
+ * pkv_pages_fork -- row children[i] becomes a copy of row parents[i]: its full
+ * pages are shared (their counts go up), a partly filled last page gets a page
+ * of its own, whose contents are still to be copied: copy_src[i] -> copy_dst[i]
+ * (both -1 where nothing is to be copied), for pkv_pages_copy on every layer's
+ * cache.  Children must be empty (seq_lens 0), each named once, and nobody's
+ * parent in the call; a parent may have several.  The child's entries past its
+ * pages become -1.  A child without a page (bit 32) stays empty.
+ *   parents, children, copy_src, copy_dst  int32 [n], n <= 8192.
+ */
+PKV_API int pkv_pages_fork(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                           const pkv_tensor* page_refs, const pkv_tensor* parents,
+                           const pkv_tensor* children, int page_size, const pkv_tensor* copy_src,
+                           const pkv_tensor* copy_dst, void* stream);
+
+/*
+ * pkv_pages_release -- row rows[i] keeps its first keep_lens[i] tokens (0 frees
+ * the row, a length it does not reach changes nothing): the entries of pages
+ * past them become -1 and their counts go down.  A row named several times is
+ * released to the smallest length.
+ *   rows, keep_lens  int32 [n].
+ */
+PKV_API int pkv_pages_release(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                              const pkv_tensor* page_refs, const pkv_tensor* rows,
+                              const pkv_tensor* keep_lens, int page_size, void* stream);
+
+/*
+ * pkv_pages_reserve -- row rows[i] grows to new_lens[i] tokens: free pages fill
+ * the entries it needs (count 1), and its length becomes new_lens[i] (unchanged
+ * if that is no more).  An entry that needs pages is granted when the free
+ * pages cover the needs of entries 0..i together; one that is not raises bit 32
+ * and changes nothing.
+ * Each row is named once.  A new length beyond the table raises bit 2.
+ *   rows, new_lens  int32 [n], n <= 8192.
+ */
+PKV_API int pkv_pages_reserve(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                              const pkv_tensor* page_refs, const pkv_tensor* rows,
+                              const pkv_tensor* new_lens, int page_size, void* stream);
+
+/*
+ * pkv_pages_compact -- move the live pages to the front of the pool: with n
+ * live pages, the k-th live page at or above n goes to the k-th free page below
+ * n.  Counts move along, owned table entries are rewritten (every row of
+ * block_table: all tables that name the pool's pages must be rows of it), and
+ * copy_src[k] -> copy_dst[k] is to be copied in every cache (pkv_pages_copy);
+ * the lists are filled up with -1.  Lists shorter than the moves make the call
+ * do the first of them only.
+ *   copy_src, copy_dst  int32 [m] (num_pages / 2 always suffice).
+ *   num_moves           int32 [1]: the number of moves.
+ */
+PKV_API int pkv_pages_compact(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                              const pkv_tensor* page_refs, int page_size, const pkv_tensor* copy_src,
+                              const pkv_tensor* copy_dst, const pkv_tensor* num_moves,
+                              void* stream);
+
+/*
+ * pkv_pages_copy -- copy page copy_src[i] to page copy_dst[i] in each of
+ * num_tensors caches (all layers' keys and values, their scales), one launch.
+ * Entries with a negative index are skipped; an index outside a cache raises
+ * bit 1 there and copies nothing.  A page may be the source of several copies,
+ * but the target of one only, and no target may be a source (the lists of
+ * pkv_pages_fork and pkv_pages_compact are so); otherwise what the pages in
+ * question hold is unspecified.
+ *   pages      num_tensors (1 to 64) descriptors [num_pages, ...] of any dtype:
+ *              a page's elements are dense, the page stride is any; 4-byte
+ *              aligned.
+ */
+PKV_API int pkv_pages_copy(const pkv_tensor* const* pages, int num_tensors,
+                           const pkv_tensor* copy_src, const pkv_tensor* copy_dst, void* stream);
+
+/*
  * pkv_check_errors -- read and clear the device error words of `device` (the
  * workspace's, and that of pkv_paged_decode_attn_noalloc's static array once
  * a call has set it up; synchronises the device).  *flags receives the OR of
  * the bits raised since the last check: 1 bad block-table entry, 2 seq_len longer than the block
  * table, 4 a pipeline wait gave up, 8 work items beyond the workspace, 16 a
- * CTA drew more work items than the launch has (the CTA stopped).
- * Returns PKV_OK when no bit was set, PKV_ERR_BAD_BLOCK_TABLE for bits 1|2,
- * PKV_ERR_CUDA otherwise (or on a failed CUDA call).
+ * CTA drew more work items than the launch has (the CTA stopped), 32 the page
+ * pool ran out, 64 a page call refused a list entry.
+ * Returns PKV_OK when no bit was set, PKV_ERR_BAD_BLOCK_TABLE for bits 1|2|64,
+ * PKV_ERR_NO_PAGES for bit 32 alone, PKV_ERR_CUDA otherwise (or on a failed
+ * CUDA call).
  */
 PKV_API int pkv_check_errors(int device, int32_t* flags);
 

@@ -17,6 +17,19 @@ Names follow the C ABI without its ``pkv_`` prefix:
     gqa_kv_append(k, v, kv_cache, block_table, seq_lens, page_size, stream=None)
     mla_kv_append(latent, latent_cache, block_table, seq_lens, qlen, page_size,
                   k_scale=None, stream=None)
+    paged_decode_attn_fp8(q, kv_cache, kv_scale, block_table, seq_lens, sinks, window,
+                          first_tokens, scale, page_size, out, lse=None, stream=None)
+    paged_window_attn(q, kv_cache, block_table, seq_lens, sinks, window, first_tokens,
+                      scale, page_size, out, lse=None, stream=None)
+    gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens,
+                      page_size, stream=None)
+    pages_fork(block_table, seq_lens, page_refs, parents, children, page_size,
+               copy_src, copy_dst, stream=None)
+    pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size, stream=None)
+    pages_reserve(block_table, seq_lens, page_refs, rows, new_lens, page_size, stream=None)
+    pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_dst,
+                  num_moves, stream=None)
+    pages_copy(pages, copy_src, copy_dst, stream=None)
     num_kv_splits(max_seq_len, batch, qlen, num_heads, sm_count, ...)
     init(device, workspace_bytes=0), check_errors(device),
     check_counters(device), shutdown(), version()
@@ -32,6 +45,8 @@ __all__ = [
     "PkvError", "load_library", "library_path", "init", "paged_decode_attn",
     "paged_decode_attn_noalloc",
     "mla_verify_attn", "gqa_kv_append", "mla_kv_append", "num_kv_splits", "check_errors", "check_counters", "shutdown",
+    "paged_decode_attn_fp8", "paged_window_attn", "gqa_kv_append_fp8", "pages_fork",
+    "pages_release", "pages_reserve", "pages_compact", "pages_copy",
     "version", "last_error",
 ]
 
@@ -42,7 +57,7 @@ PKV_OK = 0
 ERRORS = {
     -1: "PKV_ERR_INVALID_ARG", -2: "PKV_ERR_UNSUPPORTED", -3: "PKV_ERR_ALIGNMENT",
     -4: "PKV_ERR_WORKSPACE", -5: "PKV_ERR_CAPTURE", -6: "PKV_ERR_CUDA",
-    -7: "PKV_ERR_BAD_BLOCK_TABLE",
+    -7: "PKV_ERR_BAD_BLOCK_TABLE", -8: "PKV_ERR_NO_PAGES",
 }
 DTYPE_BF16, DTYPE_F32, DTYPE_I32, DTYPE_FP8 = 1, 2, 3, 4
 
@@ -92,6 +107,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                                        T, T, i32, vp]
         lib.pkv_gqa_kv_append.argtypes = [T, T, T, T, T, i32, vp]
         lib.pkv_mla_kv_append.argtypes = [T, T, T, T, i32, i32, T, vp]
+        lib.pkv_paged_decode_attn_fp8.argtypes = [T, T, T, T, T, T, i32, i32, f32, i32, T, T, vp]
+        lib.pkv_paged_window_attn.argtypes = [T, T, T, T, T, i32, i32, f32, i32, T, T, vp]
+        lib.pkv_gqa_kv_append_fp8.argtypes = [T, T, T, T, T, T, T, i32, vp]
+        lib.pkv_pages_fork.argtypes = [T, T, T, T, T, i32, T, T, vp]
+        lib.pkv_pages_release.argtypes = [T, T, T, T, T, i32, vp]
+        lib.pkv_pages_reserve.argtypes = [T, T, T, T, T, i32, vp]
+        lib.pkv_pages_compact.argtypes = [T, T, T, i32, T, T, T, vp]
+        lib.pkv_pages_copy.argtypes = [vp, i32, T, T, vp]
         lib.pkv_num_kv_splits.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_double, i32, i32]
         lib.pkv_check_errors.argtypes = [i32, ctypes.POINTER(ctypes.c_int32)]
         lib.pkv_check_counters.argtypes = [i32, ctypes.POINTER(ctypes.c_int64)]
@@ -101,8 +124,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                      "pkv_mla_verify_attn", "pkv_mla_quantize_q",
                      "pkv_mla_verify_attn_fp8_native", "pkv_gqa_kv_append", "pkv_mla_kv_append",
                      "pkv_num_kv_splits", "pkv_check_errors", "pkv_check_counters",
-                     "pkv_selftest_wait_timeout",
-                     "pkv_shutdown", "pkv_version"):
+                     "pkv_selftest_wait_timeout", "pkv_paged_decode_attn_fp8",
+                     "pkv_paged_window_attn", "pkv_gqa_kv_append_fp8", "pkv_pages_fork",
+                     "pkv_pages_release", "pkv_pages_reserve", "pkv_pages_compact",
+                     "pkv_pages_copy", "pkv_shutdown", "pkv_version"):
             getattr(lib, name).restype = i32
         if path is None:
             _lib = lib
@@ -244,6 +269,101 @@ def mla_kv_append(latent, latent_cache, block_table, seq_lens, qlen, page_size, 
                                  _desc(seq_lens), int(qlen), int(page_size), _desc(k_scale),
                                  _stream(stream, latent)))
     return latent_cache
+
+
+def paged_decode_attn_fp8(q, kv_cache, kv_scale, block_table, seq_lens, sinks, window,
+                          first_tokens, scale, page_size, out, lse=None, stream=None):
+    """GQA paged decode attention over an e4m3 cache with fp32 scales
+    ``kv_scale`` [num_blocks, Hkv, 2] (K, V) per page and kv head (C:
+    pkv_paged_decode_attn_fp8).  With ``window`` > 0 a request sees its last
+    ``window`` keys and its first ``first_tokens``.  Writes ``out`` (and
+    ``lse`` if given) in place and returns ``out``."""
+    lib = load_library()
+    _check(lib.pkv_paged_decode_attn_fp8(
+        _desc(q), _desc(kv_cache), _desc(kv_scale), _desc(block_table), _desc(seq_lens),
+        _desc(sinks), int(window or 0), int(first_tokens or 0), float(scale), int(page_size),
+        _desc(out), _desc(lse), _stream(stream, q)))
+    return out
+
+
+def paged_window_attn(q, kv_cache, block_table, seq_lens, sinks, window, first_tokens, scale,
+                      page_size, out, lse=None, stream=None):
+    """GQA paged decode attention over a bf16 cache with a sliding window and
+    first tokens that stay visible (C: pkv_paged_window_attn).  Writes ``out``
+    (and ``lse`` if given) in place and returns ``out``."""
+    lib = load_library()
+    _check(lib.pkv_paged_window_attn(
+        _desc(q), _desc(kv_cache), _desc(block_table), _desc(seq_lens), _desc(sinks),
+        int(window or 0), int(first_tokens or 0), float(scale), int(page_size), _desc(out),
+        _desc(lse), _stream(stream, q)))
+    return out
+
+
+def gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens, page_size,
+                      stream=None):
+    """Write the new tokens ``k``, ``v`` [T, Hkv, D] of all requests (request
+    b's are rows cu_tokens[b] .. cu_tokens[b + 1]; None: T / B each) into the
+    e4m3 cache at positions ending at seq_lens[b] - 1, raising the scales of
+    their pages where needed (C: pkv_gqa_kv_append_fp8).  Returns ``kv_cache``."""
+    lib = load_library()
+    _check(lib.pkv_gqa_kv_append_fp8(
+        _desc(k), _desc(v), _desc(kv_cache), _desc(kv_scale), _desc(block_table),
+        _desc(seq_lens), _desc(cu_tokens), int(page_size), _stream(stream, k)))
+    return kv_cache
+
+
+def pages_fork(block_table, seq_lens, page_refs, parents, children, page_size, copy_src,
+               copy_dst, stream=None):
+    """Make rows ``children`` copies of rows ``parents``: shared full pages, a
+    new last page where the parent's is partly filled (to be copied:
+    ``copy_src`` -> ``copy_dst``, see pages_copy) (C: pkv_pages_fork)."""
+    lib = load_library()
+    _check(lib.pkv_pages_fork(
+        _desc(block_table), _desc(seq_lens), _desc(page_refs), _desc(parents), _desc(children),
+        int(page_size), _desc(copy_src), _desc(copy_dst), _stream(stream, block_table)))
+
+
+def pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size, stream=None):
+    """Cut rows ``rows`` to ``keep_lens`` tokens and give their other pages
+    back (C: pkv_pages_release)."""
+    lib = load_library()
+    _check(lib.pkv_pages_release(
+        _desc(block_table), _desc(seq_lens), _desc(page_refs), _desc(rows), _desc(keep_lens),
+        int(page_size), _stream(stream, block_table)))
+
+
+def pages_reserve(block_table, seq_lens, page_refs, rows, new_lens, page_size, stream=None):
+    """Grow rows ``rows`` to ``new_lens`` tokens, taking free pages lowest
+    first (C: pkv_pages_reserve)."""
+    lib = load_library()
+    _check(lib.pkv_pages_reserve(
+        _desc(block_table), _desc(seq_lens), _desc(page_refs), _desc(rows), _desc(new_lens),
+        int(page_size), _stream(stream, block_table)))
+
+
+def pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_dst, num_moves,
+                  stream=None):
+    """Move the live pages to the front of the pool: rewrites the tables and
+    counts, and lists the copies to make (``copy_src`` -> ``copy_dst``, filled
+    up with -1; see pages_copy) (C: pkv_pages_compact)."""
+    lib = load_library()
+    _check(lib.pkv_pages_compact(
+        _desc(block_table), _desc(seq_lens), _desc(page_refs), int(page_size), _desc(copy_src),
+        _desc(copy_dst), _desc(num_moves), _stream(stream, block_table)))
+
+
+def pages_copy(pages, copy_src, copy_dst, stream=None):
+    """Copy page copy_src[i] to page copy_dst[i] in each cache of ``pages`` (a
+    tensor [num_pages, ...] or up to 64 of them), skipping negative entries (C:
+    pkv_pages_copy)."""
+    lib = load_library()
+    pages = [pages] if hasattr(pages, "data_ptr") else list(pages)
+    if not pages:
+        raise PkvError(-1, "pages_copy needs a page tensor")
+    descs = [_desc(t) for t in pages]
+    array = (ctypes.POINTER(PkvTensor) * len(pages))(*[ctypes.pointer(d._obj) for d in descs])
+    _check(lib.pkv_pages_copy(ctypes.cast(array, ctypes.c_void_p), len(pages), _desc(copy_src),
+                              _desc(copy_dst), _stream(stream, pages[0])))
 
 
 def num_kv_splits(max_seq_len, batch, qlen, num_heads, sm_count, block_h=64, occupancy=1.0,

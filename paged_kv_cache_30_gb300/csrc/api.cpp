@@ -16,6 +16,7 @@
 #include <initializer_list>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "pkv_internal.h"
 
@@ -47,6 +48,10 @@ struct DeviceState {
   cudaEvent_t order_event = nullptr;
   cudaStream_t last_stream = nullptr;
   bool has_last = false;
+  // Streams whose last call of the library may have written block tables,
+  // lengths or whole pages (the page calls): the attention kernels read those
+  // before their dependency wait, so the next one there is launched plainly.
+  std::vector<cudaStream_t> pages_written;
 };
 
 std::mutex g_mu;
@@ -131,12 +136,38 @@ int order_streams(DeviceState* st, cudaStream_t stream, bool capturing) {
   return PKV_OK;
 }
 
+// Remembers that `stream`'s last kernel wrote tables, lengths or pages.
+int note_pages_written(DeviceState* st, cudaStream_t stream) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  for (cudaStream_t s : st->pages_written)
+    if (s == stream) return PKV_OK;
+  try {
+    st->pages_written.push_back(stream);
+  } catch (...) {
+    return fail(PKV_ERR_INVALID_ARG, "host allocation failed");
+  }
+  return PKV_OK;
+}
+
+// Whether it did; a launch that waits for the kernel before it ends the matter.
+bool take_pages_written(DeviceState* st, cudaStream_t stream) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  for (size_t i = 0; i < st->pages_written.size(); ++i)
+    if (st->pages_written[i] == stream) {
+      st->pages_written.erase(st->pages_written.begin() + i);
+      return true;
+    }
+  return false;
+}
+
 // ------------------------------------------------------------ validation --
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_tensor(const pkv_tensor* t, const char* name, int dtype, int ndim) {
   if (!t) return fail(PKV_ERR_INVALID_ARG, "%s is NULL", name);
-  if (!t->data) return fail(PKV_ERR_INVALID_ARG, "%s has a NULL data pointer", name);
+  bool empty = false;  // an empty tensor has no memory
+  for (int i = 0; i < t->ndim && i < 5; ++i) empty |= t->shape[i] == 0;
+  if (!t->data && !empty) return fail(PKV_ERR_INVALID_ARG, "%s has a NULL data pointer", name);
   if (t->dtype != dtype)
     return fail(PKV_ERR_INVALID_ARG, "%s has dtype %d, expected %d", name, t->dtype, dtype);
   if (t->ndim != ndim)
@@ -198,6 +229,70 @@ int check_table_width(const pkv_tensor* block_table, int page_size) {
   if (block_table->shape[1] < 1 || block_table->shape[1] * int64_t(page_size) >= (int64_t(1) << 31))
     return fail(PKV_ERR_INVALID_ARG, "block_table width %lld x page_size %d must be in [1, 2^31)",
                 (long long)block_table->shape[1], page_size);
+  return PKV_OK;
+}
+
+// Whether distinct index tuples of a tensor that the call writes can name one
+// element: rows of a broadcast view, or strides that interleave.  Sorted by
+// stride, each dimension has to step over everything below it.
+int check_distinct_rows(const pkv_tensor* t, const char* name) {
+  int order[5], n = 0;
+  for (int i = 0; i < t->ndim; ++i)
+    if (t->shape[i] > 1) order[n++] = i;
+    else if (t->shape[i] == 0) return PKV_OK;
+  std::sort(order, order + n, [t](int a, int b) { return t->stride[a] < t->stride[b]; });
+  int64_t span = 1;
+  for (int i = 0; i < n; ++i) {
+    if (t->stride[order[i]] < span)
+      return fail(PKV_ERR_INVALID_ARG, "elements of %s share memory", name);
+    span += (t->shape[order[i]] - 1) * t->stride[order[i]];
+  }
+  return PKV_OK;
+}
+
+// block_table [B, W] and seq_lens [B] of a call on B requests.
+int check_requests(const pkv_tensor* block_table, const pkv_tensor* seq_lens, int64_t B,
+                   int page_size) {
+  if (block_table->shape[0] != B || seq_lens->shape[0] != B)
+    return fail(PKV_ERR_INVALID_ARG, "block_table / seq_lens batch mismatch");
+  const int rc = check_table_width(block_table, page_size);
+  if (rc != PKV_OK) return rc;
+  if (block_table->stride[1] != 1 && block_table->shape[1] > 1)
+    return fail(PKV_ERR_INVALID_ARG, "block_table rows must be contiguous");
+  if (B > 1 && seq_lens->stride[0] != 1)
+    return fail(PKV_ERR_INVALID_ARG, "seq_lens must be contiguous");
+  return PKV_OK;
+}
+
+// The cache [num_blocks, Hkv, P, 2D] and, with fp8, its scales [num_blocks, Hkv, 2].
+int check_paged_cache(const pkv_tensor* kv_cache, const pkv_tensor* kv_scale, bool fp8, int64_t D,
+                      int page_size) {
+  const int64_t nb = kv_cache->shape[0], Hkv = kv_cache->shape[1];
+  if (D != 64 && D != 128)
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %lld (64 and 128 are built)", (long long)D);
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    return fail(PKV_ERR_UNSUPPORTED, "page_size %d (16, 32, 64 and 128 are built)", page_size);
+  if (kv_cache->shape[2] != page_size || kv_cache->shape[3] != 2 * D)
+    return fail(PKV_ERR_INVALID_ARG, "kv_cache must be [num_blocks, Hkv, %d, %lld]", page_size,
+                (long long)(2 * D));
+  if (nb < 1 || nb >= (int64_t(1) << 31) || Hkv < 1 || Hkv > 65535)
+    return fail(PKV_ERR_INVALID_ARG, "kv_cache has %lld blocks of %lld heads", (long long)nb,
+                (long long)Hkv);
+  if (kv_cache->stride[3] != 1)
+    return fail(PKV_ERR_INVALID_ARG, "kv_cache rows must be contiguous");
+  const int64_t esz = fp8 ? 1 : 2;
+  for (int i = 0; i < 3; ++i)
+    if (kv_cache->stride[i] * esz % 16)
+      return fail(PKV_ERR_ALIGNMENT, "kv_cache strides must be multiples of 16 bytes");
+  if (!aligned16(kv_cache->data)) return fail(PKV_ERR_ALIGNMENT, "kv_cache must be 16-byte aligned");
+  if (!fp8) return PKV_OK;
+  if (kv_scale->shape[0] != nb || kv_scale->shape[1] != Hkv || kv_scale->shape[2] != 2)
+    return fail(PKV_ERR_INVALID_ARG, "kv_scale must be [num_blocks, Hkv, 2]");
+  if (kv_scale->stride[2] != 1)
+    return fail(PKV_ERR_INVALID_ARG, "the (K, V) pairs of kv_scale must be contiguous");
+  if (kv_scale->stride[0] % 2 || kv_scale->stride[1] % 2 ||
+      (reinterpret_cast<uintptr_t>(kv_scale->data) & 7u))
+    return fail(PKV_ERR_ALIGNMENT, "the (K, V) pairs of kv_scale must be 8-byte aligned");
   return PKV_OK;
 }
 
@@ -289,7 +384,7 @@ int encode_gqa_kv_map(EncodeTiledFn encode, const pkv_tensor* kv_cache, int page
 // =================================================================== ABI ==
 extern "C" {
 
-PKV_API int pkv_version(void) { return 100; }
+PKV_API int pkv_version(void) { return 200; }
 
 PKV_API const char* pkv_last_error(void) { return g_last_error.c_str(); }
 
@@ -356,6 +451,10 @@ PKV_API int pkv_check_errors(int device, int32_t* flags) {
   if (v == 0) return PKV_OK;
   if (v & (pkv::DEVERR_BAD_BLOCK | pkv::DEVERR_SEQ_TOO_LONG))
     return fail(PKV_ERR_BAD_BLOCK_TABLE, "device error word 0x%x: bad block table or seq_lens", v);
+  if (v & pkv::DEVERR_BAD_ROW)
+    return fail(PKV_ERR_BAD_BLOCK_TABLE, "device error word 0x%x: bad row list or reference counts", v);
+  if (v == pkv::DEVERR_NO_PAGE)
+    return fail(PKV_ERR_NO_PAGES, "device error word 0x%x: the page pool ran out", v);
   return fail(PKV_ERR_CUDA, "device error word 0x%x", v);
 }
 
@@ -482,6 +581,7 @@ PKV_API int pkv_paged_decode_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
   p.sched = ws.sched;
   p.err = ws.err;
   if ((rc = order_streams(st, stream, capturing))) return rc;
+  p.plain = take_pages_written(st, stream);
   const cudaError_t e = pkv::launch_gqa_decode(p, call.map, page_size, shape.grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gqa decode launch");
   return PKV_OK;
@@ -720,6 +820,7 @@ static int mla_verify_impl(const pkv_tensor* q, const pkv_tensor* q8, const pkv_
            units * cap;
   p.err = ws.err;
   if ((rc = order_streams(st, stream, capturing))) return rc;
+  p.plain = take_pages_written(st, stream);
   const cudaError_t e =
       native ? pkv::launch_mla_verify_native(p, kv_map, int(units * cap), stream)
       : pair ? pkv::launch_mla_verify_pair(p, q_map, kv_map, v_map, int(units * cap), stream)
@@ -963,6 +1064,435 @@ PKV_API int pkv_mla_kv_append(const pkv_tensor* latent, const pkv_tensor* latent
   p.err = st->ws.err;
   const cudaError_t e = pkv::launch_mla_kv_append(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "mla kv append launch");
+  return PKV_OK;
+}
+
+// ------------------------------------- decode with a window and first tokens --
+// Both entry points: kv_scale == nullptr is the bf16 cache.
+static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool fp8,
+                           const pkv_tensor* kv_scale, const pkv_tensor* block_table,
+                           const pkv_tensor* seq_lens, const pkv_tensor* sinks, int window,
+                           int first_tokens, float scale, int page_size, const pkv_tensor* out,
+                           const pkv_tensor* lse, void* stream_ptr) {
+  int rc;
+  if ((rc = check_tensor(q, "q", PKV_DTYPE_BF16, 3))) return rc;
+  if ((rc = check_tensor(kv_cache, "kv_cache", fp8 ? PKV_DTYPE_FP8_E4M3 : PKV_DTYPE_BF16, 4)))
+    return rc;
+  if (fp8 && (rc = check_tensor(kv_scale, "kv_scale", PKV_DTYPE_F32, 3))) return rc;
+  if ((rc = check_tensor(block_table, "block_table", PKV_DTYPE_I32, 2))) return rc;
+  if ((rc = check_tensor(seq_lens, "seq_lens", PKV_DTYPE_I32, 1))) return rc;
+  if (sinks && (rc = check_tensor(sinks, "sinks", PKV_DTYPE_F32, 1))) return rc;
+  if ((rc = check_tensor(out, "out", PKV_DTYPE_BF16, 3))) return rc;
+  if (lse && (rc = check_tensor(lse, "lse", PKV_DTYPE_F32, 2))) return rc;
+  const int64_t B = q->shape[0], Hq = q->shape[1], D = q->shape[2], Hkv = kv_cache->shape[1];
+  if ((rc = check_paged_cache(kv_cache, kv_scale, fp8, D, page_size))) return rc;
+  if (Hq < 1 || Hq % Hkv)
+    return fail(PKV_ERR_INVALID_ARG, "num_q_heads %lld is no multiple of num_kv_heads %lld",
+                (long long)Hq, (long long)Hkv);
+  if (Hq / Hkv > pkv::kPagedMaxGroup)
+    return fail(PKV_ERR_UNSUPPORTED, "%lld query heads per kv head (%d at most)",
+                (long long)(Hq / Hkv), pkv::kPagedMaxGroup);
+  if (B > pkv::kPagedMaxBatch)
+    return fail(PKV_ERR_UNSUPPORTED, "batch %lld > %d", (long long)B, pkv::kPagedMaxBatch);
+  if (B * Hkv > pkv::kTopCounters)
+    return fail(PKV_ERR_UNSUPPORTED, "%lld (request, kv head) pairs", (long long)(B * Hkv));
+  if ((rc = check_requests(block_table, seq_lens, B, page_size))) return rc;
+  if (sinks && (sinks->shape[0] != Hq || (Hq > 1 && sinks->stride[0] != 1)))
+    return fail(PKV_ERR_INVALID_ARG, "sinks must be a contiguous [Hq]");
+  if (out->shape[0] != B || out->shape[1] != Hq || out->shape[2] != D)
+    return fail(PKV_ERR_INVALID_ARG, "out must have the shape of q");
+  if (lse && (lse->shape[0] != B || lse->shape[1] != Hq))
+    return fail(PKV_ERR_INVALID_ARG, "lse must be [B, Hq]");
+  if (first_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "first_tokens %d < 0", first_tokens);
+  if (!std::isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (q->stride[2] != 1 || out->stride[2] != 1)
+    return fail(PKV_ERR_INVALID_ARG, "q and out last dims must be contiguous");
+  if (q->stride[0] % 8 || q->stride[1] % 8 || out->stride[0] % 8 || out->stride[1] % 8 ||
+      !aligned16(q->data) || !aligned16(out->data))
+    return fail(PKV_ERR_ALIGNMENT, "q and out rows must be 16-byte aligned");
+  if ((rc = check_distinct_rows(out, "out")) || (lse && (rc = check_distinct_rows(lse, "lse"))))
+    return rc;
+  if ((rc = check_no_overlap({{out, "out"}, {lse, "lse"}},
+                             {{q, "q"}, {kv_cache, "kv_cache"}, {kv_scale, "kv_scale"},
+                              {block_table, "block_table"}, {seq_lens, "seq_lens"},
+                              {sinks, "sinks"}})))
+    return rc;
+  if (B == 0) return PKV_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  int dev = 0;
+  if ((rc = device_of(q, "q", stream, &dev))) return rc;
+  DeviceState* st = nullptr;
+  bool capturing = false;
+  if ((rc = workspace_for(dev, stream, &st, &capturing))) return rc;
+  pkv::PagedParams p;
+  std::memset(&p, 0, sizeof p);
+  const int esz = fp8 ? 1 : 2;
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.q_sb = q->stride[0];
+  p.q_sh = q->stride[1];
+  p.kv = static_cast<const uint8_t*>(kv_cache->data);
+  p.kv_sblk = kv_cache->stride[0] * esz;
+  p.kv_sh = kv_cache->stride[1] * esz;
+  p.kv_stok = kv_cache->stride[2] * esz;
+  if (fp8) {
+    p.kv_scale = static_cast<const float*>(kv_scale->data);
+    p.s_sblk = kv_scale->stride[0];
+    p.s_sh = kv_scale->stride[1];
+  }
+  p.bt = static_cast<const int32_t*>(block_table->data);
+  p.bt_sb = block_table->stride[0];
+  p.max_blocks = int(block_table->shape[1]);
+  p.num_blocks = int(kv_cache->shape[0]);
+  p.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  p.sinks = sinks ? static_cast<const float*>(sinks->data) : nullptr;
+  p.out = static_cast<uint16_t*>(out->data);
+  p.o_sb = out->stride[0];
+  p.o_sh = out->stride[1];
+  p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+  p.lse_sb = lse ? lse->stride[0] : 0;
+  p.lse_sh = lse ? lse->stride[1] : 0;
+  p.B = int(B);
+  p.Hkv = int(Hkv);
+  p.G = int(Hq / Hkv);
+  p.D = int(D);
+  p.page_size = page_size;
+  p.window = window;
+  p.first = first_tokens;
+  p.scale = scale;
+  p.err = st->ws.err;
+  if ((rc = order_streams(st, stream, capturing))) return rc;
+  take_pages_written(st, stream);
+  const cudaError_t e = pkv::launch_paged_attn(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  return PKV_OK;
+}
+
+PKV_API int pkv_paged_decode_attn_fp8(const pkv_tensor* q, const pkv_tensor* kv_cache,
+                                      const pkv_tensor* kv_scale, const pkv_tensor* block_table,
+                                      const pkv_tensor* seq_lens, const pkv_tensor* sinks,
+                                      int window, int first_tokens, float scale, int page_size,
+                                      const pkv_tensor* out, const pkv_tensor* lse, void* stream) {
+  return paged_attn_impl(q, kv_cache, true, kv_scale, block_table, seq_lens, sinks, window,
+                         first_tokens, scale, page_size, out, lse, stream);
+}
+
+PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cache,
+                                  const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                                  const pkv_tensor* sinks, int window, int first_tokens, float scale,
+                                  int page_size, const pkv_tensor* out, const pkv_tensor* lse,
+                                  void* stream) {
+  return paged_attn_impl(q, kv_cache, false, nullptr, block_table, seq_lens, sinks, window,
+                         first_tokens, scale, page_size, out, lse, stream);
+}
+
+PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
+                                  const pkv_tensor* kv_cache, const pkv_tensor* kv_scale,
+                                  const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                                  const pkv_tensor* cu_tokens, int page_size, void* stream_ptr) {
+  int rc;
+  if ((rc = check_tensor(k, "k", PKV_DTYPE_BF16, 3))) return rc;
+  if ((rc = check_tensor(v, "v", PKV_DTYPE_BF16, 3))) return rc;
+  if ((rc = check_tensor(kv_cache, "kv_cache", PKV_DTYPE_FP8_E4M3, 4))) return rc;
+  if ((rc = check_tensor(kv_scale, "kv_scale", PKV_DTYPE_F32, 3))) return rc;
+  if ((rc = check_tensor(block_table, "block_table", PKV_DTYPE_I32, 2))) return rc;
+  if ((rc = check_tensor(seq_lens, "seq_lens", PKV_DTYPE_I32, 1))) return rc;
+  if (cu_tokens && (rc = check_tensor(cu_tokens, "cu_tokens", PKV_DTYPE_I32, 1))) return rc;
+  const int64_t T = k->shape[0], Hkv = k->shape[1], D = k->shape[2], B = seq_lens->shape[0];
+  for (int i = 0; i < 3; ++i)
+    if (v->shape[i] != k->shape[i] || (i < 2 && v->stride[i] != k->stride[i]))
+      return fail(PKV_ERR_INVALID_ARG, "v must have the shape and strides of k");
+  if ((rc = check_paged_cache(kv_cache, kv_scale, true, D, page_size))) return rc;
+  if (kv_cache->shape[1] != Hkv)
+    return fail(PKV_ERR_INVALID_ARG, "k has %lld heads, kv_cache %lld", (long long)Hkv,
+                (long long)kv_cache->shape[1]);
+  if ((rc = check_distinct_rows(kv_cache, "kv_cache")) ||
+      (rc = check_distinct_rows(kv_scale, "kv_scale")))
+    return rc;
+  if ((rc = check_requests(block_table, seq_lens, B, page_size))) return rc;
+  if (cu_tokens && (cu_tokens->shape[0] != B + 1 || (B > 0 && cu_tokens->stride[0] != 1)))
+    return fail(PKV_ERR_INVALID_ARG, "cu_tokens must be a contiguous [B + 1]");
+  if (!cu_tokens && (B == 0 ? T != 0 : T % B != 0))
+    return fail(PKV_ERR_INVALID_ARG, "%lld tokens do not divide among %lld requests (cu_tokens)",
+                (long long)T, (long long)B);
+  if (k->stride[2] != 1 || v->stride[2] != 1)
+    return fail(PKV_ERR_INVALID_ARG, "k and v last dims must be contiguous");
+  if (k->stride[0] % 8 || k->stride[1] % 8 || !aligned16(k->data) || !aligned16(v->data))
+    return fail(PKV_ERR_ALIGNMENT, "k and v rows must be 16-byte aligned");
+  if (T >= (int64_t(1) << 31) || T * Hkv >= (int64_t(1) << 33))
+    return fail(PKV_ERR_UNSUPPORTED, "%lld tokens x %lld heads", (long long)T, (long long)Hkv);
+  if ((rc = check_no_overlap({{kv_cache, "kv_cache"}, {kv_scale, "kv_scale"}},
+                             {{k, "k"}, {v, "v"}, {block_table, "block_table"},
+                              {seq_lens, "seq_lens"}, {cu_tokens, "cu_tokens"}})))
+    return rc;
+  if (B == 0 || T == 0) return PKV_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  int dev = 0;
+  if ((rc = device_of(kv_cache, "kv_cache", stream, &dev))) return rc;
+  DeviceState* st = nullptr;
+  bool capturing = false;
+  if ((rc = workspace_for(dev, stream, &st, &capturing))) return rc;
+  pkv::AppendFp8Params p;
+  std::memset(&p, 0, sizeof p);
+  p.k = static_cast<const uint16_t*>(k->data);
+  p.v = static_cast<const uint16_t*>(v->data);
+  p.s_st = k->stride[0];
+  p.s_sh = k->stride[1];
+  p.cache = static_cast<uint8_t*>(kv_cache->data);
+  p.c_sblk = kv_cache->stride[0];
+  p.c_sh = kv_cache->stride[1];
+  p.c_stok = kv_cache->stride[2];
+  p.scale = static_cast<float*>(kv_scale->data);
+  p.sc_sblk = kv_scale->stride[0];
+  p.sc_sh = kv_scale->stride[1];
+  p.bt = static_cast<const int32_t*>(block_table->data);
+  p.bt_sb = block_table->stride[0];
+  p.max_blocks = int(block_table->shape[1]);
+  p.num_blocks = int(kv_cache->shape[0]);
+  p.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  p.cu = cu_tokens ? static_cast<const int32_t*>(cu_tokens->data) : nullptr;
+  p.T = T;
+  p.B = int(B);
+  p.Hkv = int(Hkv);
+  p.D = int(D);
+  p.page_size = page_size;
+  p.err = st->ws.err;
+  const cudaError_t e = pkv::launch_gqa_kv_append_fp8(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "gqa fp8 kv append launch");
+  return PKV_OK;
+}
+
+// ------------------------------------------------------------ cache pages --
+// The tables of a page call, validated; device and workspace of the call.
+static int page_tables(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                       const pkv_tensor* page_refs, int page_size, pkv::PageTables* t) {
+  int rc;
+  if ((rc = check_tensor(block_table, "block_table", PKV_DTYPE_I32, 2))) return rc;
+  if ((rc = check_tensor(seq_lens, "seq_lens", PKV_DTYPE_I32, 1))) return rc;
+  if ((rc = check_tensor(page_refs, "page_refs", PKV_DTYPE_I32, 1))) return rc;
+  const int64_t rows = block_table->shape[0], pages = page_refs->shape[0];
+  if (page_size < 1 || page_size > (1 << 20))
+    return fail(PKV_ERR_INVALID_ARG, "page_size %d", page_size);
+  if ((rc = check_requests(block_table, seq_lens, rows, page_size))) return rc;
+  if ((rc = check_distinct_rows(block_table, "block_table"))) return rc;
+  if (pages < 1 || pages >= (int64_t(1) << 30) || (pages > 1 && page_refs->stride[0] != 1))
+    return fail(PKV_ERR_INVALID_ARG, "page_refs must be contiguous, with 1 to 2^30 - 1 pages");
+  if (rows > pkv::kPagesMaxRows)
+    return fail(PKV_ERR_UNSUPPORTED, "%lld rows > %d", (long long)rows, pkv::kPagesMaxRows);
+  t->bt = static_cast<int32_t*>(block_table->data);
+  t->bt_sb = block_table->stride[0];
+  t->rows = int(rows);
+  t->max_blocks = int(block_table->shape[1]);
+  t->seq_lens = static_cast<int32_t*>(seq_lens->data);
+  t->refs = static_cast<int32_t*>(page_refs->data);
+  t->num_pages = int(pages);
+  t->page_size = page_size;
+  return PKV_OK;
+}
+
+// A contiguous int32 list of a page call.
+static int check_list(const pkv_tensor* t, const char* name, int64_t n) {
+  int rc;
+  if ((rc = check_tensor(t, name, PKV_DTYPE_I32, 1))) return rc;
+  if (n >= 0 && t->shape[0] != n)
+    return fail(PKV_ERR_INVALID_ARG, "%s must have %lld entries", name, (long long)n);
+  if (t->shape[0] > 1 && t->stride[0] != 1)
+    return fail(PKV_ERR_INVALID_ARG, "%s must be contiguous", name);
+  if (t->shape[0] >= (int64_t(1) << 30))
+    return fail(PKV_ERR_INVALID_ARG, "%s is too long", name);
+  return PKV_OK;
+}
+
+// Device, workspace and `ints` of scratch of a page call.
+static int page_call(const pkv_tensor* first, const char* name, int64_t ints, cudaStream_t stream,
+                     DeviceState** st, int** scratch) {
+  int rc, dev = 0;
+  bool capturing = false;
+  if ((rc = device_of(first, name, stream, &dev))) return rc;
+  if ((rc = workspace_for(dev, stream, st, &capturing))) return rc;
+  if (ints * 4 > int64_t((*st)->ws.partial_bytes))
+    return fail(PKV_ERR_WORKSPACE, "workspace holds %lld ints, %lld needed",
+                (long long)((*st)->ws.partial_bytes / 4), (long long)ints);
+  *scratch = reinterpret_cast<int*>((*st)->ws.partials);
+  if ((rc = order_streams(*st, stream, capturing))) return rc;
+  return note_pages_written(*st, stream);
+}
+
+PKV_API int pkv_pages_fork(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                           const pkv_tensor* page_refs, const pkv_tensor* parents,
+                           const pkv_tensor* children, int page_size, const pkv_tensor* copy_src,
+                           const pkv_tensor* copy_dst, void* stream_ptr) {
+  int rc;
+  pkv::PageTables t;
+  if ((rc = page_tables(block_table, seq_lens, page_refs, page_size, &t))) return rc;
+  if ((rc = check_list(parents, "parents", -1))) return rc;
+  const int64_t n = parents->shape[0];
+  if ((rc = check_list(children, "children", n)) || (rc = check_list(copy_src, "copy_src", n)) ||
+      (rc = check_list(copy_dst, "copy_dst", n)))
+    return rc;
+  if (n > pkv::kPagesMaxRows)
+    return fail(PKV_ERR_UNSUPPORTED, "%lld entries > %d", (long long)n, pkv::kPagesMaxRows);
+  if ((rc = check_no_overlap({{block_table, "block_table"}, {seq_lens, "seq_lens"},
+                              {page_refs, "page_refs"}, {copy_src, "copy_src"},
+                              {copy_dst, "copy_dst"}},
+                             {{parents, "parents"}, {children, "children"}})))
+    return rc;
+  if (n == 0) return PKV_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  DeviceState* st = nullptr;
+  int* scratch = nullptr;
+  if ((rc = page_call(block_table, "block_table", pkv::pages_scratch_ints(n, t.num_pages), stream,
+                      &st, &scratch)))
+    return rc;
+  t.err = st->ws.err;
+  const cudaError_t e = pkv::launch_pages_fork(
+      t, static_cast<const int32_t*>(parents->data), static_cast<const int32_t*>(children->data),
+      int(n), static_cast<int32_t*>(copy_src->data), static_cast<int32_t*>(copy_dst->data), scratch,
+      stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages fork launch");
+  return PKV_OK;
+}
+
+PKV_API int pkv_pages_release(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                              const pkv_tensor* page_refs, const pkv_tensor* rows,
+                              const pkv_tensor* keep_lens, int page_size, void* stream_ptr) {
+  int rc;
+  pkv::PageTables t;
+  if ((rc = page_tables(block_table, seq_lens, page_refs, page_size, &t))) return rc;
+  if ((rc = check_list(rows, "rows", -1))) return rc;
+  const int64_t n = rows->shape[0];
+  if ((rc = check_list(keep_lens, "keep_lens", n))) return rc;
+  if ((rc = check_no_overlap({{block_table, "block_table"}, {seq_lens, "seq_lens"},
+                              {page_refs, "page_refs"}},
+                             {{rows, "rows"}, {keep_lens, "keep_lens"}})))
+    return rc;
+  if (n == 0) return PKV_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  DeviceState* st = nullptr;
+  int* scratch = nullptr;
+  if ((rc = page_call(block_table, "block_table", 0, stream, &st, &scratch))) return rc;
+  t.err = st->ws.err;
+  const cudaError_t e =
+      pkv::launch_pages_release(t, static_cast<const int32_t*>(rows->data),
+                                static_cast<const int32_t*>(keep_lens->data), int(n), stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages release launch");
+  return PKV_OK;
+}
+
+PKV_API int pkv_pages_reserve(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                              const pkv_tensor* page_refs, const pkv_tensor* rows,
+                              const pkv_tensor* new_lens, int page_size, void* stream_ptr) {
+  int rc;
+  pkv::PageTables t;
+  if ((rc = page_tables(block_table, seq_lens, page_refs, page_size, &t))) return rc;
+  if ((rc = check_list(rows, "rows", -1))) return rc;
+  const int64_t n = rows->shape[0];
+  if ((rc = check_list(new_lens, "new_lens", n))) return rc;
+  if (n > pkv::kPagesMaxRows)
+    return fail(PKV_ERR_UNSUPPORTED, "%lld entries > %d", (long long)n, pkv::kPagesMaxRows);
+  if ((rc = check_no_overlap({{block_table, "block_table"}, {seq_lens, "seq_lens"},
+                              {page_refs, "page_refs"}},
+                             {{rows, "rows"}, {new_lens, "new_lens"}})))
+    return rc;
+  if (n == 0) return PKV_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  DeviceState* st = nullptr;
+  int* scratch = nullptr;
+  if ((rc = page_call(block_table, "block_table", pkv::pages_scratch_ints(n, t.num_pages), stream,
+                      &st, &scratch)))
+    return rc;
+  t.err = st->ws.err;
+  const cudaError_t e =
+      pkv::launch_pages_reserve(t, static_cast<const int32_t*>(rows->data),
+                                static_cast<const int32_t*>(new_lens->data), int(n), scratch, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages reserve launch");
+  return PKV_OK;
+}
+
+PKV_API int pkv_pages_compact(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                              const pkv_tensor* page_refs, int page_size, const pkv_tensor* copy_src,
+                              const pkv_tensor* copy_dst, const pkv_tensor* num_moves,
+                              void* stream_ptr) {
+  int rc;
+  pkv::PageTables t;
+  if ((rc = page_tables(block_table, seq_lens, page_refs, page_size, &t))) return rc;
+  if ((rc = check_list(copy_src, "copy_src", -1))) return rc;
+  const int64_t n = copy_src->shape[0];
+  if ((rc = check_list(copy_dst, "copy_dst", n)) || (rc = check_list(num_moves, "num_moves", 1)))
+    return rc;
+  if ((rc = check_no_overlap({{block_table, "block_table"}, {seq_lens, "seq_lens"},
+                              {page_refs, "page_refs"}, {copy_src, "copy_src"},
+                              {copy_dst, "copy_dst"}, {num_moves, "num_moves"}},
+                             {})))
+    return rc;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  DeviceState* st = nullptr;
+  int* scratch = nullptr;
+  if ((rc = page_call(page_refs, "page_refs", t.num_pages, stream, &st, &scratch))) return rc;
+  t.err = st->ws.err;
+  const cudaError_t e = pkv::launch_pages_compact(
+      t, static_cast<int32_t*>(copy_src->data), static_cast<int32_t*>(copy_dst->data), int(n),
+      static_cast<int32_t*>(num_moves->data), scratch, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages compact launch");
+  return PKV_OK;
+}
+
+PKV_API int pkv_pages_copy(const pkv_tensor* const* pages, int num_tensors,
+                           const pkv_tensor* copy_src, const pkv_tensor* copy_dst,
+                           void* stream_ptr) {
+  int rc;
+  if (!pages) return fail(PKV_ERR_INVALID_ARG, "pages is NULL");
+  if (num_tensors < 1 || num_tensors > pkv::kPagesMaxTensors)
+    return fail(PKV_ERR_INVALID_ARG, "%d page tensors (1 to %d)", num_tensors,
+                pkv::kPagesMaxTensors);
+  if ((rc = check_list(copy_src, "copy_src", -1))) return rc;
+  const int64_t n = copy_src->shape[0];
+  if ((rc = check_list(copy_dst, "copy_dst", n))) return rc;
+  pkv::PagesCopyParams p;
+  std::memset(&p, 0, sizeof p);
+  for (int i = 0; i < num_tensors; ++i) {
+    const pkv_tensor* t = pages[i];
+    if (!t) return fail(PKV_ERR_INVALID_ARG, "pages[%d] is NULL", i);
+    if (t->ndim < 1 || t->ndim > 5)
+      return fail(PKV_ERR_INVALID_ARG, "pages[%d] has %d dims", i, t->ndim);
+    if ((rc = check_tensor(t, "a page tensor", t->dtype, t->ndim))) return rc;
+    int64_t count = 1, span = 1;
+    for (int d = 1; d < t->ndim; ++d) {
+      count *= t->shape[d];
+      span += (t->shape[d] - 1) * t->stride[d];
+    }
+    if (t->shape[0] < 1 || t->shape[0] >= (int64_t(1) << 30) || count < 1)
+      return fail(PKV_ERR_INVALID_ARG, "pages[%d] has no page, or too many", i);
+    if (span != count)
+      return fail(PKV_ERR_INVALID_ARG, "the pages of pages[%d] are not dense", i);
+    if (t->shape[0] > 1 && t->stride[0] < span)
+      return fail(PKV_ERR_INVALID_ARG, "the pages of pages[%d] overlap", i);
+    const int64_t esz = elem_bytes(t->dtype);
+    p.t[i].base = static_cast<uint8_t*>(t->data);
+    p.t[i].stride = t->stride[0] * esz;
+    p.t[i].bytes = count * esz;
+    p.t[i].num_pages = int(t->shape[0]);
+    if ((reinterpret_cast<uintptr_t>(t->data) | uintptr_t(p.t[i].stride) |
+         uintptr_t(p.t[i].bytes)) & 3u)
+      return fail(PKV_ERR_ALIGNMENT, "the pages of pages[%d] must be 4-byte aligned", i);
+    if ((rc = check_no_overlap({{t, "a page tensor"}},
+                               {{copy_src, "copy_src"}, {copy_dst, "copy_dst"}})))
+      return rc;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(t, pages[j]))
+        return fail(PKV_ERR_INVALID_ARG, "pages[%d] overlaps pages[%d]", i, j);
+  }
+  if (n == 0) return PKV_OK;
+  p.num_tensors = num_tensors;
+  p.src = static_cast<const int32_t*>(copy_src->data);
+  p.dst = static_cast<const int32_t*>(copy_dst->data);
+  p.n = int(n);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  DeviceState* st = nullptr;
+  int* scratch = nullptr;
+  if ((rc = page_call(pages[0], "pages[0]", 0, stream, &st, &scratch))) return rc;
+  p.err = st->ws.err;
+  const cudaError_t e = pkv::launch_pages_copy(p, st->ws.num_sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages copy launch");
   return PKV_OK;
 }
 

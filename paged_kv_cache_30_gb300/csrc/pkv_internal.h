@@ -19,6 +19,8 @@ enum : int {
   DEVERR_WAIT_TIMEOUT = 4,   // a pipeline wait gave up (the kernel drained and returned)
   DEVERR_ITEM_OVERFLOW = 8,  // more work items than the workspace holds
   DEVERR_QUEUE = 16,         // a CTA drew more items than the launch has (it stopped)
+  DEVERR_NO_PAGE = 32,       // the page pool ran out: a row was not forked or extended
+  DEVERR_BAD_ROW = 64,       // a bad row list or reference count (the entry was skipped)
 };
 
 // Per-device workspace carved out of one allocation (see api.cpp).
@@ -69,6 +71,7 @@ struct GqaParams {
   int* sched;
   int* err;
   int cluster;         // > 1: cluster mode with this many splits per cluster (see below)
+  int plain;           // host: launch after the kernel before has ended (no dependent launch)
 };
 
 // Launch the GQA decode kernel for page size 16 or 32.  p.cluster <= 1: the
@@ -165,6 +168,7 @@ struct MlaParams {
   int64_t q8_sr, q8_sh;
   const float* q_scale;
   int64_t qs_sr, qs_sh;
+  int plain;                     // host: the planning kernel is no programmatic dependent
 };
 
 // The planning kernel: writes p.plan[0, grid) (one CTA; programmatic dependent
@@ -219,6 +223,94 @@ cudaError_t launch_gqa_kv_append(const AppendParams& p, cudaStream_t stream);
 // one CTA whose bounded mbarrier wait runs out and raises DEVERR_WAIT_TIMEOUT in err
 cudaError_t launch_wait_selftest(int* err, cudaStream_t stream);
 cudaError_t launch_mla_kv_append(const AppendParams& p, cudaStream_t stream);
+
+// ----------------------------------- decode with a window and first tokens --
+constexpr int kPagedMaxGroup = 16;  // query heads per kv head
+constexpr int kPagedMaxBatch = 2048;
+
+// Decode over a bf16 cache, or an e4m3 cache with one fp32 scale for K and one
+// for V per (page, kv head).  The token of a request of length L sees keys
+// [0, first) and [L - window, L) (all of [0, L) when window <= 0).
+struct PagedParams {
+  const uint16_t* q;             // bf16 [B, Hq, D]
+  int64_t q_sb, q_sh;
+  const uint8_t* kv;             // cache base
+  int64_t kv_sblk, kv_sh, kv_stok;  // bytes: page, kv head, token
+  const float* kv_scale;         // [num_blocks, Hkv, 2] (K, V), or null (bf16 cache)
+  int64_t s_sblk, s_sh;          // its strides in floats
+  const int32_t* bt;
+  int64_t bt_sb;
+  int max_blocks, num_blocks;
+  const int32_t* seq_lens;
+  const float* sinks;            // [Hq] or null
+  uint16_t* out;                 // bf16 [B, Hq, D]
+  int64_t o_sb, o_sh;
+  float* lse;                    // [B, Hq] or null
+  int64_t lse_sb, lse_sh;
+  int B, Hkv, G, D, page_size;
+  int window, first;
+  float scale;
+  int* err;
+};
+cudaError_t launch_paged_attn(const PagedParams& p, cudaStream_t stream);
+
+// ------------------------------------------------ append to an e4m3 cache --
+struct AppendFp8Params {
+  const uint16_t *k, *v;         // bf16 [T, Hkv, D]
+  int64_t s_st, s_sh;            // source strides (elements): token, head
+  uint8_t* cache;                // e4m3 [num_blocks, Hkv, P, 2D]
+  int64_t c_sblk, c_sh, c_stok;  // bytes
+  float* scale;                  // [num_blocks, Hkv, 2]
+  int64_t sc_sblk, sc_sh;        // floats
+  const int32_t* bt;
+  int64_t bt_sb;
+  int max_blocks, num_blocks;
+  const int32_t* seq_lens;
+  const int32_t* cu;             // [B + 1] or null (T / B tokens each)
+  int64_t T;
+  int B, Hkv, D, page_size;
+  int* err;
+};
+cudaError_t launch_gqa_kv_append_fp8(const AppendFp8Params& p, cudaStream_t stream);
+
+// ---------------------------------------------------------- cache pages --
+constexpr int kPagesMaxRows = 8192;    // rows of a block table that a page call works on
+constexpr int kPagesMaxTensors = 64;   // tensors of one pages_copy call
+
+// A block table with its lengths and the pool's reference counts.
+struct PageTables {
+  int32_t* bt;
+  int64_t bt_sb;
+  int rows, max_blocks;
+  int32_t* seq_lens;
+  int32_t* refs;                 // [num_pages]: table entries that name the page
+  int num_pages, page_size;
+  int* err;
+};
+struct PagesCopyTensor {
+  uint8_t* base;
+  int64_t stride, bytes;         // of a page
+  int num_pages;
+};
+struct PagesCopyParams {
+  PagesCopyTensor t[kPagesMaxTensors];
+  int num_tensors;
+  const int32_t *src, *dst;      // [n], -1: nothing to copy
+  int n;
+  int* err;
+};
+cudaError_t launch_pages_copy(const PagesCopyParams& p, int num_sms, cudaStream_t stream);
+// scratch: pages_scratch_ints(n) (fork, reserve) or num_pages (compact) ints
+inline int64_t pages_scratch_ints(int64_t n, int64_t num_pages) { return 8 + 2 * n + num_pages; }
+cudaError_t launch_pages_fork(const PageTables& t, const int32_t* parents, const int32_t* children,
+                              int n, int32_t* copy_src, int32_t* copy_dst, int* scratch,
+                              cudaStream_t stream);
+cudaError_t launch_pages_release(const PageTables& t, const int32_t* rows, const int32_t* keep,
+                                 int n, cudaStream_t stream);
+cudaError_t launch_pages_reserve(const PageTables& t, const int32_t* rows, const int32_t* lens,
+                                 int n, int* scratch, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PageTables& t, int32_t* copy_src, int32_t* copy_dst, int n,
+                                 int32_t* num_moves, int* scratch, cudaStream_t stream);
 
 // Large dynamic shared memory is an attribute of a kernel on the current
 // device: set it the first time a kernel launches on each device.

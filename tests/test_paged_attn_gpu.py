@@ -1,0 +1,277 @@
+"""GPU decode over an e4m3 cache with a scale per (page, kv head), and over a
+bf16 cache with a window and first tokens (pkv_paged_decode_attn_fp8,
+pkv_paged_window_attn), against the 64-bit definition, element by element
+within the bounds of the kernel's roundings."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_30_gb300 as pkv
+from tests import paged_plain as plain
+
+pytestmark = pytest.mark.gpu
+
+EDGE_LENS = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129, 300, 1000]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    pkv.load_library()
+    pkv.init(0)
+
+
+def problem(seed, lens, Hkv, G, D, P, fp8, window=0, first=0, sinks=False, nhd=False, spread=3.0):
+    """Seeded CPU tensors.  Every slot that no request sees holds NaN (keys and values), and
+    so do the scales of pages that hold no visible key; unused table entries are -1."""
+    g = torch.Generator().manual_seed(seed)
+    lens = torch.tensor(lens, dtype=torch.int32)
+    B, width = len(lens), max(1, -(-int(lens.max()) // P)) + 1
+    see = [plain.visible(int(L), window, first) for L in lens]
+    pages = [sorted(set((s // P).tolist())) for s in see]
+    pool = sum(map(len, pages)) + 4
+    order = torch.randperm(pool, generator=g)
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    seen = torch.zeros(pool, P, dtype=torch.bool)
+    used = torch.zeros(pool, dtype=torch.bool)
+    at = 0
+    for b, (s, pg) in enumerate(zip(see, pages)):
+        for j in pg:
+            table[b, j] = int(order[at])
+            used[order[at]] = True
+            at += 1
+        if len(s):
+            seen[table[b].long()[s // P], s % P] = True
+    x = torch.randn(pool, Hkv, P, 2 * D, generator=g)
+    if fp8:
+        size = torch.exp2(torch.randint(-3, 4, (pool, Hkv, 2), generator=g).float()) \
+            if spread else torch.ones(pool, Hkv, 2)
+        codes = (x * 60).to(torch.float8_e4m3fn)
+        codes = torch.where(seen[:, None, :, None], codes.view(torch.uint8),
+                            torch.tensor(0x7f, dtype=torch.uint8)).view(torch.float8_e4m3fn)
+        scale = torch.where(used[:, None, None], size / 60, torch.tensor(math.nan))
+    else:
+        codes = torch.where(seen[:, None, :, None], x, torch.tensor(math.nan)).bfloat16()
+        scale = None
+    if nhd:  # [pool, P, Hkv, 2D] storage seen as [pool, Hkv, P, 2D]
+        codes = codes.view(torch.uint8 if fp8 else torch.bfloat16).transpose(1, 2).contiguous() \
+            .transpose(1, 2).view(codes.dtype)
+    q = torch.randn(B, Hkv * G, D, generator=g).bfloat16()
+    sink = torch.randn(Hkv * G, generator=g) * 2 if sinks else None
+    return dict(q=q, kv=codes, sc=scale, bt=table, sl=lens, sinks=sink, window=window, first=first,
+                scale=1 / math.sqrt(D), P=P, fp8=fp8)
+
+
+def run(pr, stream=None, lse=True, d=None):
+    d = d or {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in pr.items()}
+    if pr["kv"].stride(2) != pr["kv"].shape[3]:
+        u = torch.uint8 if pr["fp8"] else torch.bfloat16
+        d["kv"] = pr["kv"].view(u).transpose(1, 2).contiguous().cuda().transpose(1, 2).view(pr["kv"].dtype)
+    out = torch.full_like(d["q"], math.nan)
+    lse_t = torch.full(d["q"].shape[:2], math.nan, device="cuda") if lse else None
+    call(d, out, lse_t, stream)
+    torch.cuda.synchronize()
+    return out.cpu(), lse_t.cpu() if lse else None
+
+
+def call(d, out, lse, stream=None):
+    if d["fp8"]:
+        pkv.paged_decode_attn_fp8(d["q"], d["kv"], d["sc"], d["bt"], d["sl"], d["sinks"],
+                                  d["window"], d["first"], d["scale"], d["P"], out, lse, stream)
+    else:
+        pkv.paged_window_attn(d["q"], d["kv"], d["bt"], d["sl"], d["sinks"], d["window"],
+                              d["first"], d["scale"], d["P"], out, lse, stream)
+
+
+def check(pr, out, lse):
+    want, want_lse, tol, lse_tol = plain.decode(
+        pr["q"], pr["kv"], pr["sc"], pr["bt"], pr["sl"], pr["sinks"], pr["window"], pr["first"],
+        pr["scale"], pr["P"], 2.0 ** -11 if pr["fp8"] else 2.0 ** -8)
+    far = (out.double() - want).abs() - tol
+    assert out.isfinite().all()
+    assert (far <= 0).all(), f"{far.max():.3e} past the bound at {far.argmax()}"
+    if lse is not None:
+        empty = want_lse == -math.inf
+        assert torch.equal(lse == -math.inf, empty)
+        far = (lse.double() - want_lse).abs()[~empty] - lse_tol[~empty]
+        assert (far <= 0).all(), f"lse {far.max():.3e} past the bound"
+    assert pkv.check_errors(0) == 0
+    assert pkv.check_counters(0) == 0
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,Hkv,P", [(1, 3, 16), (4, 2, 32), (8, 1, 16), (8, 2, 64), (5, 2, 128),
+                                     (16, 1, 32), (9, 2, 16)])
+def test_head_layouts_and_edge_lengths(fp8, D, G, Hkv, P):
+    pr = problem(G * 100 + P + D, EDGE_LENS, Hkv, G, D, P, fp8, sinks=(G % 2 == 0))
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("window,first", [(1, 0), (1, 1), (7, 3), (16, 4), (33, 17), (100, 64),
+                                          (128, 128), (5000, 9), (64, 1000)])
+@pytest.mark.parametrize("P", [16, 32])
+def test_windows_and_first_tokens(fp8, window, first, P):
+    pr = problem(window * 7 + first, EDGE_LENS, 2, 8, 128, P, fp8, window, first, sinks=True)
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("D,G", [(128, 8), (64, 16)])
+def test_long_and_ragged_batches_split_over_many_blocks(fp8, D, G):
+    pr = problem(5, [5000, 1, 0, 4097, 16, 12001], 2, G, D, 16, fp8)
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_many_short_requests(fp8):
+    g = torch.Generator().manual_seed(9)
+    lens = torch.randint(0, 70, (700,), generator=g).tolist()
+    pr = problem(9, lens, 1, 4, 64, 16, fp8, sinks=True)
+    check(pr, *run(pr))
+
+
+def test_largest_batch_and_one_request_of_no_key():
+    pr = problem(2, [1 + i % 3 for i in range(2048)], 1, 1, 64, 16, True)
+    check(pr, *run(pr))
+    pr = problem(3, [0], 1, 8, 128, 16, True, sinks=True)
+    out, lse = run(pr)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_token_stride_of_an_nhd_cache(fp8):
+    pr = problem(4, EDGE_LENS, 3, 8, 128, 32, fp8, 40, 5, nhd=True)
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_strided_query_output_tables_and_scales(fp8):
+    pr = problem(6, EDGE_LENS, 2, 4, 128, 16, fp8)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in pr.items()}
+    B, Hq, D = pr["q"].shape
+    wide = torch.full((B, Hq + 3, D + 16), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:Hq + 1, 8:D + 8] = d["q"]
+    d["q"] = wide[:, 1:Hq + 1, 8:D + 8]
+    table = torch.full((B, pr["bt"].shape[1] + 5), 1 << 30, dtype=torch.int32, device="cuda")
+    table[:, :-5] = d["bt"]
+    d["bt"] = table[:, :-5]
+    if fp8:
+        sc = torch.full((pr["sc"].shape[0], 5, 4), math.nan, device="cuda")
+        sc[:, 1:3, 2:] = d["sc"]
+        d["sc"] = sc[:, 1:3, 2:]
+    hold = torch.full((B, Hq + 1, D + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, 2 * Hq), 7.0, device="cuda")
+    call(d, hold[:, :Hq, :D], lse[:, ::2])
+    torch.cuda.synchronize()
+    check(pr, hold[:, :Hq, :D].cpu(), lse[:, ::2].cpu())
+    assert (hold[:, Hq:] == 7).all() and (hold[:, :, D:] == 7).all() and (lse[:, 1::2] == 7).all()
+
+
+def test_without_lse():
+    pr = problem(7, EDGE_LENS, 2, 8, 128, 16, True)
+    out, _ = run(pr, lse=False)
+    check(pr, out, None)
+
+
+def test_scales_far_apart_between_pages():
+    """Values of one page 2^40 times another's: the large page's weight is small, the output is
+    right relative to its own bound; a page of scale 0 adds nothing to the output."""
+    pr = problem(8, [200, 33, 64], 1, 8, 128, 16, True, spread=0)
+    pr["sc"][int(pr["bt"][0, 2]), 0, 1] *= 2.0 ** 20
+    pr["sc"][int(pr["bt"][0, 5]), 0, 1] *= 2.0 ** -20
+    pr["sc"][int(pr["bt"][0, 7]), 0, 0] = 0.0
+    pr["sc"][int(pr["bt"][1, 1]), 0, 1] = 0.0
+    pr["sc"][:, :, 0] *= 3.7  # no power of two
+    check(pr, *run(pr))
+    pr["sc"][:, :, 1] = 0.0
+    pr["sc"][torch.isnan(pr["sc"])] = 0.0
+    out, lse = run(pr)
+    assert (out == 0).all() and lse.isfinite().all()
+
+
+def test_queries_of_any_magnitude():
+    """The query enters scaled to fp16's range by a power of two: rows of 2^60 and of 2^-60
+    next to ordinary ones, and a row of zeros."""
+    pr = problem(10, [70, 70, 70, 70], 1, 4, 128, 16, True)
+    size = torch.tensor([2.0 ** 60, 2.0 ** -60, 0.0, 1.0])[:, None, None]
+    pr["q"] = (pr["q"].float() * size).bfloat16()
+    pr["sc"][pr["bt"][0, :5].long(), 0, 0] *= 2.0 ** -62
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_bad_entries_read_as_zero_pages_and_are_flagged(fp8):
+    pr = problem(11, [50, 40], 1, 8, 128, 16, fp8)
+    pr["bt"][0, 1] = -1
+    pr["bt"][1, 0] = 1 << 20
+    out, lse = run(pr)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.check_errors(0)
+    assert e.value.code == -7
+    check(pr, out, lse)
+
+
+def test_lengths_past_the_table_are_clamped_and_flagged():
+    pr = problem(12, [64, 40], 1, 8, 128, 16, True)
+    want = run(pr)
+    pr["bt"] = pr["bt"][:, :4].contiguous()
+    pr["sl"][0] = 100000
+    out, lse = run(pr)
+    with pytest.raises(pkv.PkvError):
+        pkv.check_errors(0)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_same_results_every_time_and_on_another_stream():
+    pr = problem(13, [9000, 3000, 17, 700], 2, 8, 128, 16, True, sinks=True)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in pr.items()}
+    first = run(pr, d=d)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        a, b = run(pr, d=d), run(pr, stream=side, d=d)
+        for o in (a, b):
+            assert torch.equal(o[0], first[0]) and torch.equal(o[1], first[1])
+    check(pr, *first)
+
+
+def test_agrees_with_the_bf16_decode_call():
+    """Without first tokens the window call computes what pkv_paged_decode_attn does: both
+    within the bound of the definition, and so within twice that of each other."""
+    pr = problem(14, EDGE_LENS, 2, 8, 128, 16, False, window=50, sinks=True)
+    out, lse = run(pr)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in pr.items()}
+    o2, l2 = torch.empty_like(d["q"]), torch.empty(d["q"].shape[:2], device="cuda")
+    pkv.paged_decode_attn(d["q"], d["kv"], d["bt"], d["sl"], d["sinks"], 50, d["scale"], 16, 0, o2, l2)
+    torch.cuda.synchronize()
+    check(pr, out, lse)
+    check(pr, o2.cpu(), l2.cpu())
+
+
+def test_captured_graphs_share_the_workspace_and_see_new_lengths():
+    a = problem(15, [4000, 900, 33], 2, 8, 128, 16, True)
+    b = problem(16, [2500, 1, 800, 64], 1, 8, 128, 16, False, 300, 4)
+    da, db = ({k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in p.items()} for p in (a, b))
+    outs = [(torch.zeros_like(d["q"]), torch.zeros(d["q"].shape[:2], device="cuda")) for d in (da, db)]
+    run(a)
+    graphs = []
+    for d, (o, l) in zip((da, db), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(d, o, l)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    check(a, outs[0][0].cpu(), outs[0][1].cpu())
+    check(b, outs[1][0].cpu(), outs[1][1].cpu())
+    da["sl"].copy_(torch.tensor([37, 0, 20], dtype=torch.int32))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    short = dict(a, sl=torch.tensor([37, 0, 20], dtype=torch.int32))
+    check(short, outs[0][0].cpu(), outs[0][1].cpu())
