@@ -1126,14 +1126,9 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   if ((rc = workspace_for(dev, stream, &st, &capturing))) return rc;
   pkv::PagedParams p;
   std::memset(&p, 0, sizeof p);
-  const int esz = fp8 ? 1 : 2;
   p.q = static_cast<const uint16_t*>(q->data);
   p.q_sb = q->stride[0];
   p.q_sh = q->stride[1];
-  p.kv = static_cast<const uint8_t*>(kv_cache->data);
-  p.kv_sblk = kv_cache->stride[0] * esz;
-  p.kv_sh = kv_cache->stride[1] * esz;
-  p.kv_stok = kv_cache->stride[2] * esz;
   if (fp8) {
     p.kv_scale = static_cast<const float*>(kv_scale->data);
     p.s_sblk = kv_scale->stride[0];
@@ -1160,9 +1155,53 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   p.first = first_tokens;
   p.scale = scale;
   p.err = st->ws.err;
+  while ((1 << p.page_shift) < page_size) ++p.page_shift;
+  const pkv::PagedShape shape = pkv::paged_attn_shape(int(D), fp8, p.G);
+  // CTAs: as many as run at once, or fewer when the tables cannot hold
+  // kPagedMinTiles tiles for each
+  const int64_t width = block_table->shape[1] * int64_t(page_size) / 16;
+  int64_t tiles = width;
+  if (window > 0)
+    tiles = std::min<int64_t>(width, (int64_t(window) + 14) / 16 + 1 + (int64_t(first_tokens) + 15) / 16);
+  if (width * 16 > (int64_t(1) << 31) - 256 || B * width >= (int64_t(1) << 31) ||
+      B * Hkv * width >= (int64_t(1) << 41))
+    return fail(PKV_ERR_UNSUPPORTED, "%lld requests of up to %lld keys", (long long)B,
+                (long long)(width * 16));
+  const pkv::Workspace& ws = st->ws;
+  p.min_tiles = pkv::kPagedMinTiles;
+  p.grid = int(std::max<int64_t>(
+      1, std::min<int64_t>(std::min(ws.num_sms * shape.ctas_per_sm, pkv::kPagedMaxGrid),
+                           (B * Hkv * tiles + p.min_tiles - 1) / p.min_tiles)));
+  if (int64_t(2) * p.grid * shape.part_floats * 4 > int64_t(ws.partial_bytes))
+    return fail(PKV_ERR_WORKSPACE, "workspace holds %lld bytes of partials, %lld needed",
+                (long long)ws.partial_bytes, (long long)(int64_t(2) * p.grid * shape.part_floats * 4));
+  p.partials = ws.partials;
+  p.pair_counters = ws.counters;
+  p.slot_counters = ws.counters + pkv::kTopCounters;
+  CUtensorMap map;
+  EncodeTiledFn encode = nullptr;
+  if ((rc = get_encoder(&encode))) return rc;
+  {
+    const cuuint64_t esz = fp8 ? 1 : 2, piece = 128 / esz;
+    const cuuint64_t gdim[5] = {piece, cuuint64_t(page_size), cuuint64_t(shape.chunks),
+                                cuuint64_t(Hkv), cuuint64_t(kv_cache->shape[0])};
+    const cuuint64_t gstride[4] = {cuuint64_t(kv_cache->stride[2]) * esz, 128,
+                                   cuuint64_t(kv_cache->stride[1]) * esz,
+                                   cuuint64_t(kv_cache->stride[0]) * esz};
+    const cuuint32_t box[5] = {cuuint32_t(piece), 16, cuuint32_t(shape.chunks), 1, 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    const CUresult cr = encode(
+        &map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+        kv_cache->data, gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (cr != CUDA_SUCCESS)
+      return fail(PKV_ERR_INVALID_ARG, "cuTensorMapEncodeTiled rejected the kv_cache layout (%d)",
+                  (int)cr);
+  }
   if ((rc = order_streams(st, stream, capturing))) return rc;
   take_pages_written(st, stream);
-  const cudaError_t e = pkv::launch_paged_attn(p, stream);
+  const cudaError_t e = pkv::launch_paged_attn(p, map, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return PKV_OK;
 }

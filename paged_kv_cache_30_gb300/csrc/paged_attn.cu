@@ -8,9 +8,32 @@
 //   lse = m + log sum_j e^(x_j - m)                (keys alone; -inf without a key)
 // over j in [0, first) and [max(L - window, 0), L), m = max_j x_j.
 //
-// One warp per (request, query head): lane l holds dims [l D/32, (l + 1) D/32)
-// of q and of the output; one pass over the keys with the running maximum and
-// sum in 32 bits.
+// Bound by memory: every visible key and value is read once, from DRAM.
+//
+//  * Work: the 16-token tiles that hold a visible key, laid end to end over
+//    (request, kv head).  CTA c takes tiles [c T / grid, (c + 1) T / grid) of all
+//    T, so every CTA streams the same number of bytes whatever the lengths; a cut
+//    within a few tiles of a request's border moves to the border.  Each CTA finds
+//    its cuts in a prefix sum of the requests' tile counts, in shared memory.
+//  * Each of the four warps takes every fourth tile of the CTA's range through a
+//    ring of its own: lane 0 asks for a tile with one TMA operation, the warp reads
+//    the fragments of a landed tile into registers, and lane 0 asks for the next
+//    tile into the same stage.  No warp waits for another, and a ring runs on
+//    across the borders of requests.  Block-table entries (and scales) are read
+//    32 tiles ahead, one lane each.
+//  * S[rows x 16 tokens] = Q K^T and O^T[dims x rows] += V^T P^T on
+//    mma.m16n8k16, rows = the G query heads (one or two blocks of 8).  e4m3 keys
+//    and values become fp16 exactly; the query is scaled to fp16's range by a
+//    power of two for each row (exact but for elements below 2^-29 of the row's
+//    largest).
+//  * One pass with the running maximum m and sum l in 32 bits.  With scales, the
+//    accumulator holds sum_j 2^(x_j + log2 vs_j - R) code_j under a running
+//    maximum R of its own, so a page of large or small values keeps its
+//    precision: the weights are rounded to fp16 (11 bits) relative to the largest
+//    contribution; for the bf16 cache they are rounded to bf16, as V is bf16.
+//  * A request cut between CTAs: each publishes its 32-bit (O, m, l, R); the last
+//    CTA of a group of up to 16 (an arrival counter) merges the group in order,
+//    the last group merges the groups.  Results do not depend on timing.
 #include "pkv_internal.h"
 #include "ptx.cuh"
 
@@ -18,95 +41,697 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMergeGroup = 16;
+constexpr int kSnapTiles = 8;      // a cut this near a request's border moves there
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)c));
-  float f;
-  asm("{.reg .f16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, l;}" : "=f"(f) : "r"(h2));
-  return f;
+template <int D_, bool kFp8_, int NB_>
+struct Cfg {
+  static constexpr int D = D_, NB = NB_;
+  static constexpr bool kFp8 = kFp8_;
+  static constexpr int kRows = 8 * NB;
+  static constexpr int kChunks = 2 * D * (kFp8 ? 1 : 2) / 128;  // 128-byte pieces of a [K | V] row
+  static constexpr int kTileBytes = 16 * 128 * kChunks;
+  static constexpr int kCtas = (D == 128 && (NB == 2 || !kFp8)) ? 2 : 3;  // per SM
+  static constexpr int kWbRow = D + 4;
+  static constexpr int kWbFloats = kRows * kWbRow + 3 * kRows;  // O, m, l, R of one warp
+  static constexpr int kPartFloats = kRows * D + 3 * kRows;
+  // what the merge buffer and the prefix sums of the largest batch leave of an SM
+  static constexpr int kFixed = kWarps * kWbFloats * 4 + (kPagedMaxBatch + 1) * 4 + 2048 + 512;
+  static constexpr int kStages = (228 * 1024 / kCtas - kFixed) / (kWarps * kTileBytes);
+  static constexpr int kOffWb = kWarps * kStages * kTileBytes;
+  static constexpr int kOffBars = kOffWb + kWarps * kWbFloats * 4;
+  static constexpr int kOffMisc = kOffBars + kWarps * kStages * 8;
+  static constexpr int kOffPrefix = kOffMisc + 64;
+  static constexpr int smem_bytes(int B) { return kOffPrefix + (B + 1) * 4 + 1024; }
+  static_assert(kOffWb % 1024 == 0 && kOffBars % 8 == 0, "shared-memory offsets");
+  static_assert(kMergeGroup * 2 * 3 * kRows <= kWarps * kWbFloats, "merge scratch");
+  static_assert(kStages >= 2 && kStages <= 32, "ring stages");
+  static_assert(kCtas * (smem_bytes(kPagedMaxBatch) + 1024) <= 228 * 1024, "CTAs per SM");
+};
+
+// The tiles that a request of length L needs: [0, head) and [head + gap, end).
+struct Span {
+  int L, start, first;  // visible: j < first, or start <= j < L
+  int head, gap, tiles;
+};
+
+__device__ __forceinline__ Span span_of(const PagedParams& p, int raw) {
+  Span s;
+  s.L = min(max(raw, 0), p.max_blocks * p.page_size);
+  s.start = (p.window > 0 && s.L > p.window) ? s.L - p.window : 0;
+  s.first = min(p.first, s.start);
+  const int end = (s.L + 15) >> 4, from = s.start >> 4;
+  s.head = (s.first + 15) >> 4;
+  if (s.head >= from) s.head = from;
+  s.gap = from - s.head;
+  s.tiles = end - s.gap;
+  return s;
 }
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const PagedParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int Hq = p.Hkv * p.G;
-  if (w >= (long long)p.B * Hq) return;
-  const int b = (int)(w / Hq), h = (int)(w % Hq), kvh = h / p.G, P = p.page_size;
-  int L = __ldg(p.seq_lens + b);
-  if (L > p.max_blocks * P) {
-    if (lane == 0) atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
-    L = p.max_blocks * P;
+// Exclusive scan of one int per thread over the CTA; scratch: one int per warp.
+__device__ __forceinline__ int block_scan(int v, int* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
   }
-  const int start = (p.window > 0 && L > p.window) ? L - p.window : 0;
-  const int first = min(p.first, start);
-  float q[E], o[E];
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float((uint32_t)p.q[b * p.q_sb + h * p.q_sh + lane * E + e] << 16);
-    o[e] = 0.f;
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps - 1; ++w) before += w < warp ? scratch[w] : 0;
+  return before + incl - v;
+}
+
+// The request whose tiles hold place f, where prefix[b] is the tiles per kv head
+// before request b: the last b with prefix[b] * Hkv <= f.
+__device__ __forceinline__ int request_at(const int* prefix, int B, int Hkv, long long f) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)prefix[mid] * Hkv <= f) lo = mid; else hi = mid - 1;
   }
-  const float c2 = p.scale * kLog2e;
-  float m = -INFINITY, l = 0.f;
-  for (int j = first > 0 ? 0 : start; j < L; j = (j + 1 == first) ? start : j + 1) {
-    const int blk = __ldg(p.bt + b * p.bt_sb + j / P);
-    float k[E], v[E], ks = 1.f, vs = 1.f;
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) atomicOr(p.err, DEVERR_BAD_BLOCK);
-      for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;  // reads as zeros
-    } else {
-      const uint8_t* row = p.kv + blk * p.kv_sblk + kvh * p.kv_sh + (j % P) * p.kv_stok;
-      for (int e = 0; e < E; ++e) {
-        const int d = lane * E + e;
-        if (kFp8) {
-          k[e] = e4m3_to_f32(row[d]);
-          v[e] = e4m3_to_f32(row[D + d]);
-        } else {
-          k[e] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[d] << 16);
-          v[e] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[D + d] << 16);
+  return lo;
+}
+
+struct Pair {
+  int b, kvh, n;    // request, kv head, tiles
+  long long begin;  // place of its first tile
+};
+
+__device__ __forceinline__ Pair pair_at(const int* prefix, int B, int Hkv, long long f) {
+  Pair r;
+  r.b = request_at(prefix, B, Hkv, f);
+  r.n = prefix[r.b + 1] - prefix[r.b];
+  const long long base = (long long)prefix[r.b] * Hkv, off = f - base;
+  // 32-bit division where it suffices
+  r.kvh = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)r.n) : (int)(off / r.n);
+  r.begin = base + (long long)r.kvh * r.n;
+  return r;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {  // RNE, lo in bits 0..15
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two e4m3 codes (bits 0..15) to fp16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w) {
+  uint32_t r;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16_hi(uint32_t w) {  // bits 16..31
+  uint32_t r;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+template <bool kFp16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (kFp16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
+}
+
+// This thread's part of the output: row er (a query head of the kv head), dims
+// [ed, ed + E).
+template <class C>
+__device__ __forceinline__ void finalize(const PagedParams& p, int b, int kvh, int er, int ed,
+                                         const float (&o)[C::D / 16], float m, float l, float R) {
+  if (er >= p.G) return;
+  const int head = kvh * p.G + er;
+  float f = 0.f;
+  if (l != 0.f) {
+    const float den = l + (p.sinks ? ex2(__fmaf_rn(__ldg(p.sinks + head), kLog2e, -m)) : 0.f);
+    f = (C::kFp8 ? ex2(R - m) : 1.f) / den;
+  }
+  uint16_t* dst = p.out + b * p.o_sb + head * p.o_sh + ed;
+  if constexpr (C::D == 128)
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f),
+                   pack_bf16(o[4] * f, o[5] * f), pack_bf16(o[6] * f, o[7] * f));
+  else
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
+  if (ed == 0 && p.lse)
+    p.lse[b * p.lse_sb + head * p.lse_sh] = l != 0.f ? __fmaf_rn(m, kLn2, logf(l)) : -INFINITY;
+}
+
+// Weight of a partial with reference r under the common reference M.
+__device__ __forceinline__ float weight(float r, float M) { return r == -INFINITY ? 0.f : ex2(r - M); }
+
+template <class C>
+__device__ __forceinline__ void store_partial(const PagedParams& p, long long slot, int er, int ed,
+                                              const float (&o)[C::D / 16], float m, float l, float R) {
+  float* dst = p.partials + slot * C::kPartFloats + er * C::D + ed;
+#pragma unroll
+  for (int e = 0; e < C::D / 16; e += 4)
+    *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+  if (ed == 0) {
+    float* st = p.partials + slot * C::kPartFloats + C::kRows * C::D + er;
+    st[0] = m;
+    st[C::kRows] = l;
+    st[2 * C::kRows] = R;
+  }
+}
+
+// Merge partials k = 0 .. n - 1 (n <= 32) at slots slot_of(k) for this thread's
+// row and dims.  sml: shared scratch of n x 3 kRows floats, filled by the caller.
+template <class C, typename SlotOf>
+__device__ __forceinline__ void merge_partials(const PagedParams& p, int n, SlotOf slot_of,
+                                               const float* sml, int er, int ed,
+                                               float (&o)[C::D / 16], float& m, float& l, float& R) {
+  m = R = -INFINITY;
+  for (int k = 0; k < n; ++k) {
+    m = fmaxf(m, sml[k * 3 * C::kRows + er]);
+    R = fmaxf(R, sml[k * 3 * C::kRows + 2 * C::kRows + er]);
+  }
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < C::D / 16; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float* st = sml + k * 3 * C::kRows + er;
+    const float* src = p.partials + slot_of(k) * C::kPartFloats + er * C::D + ed;
+    l = __fmaf_rn(weight(st[0], m), st[C::kRows], l);
+    const float w = weight(st[2 * C::kRows], R);
+#pragma unroll
+    for (int e = 0; e < C::D / 16; e += 4) {
+      const float4 a = ldcg_f4(src + e);
+      o[e] = __fmaf_rn(w, a.x, o[e]);
+      o[e + 1] = __fmaf_rn(w, a.y, o[e + 1]);
+      o[e + 2] = __fmaf_rn(w, a.z, o[e + 2]);
+      o[e + 3] = __fmaf_rn(w, a.w, o[e + 3]);
+    }
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, C::kCtas)
+    paged_attn_kernel(const __grid_constant__ PagedParams p,
+                      const __grid_constant__ CUtensorMap kv_map) {
+  constexpr int D = C::D, NB = C::NB, kStages = C::kStages, E = D / 16;
+  constexpr bool kFp8 = C::kFp8;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base_u32 = (raw + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_u32 - raw);
+  float* wbuf = reinterpret_cast<float*>(base + C::kOffWb);
+  int* misc = reinterpret_cast<int*>(base + C::kOffMisc);
+  int* prefix = reinterpret_cast<int*>(base + C::kOffPrefix);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ring = base_u32 + warp * kStages * C::kTileBytes;
+  const uint32_t bars = base_u32 + C::kOffBars + warp * kStages * 8;
+  const int B = p.B, Hkv = p.Hkv;
+
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) tma_prefetch_desc(&kv_map);
+  griddep_wait();  // nothing of the caller's is read before
+
+  // ---- prefix[b]: tiles per kv head before request b ----
+  {
+    const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
+    int mine = 0;
+    for (int b = b0; b < min(b0 + per, B); ++b) {
+      const int len = __ldg(p.seq_lens + b);
+      if (blockIdx.x == 0 && len > p.max_blocks * p.page_size) atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
+      mine += span_of(p, len).tiles;
+    }
+    int run = block_scan(mine, misc);
+    for (int b = b0; b < min(b0 + per, B); ++b) {
+      prefix[b] = run;
+      run += span_of(p, __ldg(p.seq_lens + b)).tiles;
+      if (b == B - 1) prefix[B] = run;
+    }
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+
+  // requests without a key
+  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+    if (prefix[b + 1] != prefix[b]) continue;
+    for (int i = tid; i < Hkv * p.G * (D / 8); i += kThreads) {
+      const int h = i / (D / 8);
+      *reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + (i % (D / 8)) * 8) =
+          make_uint4(0, 0, 0, 0);
+      if (i % (D / 8) == 0 && p.lse) p.lse[b * p.lse_sb + h * p.lse_sh] = -INFINITY;
+    }
+  }
+
+  // ---- this CTA's tiles [f0, f1) ----
+  const long long total = (long long)prefix[B] * Hkv;
+  const long long chunk =
+      max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_tiles);
+  const long long snap = min((long long)kSnapTiles, chunk / 2);
+  auto cut = [&](long long c) -> long long {
+    const long long f = c * chunk;
+    if (f >= total) return total;
+    const Pair r = pair_at(prefix, B, Hkv, f);
+    if (f - r.begin <= snap) return r.begin;
+    if (r.begin + r.n - f <= snap) return r.begin + r.n;
+    return f;
+  };
+  const long long f0 = cut(blockIdx.x), f1 = cut((long long)blockIdx.x + 1);
+  // this warp's n-th tile is at place f0 + warp + 4 n
+  const int count = f1 - f0 > warp ? (int)((f1 - f0 - warp + kWarps - 1) / kWarps) : 0;
+
+  // ---- the loader ----
+  const int pshift = p.page_shift;
+  int l_blk = 0, l_pos = 0;     // lane's tile of the batch of 32: page; kv head, tile in the page
+  int n_blk = 0, n_pos = 0;     // the same of the next batch
+  float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;  // (ks, log2 vs) of an even, an odd batch
+  auto look_up = [&](int n) {
+    n_blk = n_pos = 0;
+    if (n >= count) return;
+    const long long f = f0 + warp + (long long)kWarps * n;
+    const Pair r = pair_at(prefix, B, Hkv, f);
+    const Span s = span_of(p, __ldg(p.seq_lens + r.b));
+    int tau = (int)(f - r.begin);
+    if (tau >= s.head) tau += s.gap;
+    const int page = tau >> (pshift - 4);
+    n_pos = (r.kvh << 3) | (tau & ((1 << (pshift - 4)) - 1));
+    n_blk = __ldg(p.bt + r.b * p.bt_sb + page);
+  };
+  // batch `at` becomes the current one, the next is looked up
+  auto turn = [&](int at) {
+    l_blk = n_blk;
+    l_pos = n_pos;
+    const bool in = 32 * at + lane < count, good = l_blk >= 0 && l_blk < p.num_blocks;
+    if (in && !good) atomicOr(p.err, DEVERR_BAD_BLOCK);  // reads as zeros
+    if (kFp8) {
+      float2 v = make_float2(0.f, 0.f);
+      if (in && good)
+        v = __ldg(reinterpret_cast<const float2*>(p.kv_scale + l_blk * p.s_sblk +
+                                                  (l_pos >> 3) * p.s_sh));
+      v.y = lg2(v.y);
+      if (at & 1) sc1 = v; else sc0 = v;
+    }
+    look_up(32 * (at + 1) + lane);
+  };
+  auto issue = [&](int n) {  // n < count; every 32nd call turns the batch
+    if ((n & 31) == 0) turn(n >> 5);
+    const int blk = __shfl_sync(0xffffffffu, l_blk, n & 31);
+    const int pos = __shfl_sync(0xffffffffu, l_pos, n & 31);
+    if (lane == 0) {
+      const int s = n % kStages;
+      mbar_arrive_expect_tx(bars + 8 * s, C::kTileBytes);
+      tma_load_5d(ring + s * C::kTileBytes, &kv_map, bars + 8 * s, 0, (pos & 7) * 16, 0, pos >> 3,
+                  blk);
+    }
+  };
+  __syncwarp();  // the ring's barriers are lane 0's
+  look_up(lane);
+  int issued = 0;
+  for (; issued < min(count, kStages); ++issued) issue(issued);
+
+  // ---- fragment addresses ----
+  // ldmatrix: matrix mi = lane / 8 takes its 8 rows from lanes 8 mi .. 8 mi + 7.
+  // K: matrices (tokens 0..7, unit u), (0..7, u + 1), (8..15, u), (8..15, u + 1).
+  // V (transposed): (tokens 0..7, unit u), (8..15, u), (0..7, u + 1), (8..15, u + 1).
+  // The 128-byte swizzle XORs a 16-byte unit's index with its token modulo 8.
+  const int g = lane >> 2, t = lane & 3, mi = lane >> 3, r8 = lane & 7;
+  const uint32_t k_row = (uint32_t)(r8 + 8 * (mi >> 1)) * 128u, v_row = (uint32_t)(r8 + 8 * (mi & 1)) * 128u;
+  const int k_unit = mi & 1, v_unit = mi >> 1;
+  // byte offset o of a [K | V] row lies in 128-byte piece o / 128, unit o % 128 / 16
+  auto k_addr = [&](int unit) {
+    return (uint32_t)(unit >> 3) * 2048u + k_row + (uint32_t)(((unit + k_unit) & 7) ^ r8) * 16u;
+  };
+  auto v_addr = [&](int unit) {
+    return (uint32_t)(unit >> 3) * 2048u + v_row + (uint32_t)(((unit + v_unit) & 7) ^ r8) * 16u;
+  };
+  constexpr int kUnits = D * (kFp8 ? 1 : 2) / 16;  // 16-byte units of a K (or V) row
+
+  const int er = tid >> 4, ed = (tid & 15) * E;  // this thread's part of an output
+  float* my_wb = wbuf + warp * C::kWbFloats;
+  bool ok = true;
+  int n = 0;
+
+  for (long long f = f0; f < f1;) {
+    const Pair pr = pair_at(prefix, B, Hkv, f);
+    const long long seg_end = min(pr.begin + pr.n, f1);
+    const Span sp = span_of(p, __ldg(p.seq_lens + pr.b));
+
+    // ---- the query rows as the A operand ----
+    uint32_t qa[D / 16][2 * NB];
+    float row_scale[NB];  // logits of row g (g + 8) in log2 units per unit of S
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = g + 8 * nb;
+      const uint16_t* q = p.q + pr.b * p.q_sb + (pr.kvh * p.G + row) * p.q_sh;
+      row_scale[nb] = p.scale * kLog2e;
+      if constexpr (kFp8) {
+        // k-step c, columns 2t, 2t + 1, 2t + 8, 2t + 9 <- dims 16 c + 4 t .. + 3
+        uint2 w[D / 16];
+        uint32_t big = 0;  // largest magnitude, as bits
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          w[c] = row < p.G ? __ldg(reinterpret_cast<const uint2*>(q + 16 * c + 4 * t))
+                           : make_uint2(0, 0);
+          big = max(max(big, max((w[c].x << 16) & 0x7fffffffu, w[c].x & 0x7fff0000u)),
+                    max((w[c].y << 16) & 0x7fffffffu, w[c].y & 0x7fff0000u));
+        }
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^up brings the largest element into [2^14, 2^15); 0 and non-finite rows stay
+        const int ex = (int)(big >> 23);
+        const int up = ex == 0 || ex == 255 ? 0 : max(min(127 + 14 - ex, 126), -126);
+        const float mul = __uint_as_float((uint32_t)(up + 127) << 23);
+        row_scale[nb] *= __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          qa[c][nb] = pack_f16(__uint_as_float(w[c].x << 16) * mul,
+                               __uint_as_float(w[c].x & 0xffff0000u) * mul);
+          qa[c][NB + nb] = pack_f16(__uint_as_float(w[c].y << 16) * mul,
+                                    __uint_as_float(w[c].y & 0xffff0000u) * mul);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(q + 16 * c + 2 * t);
+          qa[c][nb] = row < p.G ? __ldg(w) : 0u;
+          qa[c][NB + nb] = row < p.G ? __ldg(w + 4) : 0u;
         }
       }
+    }
+
+    float acc[NB][E][4];
+    float m[NB], l[NB], R[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb] = R[nb] = -INFINITY;
+      l[nb] = 0.f;
+#pragma unroll
+      for (int c = 0; c < E; ++c) acc[nb][c][0] = acc[nb][c][1] = acc[nb][c][2] = acc[nb][c][3] = 0.f;
+    }
+
+    for (; ok && f0 + warp + (long long)kWarps * n < seg_end; ++n) {
+      const int stage = n % kStages;
+      ok = mbar_wait(bars + 8 * stage, (n / kStages) & 1, p.err);
+      if (!ok) break;
+      const uint32_t tile = ring + stage * C::kTileBytes;
+      uint32_t kf[kUnits / 2][4], vf[kUnits / 2][4];
+#pragma unroll
+      for (int u = 0; u < kUnits / 2; ++u)
+        ldsm_x4(tile + k_addr(2 * u), kf[u][0], kf[u][1], kf[u][2], kf[u][3]);
+#pragma unroll
+      for (int u = 0; u < kUnits / 2; ++u)
+        ldsm_x4_trans(tile + v_addr(kUnits + 2 * u), vf[u][0], vf[u][1], vf[u][2], vf[u][3]);
+      fence_proxy_async_smem();  // the stage is refilled by TMA
+      __syncwarp();
+      // the scales of tile n, before its batch's registers can be turned over
+      float ks = 1.f, lv = 0.f;
       if (kFp8) {
-        const float* sc = p.kv_scale + blk * p.s_sblk + kvh * p.s_sh;
-        ks = sc[0];
-        vs = sc[1];
+        const bool odd = (n >> 5) & 1;
+        ks = __shfl_sync(0xffffffffu, odd ? sc1.x : sc0.x, n & 31);
+        lv = __shfl_sync(0xffffffffu, odd ? sc1.y : sc0.y, n & 31);
+      }
+      if (issued < count) issue(issued++);
+
+      // ---- S = Q K^T: tokens 0..7 (sa) and 8..15 (sb), two chains each ----
+      float sa[2][4], sb[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sa[i][e] = sb[i][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint32_t a0 = qa[c][0], a1 = NB == 2 ? qa[c][1] : 0u;
+        const uint32_t a2 = qa[c][NB], a3 = NB == 2 ? qa[c][NB + 1] : 0u;
+        if constexpr (kFp8) {
+          const uint32_t x = kf[c / 2][c & 1], y = kf[c / 2][2 + (c & 1)];
+          mma<true>(sa[c & 1], a0, a1, a2, a3, e4m3x2_f16(x), e4m3x2_f16_hi(x));
+          mma<true>(sb[c & 1], a0, a1, a2, a3, e4m3x2_f16(y), e4m3x2_f16_hi(y));
+        } else {
+          mma<false>(sa[c & 1], a0, a1, a2, a3, kf[c][0], kf[c][1]);
+          mma<false>(sb[c & 1], a0, a1, a2, a3, kf[c][2], kf[c][3]);
+        }
+      }
+
+      // ---- visibility ----
+      int tau = (int)(f0 + warp + (long long)kWarps * n - pr.begin);
+      if (tau >= sp.head) tau += sp.gap;
+      const int tok = tau * 16;
+      const bool whole = tok + 16 <= sp.L && (tok >= sp.start || tok + 16 <= sp.first);
+      bool see[4] = {true, true, true, true};  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = tok + 2 * t + (i & 1) + 8 * (i >> 1);
+          see[i] = j < sp.L && (j >= sp.start || j < sp.first);
+        }
+        // values that nobody sees may be anything: zero them, as 0 * NaN is NaN
+        const uint32_t mlo = (see[0] ? 0xffffu : 0u) | (see[1] ? 0xffff0000u : 0u);
+        const uint32_t mhi = (see[2] ? 0xffffu : 0u) | (see[3] ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int u = 0; u < kUnits / 2; ++u) {
+          vf[u][0] &= mlo; vf[u][1] &= mhi; vf[u][2] &= mlo; vf[u][3] &= mhi;
+        }
+      }
+
+      // ---- online softmax in log2 units ----
+      uint32_t pb[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float c2 = kFp8 ? row_scale[nb] * ks : row_scale[nb];
+        float x[4] = {(sa[0][2 * nb] + sa[1][2 * nb]) * c2, (sa[0][2 * nb + 1] + sa[1][2 * nb + 1]) * c2,
+                      (sb[0][2 * nb] + sb[1][2 * nb]) * c2, (sb[0][2 * nb + 1] + sb[1][2 * nb + 1]) * c2};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = see[i] ? x[i] : -INFINITY;
+        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[nb], mx), mref = mn == -INFINITY ? 0.f : mn;
+        const float alpha = ex2(m[nb] - mref);
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = ex2(x[i] - mref);
+        l[nb] = __fmaf_rn(l[nb], alpha, (e[0] + e[1]) + (e[2] + e[3]));
+        m[nb] = mn;
+        float beta = alpha;
+        if constexpr (kFp8) {
+          const float Rn = fmaxf(R[nb], mx + lv), shift = Rn == -INFINITY ? 0.f : Rn;
+          beta = ex2(R[nb] - shift);
+          R[nb] = Rn;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = ex2(x[i] + (lv - shift));
+          pb[nb][0] = pack_f16(e[0], e[1]);
+          pb[nb][1] = pack_f16(e[2], e[3]);
+        } else {
+          pb[nb][0] = pack_bf16(e[0], e[1]);
+          pb[nb][1] = pack_bf16(e[2], e[3]);
+        }
+        // rows 2t, 2t + 1 are the accumulator's columns; their factors are on lanes 8t, 8t + 4
+        if (__any_sync(0xffffffffu, beta != 1.f)) {
+          const float b0 = __shfl_sync(0xffffffffu, beta, 8 * t);
+          const float b1 = __shfl_sync(0xffffffffu, beta, 8 * t + 4);
+#pragma unroll
+          for (int c = 0; c < E; ++c) {
+            acc[nb][c][0] *= b0; acc[nb][c][1] *= b1; acc[nb][c][2] *= b0; acc[nb][c][3] *= b1;
+          }
+        }
+      }
+
+      // ---- O^T += V^T P^T ----
+#pragma unroll
+      for (int c = 0; c < E; ++c) {
+        uint32_t a0, a1, a2, a3;
+        if constexpr (kFp8) {
+          // a register holds (token 2t: dims 2g, 2g + 1; token 2t + 1: the same)
+          const uint32_t lo = vf[c / 2][2 * (c & 1)], hi = vf[c / 2][2 * (c & 1) + 1];
+          const uint32_t lp = __byte_perm(lo, 0, 0x3120), hp = __byte_perm(hi, 0, 0x3120);
+          a0 = e4m3x2_f16(lp); a1 = e4m3x2_f16_hi(lp);
+          a2 = e4m3x2_f16(hp); a3 = e4m3x2_f16_hi(hp);
+        } else {
+          // units 2c and 2c + 1 of V: dims 16c + g and 16c + 8 + g
+          a0 = vf[c][0]; a1 = vf[c][2]; a2 = vf[c][1]; a3 = vf[c][3];
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma<kFp8>(acc[nb][c], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
       }
     }
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = __fmaf_rn(q[e], k[e], s);
-    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-    const float x = s * ks * c2;
-    const float mn = fmaxf(m, x);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float alpha = ex2(m - ref), pr = ex2(x - ref);
-    l = __fmaf_rn(l, alpha, pr);
-    for (int e = 0; e < E; ++e) o[e] = __fmaf_rn(o[e], alpha, pr * vs * v[e]);
-    m = mn;
+
+    // ---- merge the warps ----
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 1);
+      l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 2);
+      float* r0 = my_wb + (8 * nb + 2 * t) * C::kWbRow;
+      float* r1 = r0 + C::kWbRow;
+#pragma unroll
+      for (int c = 0; c < E; ++c) {
+        // rows of the accumulator: dims 16c + 2g and 16c + 2g + 1 (e4m3), 16c + g and + 8 (bf16)
+        const int d0 = 16 * c + (kFp8 ? 2 * g : g), d1 = d0 + (kFp8 ? 1 : 8);
+        r0[d0] = acc[nb][c][0]; r1[d0] = acc[nb][c][1];
+        r0[d1] = acc[nb][c][2]; r1[d1] = acc[nb][c][3];
+      }
+      if (t == 0) {
+        float* st = my_wb + C::kRows * C::kWbRow + 8 * nb + g;
+        st[0] = m[nb];
+        st[C::kRows] = l[nb];
+        st[2 * C::kRows] = kFp8 ? R[nb] : m[nb];
+      }
+    }
+    __syncthreads();
+    float o[NB][E], mc[NB], lc[NB], Rc[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const float* st = wbuf + C::kRows * C::kWbRow + er + 8 * nb;
+      mc[nb] = Rc[nb] = -INFINITY;
+      lc[nb] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        mc[nb] = fmaxf(mc[nb], st[w * C::kWbFloats]);
+        Rc[nb] = fmaxf(Rc[nb], st[w * C::kWbFloats + 2 * C::kRows]);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[nb][e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* sw = st + w * C::kWbFloats;
+        lc[nb] = __fmaf_rn(weight(sw[0], mc[nb]), sw[C::kRows], lc[nb]);
+        const float wt = weight(sw[2 * C::kRows], Rc[nb]);
+        const float* ow = wbuf + w * C::kWbFloats + (er + 8 * nb) * C::kWbRow + ed;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(ow + e);
+          o[nb][e] = __fmaf_rn(wt, a.x, o[nb][e]);
+          o[nb][e + 1] = __fmaf_rn(wt, a.y, o[nb][e + 1]);
+          o[nb][e + 2] = __fmaf_rn(wt, a.z, o[nb][e + 2]);
+          o[nb][e + 3] = __fmaf_rn(wt, a.w, o[nb][e + 3]);
+        }
+      }
+    }
+
+    if (f == pr.begin && seg_end == pr.begin + pr.n) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+      __syncthreads();  // wbuf is the next request's
+    } else {
+      // Contributors: the CTA whose range holds the first tile (slot 2 c + 1) and the
+      // ones whose cuts lie inside (slot 2 c).  A cut at c * chunk lies inside when it
+      // is more than snap tiles from either border.
+      const long long c0 = (pr.begin + snap) / chunk, c1 = (pr.begin + pr.n - snap - 1) / chunk;
+      const int parts = (int)(c1 - c0 + 1), me = (int)(blockIdx.x - c0);
+      auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        store_partial<C>(p, slot_of(me), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+      const int gi = me / kMergeGroup, gfirst = gi * kMergeGroup;
+      const int gsize = min(kMergeGroup, parts - gfirst);
+      const int groups = (parts + kMergeGroup - 1) / kMergeGroup;
+      int* gcnt = p.slot_counters + slot_of(gfirst);
+      int* tcnt = p.pair_counters + pr.b * Hkv + pr.kvh;
+      // stats of partials first, first + step, ... into shared memory
+      auto gather = [&](int first, int step, int cnt) {
+        for (int i = tid; i < cnt * 3 * C::kRows; i += kThreads)
+          wbuf[i] = __ldcg(p.partials + slot_of(first + i / (3 * C::kRows) * step) * C::kPartFloats +
+                           C::kRows * D + i % (3 * C::kRows));
+        __syncthreads();
+      };
+      __syncthreads();
+      if (tid == 0) misc[8] = atomic_add_acq_rel_gpu(gcnt, 1);
+      __syncthreads();
+      if (misc[8] == gsize - 1) {
+        if (tid == 0) store_relaxed_gpu(gcnt, 0);
+        gather(gfirst, 1, gsize);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          merge_partials<C>(p, gsize, [&](int k) { return slot_of(gfirst + k); }, wbuf, er + 8 * nb,
+                            ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+          if (groups == 1)
+            finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+          else
+            store_partial<C>(p, slot_of(gfirst), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+        }
+        if (groups > 1) {
+          __syncthreads();
+          if (tid == 0) misc[9] = atomic_add_acq_rel_gpu(tcnt, 1);
+          __syncthreads();
+          if (misc[9] == groups - 1) {
+            if (tid == 0) store_relaxed_gpu(tcnt, 0);
+            gather(0, kMergeGroup, groups);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              merge_partials<C>(p, groups, [&](int k) { return slot_of(k * kMergeGroup); }, wbuf,
+                                er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+              finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+            }
+          }
+        }
+      }
+      __syncthreads();  // wbuf and misc are the next request's
+    }
+    f = seg_end;
   }
-  float inv = 0.f;
-  if (l != 0.f) inv = 1.f / (l + (p.sinks ? ex2(__ldg(p.sinks + h) * kLog2e - m) : 0.f));
-  for (int e = 0; e < E; ++e)
-    p.out[b * p.o_sb + h * p.o_sh + lane * E + e] = (uint16_t)pack_bf16(o[e] * inv, 0.f);
-  if (lane == 0 && p.lse)
-    p.lse[b * p.lse_sb + h * p.lse_sh] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
+
+  // A wait that gave up leaves copies in flight: wait for them (again with a
+  // limit) before the shared memory goes to another CTA.
+  if (!ok)
+    for (; n < issued; ++n) mbar_wait(bars + 8 * (n % kStages), (n / kStages) & 1, p.err);
 }
 
-template <int D, bool kFp8>
-cudaError_t launch_t(const PagedParams& p, cudaStream_t stream) {
-  const long long warps = (long long)p.B * p.Hkv * p.G;
-  paged_attn_kernel<D, kFp8>
-      <<<(unsigned)((warps + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+template <class C>
+cudaError_t launch_t(PagedParams p, const CUtensorMap& map, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = set_smem_attr_once(paged_attn_kernel<C>, C::smem_bytes(kPagedMaxBatch), done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::smem_bytes(p.B);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<C>, p, map);
+}
+
+template <typename F>
+auto with_cfg(int D, bool fp8, int G, F f) {
+  if (D == 64) {
+    if (fp8) return G <= 8 ? f(Cfg<64, true, 1>()) : f(Cfg<64, true, 2>());
+    return G <= 8 ? f(Cfg<64, false, 1>()) : f(Cfg<64, false, 2>());
+  }
+  if (fp8) return G <= 8 ? f(Cfg<128, true, 1>()) : f(Cfg<128, true, 2>());
+  return G <= 8 ? f(Cfg<128, false, 1>()) : f(Cfg<128, false, 2>());
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn(const PagedParams& p, cudaStream_t stream) {
-  if (p.D == 64) return p.kv_scale ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);
-  return p.kv_scale ? launch_t<128, true>(p, stream) : launch_t<128, false>(p, stream);
+PagedShape paged_attn_shape(int D, bool fp8, int G) {
+  return with_cfg(D, fp8, G, [](auto c) {
+    using C = decltype(c);
+    return PagedShape{C::kCtas, C::kPartFloats, C::kChunks};
+  });
+}
+
+cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& map, cudaStream_t stream) {
+  return with_cfg(p.D, p.kv_scale != nullptr, p.G,
+                  [&](auto c) { return launch_t<decltype(c)>(p, map, stream); });
 }
 
 }  // namespace pkv

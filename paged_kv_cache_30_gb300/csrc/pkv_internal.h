@@ -234,8 +234,6 @@ constexpr int kPagedMaxBatch = 2048;
 struct PagedParams {
   const uint16_t* q;             // bf16 [B, Hq, D]
   int64_t q_sb, q_sh;
-  const uint8_t* kv;             // cache base
-  int64_t kv_sblk, kv_sh, kv_stok;  // bytes: page, kv head, token
   const float* kv_scale;         // [num_blocks, Hkv, 2] (K, V), or null (bf16 cache)
   int64_t s_sblk, s_sh;          // its strides in floats
   const int32_t* bt;
@@ -250,9 +248,23 @@ struct PagedParams {
   int B, Hkv, G, D, page_size;
   int window, first;
   float scale;
+  int page_shift;                // log2(page_size)
+  int grid, min_tiles;           // CTAs; fewest 16-token tiles of one
+  float* partials;               // [2 * grid] slots
+  int* slot_counters;            // [2 * grid] arrival counters of merge groups
+  int* pair_counters;            // [B * Hkv] arrival counters of the groups
   int* err;
 };
-cudaError_t launch_paged_attn(const PagedParams& p, cudaStream_t stream);
+struct PagedShape {
+  int ctas_per_sm, part_floats;  // floats of one partial
+  int chunks;                    // 128-byte pieces of a token's [K | V] row
+};
+PagedShape paged_attn_shape(int D, bool fp8, int G);
+// kv_map: the cache as (128-byte piece's elements, token, piece, kv head, page),
+// box (a piece, 16 tokens, all pieces, 1, 1), 128-byte swizzle.
+cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
+constexpr int kPagedMinTiles = 16;
+constexpr int kPagedMaxGrid = 512;  // 32 merge groups of 16
 
 // ------------------------------------------------ append to an e4m3 cache --
 struct AppendFp8Params {
