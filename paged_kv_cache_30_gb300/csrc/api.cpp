@@ -1158,7 +1158,7 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
   const pkv::PagedShape shape = pkv::paged_attn_shape(int(D), fp8, p.G);
   // CTAs: as many as run at once, or fewer when the tables cannot hold
-  // kPagedMinTiles tiles for each
+  // kPagedMinCost of work for each
   const int64_t width = block_table->shape[1] * int64_t(page_size) / 16;
   int64_t tiles = width;
   if (window > 0)
@@ -1168,10 +1168,10 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
     return fail(PKV_ERR_UNSUPPORTED, "%lld requests of up to %lld keys", (long long)B,
                 (long long)(width * 16));
   const pkv::Workspace& ws = st->ws;
-  p.min_tiles = pkv::kPagedMinTiles;
+  const int64_t cost = B * Hkv * (tiles + pkv::kPagedPairCost);
   p.grid = int(std::max<int64_t>(
       1, std::min<int64_t>(std::min(ws.num_sms * shape.ctas_per_sm, pkv::kPagedMaxGrid),
-                           (B * Hkv * tiles + p.min_tiles - 1) / p.min_tiles)));
+                           (cost + pkv::kPagedMinCost - 1) / pkv::kPagedMinCost)));
   if (int64_t(2) * p.grid * shape.part_floats * 4 > int64_t(ws.partial_bytes))
     return fail(PKV_ERR_WORKSPACE, "workspace holds %lld bytes of partials, %lld needed",
                 (long long)ws.partial_bytes, (long long)(int64_t(2) * p.grid * shape.part_floats * 4));

@@ -11,10 +11,11 @@
 // Bound by memory: every visible key and value is read once, from DRAM.
 //
 //  * Work: the 16-token tiles that hold a visible key, laid end to end over
-//    (request, kv head).  CTA c takes tiles [c T / grid, (c + 1) T / grid) of all
-//    T, so every CTA streams the same number of bytes whatever the lengths; a cut
-//    within a few tiles of a request's border moves to the border.  Each CTA finds
-//    its cuts in a prefix sum of the requests' tile counts, in shared memory.
+//    (request, kv head) pairs.  CTA c takes an equal share of all tiles plus
+//    kPairCost for each pair (starting and ending a pair costs a CTA about as much
+//    as that many tiles), so the CTAs end together whatever the lengths; a cut
+//    within a few tiles of a pair's border moves to the border.  Each CTA finds its
+//    cuts in a prefix sum of the requests' tile counts, in shared memory.
 //  * Each of the four warps takes every fourth tile of the CTA's range through a
 //    ring of its own: lane 0 asks for a tile with one TMA operation, the warp reads
 //    the fragments of a landed tile into registers, and lane 0 asks for the next
@@ -43,7 +44,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMergeGroup = 16;
-constexpr int kSnapTiles = 8;      // a cut this near a request's border moves there
+constexpr int kPairCost = kPagedPairCost;
+constexpr int kSnapTiles = 8;      // a cut this near a pair's border moves there
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -59,14 +61,18 @@ struct Cfg {
   static constexpr int kWbFloats = kRows * kWbRow + 3 * kRows;  // O, m, l, R of one warp
   static constexpr int kPartFloats = kRows * D + 3 * kRows;
   // what the merge buffer and the prefix sums of the largest batch leave of an SM
-  static constexpr int kFixed = kWarps * kWbFloats * 4 + (kPagedMaxBatch + 1) * 4 + 2048 + 512;
+  // query rows of two pairs (of one where two leave the ring a single stage)
+  static constexpr int kQSlots = D == 128 && NB == 2 && !kFp8 ? 1 : 2;
+  static constexpr int kQBytes = kQSlots * kRows * D * 2;
+  static constexpr int kFixed = kWarps * kWbFloats * 4 + kQBytes + (kPagedMaxBatch + 1) * 4 + 2048 + 512;
   static constexpr int kStages = (228 * 1024 / kCtas - kFixed) / (kWarps * kTileBytes);
   static constexpr int kOffWb = kWarps * kStages * kTileBytes;
-  static constexpr int kOffBars = kOffWb + kWarps * kWbFloats * 4;
+  static constexpr int kOffQ = kOffWb + kWarps * kWbFloats * 4;
+  static constexpr int kOffBars = kOffQ + kQBytes;
   static constexpr int kOffMisc = kOffBars + kWarps * kStages * 8;
   static constexpr int kOffPrefix = kOffMisc + 64;
   static constexpr int smem_bytes(int B) { return kOffPrefix + (B + 1) * 4 + 1024; }
-  static_assert(kOffWb % 1024 == 0 && kOffBars % 8 == 0, "shared-memory offsets");
+  static_assert(kOffWb % 1024 == 0 && kOffQ % 16 == 0 && kOffBars % 8 == 0, "shared-memory offsets");
   static_assert(kMergeGroup * 2 * 3 * kRows <= kWarps * kWbFloats, "merge scratch");
   static_assert(kStages >= 2 && kStages <= 32, "ring stages");
   static_assert(kCtas * (smem_bytes(kPagedMaxBatch) + 1024) <= 228 * 1024, "CTAs per SM");
@@ -108,30 +114,27 @@ __device__ __forceinline__ int block_scan(int v, int* scratch) {
   return before + incl - v;
 }
 
-// The request whose tiles hold place f, where prefix[b] is the tiles per kv head
-// before request b: the last b with prefix[b] * Hkv <= f.
-__device__ __forceinline__ int request_at(const int* prefix, int B, int Hkv, long long f) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)prefix[mid] * Hkv <= f) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
 struct Pair {
   int b, kvh, n;    // request, kv head, tiles
   long long begin;  // place of its first tile
 };
 
+// The pair at place f, each pair being `extra` + its tiles long.
+template <int extra>
 __device__ __forceinline__ Pair pair_at(const int* prefix, int B, int Hkv, long long f) {
+  int lo = 0, hi = B - 1;  // the last request that begins at or before f
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (((long long)prefix[mid] + extra * mid) * Hkv <= f) lo = mid; else hi = mid - 1;
+  }
   Pair r;
-  r.b = request_at(prefix, B, Hkv, f);
-  r.n = prefix[r.b + 1] - prefix[r.b];
-  const long long base = (long long)prefix[r.b] * Hkv, off = f - base;
+  r.b = lo;
+  r.n = prefix[lo + 1] - prefix[lo];
+  const long long base = ((long long)prefix[lo] + extra * lo) * Hkv, off = f - base;
+  const int len = r.n + extra;
   // 32-bit division where it suffices
-  r.kvh = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)r.n) : (int)(off / r.n);
-  r.begin = base + (long long)r.kvh * r.n;
+  r.kvh = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)len) : (int)(off / len);
+  r.begin = base + (long long)r.kvh * len;
   return r;
 }
 
@@ -159,6 +162,15 @@ __device__ __forceinline__ uint32_t e4m3x2_f16_hi(uint32_t w) {  // bits 16..31
   return r;
 }
 
+// 16 bytes to shared memory, `bytes` of them from src, the rest zero.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 template <bool kFp16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -173,15 +185,15 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 }
 
 // This thread's part of the output: row er (a query head of the kv head), dims
-// [ed, ed + E).
+// [ed, ed + E); sink in log2 units, -inf for none.
 template <class C>
 __device__ __forceinline__ void finalize(const PagedParams& p, int b, int kvh, int er, int ed,
-                                         const float (&o)[C::D / 16], float m, float l, float R) {
+                                         float sink, const float (&o)[C::D / 16], float m, float l, float R) {
   if (er >= p.G) return;
   const int head = kvh * p.G + er;
   float f = 0.f;
   if (l != 0.f) {
-    const float den = l + (p.sinks ? ex2(__fmaf_rn(__ldg(p.sinks + head), kLog2e, -m)) : 0.f);
+    const float den = l + ex2(sink - m);
     f = (C::kFp8 ? ex2(R - m) : 1.f) / den;
   }
   uint16_t* dst = p.out + b * p.o_sb + head * p.o_sh + ed;
@@ -300,17 +312,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   }
 
   // ---- this CTA's tiles [f0, f1) ----
-  const long long total = (long long)prefix[B] * Hkv;
-  const long long chunk =
-      max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_tiles);
-  const long long snap = min((long long)kSnapTiles, chunk / 2);
+  // cuts are placed in the space of costs and turned into places of tiles
+  const long long total = ((long long)prefix[B] + (long long)kPairCost * B) * Hkv;
+  const long long chunk = max((total + gridDim.x - 1) / gridDim.x, (long long)kPagedMinCost);
+  const int snap = (int)min((long long)kSnapTiles, chunk / 2);
   auto cut = [&](long long c) -> long long {
-    const long long f = c * chunk;
-    if (f >= total) return total;
-    const Pair r = pair_at(prefix, B, Hkv, f);
-    if (f - r.begin <= snap) return r.begin;
-    if (r.begin + r.n - f <= snap) return r.begin + r.n;
-    return f;
+    const long long x = c * chunk;
+    if (x >= total) return (long long)prefix[B] * Hkv;
+    const Pair r = pair_at<kPairCost>(prefix, B, Hkv, x);
+    const long long first = (long long)prefix[r.b] * Hkv + (long long)r.kvh * r.n;
+    const long long at = x - r.begin - kPairCost;  // tiles of the pair before the cut
+    return first + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
   };
   const long long f0 = cut(blockIdx.x), f1 = cut((long long)blockIdx.x + 1);
   // this warp's n-th tile is at place f0 + warp + 4 n
@@ -320,12 +332,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   const int pshift = p.page_shift;
   int l_blk = 0, l_pos = 0;     // lane's tile of the batch of 32: page; kv head, tile in the page
   int n_blk = 0, n_pos = 0;     // the same of the next batch
-  float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;  // (ks, log2 vs) of an even, an odd batch
+  float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;  // (ks, vs) of an even, an odd batch
   auto look_up = [&](int n) {
     n_blk = n_pos = 0;
     if (n >= count) return;
     const long long f = f0 + warp + (long long)kWarps * n;
-    const Pair r = pair_at(prefix, B, Hkv, f);
+    const Pair r = pair_at<0>(prefix, B, Hkv, f);
     const Span s = span_of(p, __ldg(p.seq_lens + r.b));
     int tau = (int)(f - r.begin);
     if (tau >= s.head) tau += s.gap;
@@ -344,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       if (in && good)
         v = __ldg(reinterpret_cast<const float2*>(p.kv_scale + l_blk * p.s_sblk +
                                                   (l_pos >> 3) * p.s_sh));
-      v.y = lg2(v.y);
       if (at & 1) sc1 = v; else sc0 = v;
     }
     look_up(32 * (at + 1) + lane);
@@ -360,6 +371,23 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                   blk);
     }
   };
+  // The 8 (16) query rows of a pair, 16 bytes a thread, rows past the group zero.
+  uint16_t* qbuf = reinterpret_cast<uint16_t*>(base + C::kOffQ);
+  auto load_q = [&](const Pair& r, int slot) {
+#pragma unroll
+    for (int i = tid; i < C::kRows * D / 8; i += kThreads) {
+      const int row = i / (D / 8), d = i % (D / 8) * 8;
+      const bool in = row < p.G;
+      cp_async_16(smem_u32(qbuf + (slot * C::kRows + row) * D + d),
+                  p.q + r.b * p.q_sb + (r.kvh * p.G + (in ? row : 0)) * p.q_sh + d, in ? 16 : 0);
+    }
+  };
+  Pair next = {};
+  int slot = 0;
+  if (f0 < f1) {
+    next = pair_at<0>(prefix, B, Hkv, f0);
+    load_q(next, 0);
+  }
   __syncwarp();  // the ring's barriers are lane 0's
   look_up(lane);
   int issued = 0;
@@ -388,17 +416,28 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   int n = 0;
 
   for (long long f = f0; f < f1;) {
-    const Pair pr = pair_at(prefix, B, Hkv, f);
+    const Pair pr = next;
+    cp_async_wait_all();
+    __syncthreads();  // the query rows are in; wbuf and misc are free
     const long long seg_end = min(pr.begin + pr.n, f1);
     const Span sp = span_of(p, __ldg(p.seq_lens + pr.b));
 
-    // ---- the query rows as the A operand ----
+    // ---- the query rows as the A operand; the next pair's rows are asked for ----
+    const uint16_t* q_rows = qbuf + slot * C::kRows * D;
+    if (seg_end < f1) {
+      next = pair_at<0>(prefix, B, Hkv, seg_end);
+      if (C::kQSlots == 2) load_q(next, slot ^ 1);
+    }
+    float sink[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+      sink[nb] = p.sinks && er + 8 * nb < p.G
+                     ? __ldg(p.sinks + pr.kvh * p.G + er + 8 * nb) * kLog2e : -INFINITY;
     uint32_t qa[D / 16][2 * NB];
     float row_scale[NB];  // logits of row g (g + 8) in log2 units per unit of S
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int row = g + 8 * nb;
-      const uint16_t* q = p.q + pr.b * p.q_sb + (pr.kvh * p.G + row) * p.q_sh;
+      const uint16_t* q = q_rows + (g + 8 * nb) * D;
       row_scale[nb] = p.scale * kLog2e;
       if constexpr (kFp8) {
         // k-step c, columns 2t, 2t + 1, 2t + 8, 2t + 9 <- dims 16 c + 4 t .. + 3
@@ -406,8 +445,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         uint32_t big = 0;  // largest magnitude, as bits
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-          w[c] = row < p.G ? __ldg(reinterpret_cast<const uint2*>(q + 16 * c + 4 * t))
-                           : make_uint2(0, 0);
+          w[c] = *reinterpret_cast<const uint2*>(q + 16 * c + 4 * t);
           big = max(max(big, max((w[c].x << 16) & 0x7fffffffu, w[c].x & 0x7fff0000u)),
                     max((w[c].y << 16) & 0x7fffffffu, w[c].y & 0x7fff0000u));
         }
@@ -428,11 +466,15 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       } else {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(q + 16 * c + 2 * t);
-          qa[c][nb] = row < p.G ? __ldg(w) : 0u;
-          qa[c][NB + nb] = row < p.G ? __ldg(w + 4) : 0u;
+          qa[c][nb] = *reinterpret_cast<const uint32_t*>(q + 16 * c + 2 * t);
+          qa[c][NB + nb] = *reinterpret_cast<const uint32_t*>(q + 16 * c + 8 + 2 * t);
         }
       }
+    }
+
+    if (C::kQSlots == 1 && seg_end < f1) {
+      __syncthreads();  // every warp has its rows
+      load_q(next, 0);
     }
 
     float acc[NB][E][4];
@@ -464,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       if (kFp8) {
         const bool odd = (n >> 5) & 1;
         ks = __shfl_sync(0xffffffffu, odd ? sc1.x : sc0.x, n & 31);
-        lv = __shfl_sync(0xffffffffu, odd ? sc1.y : sc0.y, n & 31);
+        lv = lg2(__shfl_sync(0xffffffffu, odd ? sc1.y : sc0.y, n & 31));
       }
       if (issued < count) issue(issued++);
 
@@ -626,13 +668,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     if (f == pr.begin && seg_end == pr.begin + pr.n) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-      __syncthreads();  // wbuf is the next request's
+        finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
     } else {
       // Contributors: the CTA whose range holds the first tile (slot 2 c + 1) and the
-      // ones whose cuts lie inside (slot 2 c).  A cut at c * chunk lies inside when it
-      // is more than snap tiles from either border.
-      const long long c0 = (pr.begin + snap) / chunk, c1 = (pr.begin + pr.n - snap - 1) / chunk;
+      // ones whose cuts lie inside (slot 2 c), more than snap tiles from either border.
+      const long long x0 = pr.begin + ((long long)pr.b * Hkv + pr.kvh + 1) * kPairCost;
+      const long long c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
       const int parts = (int)(c1 - c0 + 1), me = (int)(blockIdx.x - c0);
       auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
 #pragma unroll
@@ -661,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
           merge_partials<C>(p, gsize, [&](int k) { return slot_of(gfirst + k); }, wbuf, er + 8 * nb,
                             ed, o[nb], mc[nb], lc[nb], Rc[nb]);
           if (groups == 1)
-            finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+            finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
           else
             store_partial<C>(p, slot_of(gfirst), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
         }
@@ -676,14 +717,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             for (int nb = 0; nb < NB; ++nb) {
               merge_partials<C>(p, groups, [&](int k) { return slot_of(k * kMergeGroup); }, wbuf,
                                 er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-              finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+              finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
             }
           }
         }
       }
-      __syncthreads();  // wbuf and misc are the next request's
     }
     f = seg_end;
+    slot ^= C::kQSlots - 1;
   }
 
   // A wait that gave up leaves copies in flight: wait for them (again with a

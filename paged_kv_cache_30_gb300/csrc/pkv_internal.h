@@ -249,7 +249,7 @@ struct PagedParams {
   int window, first;
   float scale;
   int page_shift;                // log2(page_size)
-  int grid, min_tiles;           // CTAs; fewest 16-token tiles of one
+  int grid;
   float* partials;               // [2 * grid] slots
   int* slot_counters;            // [2 * grid] arrival counters of merge groups
   int* pair_counters;            // [B * Hkv] arrival counters of the groups
@@ -263,7 +263,10 @@ PagedShape paged_attn_shape(int D, bool fp8, int G);
 // kv_map: the cache as (128-byte piece's elements, token, piece, kv head, page),
 // box (a piece, 16 tokens, all pieces, 1, 1), 128-byte swizzle.
 cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
-constexpr int kPagedMinTiles = 16;
+// A CTA's share of the work is counted in 16-token tiles plus a cost for each
+// (request, kv head) pair, and is no smaller than kPagedMinCost.
+constexpr int kPagedPairCost = 8;
+constexpr int kPagedMinCost = 16;
 constexpr int kPagedMaxGrid = 512;  // 32 merge groups of 16
 
 // ------------------------------------------------ append to an e4m3 cache --
