@@ -1163,10 +1163,10 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   int64_t tiles = width;
   if (window > 0)
     tiles = std::min<int64_t>(width, (int64_t(window) + 14) / 16 + 1 + (int64_t(first_tokens) + 15) / 16);
-  if (width * 16 > (int64_t(1) << 31) - 256 || B * width >= (int64_t(1) << 31) ||
-      B * Hkv * width >= (int64_t(1) << 41))
-    return fail(PKV_ERR_UNSUPPORTED, "%lld requests of up to %lld keys", (long long)B,
-                (long long)(width * 16));
+  if (width * 16 > (int64_t(1) << 31) - 256 ||
+      B * Hkv * (tiles + pkv::kPagedPairCost) >= (int64_t(1) << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "%lld requests x %lld kv heads of up to %lld tiles of 16 keys",
+                (long long)B, (long long)Hkv, (long long)tiles);
   const pkv::Workspace& ws = st->ws;
   const int64_t cost = B * Hkv * (tiles + pkv::kPagedPairCost);
   p.grid = int(std::max<int64_t>(

@@ -73,7 +73,6 @@ struct Cfg {
   static constexpr int kOffPrefix = kOffMisc + 64;
   static constexpr int smem_bytes(int B) { return kOffPrefix + (B + 1) * 4 + 1024; }
   static_assert(kOffWb % 1024 == 0 && kOffQ % 16 == 0 && kOffBars % 8 == 0, "shared-memory offsets");
-  static_assert(kMergeGroup * 2 * 3 * kRows <= kWarps * kWbFloats, "merge scratch");
   static_assert(kStages >= 2 && kStages <= 32, "ring stages");
   static_assert(kCtas * (smem_bytes(kPagedMaxBatch) + 1024) <= 228 * 1024, "CTAs per SM");
 };
@@ -114,28 +113,53 @@ __device__ __forceinline__ int block_scan(int v, int* scratch) {
   return before + incl - v;
 }
 
+// Places count tiles of all pairs in order (or tiles and pair costs): below 2^31,
+// which the host sees to.
 struct Pair {
-  int b, kvh, n;    // request, kv head, tiles
-  long long begin;  // place of its first tile
+  int b, kvh, n;  // request, kv head, tiles
+  int begin;      // place of its first tile
 };
 
-// The pair at place f, each pair being `extra` + its tiles long.
+// The pair at place f when request b's pairs begin at place (prefix[b] + extra b) Hkv
+// and are `extra` + its tiles long.  lo: the request.
 template <int extra>
-__device__ __forceinline__ Pair pair_at(const int* prefix, int B, int Hkv, long long f) {
-  int lo = 0, hi = B - 1;  // the last request that begins at or before f
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (((long long)prefix[mid] + extra * mid) * Hkv <= f) lo = mid; else hi = mid - 1;
-  }
+__device__ __forceinline__ Pair pair_of(const int* prefix, int Hkv, int f, int lo) {
   Pair r;
   r.b = lo;
   r.n = prefix[lo + 1] - prefix[lo];
-  const long long base = ((long long)prefix[lo] + extra * lo) * Hkv, off = f - base;
-  const int len = r.n + extra;
-  // 32-bit division where it suffices
-  r.kvh = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)len) : (int)(off / len);
-  r.begin = base + (long long)r.kvh * len;
+  const int base = (prefix[lo] + extra * lo) * Hkv, len = r.n + extra;
+  r.kvh = (int)((uint32_t)(f - base) / (uint32_t)len);
+  r.begin = base + r.kvh * len;
   return r;
+}
+
+// For one lane: the last request that begins at or before f, by bisection.
+template <int extra>
+__device__ __forceinline__ Pair pair_at_lane(const int* prefix, int B, int Hkv, int f) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((prefix[mid] + extra * mid) * Hkv <= f) lo = mid; else hi = mid - 1;
+  }
+  return pair_of<extra>(prefix, Hkv, f, lo);
+}
+
+// For a warp with one f: 32 requests at a time (2 steps for up to 1024 requests).
+template <int extra>
+__device__ __forceinline__ Pair pair_at_warp(const int* prefix, int B, int Hkv, int f) {
+  const int lane = threadIdx.x & 31, step = (B + 31) >> 5;
+  auto before = [&](int b) {  // requests from b on, one a lane, that begin at or before f
+    const bool yes = b < B && (prefix[b] + extra * b) * Hkv <= f;
+    return __popc(__ballot_sync(0xffffffffu, yes));
+  };
+  int lo = before(min(lane * step, B)) - 1;
+  if (step > 1) {
+    const int base = lo * step, end = min(base + step, B);
+    int cnt = 0;
+    for (int i = 0; i < step; i += 32) cnt += before(base + i + lane < end ? base + i + lane : B);
+    lo = base + cnt - 1;
+  }
+  return pair_of<extra>(prefix, Hkv, f, lo);
 }
 
 __device__ __forceinline__ float lg2(float x) {
@@ -212,47 +236,59 @@ __device__ __forceinline__ void finalize(const PagedParams& p, int b, int kvh, i
 __device__ __forceinline__ float weight(float r, float M) { return r == -INFINITY ? 0.f : ex2(r - M); }
 
 template <class C>
-__device__ __forceinline__ void store_partial(const PagedParams& p, long long slot, int er, int ed,
+__device__ __forceinline__ void store_partial(const PagedParams& p, int slot, int er, int ed,
                                               const float (&o)[C::D / 16], float m, float l, float R) {
-  float* dst = p.partials + slot * C::kPartFloats + er * C::D + ed;
+  float* dst = p.partials + (int64_t)slot * C::kPartFloats + er * C::D + ed;
 #pragma unroll
   for (int e = 0; e < C::D / 16; e += 4)
     *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
   if (ed == 0) {
-    float* st = p.partials + slot * C::kPartFloats + C::kRows * C::D + er;
+    float* st = p.partials + (int64_t)slot * C::kPartFloats + C::kRows * C::D + er;
     st[0] = m;
     st[C::kRows] = l;
     st[2 * C::kRows] = R;
   }
 }
 
-// Merge partials k = 0 .. n - 1 (n <= 32) at slots slot_of(k) for this thread's
-// row and dims.  sml: shared scratch of n x 3 kRows floats, filled by the caller.
+// Merge partials k = 0 .. n - 1 at slots slot_of(k), in order, for this thread's
+// row and dims: the loads of four partials are in flight at once.
 template <class C, typename SlotOf>
-__device__ __forceinline__ void merge_partials(const PagedParams& p, int n, SlotOf slot_of,
-                                               const float* sml, int er, int ed,
-                                               float (&o)[C::D / 16], float& m, float& l, float& R) {
+__device__ __forceinline__ void merge_partials(const PagedParams& p, int n, SlotOf slot_of, int er,
+                                               int ed, float (&o)[C::D / 16], float& m, float& l,
+                                               float& R) {
+  constexpr int E = C::D / 16;
   m = R = -INFINITY;
-  for (int k = 0; k < n; ++k) {
-    m = fmaxf(m, sml[k * 3 * C::kRows + er]);
-    R = fmaxf(R, sml[k * 3 * C::kRows + 2 * C::kRows + er]);
-  }
   l = 0.f;
 #pragma unroll
-  for (int e = 0; e < C::D / 16; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float* st = sml + k * 3 * C::kRows + er;
-    const float* src = p.partials + slot_of(k) * C::kPartFloats + er * C::D + ed;
-    l = __fmaf_rn(weight(st[0], m), st[C::kRows], l);
-    const float w = weight(st[2 * C::kRows], R);
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 4) {
+    float mk[4], lk[4], Rk[4];
+    float4 ok[4][E / 4];
 #pragma unroll
-    for (int e = 0; e < C::D / 16; e += 4) {
-      const float4 a = ldcg_f4(src + e);
-      o[e] = __fmaf_rn(w, a.x, o[e]);
-      o[e + 1] = __fmaf_rn(w, a.y, o[e + 1]);
-      o[e + 2] = __fmaf_rn(w, a.z, o[e + 2]);
-      o[e + 3] = __fmaf_rn(w, a.w, o[e + 3]);
+    for (int i = 0; i < 4; ++i) {
+      const float* src = p.partials + (int64_t)slot_of(min(k0 + i, n - 1)) * C::kPartFloats;
+      const float* st = src + C::kRows * C::D + er;
+      mk[i] = __ldcg(st);
+      lk[i] = __ldcg(st + C::kRows);
+      Rk[i] = __ldcg(st + 2 * C::kRows);
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) ok[i][e] = ldcg_f4(src + er * C::D + ed + 4 * e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (k0 + i >= n) break;
+      const float mn = fmaxf(m, mk[i]), Rn = fmaxf(R, Rk[i]);
+      l = __fmaf_rn(weight(m, mn), l, weight(mk[i], mn) * lk[i]);
+      const float a = weight(R, Rn), w = weight(Rk[i], Rn);
+      m = mn;
+      R = Rn;
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) {
+        o[4 * e] = __fmaf_rn(a, o[4 * e], w * ok[i][e].x);
+        o[4 * e + 1] = __fmaf_rn(a, o[4 * e + 1], w * ok[i][e].y);
+        o[4 * e + 2] = __fmaf_rn(a, o[4 * e + 2], w * ok[i][e].z);
+        o[4 * e + 3] = __fmaf_rn(a, o[4 * e + 3], w * ok[i][e].w);
+      }
     }
   }
 }
@@ -313,20 +349,19 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
 
   // ---- this CTA's tiles [f0, f1) ----
   // cuts are placed in the space of costs and turned into places of tiles
-  const long long total = ((long long)prefix[B] + (long long)kPairCost * B) * Hkv;
-  const long long chunk = max((total + gridDim.x - 1) / gridDim.x, (long long)kPagedMinCost);
-  const int snap = (int)min((long long)kSnapTiles, chunk / 2);
-  auto cut = [&](long long c) -> long long {
-    const long long x = c * chunk;
-    if (x >= total) return (long long)prefix[B] * Hkv;
-    const Pair r = pair_at<kPairCost>(prefix, B, Hkv, x);
-    const long long first = (long long)prefix[r.b] * Hkv + (long long)r.kvh * r.n;
-    const long long at = x - r.begin - kPairCost;  // tiles of the pair before the cut
-    return first + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
+  const int tiles = prefix[B] * Hkv, total = tiles + kPairCost * B * Hkv;
+  const int chunk = max((int)(((uint32_t)total + gridDim.x - 1) / gridDim.x), kPagedMinCost);
+  const int snap = min(kSnapTiles, chunk / 2);
+  auto cut = [&](int c) {
+    const long long x = (long long)c * chunk;
+    if (x >= total) return tiles;
+    const Pair r = pair_at_warp<kPairCost>(prefix, B, Hkv, (int)x);
+    const int at = (int)x - r.begin - kPairCost;  // tiles of the pair before the cut
+    return prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
   };
-  const long long f0 = cut(blockIdx.x), f1 = cut((long long)blockIdx.x + 1);
+  const int f0 = cut(blockIdx.x), f1 = cut(blockIdx.x + 1);
   // this warp's n-th tile is at place f0 + warp + 4 n
-  const int count = f1 - f0 > warp ? (int)((f1 - f0 - warp + kWarps - 1) / kWarps) : 0;
+  const int count = f1 - f0 > warp ? (f1 - f0 - warp + kWarps - 1) / kWarps : 0;
 
   // ---- the loader ----
   const int pshift = p.page_shift;
@@ -336,16 +371,16 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   auto look_up = [&](int n) {
     n_blk = n_pos = 0;
     if (n >= count) return;
-    const long long f = f0 + warp + (long long)kWarps * n;
-    const Pair r = pair_at<0>(prefix, B, Hkv, f);
+    const int f = f0 + warp + kWarps * n;
+    const Pair r = pair_at_lane<0>(prefix, B, Hkv, f);
     const Span s = span_of(p, __ldg(p.seq_lens + r.b));
-    int tau = (int)(f - r.begin);
+    int tau = f - r.begin;
     if (tau >= s.head) tau += s.gap;
     const int page = tau >> (pshift - 4);
     n_pos = (r.kvh << 3) | (tau & ((1 << (pshift - 4)) - 1));
     n_blk = __ldg(p.bt + r.b * p.bt_sb + page);
   };
-  // batch `at` becomes the current one, the next is looked up
+  // batch `at` becomes the current one
   auto turn = [&](int at) {
     l_blk = n_blk;
     l_pos = n_pos;
@@ -358,10 +393,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                                                   (l_pos >> 3) * p.s_sh));
       if (at & 1) sc1 = v; else sc0 = v;
     }
-    look_up(32 * (at + 1) + lane);
   };
-  auto issue = [&](int n) {  // n < count; every 32nd call turns the batch
+  auto issue = [&](int n) {  // n < count
     if ((n & 31) == 0) turn(n >> 5);
+    if ((n & 31) == 16) look_up((n & ~31) + 32 + lane);  // the next batch
     const int blk = __shfl_sync(0xffffffffu, l_blk, n & 31);
     const int pos = __shfl_sync(0xffffffffu, l_pos, n & 31);
     if (lane == 0) {
@@ -385,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   Pair next = {};
   int slot = 0;
   if (f0 < f1) {
-    next = pair_at<0>(prefix, B, Hkv, f0);
+    next = pair_at_warp<0>(prefix, B, Hkv, f0);
     load_q(next, 0);
   }
   __syncwarp();  // the ring's barriers are lane 0's
@@ -415,17 +450,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   bool ok = true;
   int n = 0;
 
-  for (long long f = f0; f < f1;) {
+  for (int f = f0; f < f1;) {
     const Pair pr = next;
     cp_async_wait_all();
     __syncthreads();  // the query rows are in; wbuf and misc are free
-    const long long seg_end = min(pr.begin + pr.n, f1);
+    const int seg_end = min(pr.begin + pr.n, f1);
     const Span sp = span_of(p, __ldg(p.seq_lens + pr.b));
 
     // ---- the query rows as the A operand; the next pair's rows are asked for ----
     const uint16_t* q_rows = qbuf + slot * C::kRows * D;
     if (seg_end < f1) {
-      next = pair_at<0>(prefix, B, Hkv, seg_end);
+      next = pair_at_warp<0>(prefix, B, Hkv, seg_end);
       if (C::kQSlots == 2) load_q(next, slot ^ 1);
     }
     float sink[NB];
@@ -487,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       for (int c = 0; c < E; ++c) acc[nb][c][0] = acc[nb][c][1] = acc[nb][c][2] = acc[nb][c][3] = 0.f;
     }
 
-    for (; ok && f0 + warp + (long long)kWarps * n < seg_end; ++n) {
+    for (; ok && f0 + warp + kWarps * n < seg_end; ++n) {
       const int stage = n % kStages;
       ok = mbar_wait(bars + 8 * stage, (n / kStages) & 1, p.err);
       if (!ok) break;
@@ -531,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       }
 
       // ---- visibility ----
-      int tau = (int)(f0 + warp + (long long)kWarps * n - pr.begin);
+      int tau = f0 + warp + kWarps * n - pr.begin;
       if (tau >= sp.head) tau += sp.gap;
       const int tok = tau * 16;
       const bool whole = tok + 16 <= sp.L && (tok >= sp.start || tok + 16 <= sp.first);
@@ -672,9 +707,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     } else {
       // Contributors: the CTA whose range holds the first tile (slot 2 c + 1) and the
       // ones whose cuts lie inside (slot 2 c), more than snap tiles from either border.
-      const long long x0 = pr.begin + ((long long)pr.b * Hkv + pr.kvh + 1) * kPairCost;
-      const long long c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
-      const int parts = (int)(c1 - c0 + 1), me = (int)(blockIdx.x - c0);
+      const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kPairCost;
+      const int c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
+      const int parts = c1 - c0 + 1, me = (int)blockIdx.x - c0;
       auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -684,22 +719,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       const int groups = (parts + kMergeGroup - 1) / kMergeGroup;
       int* gcnt = p.slot_counters + slot_of(gfirst);
       int* tcnt = p.pair_counters + pr.b * Hkv + pr.kvh;
-      // stats of partials first, first + step, ... into shared memory
-      auto gather = [&](int first, int step, int cnt) {
-        for (int i = tid; i < cnt * 3 * C::kRows; i += kThreads)
-          wbuf[i] = __ldcg(p.partials + slot_of(first + i / (3 * C::kRows) * step) * C::kPartFloats +
-                           C::kRows * D + i % (3 * C::kRows));
-        __syncthreads();
-      };
       __syncthreads();
       if (tid == 0) misc[8] = atomic_add_acq_rel_gpu(gcnt, 1);
       __syncthreads();
       if (misc[8] == gsize - 1) {
         if (tid == 0) store_relaxed_gpu(gcnt, 0);
-        gather(gfirst, 1, gsize);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          merge_partials<C>(p, gsize, [&](int k) { return slot_of(gfirst + k); }, wbuf, er + 8 * nb,
+          merge_partials<C>(p, gsize, [&](int k) { return slot_of(gfirst + k); }, er + 8 * nb,
                             ed, o[nb], mc[nb], lc[nb], Rc[nb]);
           if (groups == 1)
             finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
@@ -712,10 +739,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
           __syncthreads();
           if (misc[9] == groups - 1) {
             if (tid == 0) store_relaxed_gpu(tcnt, 0);
-            gather(0, kMergeGroup, groups);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              merge_partials<C>(p, groups, [&](int k) { return slot_of(k * kMergeGroup); }, wbuf,
+              merge_partials<C>(p, groups, [&](int k) { return slot_of(k * kMergeGroup); },
                                 er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
               finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
             }

@@ -265,7 +265,7 @@ PagedShape paged_attn_shape(int D, bool fp8, int G);
 cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
 // A CTA's share of the work is counted in 16-token tiles plus a cost for each
 // (request, kv head) pair, and is no smaller than kPagedMinCost.
-constexpr int kPagedPairCost = 8;
+constexpr int kPagedPairCost = 16;
 constexpr int kPagedMinCost = 16;
 constexpr int kPagedMaxGrid = 512;  // 32 merge groups of 16
 
