@@ -107,14 +107,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                                        T, T, i32, vp]
         lib.pkv_gqa_kv_append.argtypes = [T, T, T, T, T, i32, vp]
         lib.pkv_mla_kv_append.argtypes = [T, T, T, T, i32, i32, T, vp]
-        lib.pkv_paged_decode_attn_fp8.argtypes = [T, T, T, T, T, T, i32, i32, f32, i32, T, T, vp]
-        lib.pkv_paged_window_attn.argtypes = [T, T, T, T, T, i32, i32, f32, i32, T, T, vp]
-        lib.pkv_gqa_kv_append_fp8.argtypes = [T, T, T, T, T, T, T, i32, vp]
-        lib.pkv_pages_fork.argtypes = [T, T, T, T, T, i32, T, T, vp]
-        lib.pkv_pages_release.argtypes = [T, T, T, T, T, i32, vp]
-        lib.pkv_pages_reserve.argtypes = [T, T, T, T, T, i32, vp]
-        lib.pkv_pages_compact.argtypes = [T, T, T, i32, T, T, T, vp]
-        lib.pkv_pages_copy.argtypes = [vp, i32, T, T, vp]
+        # descriptors of the calls below come as addresses (_descs)
+        lib.pkv_paged_decode_attn_fp8.argtypes = [vp] * 6 + [i32, i32, f32, i32, vp, vp, vp]
+        lib.pkv_paged_window_attn.argtypes = [vp] * 5 + [i32, i32, f32, i32, vp, vp, vp]
+        lib.pkv_gqa_kv_append_fp8.argtypes = [vp] * 7 + [i32, vp]
+        lib.pkv_pages_fork.argtypes = [vp] * 5 + [i32, vp, vp, vp]
+        lib.pkv_pages_release.argtypes = [vp] * 5 + [i32, vp]
+        lib.pkv_pages_reserve.argtypes = [vp] * 5 + [i32, vp]
+        lib.pkv_pages_compact.argtypes = [vp] * 3 + [i32, vp, vp, vp, vp]
+        lib.pkv_pages_copy.argtypes = [vp, i32, vp, vp, vp]
         lib.pkv_num_kv_splits.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_double, i32, i32]
         lib.pkv_check_errors.argtypes = [i32, ctypes.POINTER(ctypes.c_int32)]
         lib.pkv_check_counters.argtypes = [i32, ctypes.POINTER(ctypes.c_int64)]
@@ -147,13 +148,16 @@ def _check(rc: int) -> int:
 _DTYPES = None
 
 
-def _dtype_code(t) -> int:
+def _dtypes() -> dict:
     global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32, torch.int32: DTYPE_I32,
-                   torch.float8_e4m3fn: DTYPE_FP8}
-    code = _DTYPES.get(t.dtype)
+    import torch
+    _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32, torch.int32: DTYPE_I32,
+               torch.float8_e4m3fn: DTYPE_FP8}
+    return _DTYPES
+
+
+def _dtype_code(t) -> int:
+    code = (_DTYPES or _dtypes()).get(t.dtype)
     if code is None:
         raise PkvError(-1, f"unsupported tensor dtype {t.dtype}")
     return code
@@ -161,6 +165,37 @@ def _dtype_code(t) -> int:
 
 _PACK = struct.Struct("<Qii5q5q")  # the byte layout of pkv_tensor (96 bytes)
 _PAD = tuple((0,) * k for k in range(6))
+
+
+class _Args(threading.local):
+    """One buffer of descriptors per thread: the C calls read their descriptors before they
+    return, so every call fills the same memory."""
+
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(96 * 80)
+        self.at = tuple(ctypes.addressof(self.buf) + 96 * i for i in range(80))
+
+
+_args = _Args()
+
+
+def _descs(*tensors):
+    """Addresses of the pkv_tensor descriptors of torch tensors (None -> NULL)."""
+    buf, at, pack, pad, codes = _args.buf, _args.at, _PACK.pack_into, _PAD, _DTYPES or _dtypes()
+    out = []
+    for i, t in enumerate(tensors):
+        if t is None:
+            out.append(None)
+            continue
+        shape = t.shape
+        n = len(shape)
+        code = codes.get(t.dtype)
+        if n > 5 or code is None:
+            _desc(t)  # says what is wrong
+        fill = pad[5 - n]
+        pack(buf, 96 * i, t.data_ptr(), code, n, *shape, *fill, *t.stride(), *fill)
+        out.append(at[i])
+    return out
 
 
 def _desc(t):
@@ -176,10 +211,31 @@ def _desc(t):
     return ctypes.byref(d)
 
 
+# The current stream's handle without building a Stream object (2 us a call), where torch has it.
+_raw_stream = None
+
+
+def _current_stream(device) -> int:
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    if device.type != "cuda":
+        raise PkvError(-1, f"a tensor on {device} has no CUDA stream")
+    return _raw_stream(device.index)
+
+
+def _handle(stream, device_tensor):
+    """A stream argument as an address: None is torch's current stream of the tensor's device."""
+    if stream is None:
+        return _current_stream(device_tensor.device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _stream(stream, device_tensor):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream(device_tensor.device).cuda_stream)
+        return ctypes.c_void_p(_current_stream(device_tensor.device))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -278,11 +334,10 @@ def paged_decode_attn_fp8(q, kv_cache, kv_scale, block_table, seq_lens, sinks, w
     pkv_paged_decode_attn_fp8).  With ``window`` > 0 a request sees its last
     ``window`` keys and its first ``first_tokens``.  Writes ``out`` (and
     ``lse`` if given) in place and returns ``out``."""
-    lib = load_library()
-    _check(lib.pkv_paged_decode_attn_fp8(
-        _desc(q), _desc(kv_cache), _desc(kv_scale), _desc(block_table), _desc(seq_lens),
-        _desc(sinks), int(window or 0), int(first_tokens or 0), float(scale), int(page_size),
-        _desc(out), _desc(lse), _stream(stream, q)))
+    d = _descs(q, kv_cache, kv_scale, block_table, seq_lens, sinks, out, lse)
+    _check((_lib or load_library()).pkv_paged_decode_attn_fp8(
+        d[0], d[1], d[2], d[3], d[4], d[5], int(window or 0), int(first_tokens or 0), float(scale),
+        int(page_size), d[6], d[7], _handle(stream, q)))
     return out
 
 
@@ -291,11 +346,10 @@ def paged_window_attn(q, kv_cache, block_table, seq_lens, sinks, window, first_t
     """GQA paged decode attention over a bf16 cache with a sliding window and
     first tokens that stay visible (C: pkv_paged_window_attn).  Writes ``out``
     (and ``lse`` if given) in place and returns ``out``."""
-    lib = load_library()
-    _check(lib.pkv_paged_window_attn(
-        _desc(q), _desc(kv_cache), _desc(block_table), _desc(seq_lens), _desc(sinks),
-        int(window or 0), int(first_tokens or 0), float(scale), int(page_size), _desc(out),
-        _desc(lse), _stream(stream, q)))
+    d = _descs(q, kv_cache, block_table, seq_lens, sinks, out, lse)
+    _check((_lib or load_library()).pkv_paged_window_attn(
+        d[0], d[1], d[2], d[3], d[4], int(window or 0), int(first_tokens or 0), float(scale),
+        int(page_size), d[5], d[6], _handle(stream, q)))
     return out
 
 
@@ -305,10 +359,8 @@ def gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens
     b's are rows cu_tokens[b] .. cu_tokens[b + 1]; None: T / B each) into the
     e4m3 cache at positions ending at seq_lens[b] - 1, raising the scales of
     their pages where needed (C: pkv_gqa_kv_append_fp8).  Returns ``kv_cache``."""
-    lib = load_library()
-    _check(lib.pkv_gqa_kv_append_fp8(
-        _desc(k), _desc(v), _desc(kv_cache), _desc(kv_scale), _desc(block_table),
-        _desc(seq_lens), _desc(cu_tokens), int(page_size), _stream(stream, k)))
+    d = _descs(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens)
+    _check((_lib or load_library()).pkv_gqa_kv_append_fp8(*d, int(page_size), _handle(stream, k)))
     return kv_cache
 
 
@@ -317,28 +369,23 @@ def pages_fork(block_table, seq_lens, page_refs, parents, children, page_size, c
     """Make rows ``children`` copies of rows ``parents``: shared full pages, a
     new last page where the parent's is partly filled (to be copied:
     ``copy_src`` -> ``copy_dst``, see pages_copy) (C: pkv_pages_fork)."""
-    lib = load_library()
-    _check(lib.pkv_pages_fork(
-        _desc(block_table), _desc(seq_lens), _desc(page_refs), _desc(parents), _desc(children),
-        int(page_size), _desc(copy_src), _desc(copy_dst), _stream(stream, block_table)))
+    d = _descs(block_table, seq_lens, page_refs, parents, children, copy_src, copy_dst)
+    _check((_lib or load_library()).pkv_pages_fork(
+        d[0], d[1], d[2], d[3], d[4], int(page_size), d[5], d[6], _handle(stream, block_table)))
 
 
 def pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size, stream=None):
     """Cut rows ``rows`` to ``keep_lens`` tokens and give their other pages
     back (C: pkv_pages_release)."""
-    lib = load_library()
-    _check(lib.pkv_pages_release(
-        _desc(block_table), _desc(seq_lens), _desc(page_refs), _desc(rows), _desc(keep_lens),
-        int(page_size), _stream(stream, block_table)))
+    d = _descs(block_table, seq_lens, page_refs, rows, keep_lens)
+    _check((_lib or load_library()).pkv_pages_release(*d, int(page_size), _handle(stream, block_table)))
 
 
 def pages_reserve(block_table, seq_lens, page_refs, rows, new_lens, page_size, stream=None):
     """Grow rows ``rows`` to ``new_lens`` tokens, taking free pages lowest
     first (C: pkv_pages_reserve)."""
-    lib = load_library()
-    _check(lib.pkv_pages_reserve(
-        _desc(block_table), _desc(seq_lens), _desc(page_refs), _desc(rows), _desc(new_lens),
-        int(page_size), _stream(stream, block_table)))
+    d = _descs(block_table, seq_lens, page_refs, rows, new_lens)
+    _check((_lib or load_library()).pkv_pages_reserve(*d, int(page_size), _handle(stream, block_table)))
 
 
 def pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_dst, num_moves,
@@ -346,24 +393,22 @@ def pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_ds
     """Move the live pages to the front of the pool: rewrites the tables and
     counts, and lists the copies to make (``copy_src`` -> ``copy_dst``, filled
     up with -1; see pages_copy) (C: pkv_pages_compact)."""
-    lib = load_library()
-    _check(lib.pkv_pages_compact(
-        _desc(block_table), _desc(seq_lens), _desc(page_refs), int(page_size), _desc(copy_src),
-        _desc(copy_dst), _desc(num_moves), _stream(stream, block_table)))
+    d = _descs(block_table, seq_lens, page_refs, copy_src, copy_dst, num_moves)
+    _check((_lib or load_library()).pkv_pages_compact(
+        d[0], d[1], d[2], int(page_size), d[3], d[4], d[5], _handle(stream, block_table)))
 
 
 def pages_copy(pages, copy_src, copy_dst, stream=None):
     """Copy page copy_src[i] to page copy_dst[i] in each cache of ``pages`` (a
     tensor [num_pages, ...] or up to 64 of them), skipping negative entries (C:
     pkv_pages_copy)."""
-    lib = load_library()
     pages = [pages] if hasattr(pages, "data_ptr") else list(pages)
-    if not pages:
-        raise PkvError(-1, "pages_copy needs a page tensor")
-    descs = [_desc(t) for t in pages]
-    array = (ctypes.POINTER(PkvTensor) * len(pages))(*[ctypes.pointer(d._obj) for d in descs])
-    _check(lib.pkv_pages_copy(ctypes.cast(array, ctypes.c_void_p), len(pages), _desc(copy_src),
-                              _desc(copy_dst), _stream(stream, pages[0])))
+    if not 1 <= len(pages) <= 64 or any(t is None for t in pages):
+        raise PkvError(-1, f"pages_copy takes 1 to 64 page tensors, not {pages!r:.60}")
+    d = _descs(copy_src, copy_dst, *pages)
+    array = (ctypes.c_void_p * len(pages))(*d[2:])
+    _check((_lib or load_library()).pkv_pages_copy(
+        ctypes.addressof(array), len(pages), d[0], d[1], _handle(stream, pages[0])))
 
 
 def num_kv_splits(max_seq_len, batch, qlen, num_heads, sm_count, block_h=64, occupancy=1.0,

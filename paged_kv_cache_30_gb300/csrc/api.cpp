@@ -1466,7 +1466,7 @@ PKV_API int pkv_pages_compact(const pkv_tensor* block_table, const pkv_tensor* s
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   DeviceState* st = nullptr;
   int* scratch = nullptr;
-  if ((rc = page_call(page_refs, "page_refs", t.num_pages, stream, &st, &scratch))) return rc;
+  if ((rc = page_call(page_refs, "page_refs", pkv::pages_compact_ints(t.num_pages), stream, &st, &scratch))) return rc;
   t.err = st->ws.err;
   const cudaError_t e = pkv::launch_pages_compact(
       t, static_cast<int32_t*>(copy_src->data), static_cast<int32_t*>(copy_dst->data), int(n),

@@ -11,15 +11,20 @@
 // Scales that grow are powers of two, so re-encoding the held tokens is exact
 // but for codes that leave e4m3's normal range (below 2^-6 of the new scale).
 //
-// One warp per (token, kv head); the warp of a page's first new token (its
-// leader) does the page's work, the others leave.
+// Bound by memory for prompts (bf16 read once, codes written once), by latency
+// for single tokens.  A warp takes one kv head of `slab` consecutive rows (1 when
+// there are few, 16 when there are many): it finds the first row's request with a
+// 32-way search of cu_tokens and walks the pages that begin in its rows, loading
+// the rows of a page at once (16 16-byte loads a lane) before it reduces, and
+// encoding them from the registers.
 #include "pkv_internal.h"
 #include "ptx.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kFullWarps = 16384;
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
 
 // Smallest power of two s >= 2^-100 with a <= 448 s (448 = 1.75 * 2^8); 0 for a = 0.
@@ -51,6 +56,15 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   }
 }
 
+// Largest magnitudes of two interleaved lists of bf16 values, as bit patterns.
+__device__ __forceinline__ uint32_t max_abs(uint32_t big, const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("max.u16x2 %0, %0, %1;" : "+r"(big) : "r"(w[i] & 0x7fff7fffu));
+  return big;
+}
+
 __device__ __forceinline__ uint2 encode8(const float (&f)[8]) {
   uint32_t w[2];
 #pragma unroll
@@ -72,75 +86,80 @@ __device__ __forceinline__ void decode8(const uint2& u, float (&f)[8]) {
   }
 }
 
-// A row [K | V] of 2D values takes 2D/8 lanes of 8 values; a warp covers
-// 32 / (2D/8) rows at once.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendFp8Params p) {
-  constexpr int LPR = 2 * D / 8, RPW = 32 / LPR;
+// The last request that begins at or before row r (-1: none), 32 requests at a time.
+__device__ __forceinline__ int request_of(const AppendFp8Params& p, long long r) {
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (w >= p.T * p.Hkv) return;
-  const long long r = w / p.Hkv;
-  const int h = (int)(w % p.Hkv), P = p.page_size;
+  int lo = 0, len = p.B;  // among requests [lo, lo + len); an earlier one begins before r
+  int found = -1;
+  while (len > 0) {
+    const int step = (len + 31) >> 5, at = lo + lane * step;
+    const bool yes = lane * step < len && __ldg(p.cu + at) <= r;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, yes));
+    if (cnt == 0) break;
+    found = lo + (cnt - 1) * step;
+    len = min(step - 1, lo + len - found - 1);
+    lo = found + 1;
+  }
+  return found;
+}
 
-  // request b of row r, its first row r0 and the row after its last one
-  int b;
-  long long r0, r1;
-  if (p.cu) {
-    int lo = 0, hi = p.B;  // the number of requests that begin at or before r
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.cu + mid) <= r) lo = mid + 1; else hi = mid;
-    }
-    b = lo - 1;
-    if (b < 0) return;
-    r0 = __ldg(p.cu + b);
-    r1 = min((long long)__ldg(p.cu + b + 1), (long long)p.T);
-    if (r0 < 0 || r >= r1) return;  // rows outside every request are left alone
-  } else {
-    const long long n = p.T / p.B;
-    b = (int)(r / n);
-    r0 = b * n;
-    r1 = r0 + n;
-  }
-  const long long pos = (long long)__ldg(p.seq_lens + b) - (r1 - r);
-  if (pos < 0 || (r != r0 && pos % P != 0)) return;  // not the page's first new token
-  const long long pg = pos / P;
-  const int slot0 = (int)(pos % P);
-  const int n = (int)min((long long)(P - slot0), r1 - r);
-  if (pg >= p.max_blocks) {
-    if (lane == 0) atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
-    return;
-  }
-  const int blk = __ldg(p.bt + b * p.bt_sb + pg);
-  if (blk < 0 || blk >= p.num_blocks) {
-    if (lane == 0) atomicOr(p.err, DEVERR_BAD_BLOCK);
-    return;
-  }
-  const int sub = lane / LPR, unit = lane % LPR;
+// A row [K | V] of 2D values takes 2D/8 lanes of 8 values; a warp covers
+// RPW = 32 / (2D/8) rows at once, kHold times RPW rows in registers.
+template <int D>
+__device__ __forceinline__ bool append_page(const AppendFp8Params& p, int h, long long r, int n,
+                                            int blk, int slot0) {
+  constexpr int LPR = 2 * D / 8, RPW = 32 / LPR, kHold = 16;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, unit = lane % LPR;
   const bool is_v = unit >= LPR / 2;
-  const uint16_t* src = (is_v ? p.v : p.k) + h * p.s_sh + (unit % (LPR / 2)) * 8;
-  uint8_t* dst = p.cache + blk * p.c_sblk + h * p.c_sh + unit * 8;
-  float* scale = p.scale + blk * p.sc_sblk + h * p.sc_sh + (is_v ? 1 : 0);
-
-  float a = 0.f;
-  for (int i = sub; i < n; i += RPW) {
-    float f[8];
-    unpack8(*reinterpret_cast<const uint4*>(src + (r + i) * p.s_st), f);
+  const uint16_t* src =
+      (is_v ? p.v : p.k) + (r + sub) * p.s_st + h * p.s_sh + (unit % (LPR / 2)) * 8;
+  // rows sub, sub + RPW, ...: the first kHold of a lane stay in registers, loaded at
+  // once; magnitudes are compared as bf16 bit patterns, two at a time
+  auto load = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(src + i * RPW * p.s_st)); };
+  uint4 x[kHold];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a = fmaxf(a, finite_abs(f[e]));
+  for (int g = 0; g < kHold; g += 4)
+    if (g * RPW < n) {
+#pragma unroll
+      for (int i = g; i < g + 4; ++i) x[i] = sub + i * RPW < n ? load(i) : make_uint4(0, 0, 0, 0);
+    }
+  // the page is needed from here on
+  if (blk < 0 || blk >= p.num_blocks) return false;
+  uint8_t* dst = p.cache + blk * p.c_sblk + h * p.c_sh + sub * p.c_stok + unit * 8;
+  float* scale = p.scale + blk * p.sc_sblk + h * p.sc_sh + (is_v ? 1 : 0);
+  const float s_old = slot0 > 0 ? *scale : 0.f;
+  uint32_t big = 0;
+#pragma unroll
+  for (int g = 0; g < kHold; g += 4)
+    if (g * RPW < n) {
+#pragma unroll
+      for (int i = g; i < g + 4; ++i) big = max_abs(big, x[i]);
+    }
+  for (int i = kHold; sub + i * RPW < n; ++i) big = max_abs(big, load(i));
+  float a = __uint_as_float(max(big << 16, big & 0xffff0000u));
+  __syncwarp();
+  if (__any_sync(0xffffffffu, !(a < INFINITY))) {  // NaN and infinities set no scale
+    a = 0.f;
+#pragma unroll 1
+    for (int i = 0; sub + i * RPW < n; ++i) {
+      float f[8];
+      unpack8(load(i), f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = fmaxf(a, finite_abs(f[e]));
+    }
+    __syncwarp();
   }
 #pragma unroll
   for (int o = 1; o < LPR / 2; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   if (RPW > 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
 
-  const float s_old = slot0 > 0 ? *scale : 0.f;
   const float s = fmaxf(s_old, pow2_scale(a));
   __syncwarp();  // every lane has read the old scale
   if (sub == 0 && unit % (LPR / 2) == 0) *scale = s;
   if (s > s_old && slot0 > 0) {
     const float f0 = __fdiv_rn(s_old, s);
-    for (int i = sub; i < slot0; i += RPW) {
+#pragma unroll 4
+    for (int i = 0; sub + i < slot0; i += RPW) {
       uint2* at = reinterpret_cast<uint2*>(dst + i * p.c_stok);
       float f[8];
       decode8(*at, f);
@@ -150,25 +169,96 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendFp8Para
     }
   }
   const float div = s > 0.f ? s : 1.f;
-  for (int i = sub; i < n; i += RPW) {
-    float f[8];
-    unpack8(*reinterpret_cast<const uint4*>(src + (r + i) * p.s_st), f);
+  dst += slot0 * p.c_stok;
+  if ((__float_as_uint(div) & 0x7fffffu) == 0) {
+    // s is a power of two (a grown scale is one): x / s is the product with 1 / s
+    const float inv = 1.f / div;
+    auto put = [&](const uint4& u, int i) {
+      float f[8];
+      unpack8(u, f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], div);
-    *reinterpret_cast<uint2*>(dst + (slot0 + i) * p.c_stok) = encode8(f);
+      for (int e = 0; e < 8; ++e) f[e] *= inv;
+      *reinterpret_cast<uint2*>(dst + i * RPW * p.c_stok) = encode8(f);
+    };
+#pragma unroll
+    for (int g = 0; g < kHold; g += 4)
+      if (g * RPW < n) {
+#pragma unroll
+        for (int i = g; i < g + 4; ++i)
+          if (sub + i * RPW < n) put(x[i], i);
+      }
+    for (int i = kHold; sub + i * RPW < n; ++i) put(load(i), i);
+  } else {
+#pragma unroll 1
+    for (int i = 0; sub + i * RPW < n; ++i) {
+      float f[8];
+      unpack8(load(i), f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], div);
+      *reinterpret_cast<uint2*>(dst + i * RPW * p.c_stok) = encode8(f);
+    }
+  }
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendFp8Params p, int slab) {
+  griddep_wait();
+  const int lane = threadIdx.x & 31, P = p.page_size;
+  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int h = (int)(w % p.Hkv);
+  long long r = w / p.Hkv * slab;
+  const long long end = min(r + slab, (long long)p.T);
+  if (r >= end) return;
+
+  const long long each = p.cu ? 0 : p.T / p.B;
+  int b = p.cu ? request_of(p, r) : (int)(r / each);
+  if (b < 0) {  // rows before the first request are padding
+    b = 0;
+    r = __ldg(p.cu);
+    if (r < 0) return;
+  }
+  for (; r < end && b < p.B; ++b) {
+    const long long r0 = p.cu ? __ldg(p.cu + b) : b * each;
+    const long long r1 = p.cu ? min((long long)__ldg(p.cu + b + 1), (long long)p.T) : r0 + each;
+    if (r0 < 0) return;
+    if (r >= r1) continue;  // an empty request (or padding behind the last one)
+    const long long first = (long long)__ldg(p.seq_lens + b) - r1;  // position of row i: first + i
+    r = max(r, -first);  // tokens at negative positions are dropped
+    while (r < end && r < r1) {
+      const long long pos = first + r;
+      const int slot0 = (int)(pos % P);
+      const int n = (int)min((long long)(P - slot0), r1 - r);
+      // a page belongs to the warp of its first new row
+      if (r == r0 || r == -first || slot0 == 0) {
+        const long long pg = pos / P;
+        const int blk = pg < p.max_blocks ? __ldg(p.bt + b * p.bt_sb + pg) : -1;
+        if (!append_page<D>(p, h, r, n, blk, slot0) && lane == 0)
+          atomicOr(p.err, pg < p.max_blocks ? DEVERR_BAD_BLOCK : DEVERR_SEQ_TOO_LONG);
+      }
+      r += n;
+    }
+    if (r < r1) return;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_gqa_kv_append_fp8(const AppendFp8Params& p, cudaStream_t stream) {
-  const long long warps = p.T * p.Hkv;
-  const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
-  if (p.D == 64)
-    append_kernel<64><<<grid, kWarps * 32, 0, stream>>>(p);
-  else
-    append_kernel<128><<<grid, kWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  // rows a warp walks: 16 once the rows alone give every SM warps enough
+  int slab = 1;
+  while (slab < 16 && p.T * p.Hkv / slab > kFullWarps) slab *= 2;
+  const long long warps = (p.T + slab - 1) / slab * p.Hkv;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((warps + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.D == 64 ? append_kernel<64> : append_kernel<128>, p, slab);
 }
 
 }  // namespace pkv

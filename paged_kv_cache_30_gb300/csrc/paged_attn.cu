@@ -54,6 +54,8 @@ struct Cfg {
   static constexpr int D = D_, NB = NB_;
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kRows = 8 * NB;
+  // tiles of a step: two of 2 KB share the softmax's shuffles and rescale
+  static constexpr int U = D == 64 && kFp8 ? 2 : 1;
   static constexpr int kChunks = 2 * D * (kFp8 ? 1 : 2) / 128;  // 128-byte pieces of a [K | V] row
   static constexpr int kTileBytes = 16 * 128 * kChunks;
   static constexpr int kCtas = (D == 128 && (NB == 2 || !kFp8)) ? 2 : 3;  // per SM
@@ -144,19 +146,22 @@ __device__ __forceinline__ Pair pair_at_lane(const int* prefix, int B, int Hkv, 
   return pair_of<extra>(prefix, Hkv, f, lo);
 }
 
-// For a warp with one f: 32 requests at a time (2 steps for up to 1024 requests).
-template <int extra>
-__device__ __forceinline__ Pair pair_at_warp(const int* prefix, int B, int Hkv, int f) {
-  const int lane = threadIdx.x & 31, step = (B + 31) >> 5;
-  auto before = [&](int b) {  // requests from b on, one a lane, that begin at or before f
+// For groups of kLanes lanes (a warp, or its halves) with one f each: kLanes
+// requests at a time (2 steps for up to kLanes^2 requests).
+template <int extra, int kLanes>
+__device__ __forceinline__ Pair pair_at_group(const int* prefix, int B, int Hkv, int f) {
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, step = (B + kLanes - 1) / kLanes;
+  const uint32_t group = kLanes == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
+  auto before = [&](int b) {  // how many of the group's requests begin at or before f
     const bool yes = b < B && (prefix[b] + extra * b) * Hkv <= f;
-    return __popc(__ballot_sync(0xffffffffu, yes));
+    return __popc(__ballot_sync(0xffffffffu, yes) & group);
   };
-  int lo = before(min(lane * step, B)) - 1;
+  int lo = before(min(sub * step, B)) - 1;
   if (step > 1) {
     const int base = lo * step, end = min(base + step, B);
     int cnt = 0;
-    for (int i = 0; i < step; i += 32) cnt += before(base + i + lane < end ? base + i + lane : B);
+    for (int i = 0; i < step; i += kLanes)
+      cnt += before(base + i + sub < end ? base + i + sub : B);
     lo = base + cnt - 1;
   }
   return pair_of<extra>(prefix, Hkv, f, lo);
@@ -297,7 +302,7 @@ template <class C>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedParams p,
                       const __grid_constant__ CUtensorMap kv_map) {
-  constexpr int D = C::D, NB = C::NB, kStages = C::kStages, E = D / 16;
+  constexpr int D = C::D, NB = C::NB, U = C::U, kStages = C::kStages, E = D / 16;
   constexpr bool kFp8 = C::kFp8;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base_u32 = (raw + 1023u) & ~1023u;
@@ -352,14 +357,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   const int tiles = prefix[B] * Hkv, total = tiles + kPairCost * B * Hkv;
   const int chunk = max((int)(((uint32_t)total + gridDim.x - 1) / gridDim.x), kPagedMinCost);
   const int snap = min(kSnapTiles, chunk / 2);
-  auto cut = [&](int c) {
-    const long long x = (long long)c * chunk;
-    if (x >= total) return tiles;
-    const Pair r = pair_at_warp<kPairCost>(prefix, B, Hkv, (int)x);
-    const int at = (int)x - r.begin - kPairCost;  // tiles of the pair before the cut
-    return prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
-  };
-  const int f0 = cut(blockIdx.x), f1 = cut(blockIdx.x + 1);
+  int f0, f1;
+  {
+    // lanes 0..15 place this CTA's cut, lanes 16..31 the next one's
+    const long long x = ((long long)blockIdx.x + (lane >> 4)) * chunk;
+    const Pair r = pair_at_group<kPairCost, 16>(prefix, B, Hkv, (int)min(x, (long long)total - 1));
+    const int at = (int)min(x, (long long)total - 1) - r.begin - kPairCost;  // the pair's tiles before the cut
+    int f = prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
+    if (x >= total) f = tiles;
+    f0 = __shfl_sync(0xffffffffu, f, 0);
+    f1 = __shfl_sync(0xffffffffu, f, 16);
+  }
   // this warp's n-th tile is at place f0 + warp + 4 n
   const int count = f1 - f0 > warp ? (f1 - f0 - warp + kWarps - 1) / kWarps : 0;
 
@@ -368,11 +376,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   int l_blk = 0, l_pos = 0;     // lane's tile of the batch of 32: page; kv head, tile in the page
   int n_blk = 0, n_pos = 0;     // the same of the next batch
   float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;  // (ks, vs) of an even, an odd batch
+  Pair next = {};  // the pair after the current one
   auto look_up = [&](int n) {
     n_blk = n_pos = 0;
     if (n >= count) return;
     const int f = f0 + warp + kWarps * n;
-    const Pair r = pair_at_lane<0>(prefix, B, Hkv, f);
+    const Pair r = f >= next.begin && f < next.begin + next.n
+                       ? next : pair_at_lane<0>(prefix, B, Hkv, f);
     const Span s = span_of(p, __ldg(p.seq_lens + r.b));
     int tau = f - r.begin;
     if (tau >= s.head) tau += s.gap;
@@ -387,11 +397,16 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const bool in = 32 * at + lane < count, good = l_blk >= 0 && l_blk < p.num_blocks;
     if (in && !good) atomicOr(p.err, DEVERR_BAD_BLOCK);  // reads as zeros
     if (kFp8) {
-      float2 v = make_float2(0.f, 0.f);
-      if (in && good)
-        v = __ldg(reinterpret_cast<const float2*>(p.kv_scale + l_blk * p.s_sblk +
-                                                  (l_pos >> 3) * p.s_sh));
-      if (at & 1) sc1 = v; else sc0 = v;
+      const float2* at_scale = reinterpret_cast<const float2*>(
+          p.kv_scale + (int64_t)l_blk * p.s_sblk + (l_pos >> 3) * p.s_sh);
+      // no use of the loaded value here: nothing waits for it
+      if (at & 1) {
+        sc1 = make_float2(0.f, 0.f);
+        if (in && good) sc1 = __ldg(at_scale);
+      } else {
+        sc0 = make_float2(0.f, 0.f);
+        if (in && good) sc0 = __ldg(at_scale);
+      }
     }
   };
   auto issue = [&](int n) {  // n < count
@@ -417,10 +432,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                   p.q + r.b * p.q_sb + (r.kvh * p.G + (in ? row : 0)) * p.q_sh + d, in ? 16 : 0);
     }
   };
-  Pair next = {};
   int slot = 0;
   if (f0 < f1) {
-    next = pair_at_warp<0>(prefix, B, Hkv, f0);
+    next = pair_at_group<0, 32>(prefix, B, Hkv, f0);
     load_q(next, 0);
   }
   __syncwarp();  // the ring's barriers are lane 0's
@@ -460,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     // ---- the query rows as the A operand; the next pair's rows are asked for ----
     const uint16_t* q_rows = qbuf + slot * C::kRows * D;
     if (seg_end < f1) {
-      next = pair_at_warp<0>(prefix, B, Hkv, seg_end);
+      next = pair_at_group<0, 32>(prefix, B, Hkv, seg_end);
       if (C::kQSlots == 2) load_q(next, slot ^ 1);
     }
     float sink[NB];
@@ -522,101 +536,145 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       for (int c = 0; c < E; ++c) acc[nb][c][0] = acc[nb][c][1] = acc[nb][c][2] = acc[nb][c][3] = 0.f;
     }
 
-    for (; ok && f0 + warp + kWarps * n < seg_end; ++n) {
-      const int stage = n % kStages;
-      ok = mbar_wait(bars + 8 * stage, (n / kStages) & 1, p.err);
+    for (int took; ok && f0 + warp + kWarps * n < seg_end; n += took) {
+      took = U == 2 && f0 + warp + kWarps * (n + 1) < seg_end ? 2 : 1;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < took)
+          ok = mbar_wait(bars + 8 * ((n + u) % kStages), ((n + u) / kStages) & 1, p.err) && ok;
       if (!ok) break;
-      const uint32_t tile = ring + stage * C::kTileBytes;
-      uint32_t kf[kUnits / 2][4], vf[kUnits / 2][4];
+      uint32_t kf[U][kUnits / 2][4], vf[U][kUnits / 2][4];
 #pragma unroll
-      for (int u = 0; u < kUnits / 2; ++u)
-        ldsm_x4(tile + k_addr(2 * u), kf[u][0], kf[u][1], kf[u][2], kf[u][3]);
+      for (int u = 0; u < U; ++u) {
+        // an absent second tile reads the first again and counts for nothing
+        const uint32_t tile = ring + ((n + (u < took ? u : 0)) % kStages) * C::kTileBytes;
 #pragma unroll
-      for (int u = 0; u < kUnits / 2; ++u)
-        ldsm_x4_trans(tile + v_addr(kUnits + 2 * u), vf[u][0], vf[u][1], vf[u][2], vf[u][3]);
-      fence_proxy_async_smem();  // the stage is refilled by TMA
-      __syncwarp();
-      // the scales of tile n, before its batch's registers can be turned over
-      float ks = 1.f, lv = 0.f;
-      if (kFp8) {
-        const bool odd = (n >> 5) & 1;
-        ks = __shfl_sync(0xffffffffu, odd ? sc1.x : sc0.x, n & 31);
-        lv = lg2(__shfl_sync(0xffffffffu, odd ? sc1.y : sc0.y, n & 31));
+        for (int i = 0; i < kUnits / 2; ++i)
+          ldsm_x4(tile + k_addr(2 * i), kf[u][i][0], kf[u][i][1], kf[u][i][2], kf[u][i][3]);
+#pragma unroll
+        for (int i = 0; i < kUnits / 2; ++i)
+          ldsm_x4_trans(tile + v_addr(kUnits + 2 * i), vf[u][i][0], vf[u][i][1], vf[u][i][2],
+                        vf[u][i][3]);
       }
-      if (issued < count) issue(issued++);
+      fence_proxy_async_smem();  // the stages are refilled by TMA
+      __syncwarp();
+      // the scales of the tiles, before their batch's registers can be turned over
+      float ks[U], lv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        ks[u] = 1.f;
+        lv[u] = 0.f;
+        if (kFp8) {
+          const int k = n + (u < took ? u : 0);
+          const bool odd = (k >> 5) & 1;
+          ks[u] = __shfl_sync(0xffffffffu, odd ? sc1.x : sc0.x, k & 31);
+          lv[u] = lg2(__shfl_sync(0xffffffffu, odd ? sc1.y : sc0.y, k & 31));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < took && issued < count) issue(issued++);
 
       // ---- S = Q K^T: tokens 0..7 (sa) and 8..15 (sb), two chains each ----
-      float sa[2][4], sb[2][4];
+      float sa[U][2][4], sb[U][2][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sa[i][e] = sb[i][e] = 0.f;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sa[u][i][e] = sb[u][i][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const uint32_t a0 = qa[c][0], a1 = NB == 2 ? qa[c][1] : 0u;
         const uint32_t a2 = qa[c][NB], a3 = NB == 2 ? qa[c][NB + 1] : 0u;
-        if constexpr (kFp8) {
-          const uint32_t x = kf[c / 2][c & 1], y = kf[c / 2][2 + (c & 1)];
-          mma<true>(sa[c & 1], a0, a1, a2, a3, e4m3x2_f16(x), e4m3x2_f16_hi(x));
-          mma<true>(sb[c & 1], a0, a1, a2, a3, e4m3x2_f16(y), e4m3x2_f16_hi(y));
-        } else {
-          mma<false>(sa[c & 1], a0, a1, a2, a3, kf[c][0], kf[c][1]);
-          mma<false>(sb[c & 1], a0, a1, a2, a3, kf[c][2], kf[c][3]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if constexpr (kFp8) {
+            const uint32_t x = kf[u][c / 2][c & 1], y = kf[u][c / 2][2 + (c & 1)];
+            mma<true>(sa[u][c & 1], a0, a1, a2, a3, e4m3x2_f16(x), e4m3x2_f16_hi(x));
+            mma<true>(sb[u][c & 1], a0, a1, a2, a3, e4m3x2_f16(y), e4m3x2_f16_hi(y));
+          } else {
+            mma<false>(sa[u][c & 1], a0, a1, a2, a3, kf[u][c][0], kf[u][c][1]);
+            mma<false>(sb[u][c & 1], a0, a1, a2, a3, kf[u][c][2], kf[u][c][3]);
+          }
         }
       }
 
       // ---- visibility ----
-      int tau = f0 + warp + kWarps * n - pr.begin;
-      if (tau >= sp.head) tau += sp.gap;
-      const int tok = tau * 16;
-      const bool whole = tok + 16 <= sp.L && (tok >= sp.start || tok + 16 <= sp.first);
-      bool see[4] = {true, true, true, true};  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-      if (!whole) {
+      bool see[U][4];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = tok + 2 * t + (i & 1) + 8 * (i >> 1);
-          see[i] = j < sp.L && (j >= sp.start || j < sp.first);
-        }
-        // values that nobody sees may be anything: zero them, as 0 * NaN is NaN
-        const uint32_t mlo = (see[0] ? 0xffffu : 0u) | (see[1] ? 0xffff0000u : 0u);
-        const uint32_t mhi = (see[2] ? 0xffffu : 0u) | (see[3] ? 0xffff0000u : 0u);
+      for (int u = 0; u < U; ++u) {
+        int tau = f0 + warp + kWarps * (n + u) - pr.begin;
+        if (tau >= sp.head) tau += sp.gap;
+        const int tok = tau * 16;
+        const bool whole =
+            u < took && tok + 16 <= sp.L && (tok >= sp.start || tok + 16 <= sp.first);
 #pragma unroll
-        for (int u = 0; u < kUnits / 2; ++u) {
-          vf[u][0] &= mlo; vf[u][1] &= mhi; vf[u][2] &= mlo; vf[u][3] &= mhi;
+        for (int i = 0; i < 4; ++i) see[u][i] = true;
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = tok + 2 * t + (i & 1) + 8 * (i >> 1);
+            see[u][i] = u < took && j < sp.L && (j >= sp.start || j < sp.first);
+          }
+          // values that nobody sees may be anything: zero them, as 0 * NaN is NaN
+          const uint32_t mlo = (see[u][0] ? 0xffffu : 0u) | (see[u][1] ? 0xffff0000u : 0u);
+          const uint32_t mhi = (see[u][2] ? 0xffffu : 0u) | (see[u][3] ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int i = 0; i < kUnits / 2; ++i) {
+            vf[u][i][0] &= mlo; vf[u][i][1] &= mhi; vf[u][i][2] &= mlo; vf[u][i][3] &= mhi;
+          }
         }
       }
 
       // ---- online softmax in log2 units ----
-      uint32_t pb[NB][2];
+      uint32_t pb[NB][U][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const float c2 = kFp8 ? row_scale[nb] * ks : row_scale[nb];
-        float x[4] = {(sa[0][2 * nb] + sa[1][2 * nb]) * c2, (sa[0][2 * nb + 1] + sa[1][2 * nb + 1]) * c2,
-                      (sb[0][2 * nb] + sb[1][2 * nb]) * c2, (sb[0][2 * nb + 1] + sb[1][2 * nb + 1]) * c2};
+        float x[U][4], tile_max[U];
+        float mx = -INFINITY, mu = -INFINITY;  // largest logit; largest with its value's scale
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = see[i] ? x[i] : -INFINITY;
-        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        for (int u = 0; u < U; ++u) {
+          const float c2 = kFp8 ? row_scale[nb] * ks[u] : row_scale[nb];
+          x[u][0] = (sa[u][0][2 * nb] + sa[u][1][2 * nb]) * c2;
+          x[u][1] = (sa[u][0][2 * nb + 1] + sa[u][1][2 * nb + 1]) * c2;
+          x[u][2] = (sb[u][0][2 * nb] + sb[u][1][2 * nb]) * c2;
+          x[u][3] = (sb[u][0][2 * nb + 1] + sb[u][1][2 * nb + 1]) * c2;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[u][i] = see[u][i] ? x[u][i] : -INFINITY;
+          tile_max[u] = fmaxf(fmaxf(x[u][0], x[u][1]), fmaxf(x[u][2], x[u][3]));
+          tile_max[u] = fmaxf(tile_max[u], __shfl_xor_sync(0xffffffffu, tile_max[u], 1));
+          tile_max[u] = fmaxf(tile_max[u], __shfl_xor_sync(0xffffffffu, tile_max[u], 2));
+          mx = fmaxf(mx, tile_max[u]);
+          mu = fmaxf(mu, tile_max[u] + lv[u]);
+        }
         const float mn = fmaxf(m[nb], mx), mref = mn == -INFINITY ? 0.f : mn;
         const float alpha = ex2(m[nb] - mref);
-        float e[4];
+        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = ex2(x[i] - mref);
-        l[nb] = __fmaf_rn(l[nb], alpha, (e[0] + e[1]) + (e[2] + e[3]));
+        for (int u = 0; u < U; ++u) {
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = ex2(x[u][i] - mref);
+          sum += (e[0] + e[1]) + (e[2] + e[3]);
+          if constexpr (!kFp8) {
+            pb[nb][u][0] = pack_bf16(e[0], e[1]);
+            pb[nb][u][1] = pack_bf16(e[2], e[3]);
+          }
+        }
+        l[nb] = __fmaf_rn(l[nb], alpha, sum);
         m[nb] = mn;
         float beta = alpha;
         if constexpr (kFp8) {
-          const float Rn = fmaxf(R[nb], mx + lv), shift = Rn == -INFINITY ? 0.f : Rn;
+          const float Rn = fmaxf(R[nb], mu), shift = Rn == -INFINITY ? 0.f : Rn;
           beta = ex2(R[nb] - shift);
           R[nb] = Rn;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = ex2(x[i] + (lv - shift));
-          pb[nb][0] = pack_f16(e[0], e[1]);
-          pb[nb][1] = pack_f16(e[2], e[3]);
-        } else {
-          pb[nb][0] = pack_bf16(e[0], e[1]);
-          pb[nb][1] = pack_bf16(e[2], e[3]);
+          for (int u = 0; u < U; ++u) {
+            const float d = lv[u] - shift;
+            pb[nb][u][0] = pack_f16(ex2(x[u][0] + d), ex2(x[u][1] + d));
+            pb[nb][u][1] = pack_f16(ex2(x[u][2] + d), ex2(x[u][3] + d));
+          }
         }
         // rows 2t, 2t + 1 are the accumulator's columns; their factors are on lanes 8t, 8t + 4
         if (__any_sync(0xffffffffu, beta != 1.f)) {
@@ -631,21 +689,24 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
 
       // ---- O^T += V^T P^T ----
 #pragma unroll
-      for (int c = 0; c < E; ++c) {
-        uint32_t a0, a1, a2, a3;
-        if constexpr (kFp8) {
-          // a register holds (token 2t: dims 2g, 2g + 1; token 2t + 1: the same)
-          const uint32_t lo = vf[c / 2][2 * (c & 1)], hi = vf[c / 2][2 * (c & 1) + 1];
-          const uint32_t lp = __byte_perm(lo, 0, 0x3120), hp = __byte_perm(hi, 0, 0x3120);
-          a0 = e4m3x2_f16(lp); a1 = e4m3x2_f16_hi(lp);
-          a2 = e4m3x2_f16(hp); a3 = e4m3x2_f16_hi(hp);
-        } else {
-          // units 2c and 2c + 1 of V: dims 16c + g and 16c + 8 + g
-          a0 = vf[c][0]; a1 = vf[c][2]; a2 = vf[c][1]; a3 = vf[c][3];
-        }
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma<kFp8>(acc[nb][c], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
-      }
+        for (int c = 0; c < E; ++c) {
+          uint32_t a0, a1, a2, a3;
+          if constexpr (kFp8) {
+            // a register holds (token 2t: dims 2g, 2g + 1; token 2t + 1: the same)
+            const uint32_t lo = vf[u][c / 2][2 * (c & 1)], hi = vf[u][c / 2][2 * (c & 1) + 1];
+            const uint32_t lp = __byte_perm(lo, 0, 0x3120), hp = __byte_perm(hi, 0, 0x3120);
+            a0 = e4m3x2_f16(lp); a1 = e4m3x2_f16_hi(lp);
+            a2 = e4m3x2_f16(hp); a3 = e4m3x2_f16_hi(hp);
+          } else {
+            // units 2c and 2c + 1 of V: dims 16c + g and 16c + 8 + g
+            a0 = vf[u][c][0]; a1 = vf[u][c][2]; a2 = vf[u][c][1]; a3 = vf[u][c][3];
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            mma<kFp8>(acc[nb][c], a0, a1, a2, a3, pb[nb][u][0], pb[nb][u][1]);
+        }
     }
 
     // ---- merge the warps ----

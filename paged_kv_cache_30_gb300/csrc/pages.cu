@@ -19,6 +19,8 @@
 // bound by memory.
 #include <limits.h>
 
+#include <algorithm>
+
 #include "pkv_internal.h"
 #include "ptx.cuh"
 
@@ -26,7 +28,6 @@ namespace pkv {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
 
 // Exclusive scan over the CTA; *total = the sum.
 template <typename T>
@@ -41,7 +42,7 @@ __device__ T block_scan(T v, T* scratch, T* total) {
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    const T s = scratch[lane];
+    const T s = lane < (int)(blockDim.x >> 5) ? scratch[lane] : 0;
     T t = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -56,6 +57,23 @@ __device__ T block_scan(T v, T* scratch, T* total) {
   *total = scratch[32];
   __syncthreads();
   return res;
+}
+
+// Bit i: page p + i is free (p a multiple of 16).
+__device__ __forceinline__ uint32_t free_pages16(const PageTables& t, int p) {
+  uint32_t bits = 0;
+  if (p + 16 <= t.num_pages && (reinterpret_cast<uintptr_t>(t.refs) & 15) == 0) {
+    const int4* refs = reinterpret_cast<const int4*>(t.refs + p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int4 r = refs[i];
+      bits |= (uint32_t)((r.x <= 0) | (r.y <= 0) << 1 | (r.z <= 0) << 2 | (r.w <= 0) << 3) << 4 * i;
+    }
+  } else {
+    for (int i = 0; i < 16; ++i)
+      if (p + i < t.num_pages && t.refs[p + i] <= 0) bits |= 1u << i;
+  }
+  return bits;
 }
 
 __device__ __forceinline__ int pages_of(long long len, int P) { return (int)((len + P - 1) / P); }
@@ -83,6 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ long long scratch64[33];
   const int tid = threadIdx.x;
   int* parent = tag + t.rows;
+  griddep_wait();
   for (int i = tid; i < t.rows; i += kPlanThreads) {
     tag[i] = INT_MAX;
     if (kFork) parent[i] = 0;
@@ -127,25 +146,13 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     run += total;
   }
-  // the free pages of the first `run` ranks, lowest first
+  // the free pages of the first `run` ranks, lowest first, 16 a thread
   int found = 0;
-  for (int p0 = 0; p0 < t.num_pages && found < run; p0 += 4 * kPlanThreads) {
-    const int p = p0 + 4 * tid;
-    int free4[4], c = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      free4[k] = p + k < t.num_pages && t.refs[p + k] == 0;
-      c += free4[k];
-    }
-    int total;
-    int at = found + block_scan(c, scratch, &total);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (free4[k]) {
-        if (at < run) ws[8 + 2 * n + at] = p + k;
-        ++at;
-      }
-    }
+  for (int p0 = 0; p0 < t.num_pages && found < run; p0 += 16 * kPlanThreads) {
+    const int p = p0 + 16 * tid;
+    uint32_t free16 = free_pages16(t, p);
+    int total, at = found + block_scan((int)__popc(free16), scratch, &total);
+    for (; free16 && at < run; free16 &= free16 - 1) ws[8 + 2 * n + at++] = p + __ffs(free16) - 1;
     found += total;
   }
   if (tid == 0) ws[0] = found;
@@ -153,6 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 __global__ void fork_kernel(const PageTables t, const int32_t* parents, const int32_t* children,
                             int n, int32_t* copy_src, int32_t* copy_dst, const int* ws) {
+  griddep_wait();
   const int i = blockIdx.x, tid = threadIdx.x;
   int L = ws[8 + n + i], src = -1, dst = -1;
   if (L >= 0) {
@@ -196,6 +204,7 @@ __global__ void fork_kernel(const PageTables t, const int32_t* parents, const in
 
 __global__ void release_kernel(const PageTables t, const int32_t* rows, const int32_t* keep) {
   __shared__ int sL;
+  griddep_wait();
   const int i = blockIdx.x, tid = threadIdx.x, row = rows[i];
   if (row < 0 || row >= t.rows) {
     if (tid == 0) atomicOr(t.err, DEVERR_BAD_ROW);
@@ -219,6 +228,7 @@ __global__ void release_kernel(const PageTables t, const int32_t* rows, const in
 
 __global__ void reserve_kernel(const PageTables t, const int32_t* rows, const int32_t* lens, int n,
                                const int* ws) {
+  griddep_wait();
   const int i = blockIdx.x, tid = threadIdx.x, need = ws[8 + n + i];
   if (need < 0) return;
   const int row = rows[i], base = ws[8 + i];
@@ -236,78 +246,195 @@ __global__ void reserve_kernel(const PageTables t, const int32_t* rows, const in
   if (tid == 0 && lens[i] > L) t.seq_lens[row] = lens[i];
 }
 
-// One CTA: the moves, and each page's new index in ws.
-__global__ void __launch_bounds__(kPlanThreads)
-    compact_kernel(const PageTables t, int32_t* copy_src, int32_t* copy_dst, int n,
-                   int32_t* num_moves, int* ws) {
-  __shared__ int scratch[33];
-  const int tid = threadIdx.x;
-  int c = 0, live;
-  for (int p = tid; p < t.num_pages; p += kPlanThreads) c += t.refs[p] > 0;
-  block_scan(c, scratch, &live);
-  int nsrc = 0, ndst = 0;
-  for (int p0 = 0; p0 < t.num_pages; p0 += kPlanThreads) {
-    const int p = p0 + tid;
-    const bool in = p < t.num_pages, used = in && t.refs[p] > 0;
-    const int is_src = used && p >= live, is_dst = in && !used && p < live;
-    int total_src, total_dst;
-    const int at_src = nsrc + block_scan(is_src, scratch, &total_src);
-    const int at_dst = ndst + block_scan(is_dst, scratch, &total_dst);
-    if (is_src && at_src < n) copy_src[at_src] = p;
-    if (is_dst && at_dst < n) copy_dst[at_dst] = p;
-    if (in) ws[p] = p;
-    nsrc += total_src;
-    ndst += total_dst;
+// Compaction in three steps over blocks of kBlockPages pages.  With used(p) the
+// live pages below p and n = used(num_pages): the live page p >= n is move
+// used(p) - used(n), the free page p < n is target p - used(p).
+constexpr int kBlockThreads = 256;
+constexpr int kBlockPages = 16 * kBlockThreads;
+
+// Live pages of p .. p + 15 as bits.
+__device__ __forceinline__ uint32_t live_pages16(const PageTables& t, int p) {
+  if (p >= t.num_pages) return 0;
+  const uint32_t in = t.num_pages - p >= 16 ? 0xffffu : (1u << (t.num_pages - p)) - 1;
+  return ~free_pages16(t, p) & in;
+}
+
+// ws[block]: live pages of each block.
+__global__ void __launch_bounds__(kBlockThreads) compact_count_kernel(const PageTables t, int* ws) {
+  griddep_wait();
+  const int p = blockIdx.x * kBlockPages + 16 * threadIdx.x;
+  const int c = __popc(live_pages16(t, p));
+  __shared__ int sum;
+  if (threadIdx.x == 0) sum = 0;
+  __syncthreads();
+  const int w = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&sum, w);
+  __syncthreads();
+  if (threadIdx.x == 0) ws[blockIdx.x] = sum;
+}
+
+// Lists the moves and targets; ws[blocks + p]: the move of live page p >= n.
+__global__ void __launch_bounds__(kBlockThreads)
+    compact_list_kernel(const PageTables t, int32_t* copy_src, int32_t* copy_dst, int m,
+                        int32_t* num_moves, int* ws) {
+  griddep_wait();
+  const int tid = threadIdx.x, blocks = gridDim.x;
+  __shared__ int sums[3], scratch[33];
+  if (tid < 3) sums[tid] = 0;
+  __syncthreads();
+  // live pages of all blocks, and of the ones before this
+  int all = 0, before = 0;
+  for (int b = tid; b < blocks; b += kBlockThreads) {
+    const int c = ws[b];
+    all += c;
+    before += b < (int)blockIdx.x ? c : 0;
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if ((tid & 31) == 0) {
+    atomicAdd(&sums[0], all);
+    atomicAdd(&sums[1], before);
   }
   __syncthreads();
-  const int moves = min(nsrc, n);
-  for (int k = tid; k < n; k += kPlanThreads) {
-    if (k < moves) {
-      const int s = copy_src[k], d = copy_dst[k];
-      t.refs[d] = t.refs[s];
-      t.refs[s] = 0;
-      ws[s] = d;
-    } else {
-      copy_src[k] = copy_dst[k] = -1;
+  const int n = sums[0];
+  before = sums[1];
+  // used(n): live pages of the blocks before page n's, and of its own below n
+  const int nb = n / kBlockPages;
+  int below = 0;
+  for (int b = tid; b < nb; b += kBlockThreads) below += ws[b];
+  {
+    const int p = nb * kBlockPages + 16 * tid;
+    if (p < n) below += __popc(live_pages16(t, p) & (n - p >= 16 ? 0xffffu : (1u << (n - p)) - 1));
+  }
+  below = __reduce_add_sync(0xffffffffu, below);
+  if ((tid & 31) == 0) atomicAdd(&sums[2], below);
+  __syncthreads();
+  below = sums[2];
+  const int moves = min(n - below, m);
+
+  const int p0 = blockIdx.x * kBlockPages + 16 * tid;
+  const uint32_t live = live_pages16(t, p0);
+  int total, used = before + block_scan((int)__popc(live), scratch, &total);
+  for (int i = 0; i < 16 && p0 + i < t.num_pages; ++i) {
+    const int p = p0 + i;
+    if (live >> i & 1) {
+      if (p >= n) {
+        ws[blocks + p] = used - below;
+        if (used - below < m) copy_src[used - below] = p;
+      }
+      ++used;
+    } else if (p < n && p - used < m) {
+      copy_dst[p - used] = p;
     }
   }
-  if (tid == 0) *num_moves = moves;
-}
-
-__global__ void remap_kernel(const PageTables t, const int* to) {
-  const int row = blockIdx.x, used = pages_of(row_len(t, row), t.page_size);
-  int32_t* bt = t.bt + row * t.bt_sb;
-  for (int j = threadIdx.x; j < used; j += blockDim.x) {
-    const int page = bt[j];
-    if (page >= 0 && page < t.num_pages)
-      bt[j] = to[page];
-    else
-      atomicOr(t.err, DEVERR_BAD_BLOCK);
+  for (int k = moves + blockIdx.x * kBlockThreads + tid; k < m; k += blocks * kBlockThreads)
+    copy_src[k] = copy_dst[k] = -1;
+  if (blockIdx.x == 0 && tid == 0) {
+    *num_moves = moves;
+    ws[blocks + t.num_pages] = n;
   }
 }
 
-__global__ void copy_kernel(const __grid_constant__ PagesCopyParams p) {
+// CTAs [0, rows): the tables' rows; the others: the counts of the moved pages.
+__global__ void __launch_bounds__(kBlockThreads)
+    compact_apply_kernel(const PageTables t, const int32_t* copy_src, const int32_t* copy_dst, int m,
+                         const int32_t* num_moves, int blocks, const int* ws) {
+  griddep_wait();
+  const int moves = *num_moves;
+  if ((int)blockIdx.x < t.rows) {
+    const int n = ws[blocks + t.num_pages];
+    const int row = blockIdx.x, used = pages_of(row_len(t, row), t.page_size);
+    int32_t* bt = t.bt + row * t.bt_sb;
+    for (int j = threadIdx.x; j < used; j += kBlockThreads) {
+      const int page = bt[j];
+      if (page < 0 || page >= t.num_pages) {
+        atomicOr(t.err, DEVERR_BAD_BLOCK);
+      } else if (page >= n) {
+        // a page with no count is no one's: its entry stays, as the page does
+        const int k = ws[blocks + page];
+        if (k >= 0 && k < moves && copy_src[k] == page) bt[j] = copy_dst[k];
+      }
+    }
+  } else {
+    for (int k = (blockIdx.x - t.rows) * kBlockThreads + threadIdx.x; k < moves;
+         k += (gridDim.x - t.rows) * kBlockThreads) {
+      t.refs[copy_dst[k]] = t.refs[copy_src[k]];
+      t.refs[copy_src[k]] = 0;
+    }
+  }
+}
+
+// A CTA copies pieces of kPiece bytes of the listed pages of one tensor.
+constexpr int kCopyThreads = 128;
+constexpr int kCopyLoads = 4;
+
+template <typename V>
+__device__ __forceinline__ void copy_piece(uint8_t* to, const uint8_t* from, int64_t bytes) {
+  // kCopyLoads loads of a thread are in flight at once
+  for (int64_t k0 = threadIdx.x * sizeof(V); k0 < bytes; k0 += kCopyThreads * kCopyLoads * sizeof(V)) {
+    V v[kCopyLoads];
+#pragma unroll
+    for (int i = 0; i < kCopyLoads; ++i) {
+      const int64_t k = k0 + i * kCopyThreads * (int64_t)sizeof(V);
+      if (k < bytes) v[i] = *reinterpret_cast<const V*>(from + k);
+    }
+#pragma unroll
+    for (int i = 0; i < kCopyLoads; ++i) {
+      const int64_t k = k0 + i * kCopyThreads * (int64_t)sizeof(V);
+      if (k < bytes) *reinterpret_cast<V*>(to + k) = v[i];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ PagesCopyParams p) {
+  griddep_wait();
+  constexpr int64_t kPiece = kCopyThreads * kCopyLoads * 16;
   const PagesCopyTensor& t = p.t[blockIdx.y];
-  for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
-    const int s = p.src[i], d = p.dst[i];
+  const int64_t pieces = (t.bytes + kPiece - 1) / kPiece;
+  const bool wide = ((reinterpret_cast<uintptr_t>(t.base) | t.stride | t.bytes) & 15) == 0;
+  for (int64_t u = blockIdx.x; u < pieces * p.n; u += gridDim.x) {
+    const int64_t i = pieces == 1 ? u : u / pieces, at = (u - i * pieces) * kPiece;
+    const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
     if (s < 0 || d < 0) continue;
     if (s >= t.num_pages || d >= t.num_pages) {
       if (threadIdx.x == 0) atomicOr(p.err, DEVERR_BAD_BLOCK);
       continue;
     }
-    const uint8_t* from = t.base + s * t.stride;
-    uint8_t* to = t.base + d * t.stride;
-    for (int64_t k = threadIdx.x * 4; k < t.bytes; k += blockDim.x * 4)
-      *reinterpret_cast<uint32_t*>(to + k) = *reinterpret_cast<const uint32_t*>(from + k);
+    const uint8_t* from = t.base + s * t.stride + at;
+    uint8_t* to = t.base + d * t.stride + at;
+    const int64_t bytes = min(kPiece, (int64_t)(t.bytes - at));
+    if (wide)
+      copy_piece<uint4>(to, from, bytes);
+    else
+      copy_piece<uint32_t>(to, from, bytes);
   }
+}
+
+// Every kernel here launches as a programmatic dependent and reads nothing of the
+// caller's before its wait.
+template <typename... P, typename... A>
+cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(a)...);
 }
 
 }  // namespace
 
 cudaError_t launch_pages_copy(const PagesCopyParams& p, int num_sms, cudaStream_t stream) {
-  const int grid = p.n < 8 * num_sms ? p.n : 8 * num_sms;
-  copy_kernel<<<dim3(grid, p.num_tensors), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  int64_t units = 0;
+  for (int i = 0; i < p.num_tensors; ++i)
+    units = std::max(units, (p.t[i].bytes + 8191) / 8192 * p.n);
+  return launch(copy_kernel, dim3((unsigned)std::min<int64_t>(units, 16 * num_sms), p.num_tensors),
+                kCopyThreads, 0, stream, p);
 }
 
 cudaError_t launch_pages_fork(const PageTables& t, const int32_t* parents, const int32_t* children,
@@ -316,17 +443,16 @@ cudaError_t launch_pages_fork(const PageTables& t, const int32_t* parents, const
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_smem_attr_once(plan_kernel<true>, kPagesMaxRows * 8, done);
   if (e != cudaSuccess) return e;
-  plan_kernel<true><<<1, kPlanThreads, t.rows * 8, stream>>>(t, children, parents, n, scratch);
-  e = cudaGetLastError();
+  e = launch(plan_kernel<true>, dim3(1), kPlanThreads, t.rows * 8, stream, t, children, parents, n,
+             scratch);
   if (e != cudaSuccess) return e;
-  fork_kernel<<<n, 256, 0, stream>>>(t, parents, children, n, copy_src, copy_dst, scratch);
-  return cudaGetLastError();
+  return launch(fork_kernel, dim3(n), 256, 0, stream, t, parents, children, n, copy_src, copy_dst,
+                scratch);
 }
 
 cudaError_t launch_pages_release(const PageTables& t, const int32_t* rows, const int32_t* keep,
                                  int n, cudaStream_t stream) {
-  release_kernel<<<n, 64, 0, stream>>>(t, rows, keep);
-  return cudaGetLastError();
+  return launch(release_kernel, dim3(n), 64, 0, stream, t, rows, keep);
 }
 
 cudaError_t launch_pages_reserve(const PageTables& t, const int32_t* rows, const int32_t* lens,
@@ -334,20 +460,23 @@ cudaError_t launch_pages_reserve(const PageTables& t, const int32_t* rows, const
   static std::atomic<uint64_t> done{0};
   cudaError_t e = set_smem_attr_once(plan_kernel<false>, kPagesMaxRows * 8, done);
   if (e != cudaSuccess) return e;
-  plan_kernel<false><<<1, kPlanThreads, t.rows * 4, stream>>>(t, rows, lens, n, scratch);
-  e = cudaGetLastError();
+  e = launch(plan_kernel<false>, dim3(1), kPlanThreads, t.rows * 4, stream, t, rows, lens, n,
+             scratch);
   if (e != cudaSuccess) return e;
-  reserve_kernel<<<n, 64, 0, stream>>>(t, rows, lens, n, scratch);
-  return cudaGetLastError();
+  return launch(reserve_kernel, dim3(n), 64, 0, stream, t, rows, lens, n, scratch);
 }
 
 cudaError_t launch_pages_compact(const PageTables& t, int32_t* copy_src, int32_t* copy_dst, int n,
                                  int32_t* num_moves, int* scratch, cudaStream_t stream) {
-  compact_kernel<<<1, kPlanThreads, 0, stream>>>(t, copy_src, copy_dst, n, num_moves, scratch);
-  const cudaError_t e = cudaGetLastError();
+  const int blocks = (t.num_pages + kBlockPages - 1) / kBlockPages;
+  cudaError_t e = launch(compact_count_kernel, dim3(blocks), kBlockThreads, 0, stream, t, scratch);
   if (e != cudaSuccess) return e;
-  remap_kernel<<<t.rows, 128, 0, stream>>>(t, scratch);
-  return cudaGetLastError();
+  e = launch(compact_list_kernel, dim3(blocks), kBlockThreads, 0, stream, t, copy_src, copy_dst, n,
+             num_moves, scratch);
+  if (e != cudaSuccess) return e;
+  const int movers = std::max(1, std::min(64, n / kBlockThreads));
+  return launch(compact_apply_kernel, dim3(t.rows + movers), kBlockThreads, 0, stream, t, copy_src,
+                copy_dst, n, num_moves, blocks, scratch);
 }
 
 }  // namespace pkv

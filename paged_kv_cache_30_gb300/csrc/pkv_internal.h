@@ -265,7 +265,7 @@ PagedShape paged_attn_shape(int D, bool fp8, int G);
 cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
 // A CTA's share of the work is counted in 16-token tiles plus a cost for each
 // (request, kv head) pair, and is no smaller than kPagedMinCost.
-constexpr int kPagedPairCost = 16;
+constexpr int kPagedPairCost = 12;
 constexpr int kPagedMinCost = 16;
 constexpr int kPagedMaxGrid = 512;  // 32 merge groups of 16
 
@@ -315,8 +315,9 @@ struct PagesCopyParams {
   int* err;
 };
 cudaError_t launch_pages_copy(const PagesCopyParams& p, int num_sms, cudaStream_t stream);
-// scratch: pages_scratch_ints(n) (fork, reserve) or num_pages (compact) ints
+// scratch of fork and reserve (n entries), and of compact, in ints
 inline int64_t pages_scratch_ints(int64_t n, int64_t num_pages) { return 8 + 2 * n + num_pages; }
+inline int64_t pages_compact_ints(int64_t num_pages) { return num_pages + num_pages / 4096 + 2; }
 cudaError_t launch_pages_fork(const PageTables& t, const int32_t* parents, const int32_t* children,
                               int n, int32_t* copy_src, int32_t* copy_dst, int* scratch,
                               cudaStream_t stream);
