@@ -37,6 +37,8 @@ Names follow the C ABI without its ``pkv_`` prefix:
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 import threading
@@ -78,6 +80,30 @@ assert ctypes.sizeof(PkvTensor) == 96
 
 _lock = threading.Lock()
 _lib = None
+_call = None  # the compiled binding of the calls that come many times a step (csrc/pycall.c)
+_CALLS = ("pkv_paged_decode_attn_fp8", "pkv_paged_window_attn", "pkv_gqa_kv_append_fp8",
+          "pkv_pages_fork", "pkv_pages_release", "pkv_pages_reserve", "pkv_pages_compact",
+          "pkv_pages_copy", "pkv_last_error")
+
+
+def _calls():
+    """The compiled binding, bound to the library."""
+    global _call
+    if _call is None:
+        lib = load_library()
+        with _lock:
+            path = os.path.join(_HERE, "_build", "_pkvcall.so")
+            if not os.path.exists(path):
+                raise ImportError(f"{path} is missing: build it with __graft_entry__.build()")
+            loader = importlib.machinery.ExtensionFileLoader("_pkvcall", path)
+            module = importlib.util.module_from_spec(
+                importlib.util.spec_from_file_location("_pkvcall", path, loader=loader))
+            loader.exec_module(module)
+            codes = {code: dtype for dtype, code in (_DTYPES or _dtypes()).items()}
+            module.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _CALLS),
+                        tuple(codes[i] for i in (1, 2, 3, 4)), _raw_stream_fn(), PkvError)
+            _call = module
+    return _call
 
 
 def library_path() -> str:
@@ -107,15 +133,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                                        T, T, i32, vp]
         lib.pkv_gqa_kv_append.argtypes = [T, T, T, T, T, i32, vp]
         lib.pkv_mla_kv_append.argtypes = [T, T, T, T, i32, i32, T, vp]
-        # descriptors of the calls below come as addresses (_descs)
-        lib.pkv_paged_decode_attn_fp8.argtypes = [vp] * 6 + [i32, i32, f32, i32, vp, vp, vp]
-        lib.pkv_paged_window_attn.argtypes = [vp] * 5 + [i32, i32, f32, i32, vp, vp, vp]
-        lib.pkv_gqa_kv_append_fp8.argtypes = [vp] * 7 + [i32, vp]
-        lib.pkv_pages_fork.argtypes = [vp] * 5 + [i32, vp, vp, vp]
-        lib.pkv_pages_release.argtypes = [vp] * 5 + [i32, vp]
-        lib.pkv_pages_reserve.argtypes = [vp] * 5 + [i32, vp]
-        lib.pkv_pages_compact.argtypes = [vp] * 3 + [i32, vp, vp, vp, vp]
-        lib.pkv_pages_copy.argtypes = [vp, i32, vp, vp, vp]
+        lib.pkv_paged_decode_attn_fp8.argtypes = [T, T, T, T, T, T, i32, i32, f32, i32, T, T, vp]
+        lib.pkv_paged_window_attn.argtypes = [T, T, T, T, T, i32, i32, f32, i32, T, T, vp]
+        lib.pkv_gqa_kv_append_fp8.argtypes = [T, T, T, T, T, T, T, i32, vp]
+        lib.pkv_pages_fork.argtypes = [T, T, T, T, T, i32, T, T, vp]
+        lib.pkv_pages_release.argtypes = [T, T, T, T, T, i32, vp]
+        lib.pkv_pages_reserve.argtypes = [T, T, T, T, T, i32, vp]
+        lib.pkv_pages_compact.argtypes = [T, T, T, i32, T, T, T, vp]
+        lib.pkv_pages_copy.argtypes = [vp, i32, T, T, vp]
         lib.pkv_num_kv_splits.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_double, i32, i32]
         lib.pkv_check_errors.argtypes = [i32, ctypes.POINTER(ctypes.c_int32)]
         lib.pkv_check_counters.argtypes = [i32, ctypes.POINTER(ctypes.c_int64)]
@@ -167,37 +192,6 @@ _PACK = struct.Struct("<Qii5q5q")  # the byte layout of pkv_tensor (96 bytes)
 _PAD = tuple((0,) * k for k in range(6))
 
 
-class _Args(threading.local):
-    """One buffer of descriptors per thread: the C calls read their descriptors before they
-    return, so every call fills the same memory."""
-
-    def __init__(self):
-        self.buf = ctypes.create_string_buffer(96 * 80)
-        self.at = tuple(ctypes.addressof(self.buf) + 96 * i for i in range(80))
-
-
-_args = _Args()
-
-
-def _descs(*tensors):
-    """Addresses of the pkv_tensor descriptors of torch tensors (None -> NULL)."""
-    buf, at, pack, pad, codes = _args.buf, _args.at, _PACK.pack_into, _PAD, _DTYPES or _dtypes()
-    out = []
-    for i, t in enumerate(tensors):
-        if t is None:
-            out.append(None)
-            continue
-        shape = t.shape
-        n = len(shape)
-        code = codes.get(t.dtype)
-        if n > 5 or code is None:
-            _desc(t)  # says what is wrong
-        fill = pad[5 - n]
-        pack(buf, 96 * i, t.data_ptr(), code, n, *shape, *fill, *t.stride(), *fill)
-        out.append(at[i])
-    return out
-
-
 def _desc(t):
     """pkv_tensor for a torch tensor (None -> NULL), packed in one call."""
     if t is None:
@@ -215,27 +209,20 @@ def _desc(t):
 _raw_stream = None
 
 
-def _current_stream(device) -> int:
+def _raw_stream_fn():
     global _raw_stream
     if _raw_stream is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
-    if device.type != "cuda":
-        raise PkvError(-1, f"a tensor on {device} has no CUDA stream")
-    return _raw_stream(device.index)
-
-
-def _handle(stream, device_tensor):
-    """A stream argument as an address: None is torch's current stream of the tensor's device."""
-    if stream is None:
-        return _current_stream(device_tensor.device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    return _raw_stream
 
 
 def _stream(stream, device_tensor):
     if stream is None:
-        return ctypes.c_void_p(_current_stream(device_tensor.device))
+        if device_tensor.device.type != "cuda":
+            raise PkvError(-1, f"a tensor on {device_tensor.device} has no CUDA stream")
+        return ctypes.c_void_p(_raw_stream_fn()(device_tensor.device.index))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -334,10 +321,9 @@ def paged_decode_attn_fp8(q, kv_cache, kv_scale, block_table, seq_lens, sinks, w
     pkv_paged_decode_attn_fp8).  With ``window`` > 0 a request sees its last
     ``window`` keys and its first ``first_tokens``.  Writes ``out`` (and
     ``lse`` if given) in place and returns ``out``."""
-    d = _descs(q, kv_cache, kv_scale, block_table, seq_lens, sinks, out, lse)
-    _check((_lib or load_library()).pkv_paged_decode_attn_fp8(
-        d[0], d[1], d[2], d[3], d[4], d[5], int(window or 0), int(first_tokens or 0), float(scale),
-        int(page_size), d[6], d[7], _handle(stream, q)))
+    (_call or _calls()).paged_decode_attn_fp8(q, kv_cache, kv_scale, block_table, seq_lens, sinks,
+                                              window, first_tokens, scale, page_size, out, lse,
+                                              stream)
     return out
 
 
@@ -346,10 +332,8 @@ def paged_window_attn(q, kv_cache, block_table, seq_lens, sinks, window, first_t
     """GQA paged decode attention over a bf16 cache with a sliding window and
     first tokens that stay visible (C: pkv_paged_window_attn).  Writes ``out``
     (and ``lse`` if given) in place and returns ``out``."""
-    d = _descs(q, kv_cache, block_table, seq_lens, sinks, out, lse)
-    _check((_lib or load_library()).pkv_paged_window_attn(
-        d[0], d[1], d[2], d[3], d[4], int(window or 0), int(first_tokens or 0), float(scale),
-        int(page_size), d[5], d[6], _handle(stream, q)))
+    (_call or _calls()).paged_window_attn(q, kv_cache, block_table, seq_lens, sinks, window,
+                                          first_tokens, scale, page_size, out, lse, stream)
     return out
 
 
@@ -359,8 +343,8 @@ def gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens
     b's are rows cu_tokens[b] .. cu_tokens[b + 1]; None: T / B each) into the
     e4m3 cache at positions ending at seq_lens[b] - 1, raising the scales of
     their pages where needed (C: pkv_gqa_kv_append_fp8).  Returns ``kv_cache``."""
-    d = _descs(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens)
-    _check((_lib or load_library()).pkv_gqa_kv_append_fp8(*d, int(page_size), _handle(stream, k)))
+    (_call or _calls()).gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens,
+                                          page_size, stream)
     return kv_cache
 
 
@@ -369,23 +353,22 @@ def pages_fork(block_table, seq_lens, page_refs, parents, children, page_size, c
     """Make rows ``children`` copies of rows ``parents``: shared full pages, a
     new last page where the parent's is partly filled (to be copied:
     ``copy_src`` -> ``copy_dst``, see pages_copy) (C: pkv_pages_fork)."""
-    d = _descs(block_table, seq_lens, page_refs, parents, children, copy_src, copy_dst)
-    _check((_lib or load_library()).pkv_pages_fork(
-        d[0], d[1], d[2], d[3], d[4], int(page_size), d[5], d[6], _handle(stream, block_table)))
+    (_call or _calls()).pages_fork(block_table, seq_lens, page_refs, parents, children, page_size,
+                                   copy_src, copy_dst, stream)
 
 
 def pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size, stream=None):
     """Cut rows ``rows`` to ``keep_lens`` tokens and give their other pages
     back (C: pkv_pages_release)."""
-    d = _descs(block_table, seq_lens, page_refs, rows, keep_lens)
-    _check((_lib or load_library()).pkv_pages_release(*d, int(page_size), _handle(stream, block_table)))
+    (_call or _calls()).pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size,
+                                      stream)
 
 
 def pages_reserve(block_table, seq_lens, page_refs, rows, new_lens, page_size, stream=None):
     """Grow rows ``rows`` to ``new_lens`` tokens, taking free pages lowest
     first (C: pkv_pages_reserve)."""
-    d = _descs(block_table, seq_lens, page_refs, rows, new_lens)
-    _check((_lib or load_library()).pkv_pages_reserve(*d, int(page_size), _handle(stream, block_table)))
+    (_call or _calls()).pages_reserve(block_table, seq_lens, page_refs, rows, new_lens, page_size,
+                                      stream)
 
 
 def pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_dst, num_moves,
@@ -393,22 +376,16 @@ def pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_ds
     """Move the live pages to the front of the pool: rewrites the tables and
     counts, and lists the copies to make (``copy_src`` -> ``copy_dst``, filled
     up with -1; see pages_copy) (C: pkv_pages_compact)."""
-    d = _descs(block_table, seq_lens, page_refs, copy_src, copy_dst, num_moves)
-    _check((_lib or load_library()).pkv_pages_compact(
-        d[0], d[1], d[2], int(page_size), d[3], d[4], d[5], _handle(stream, block_table)))
+    (_call or _calls()).pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_dst,
+                                      num_moves, stream)
 
 
 def pages_copy(pages, copy_src, copy_dst, stream=None):
     """Copy page copy_src[i] to page copy_dst[i] in each cache of ``pages`` (a
     tensor [num_pages, ...] or up to 64 of them), skipping negative entries (C:
     pkv_pages_copy)."""
-    pages = [pages] if hasattr(pages, "data_ptr") else list(pages)
-    if not 1 <= len(pages) <= 64 or any(t is None for t in pages):
-        raise PkvError(-1, f"pages_copy takes 1 to 64 page tensors, not {pages!r:.60}")
-    d = _descs(copy_src, copy_dst, *pages)
-    array = (ctypes.c_void_p * len(pages))(*d[2:])
-    _check((_lib or load_library()).pkv_pages_copy(
-        ctypes.addressof(array), len(pages), d[0], d[1], _handle(stream, pages[0])))
+    (_call or _calls()).pages_copy([pages] if hasattr(pages, "data_ptr") else pages, copy_src,
+                                   copy_dst, stream)
 
 
 def num_kv_splits(max_seq_len, batch, qlen, num_heads, sm_count, block_h=64, occupancy=1.0,

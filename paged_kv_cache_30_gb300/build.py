@@ -8,6 +8,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +19,7 @@ LIB = os.path.join(BUILD, "libpkv.so")
 SOURCES = ["api.cpp", "gqa_decode.cu", "gqa_noalloc.cu", "mla_verify.cu", "mla_verify_native.cu",
            "mla_verify_pair.cu", "kv_append.cu", "paged_attn.cu", "kv_append_fp8.cu", "pages.cu"]
 HEADERS = ["pkv_internal.h", "ptx.cuh", "tcgen05.cuh", "mla_common.cuh"]
+PYCALL = os.path.join(BUILD, "_pkvcall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
@@ -46,6 +48,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     flags = NVCC_FLAGS + (extra_flags or [])
     exe = nvcc()
 
+    def compile_pycall():
+        """The Python binding of the per-step calls (no CUDA: the host compiler alone)."""
+        src = os.path.join(CSRC, "pycall.c")
+        if not force and not _stale(PYCALL, [src, hdrs[-1], __file__]):
+            return
+        tmp = PYCALL + f".tmp{os.getpid()}"
+        cmd = [shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
+               "-I", sysconfig.get_paths()["include"], src, "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the host compiler failed for {src}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, PYCALL)
+
     def compile_one(i):
         if not force and not _stale(objs[i], [srcs[i], *hdrs, __file__]):
             return None
@@ -58,8 +73,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         os.replace(objs[i] + ".tmp", objs[i])
         return srcs[i]
 
-    with ThreadPoolExecutor(len(srcs)) as ex:
+    with ThreadPoolExecutor(len(srcs) + 1) as ex:
+        binding = ex.submit(compile_pycall)
         list(ex.map(compile_one, range(len(srcs))))
+        binding.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs]

@@ -28,6 +28,7 @@ namespace pkv {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kOneCtaEntries = 16384;  // table entries that the planning CTA handles itself
 
 // Exclusive scan over the CTA; *total = the sum.
 template <typename T>
@@ -88,14 +89,83 @@ __device__ __forceinline__ int row_len(const PageTables& t, int row) {
   return L;
 }
 
+// Entry i of a fork, by kLanes threads (a warp, or a CTA).
+template <int kLanes>
+__device__ __forceinline__ void apply_fork(const PageTables& t, const int32_t* children,
+                                           const int32_t* parents, int n, int i, int32_t* copy_src,
+                                           int32_t* copy_dst, const int* ws) {
+  const int lane = threadIdx.x % kLanes, L = ws[8 + n + i];
+  int src = -1, dst = -1;
+  if (L >= 0) {
+    const int full = L / t.page_size, child = children[i];
+    const bool part = L % t.page_size != 0;
+    const bool granted = !part || ws[8 + i] < ws[0];
+    const int32_t* from = t.bt + parents[i] * t.bt_sb;
+    int32_t* to = t.bt + child * t.bt_sb;
+    if (part && granted) {
+      src = from[full];
+      dst = ws[8 + 2 * n + ws[8 + i]];
+    }
+#pragma unroll 4
+    for (int j = lane; j < t.max_blocks; j += kLanes) {
+      int page = -1;
+      if (granted && j < full) {
+        page = from[j];
+        if (page >= 0 && page < t.num_pages)
+          atomicAdd(t.refs + page, 1);
+        else
+          atomicOr(t.err, DEVERR_BAD_BLOCK);
+      } else if (j == full) {
+        page = dst;
+      }
+      to[j] = page;
+    }
+    if (lane == 0) {
+      if (dst >= 0) t.refs[dst] = 1;
+      if (!granted) atomicOr(t.err, DEVERR_NO_PAGE);
+      t.seq_lens[child] = granted ? L : 0;
+      if (dst >= 0 && (src < 0 || src >= t.num_pages)) {
+        atomicOr(t.err, DEVERR_BAD_BLOCK);
+        src = -1;
+      }
+    }
+  }
+  if (lane == 0) {
+    copy_src[i] = src;
+    copy_dst[i] = src < 0 ? -1 : dst;
+  }
+}
+
+// Entry i of a reservation, by kLanes threads.
+template <int kLanes>
+__device__ __forceinline__ void apply_reserve(const PageTables& t, const int32_t* rows,
+                                              const int32_t* lens, int n, int i, const int* ws) {
+  const int lane = threadIdx.x % kLanes, need = ws[8 + n + i], base = ws[8 + i];
+  if (need < 0) return;
+  if (need > 0 && (long long)base + need > ws[0]) {
+    if (lane == 0) atomicOr(t.err, DEVERR_NO_PAGE);
+    return;
+  }
+  const int row = rows[i], L = row_len(t, row), have = pages_of(L, t.page_size);
+  for (int j = lane; j < need; j += kLanes) {
+    const int page = ws[8 + 2 * n + base + j];
+    t.refs[page] = 1;
+    t.bt[row * t.bt_sb + have + j] = page;
+  }
+  if (kLanes == 32) __syncwarp(); else __syncthreads();  // every thread has read the length
+  if (lane == 0 && lens[i] > L) t.seq_lens[row] = lens[i];
+}
+
 // scratch: [0] free pages found, [8 + i] first rank of entry i, [8 + n + i] pages
 // it wants (-1: skipped) or, for fork, the parent's length; [8 + 2n + k] the
 // free page of rank k.
 //
-// Fork (rows = children, other = parents) or reserve (rows, other = new lengths).
+// Fork (rows = children, other = parents) or reserve (rows, other = new lengths):
+// which entries get which pages; with `apply` this CTA carries them out too.
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads)
-    plan_kernel(const PageTables t, const int32_t* rows, const int32_t* other, int n, int* ws) {
+    plan_kernel(const PageTables t, const int32_t* rows, const int32_t* other, int n,
+                int32_t* copy_src, int32_t* copy_dst, int* ws, bool apply) {
   extern __shared__ int tag[];  // [rows] first entry that names the row; then parent marks
   __shared__ int scratch[33];
   __shared__ long long scratch64[33];
@@ -156,49 +226,13 @@ __global__ void __launch_bounds__(kPlanThreads)
     found += total;
   }
   if (tid == 0) ws[0] = found;
-}
-
-__global__ void fork_kernel(const PageTables t, const int32_t* parents, const int32_t* children,
-                            int n, int32_t* copy_src, int32_t* copy_dst, const int* ws) {
-  griddep_wait();
-  const int i = blockIdx.x, tid = threadIdx.x;
-  int L = ws[8 + n + i], src = -1, dst = -1;
-  if (L >= 0) {
-    const int full = L / t.page_size;
-    const bool part = L % t.page_size != 0;
-    const bool granted = !part || ws[8 + i] < ws[0];
-    const int32_t* from = t.bt + parents[i] * t.bt_sb;
-    int32_t* to = t.bt + children[i] * t.bt_sb;
-    if (part && granted) {
-      src = from[full];
-      dst = ws[8 + 2 * n + ws[8 + i]];
-    }
-    for (int j = tid; j < t.max_blocks; j += blockDim.x) {
-      int page = -1;
-      if (granted && j < full) {
-        page = from[j];
-        if (page >= 0 && page < t.num_pages)
-          atomicAdd(t.refs + page, 1);
-        else
-          atomicOr(t.err, DEVERR_BAD_BLOCK);
-      } else if (j == full) {
-        page = dst;
-      }
-      to[j] = page;
-    }
-    if (tid == 0) {
-      if (dst >= 0) t.refs[dst] = 1;
-      if (!granted) atomicOr(t.err, DEVERR_NO_PAGE);
-      t.seq_lens[children[i]] = granted ? L : 0;
-      if (dst >= 0 && (src < 0 || src >= t.num_pages)) {
-        atomicOr(t.err, DEVERR_BAD_BLOCK);
-        src = -1;
-      }
-    }
-  }
-  if (tid == 0) {
-    copy_src[i] = src;
-    copy_dst[i] = src < 0 ? -1 : dst;
+  if (!apply) return;
+  __syncthreads();
+  for (int i = tid >> 5; i < n; i += kPlanThreads / 32) {
+    if (kFork)
+      apply_fork<32>(t, rows, other, n, i, copy_src, copy_dst, ws);
+    else
+      apply_reserve<32>(t, rows, other, n, i, ws);
   }
 }
 
@@ -226,24 +260,17 @@ __global__ void release_kernel(const PageTables t, const int32_t* rows, const in
   if (tid == 0) atomicMin(t.seq_lens + row, k);
 }
 
-__global__ void reserve_kernel(const PageTables t, const int32_t* rows, const int32_t* lens, int n,
-                               const int* ws) {
+constexpr int kApplyThreads = 128;
+
+template <bool kFork>
+__global__ void __launch_bounds__(kApplyThreads)
+    apply_kernel(const PageTables t, const int32_t* rows, const int32_t* other, int n,
+                 int32_t* copy_src, int32_t* copy_dst, const int* ws) {
   griddep_wait();
-  const int i = blockIdx.x, tid = threadIdx.x, need = ws[8 + n + i];
-  if (need < 0) return;
-  const int row = rows[i], base = ws[8 + i];
-  if (need > 0 && (long long)base + need > ws[0]) {
-    if (tid == 0) atomicOr(t.err, DEVERR_NO_PAGE);
-    return;
-  }
-  const int L = row_len(t, row), have = pages_of(L, t.page_size);
-  for (int j = tid; j < need; j += blockDim.x) {
-    const int page = ws[8 + 2 * n + base + j];
-    t.refs[page] = 1;
-    t.bt[row * t.bt_sb + have + j] = page;
-  }
-  __syncthreads();
-  if (tid == 0 && lens[i] > L) t.seq_lens[row] = lens[i];
+  if (kFork)
+    apply_fork<kApplyThreads>(t, rows, other, n, blockIdx.x, copy_src, copy_dst, ws);
+  else
+    apply_reserve<kApplyThreads>(t, rows, other, n, blockIdx.x, ws);
 }
 
 // Compaction in three steps over blocks of kBlockPages pages.  With used(p) the
@@ -364,9 +391,10 @@ __global__ void __launch_bounds__(kBlockThreads)
   }
 }
 
-// A CTA copies pieces of kPiece bytes of the listed pages of one tensor.
+// A CTA copies pieces of kCopyPiece bytes of the listed pages of one tensor.
 constexpr int kCopyThreads = 128;
-constexpr int kCopyLoads = 4;
+constexpr int kCopyLoads = 8;
+constexpr int64_t kCopyPiece = kCopyThreads * kCopyLoads * 16;
 
 template <typename V>
 __device__ __forceinline__ void copy_piece(uint8_t* to, const uint8_t* from, int64_t bytes) {
@@ -388,12 +416,11 @@ __device__ __forceinline__ void copy_piece(uint8_t* to, const uint8_t* from, int
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ PagesCopyParams p) {
   griddep_wait();
-  constexpr int64_t kPiece = kCopyThreads * kCopyLoads * 16;
   const PagesCopyTensor& t = p.t[blockIdx.y];
-  const int64_t pieces = (t.bytes + kPiece - 1) / kPiece;
+  const int64_t pieces = (t.bytes + kCopyPiece - 1) / kCopyPiece;
   const bool wide = ((reinterpret_cast<uintptr_t>(t.base) | t.stride | t.bytes) & 15) == 0;
   for (int64_t u = blockIdx.x; u < pieces * p.n; u += gridDim.x) {
-    const int64_t i = pieces == 1 ? u : u / pieces, at = (u - i * pieces) * kPiece;
+    const int64_t i = pieces == 1 ? u : u / pieces, at = (u - i * pieces) * kCopyPiece;
     const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
     if (s < 0 || d < 0) continue;
     if (s >= t.num_pages || d >= t.num_pages) {
@@ -402,7 +429,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     }
     const uint8_t* from = t.base + s * t.stride + at;
     uint8_t* to = t.base + d * t.stride + at;
-    const int64_t bytes = min(kPiece, (int64_t)(t.bytes - at));
+    const int64_t bytes = min(kCopyPiece, (int64_t)(t.bytes - at));
     if (wide)
       copy_piece<uint4>(to, from, bytes);
     else
@@ -432,22 +459,31 @@ cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, int smem, cudaStrea
 cudaError_t launch_pages_copy(const PagesCopyParams& p, int num_sms, cudaStream_t stream) {
   int64_t units = 0;
   for (int i = 0; i < p.num_tensors; ++i)
-    units = std::max(units, (p.t[i].bytes + 8191) / 8192 * p.n);
+    units = std::max(units, (p.t[i].bytes + kCopyPiece - 1) / kCopyPiece * p.n);
   return launch(copy_kernel, dim3((unsigned)std::min<int64_t>(units, 16 * num_sms), p.num_tensors),
                 kCopyThreads, 0, stream, p);
+}
+
+// One launch when the planning CTA can do the rest too, else two.
+template <bool kFork>
+static cudaError_t plan_and_apply(const PageTables& t, const int32_t* rows, const int32_t* other,
+                                  int n, int32_t* copy_src, int32_t* copy_dst, int* scratch,
+                                  cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = set_smem_attr_once(plan_kernel<kFork>, kPagesMaxRows * 8, done);
+  if (e != cudaSuccess) return e;
+  const bool apply = (int64_t)n * t.max_blocks <= kOneCtaEntries;
+  e = launch(plan_kernel<kFork>, dim3(1), kPlanThreads, t.rows * (kFork ? 8 : 4), stream, t, rows,
+             other, n, copy_src, copy_dst, scratch, apply);
+  if (e != cudaSuccess || apply) return e;
+  return launch(apply_kernel<kFork>, dim3(n), kApplyThreads, 0,
+                stream, t, rows, other, n, copy_src, copy_dst, scratch);
 }
 
 cudaError_t launch_pages_fork(const PageTables& t, const int32_t* parents, const int32_t* children,
                               int n, int32_t* copy_src, int32_t* copy_dst, int* scratch,
                               cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = set_smem_attr_once(plan_kernel<true>, kPagesMaxRows * 8, done);
-  if (e != cudaSuccess) return e;
-  e = launch(plan_kernel<true>, dim3(1), kPlanThreads, t.rows * 8, stream, t, children, parents, n,
-             scratch);
-  if (e != cudaSuccess) return e;
-  return launch(fork_kernel, dim3(n), 256, 0, stream, t, parents, children, n, copy_src, copy_dst,
-                scratch);
+  return plan_and_apply<true>(t, children, parents, n, copy_src, copy_dst, scratch, stream);
 }
 
 cudaError_t launch_pages_release(const PageTables& t, const int32_t* rows, const int32_t* keep,
@@ -457,13 +493,7 @@ cudaError_t launch_pages_release(const PageTables& t, const int32_t* rows, const
 
 cudaError_t launch_pages_reserve(const PageTables& t, const int32_t* rows, const int32_t* lens,
                                  int n, int* scratch, cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = set_smem_attr_once(plan_kernel<false>, kPagesMaxRows * 8, done);
-  if (e != cudaSuccess) return e;
-  e = launch(plan_kernel<false>, dim3(1), kPlanThreads, t.rows * 4, stream, t, rows, lens, n,
-             scratch);
-  if (e != cudaSuccess) return e;
-  return launch(reserve_kernel, dim3(n), 64, 0, stream, t, rows, lens, n, scratch);
+  return plan_and_apply<false>(t, rows, lens, n, nullptr, nullptr, scratch, stream);
 }
 
 cudaError_t launch_pages_compact(const PageTables& t, int32_t* copy_src, int32_t* copy_dst, int n,
