@@ -17,9 +17,9 @@
 //    within a few tiles of a pair's border moves to the border.  Each CTA finds its
 //    cuts in a prefix sum of the requests' tile counts, in shared memory.
 //  * Each of the four warps takes every fourth tile of the CTA's range through a
-//    ring of its own: lane 0 asks for a tile with one TMA operation, the warp reads
-//    the fragments of a landed tile into registers, and lane 0 asks for the next
-//    tile into the same stage.  No warp waits for another, and a ring runs on
+//    ring of its own: a lane asks for a tile with one TMA operation, the warp reads the
+//    fragments of a landed tile into registers, and a lane asks for the next tile
+//    into the same stage.  No warp waits for another, and a ring runs on
 //    across the borders of requests.  Block-table entries (and scales) are read
 //    32 tiles ahead, one lane each.
 //  * S[rows x 16 tokens] = Q K^T and O^T[dims x rows] += V^T P^T on
@@ -58,7 +58,8 @@ struct Cfg {
   static constexpr int U = D == 64 && kFp8 ? 2 : 1;
   static constexpr int kChunks = 2 * D * (kFp8 ? 1 : 2) / 128;  // 128-byte pieces of a [K | V] row
   static constexpr int kTileBytes = 16 * 128 * kChunks;
-  static constexpr int kCtas = (D == 128 && (NB == 2 || !kFp8)) ? 2 : 3;  // per SM
+  // CTAs per SM, as many as the registers of the loop allow without spilling
+  static constexpr int kCtas = D == 128 ? (NB == 1 && kFp8 ? 3 : 2) : (NB == 1 && !kFp8 ? 4 : 3);
   static constexpr int kWbRow = D + 4;
   static constexpr int kWbFloats = kRows * kWbRow + 3 * kRows;  // O, m, l, R of one warp
   static constexpr int kPartFloats = kRows * D + 3 * kRows;
@@ -211,6 +212,24 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
+}
+
+// The same with C = 0.
+template <bool kFp16>
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                     uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (kFp16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // This thread's part of the output: row er (a query head of the kv head), dims
@@ -409,16 +428,15 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       }
     }
   };
-  auto issue = [&](int n) {  // n < count
-    if ((n & 31) == 0) turn(n >> 5);
-    if ((n & 31) == 16) look_up((n & ~31) + 32 + lane);  // the next batch
-    const int blk = __shfl_sync(0xffffffffu, l_blk, n & 31);
-    const int pos = __shfl_sync(0xffffffffu, l_pos, n & 31);
-    if (lane == 0) {
-      const int s = n % kStages;
+  auto issue = [&](int n, int s) {  // tile n < count into stage s = n % kStages
+    if ((n & 15) == 0) {
+      if (n & 16) look_up((n & ~31) + 32 + lane);  // the next batch
+      else turn(n >> 5);
+    }
+    if (lane == (n & 31)) {  // the lane that looked the tile up
       mbar_arrive_expect_tx(bars + 8 * s, C::kTileBytes);
-      tma_load_5d(ring + s * C::kTileBytes, &kv_map, bars + 8 * s, 0, (pos & 7) * 16, 0, pos >> 3,
-                  blk);
+      tma_load_5d(ring + s * C::kTileBytes, &kv_map, bars + 8 * s, 0, (l_pos & 7) * 16, 0,
+                  l_pos >> 3, l_blk);
     }
   };
   // The 8 (16) query rows of a pair, 16 bytes a thread, rows past the group zero.
@@ -440,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   __syncwarp();  // the ring's barriers are lane 0's
   look_up(lane);
   int issued = 0;
-  for (; issued < min(count, kStages); ++issued) issue(issued);
+  for (; issued < min(count, kStages); ++issued) issue(issued, issued);
 
   // ---- fragment addresses ----
   // ldmatrix: matrix mi = lane / 8 takes its 8 rows from lanes 8 mi .. 8 mi + 7.
@@ -448,21 +466,20 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   // V (transposed): (tokens 0..7, unit u), (8..15, u), (0..7, u + 1), (8..15, u + 1).
   // The 128-byte swizzle XORs a 16-byte unit's index with its token modulo 8.
   const int g = lane >> 2, t = lane & 3, mi = lane >> 3, r8 = lane & 7;
-  const uint32_t k_row = (uint32_t)(r8 + 8 * (mi >> 1)) * 128u, v_row = (uint32_t)(r8 + 8 * (mi & 1)) * 128u;
-  const int k_unit = mi & 1, v_unit = mi >> 1;
-  // byte offset o of a [K | V] row lies in 128-byte piece o / 128, unit o % 128 / 16
-  auto k_addr = [&](int unit) {
-    return (uint32_t)(unit >> 3) * 2048u + k_row + (uint32_t)(((unit + k_unit) & 7) ^ r8) * 16u;
-  };
-  auto v_addr = [&](int unit) {
-    return (uint32_t)(unit >> 3) * 2048u + v_row + (uint32_t)(((unit + v_unit) & 7) ^ r8) * 16u;
+  // A row's unit u = 8 c + v is unit v of 128-byte piece c: 2048 c bytes on, and, with
+  // the lane's own bit of v and its row's swizzle in the base, v's other bits by XOR.
+  const uint32_t k_base = (uint32_t)(r8 + 8 * (mi >> 1)) * 128u + (uint32_t)((mi & 1) ^ r8) * 16u;
+  const uint32_t v_base = (uint32_t)(r8 + 8 * (mi & 1)) * 128u + (uint32_t)((mi >> 1) ^ r8) * 16u;
+  auto at_unit = [](uint32_t row_base, int unit) {  // unit even
+    return (row_base ^ (uint32_t)(unit & 7) * 16u) + (uint32_t)(unit >> 3) * 2048u;
   };
   constexpr int kUnits = D * (kFp8 ? 1 : 2) / 16;  // 16-byte units of a K (or V) row
 
   const int er = tid >> 4, ed = (tid & 15) * E;  // this thread's part of an output
   float* my_wb = wbuf + warp * C::kWbFloats;
   bool ok = true;
-  int n = 0;
+  int n = 0, stage = 0;  // the warp's next tile and its stage
+  uint32_t parity = 0;
 
   for (int f = f0; f < f1;) {
     const Pair pr = next;
@@ -536,25 +553,33 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       for (int c = 0; c < E; ++c) acc[nb][c][0] = acc[nb][c][1] = acc[nb][c][2] = acc[nb][c][3] = 0.f;
     }
 
-    for (int took; ok && f0 + warp + kWarps * n < seg_end; n += took) {
-      took = U == 2 && f0 + warp + kWarps * (n + 1) < seg_end ? 2 : 1;
+    const int seg_n = (seg_end - f0 - warp + kWarps - 1) / kWarps;  // this warp's tiles end here
+    for (int took; ok && n < seg_n; n += took) {
+      took = min(U, seg_n - n);
+      int at[U];  // stages; an absent second tile reads the first again and counts for nothing
+      uint32_t par[U];
+      at[0] = stage;
+      par[0] = parity;
+      if (++stage == kStages) stage = 0, parity ^= 1;
+      if (U == 2) {
+        at[U - 1] = took == 2 ? stage : at[0];
+        par[U - 1] = took == 2 ? parity : par[0];
+        if (took == 2 && ++stage == kStages) stage = 0, parity ^= 1;
+      }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < took)
-          ok = mbar_wait(bars + 8 * ((n + u) % kStages), ((n + u) / kStages) & 1, p.err) && ok;
+      for (int u = 0; u < U; ++u) ok = mbar_wait(bars + 8 * at[u], par[u], p.err) && ok;
       if (!ok) break;
       uint32_t kf[U][kUnits / 2][4], vf[U][kUnits / 2][4];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        // an absent second tile reads the first again and counts for nothing
-        const uint32_t tile = ring + ((n + (u < took ? u : 0)) % kStages) * C::kTileBytes;
+        const uint32_t tile = ring + at[u] * C::kTileBytes;
 #pragma unroll
         for (int i = 0; i < kUnits / 2; ++i)
-          ldsm_x4(tile + k_addr(2 * i), kf[u][i][0], kf[u][i][1], kf[u][i][2], kf[u][i][3]);
+          ldsm_x4(at_unit(tile + k_base, 2 * i), kf[u][i][0], kf[u][i][1], kf[u][i][2], kf[u][i][3]);
 #pragma unroll
         for (int i = 0; i < kUnits / 2; ++i)
-          ldsm_x4_trans(tile + v_addr(kUnits + 2 * i), vf[u][i][0], vf[u][i][1], vf[u][i][2],
-                        vf[u][i][3]);
+          ldsm_x4_trans(at_unit(tile + v_base, kUnits + 2 * i), vf[u][i][0], vf[u][i][1],
+                        vf[u][i][2], vf[u][i][3]);
       }
       fence_proxy_async_smem();  // the stages are refilled by TMA
       __syncwarp();
@@ -565,88 +590,97 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         ks[u] = 1.f;
         lv[u] = 0.f;
         if (kFp8) {
-          const int k = n + (u < took ? u : 0);
-          const bool odd = (k >> 5) & 1;
+          const int k = U == 2 && u >= took ? n : n + u;
+          const bool odd = k & 32;
           ks[u] = __shfl_sync(0xffffffffu, odd ? sc1.x : sc0.x, k & 31);
           lv[u] = lg2(__shfl_sync(0xffffffffu, odd ? sc1.y : sc0.y, k & 31));
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (u < took && issued < count) issue(issued++);
+        if (u < took && issued < count) issue(issued++, at[u]);
 
-      // ---- S = Q K^T: tokens 0..7 (sa) and 8..15 (sb), two chains each ----
-      float sa[U][2][4], sb[U][2][4];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sa[u][i][e] = sb[u][i][e] = 0.f;
+      // ---- S = Q K^T: tokens 0..7 (sa) and 8..15 (sb), kChains sums each ----
+      constexpr int kChains = D == 128 ? 2 : 1;
+      float sa[U][kChains][4], sb[U][kChains][4];
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const uint32_t a0 = qa[c][0], a1 = NB == 2 ? qa[c][1] : 0u;
         const uint32_t a2 = qa[c][NB], a3 = NB == 2 ? qa[c][NB + 1] : 0u;
+        const int ch = c % kChains;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+          uint32_t x0, x1, y0, y1;
           if constexpr (kFp8) {
             const uint32_t x = kf[u][c / 2][c & 1], y = kf[u][c / 2][2 + (c & 1)];
-            mma<true>(sa[u][c & 1], a0, a1, a2, a3, e4m3x2_f16(x), e4m3x2_f16_hi(x));
-            mma<true>(sb[u][c & 1], a0, a1, a2, a3, e4m3x2_f16(y), e4m3x2_f16_hi(y));
+            x0 = e4m3x2_f16(x); x1 = e4m3x2_f16_hi(x);
+            y0 = e4m3x2_f16(y); y1 = e4m3x2_f16_hi(y);
           } else {
-            mma<false>(sa[u][c & 1], a0, a1, a2, a3, kf[u][c][0], kf[u][c][1]);
-            mma<false>(sb[u][c & 1], a0, a1, a2, a3, kf[u][c][2], kf[u][c][3]);
+            x0 = kf[u][c][0]; x1 = kf[u][c][1];
+            y0 = kf[u][c][2]; y1 = kf[u][c][3];
+          }
+          if (c < kChains) {
+            mma0<kFp8>(sa[u][ch], a0, a1, a2, a3, x0, x1);
+            mma0<kFp8>(sb[u][ch], a0, a1, a2, a3, y0, y1);
+          } else {
+            mma<kFp8>(sa[u][ch], a0, a1, a2, a3, x0, x1);
+            mma<kFp8>(sb[u][ch], a0, a1, a2, a3, y0, y1);
           }
         }
       }
-
-      // ---- visibility ----
-      bool see[U][4];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+      // logits in log2 units: tokens 2t, 2t + 1, 2t + 8, 2t + 9
+      float x[NB][U][4];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        int tau = f0 + warp + kWarps * (n + u) - pr.begin;
-        if (tau >= sp.head) tau += sp.gap;
-        const int tok = tau * 16;
-        const bool whole =
-            u < took && tok + 16 <= sp.L && (tok >= sp.start || tok + 16 <= sp.first);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) see[u][i] = true;
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = tok + 2 * t + (i & 1) + 8 * (i >> 1);
-            see[u][i] = u < took && j < sp.L && (j >= sp.start || j < sp.first);
-          }
-          // values that nobody sees may be anything: zero them, as 0 * NaN is NaN
-          const uint32_t mlo = (see[u][0] ? 0xffffu : 0u) | (see[u][1] ? 0xffff0000u : 0u);
-          const uint32_t mhi = (see[u][2] ? 0xffffu : 0u) | (see[u][3] ? 0xffff0000u : 0u);
-#pragma unroll
-          for (int i = 0; i < kUnits / 2; ++i) {
-            vf[u][i][0] &= mlo; vf[u][i][1] &= mhi; vf[u][i][2] &= mlo; vf[u][i][3] &= mhi;
-          }
-        }
-      }
-
-      // ---- online softmax in log2 units ----
-      uint32_t pb[NB][U][2];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float x[U][4], tile_max[U];
-        float mx = -INFINITY, mu = -INFINITY;  // largest logit; largest with its value's scale
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float c2 = kFp8 ? row_scale[nb] * ks[u] : row_scale[nb];
-          x[u][0] = (sa[u][0][2 * nb] + sa[u][1][2 * nb]) * c2;
-          x[u][1] = (sa[u][0][2 * nb + 1] + sa[u][1][2 * nb + 1]) * c2;
-          x[u][2] = (sb[u][0][2 * nb] + sb[u][1][2 * nb]) * c2;
-          x[u][3] = (sb[u][0][2 * nb + 1] + sb[u][1][2 * nb + 1]) * c2;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[u][i] = see[u][i] ? x[u][i] : -INFINITY;
-          tile_max[u] = fmaxf(fmaxf(x[u][0], x[u][1]), fmaxf(x[u][2], x[u][3]));
-          tile_max[u] = fmaxf(tile_max[u], __shfl_xor_sync(0xffffffffu, tile_max[u], 1));
-          tile_max[u] = fmaxf(tile_max[u], __shfl_xor_sync(0xffffffffu, tile_max[u], 2));
-          mx = fmaxf(mx, tile_max[u]);
-          mu = fmaxf(mu, tile_max[u] + lv[u]);
+          for (int i = 0; i < 4; ++i) {
+            const float(&sx)[kChains][4] = i < 2 ? sa[u] : sb[u];
+            const int e = 2 * nb + (i & 1);
+            x[nb][u][i] = (kChains == 2 ? sx[0][e] + sx[kChains - 1][e] : sx[0][e]) * c2;
+          }
+        }
+
+      // ---- visibility ----
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        int tau = f0 + warp - pr.begin + kWarps * (n + u);
+        if (tau >= sp.head) tau += sp.gap;
+        const int tok = tau * 16;
+        if (u < took && tok + 16 <= sp.L && (tok >= sp.start || tok + 16 <= sp.first)) continue;
+        bool see[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = tok + 2 * t + (i & 1) + 8 * (i >> 1);
+          see[i] = u < took && j < sp.L && (j >= sp.start || j < sp.first);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            if (!see[i]) x[nb][u][i] = -INFINITY;
+        }
+        // values that nobody sees may be anything: zero them, as 0 * NaN is NaN
+        const uint32_t mlo = (see[0] ? 0xffffu : 0u) | (see[1] ? 0xffff0000u : 0u);
+        const uint32_t mhi = (see[2] ? 0xffffu : 0u) | (see[3] ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int i = 0; i < kUnits / 2; ++i) {
+          vf[u][i][0] &= mlo; vf[u][i][1] &= mhi; vf[u][i][2] &= mlo; vf[u][i][3] &= mhi;
+        }
+      }
+
+      // ---- online softmax ----
+      uint32_t pb[NB][U][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float mx = -INFINITY, mu = -INFINITY;  // largest logit; largest with its value's scale
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float(&y)[4] = x[nb][u];
+          float tm = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
+          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
+          mx = fmaxf(mx, tm);
+          mu = fmaxf(mu, tm + lv[u]);
         }
         const float mn = fmaxf(m[nb], mx), mref = mn == -INFINITY ? 0.f : mn;
         const float alpha = ex2(m[nb] - mref);
@@ -655,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         for (int u = 0; u < U; ++u) {
           float e[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = ex2(x[u][i] - mref);
+          for (int i = 0; i < 4; ++i) e[i] = ex2(x[nb][u][i] - mref);
           sum += (e[0] + e[1]) + (e[2] + e[3]);
           if constexpr (!kFp8) {
             pb[nb][u][0] = pack_bf16(e[0], e[1]);
@@ -672,8 +706,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const float d = lv[u] - shift;
-            pb[nb][u][0] = pack_f16(ex2(x[u][0] + d), ex2(x[u][1] + d));
-            pb[nb][u][1] = pack_f16(ex2(x[u][2] + d), ex2(x[u][3] + d));
+            const float(&y)[4] = x[nb][u];
+            pb[nb][u][0] = pack_f16(ex2(y[0] + d), ex2(y[1] + d));
+            pb[nb][u][1] = pack_f16(ex2(y[2] + d), ex2(y[3] + d));
           }
         }
         // rows 2t, 2t + 1 are the accumulator's columns; their factors are on lanes 8t, 8t + 4
