@@ -12,11 +12,14 @@
 // but for codes that leave e4m3's normal range (below 2^-6 of the new scale).
 //
 // Bound by memory for prompts (bf16 read once, codes written once), by latency
-// for single tokens.  A warp takes one kv head of `slab` consecutive rows (1 when
-// there are few, 16 when there are many): it finds the first row's request with a
+// for single tokens.  A team of warps (1, 2 or 4, so that a page's rows are about
+// 16 loads a lane) takes one kv head of `slab` consecutive rows (1 when there are
+// few, a page's when there are many): it finds the first row's request with a
 // 32-way search of cu_tokens and walks the pages that begin in its rows, loading
-// the rows of a page at once (16 16-byte loads a lane) before it reduces, and
-// encoding them from the registers.
+// the rows of a page to shared memory at once (up to 16 16-byte copies a lane)
+// before it reduces, and encoding them from there.
+#include <algorithm>
+
 #include "pkv_internal.h"
 #include "ptx.cuh"
 
@@ -24,7 +27,8 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kFullWarps = 16384;
+constexpr int kFullWarps = 8192;
+constexpr int kMaxHeld = 32;
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
 
 // Smallest power of two s >= 2^-100 with a <= 448 s (448 = 1.75 * 2^8); 0 for a = 0.
@@ -103,45 +107,53 @@ __device__ __forceinline__ int request_of(const AppendFp8Params& p, long long r)
   return found;
 }
 
+__device__ __forceinline__ void cp_async_16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // A row [K | V] of 2D values takes 2D/8 lanes of 8 values; a warp covers
-// RPW = 32 / (2D/8) rows at once, kHold times RPW rows in registers.
-template <int D>
+// RPW = 32 / (2D/8) rows at once, a team of kTeam warps kTeam times as many.  `hold`
+// keeps the first `held` 16-byte units of each lane in shared memory
+// (hold[32 i + lane] is read by the lane that asked for it); later ones are read
+// twice.  exchange: 2 x 2 floats per warp, turn: pages of the team so far.  False: the page is not in the cache.
+template <int D, int kTeam>
 __device__ __forceinline__ bool append_page(const AppendFp8Params& p, int h, long long r, int n,
-                                            int blk, int slot0) {
-  constexpr int LPR = 2 * D / 8, RPW = 32 / LPR, kHold = 16;
-  const int lane = threadIdx.x & 31, sub = lane / LPR, unit = lane % LPR;
+                                            int blk, int slot0, uint4* hold, int held,
+                                            float* exchange, int& turn) {
+  constexpr int LPR = 2 * D / 8, RPW = 32 / LPR, RPT = RPW * kTeam;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, unit = lane % LPR;
+  const int sub = warp % kTeam * RPW + lane / LPR;  // this lane's rows: sub, sub + RPT, ...
   const bool is_v = unit >= LPR / 2;
   const uint16_t* src =
       (is_v ? p.v : p.k) + (r + sub) * p.s_st + h * p.s_sh + (unit % (LPR / 2)) * 8;
-  // rows sub, sub + RPW, ...: the first kHold of a lane stay in registers, loaded at
-  // once; magnitudes are compared as bf16 bit patterns, two at a time
-  auto load = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(src + i * RPW * p.s_st)); };
-  uint4 x[kHold];
-#pragma unroll
-  for (int g = 0; g < kHold; g += 4)
-    if (g * RPW < n) {
-#pragma unroll
-      for (int i = g; i < g + 4; ++i) x[i] = sub + i * RPW < n ? load(i) : make_uint4(0, 0, 0, 0);
-    }
+  const int64_t step = RPT * p.s_st;
+  const int mine = n > sub ? (n - sub + RPT - 1) / RPT : 0;  // this lane's units
+  const int first = min(mine, held);
+  hold += lane;
+  for (int i = 0; i < first; ++i) cp_async_16(hold + 32 * i, src + i * step);
+  auto load = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(src + i * step)); };
+
   // the page is needed from here on
-  if (blk < 0 || blk >= p.num_blocks) return false;
-  uint8_t* dst = p.cache + blk * p.c_sblk + h * p.c_sh + sub * p.c_stok + unit * 8;
-  float* scale = p.scale + blk * p.sc_sblk + h * p.sc_sh + (is_v ? 1 : 0);
-  const float s_old = slot0 > 0 ? *scale : 0.f;
-  uint32_t big = 0;
-#pragma unroll
-  for (int g = 0; g < kHold; g += 4)
-    if (g * RPW < n) {
-#pragma unroll
-      for (int i = g; i < g + 4; ++i) big = max_abs(big, x[i]);
-    }
-  for (int i = kHold; sub + i * RPW < n; ++i) big = max_abs(big, load(i));
+  const bool good = blk >= 0 && blk < p.num_blocks;
+  uint8_t* dst = p.cache + (good ? blk : 0) * p.c_sblk + h * p.c_sh + sub * p.c_stok + unit * 8;
+  float* scale = p.scale + (good ? blk : 0) * p.sc_sblk + h * p.sc_sh + (is_v ? 1 : 0);
+  const float s_old = good && slot0 > 0 ? *scale : 0.f;
+  uint32_t big = 0;  // magnitudes are compared as bf16 bit patterns, two at a time
+  for (int i = first; i < mine; ++i) big = max_abs(big, load(i));
+  cp_async_wait_all();
+  if (!good) return false;
+#pragma unroll 4
+  for (int i = 0; i < first; ++i) big = max_abs(big, hold[32 * i]);
   float a = __uint_as_float(max(big << 16, big & 0xffff0000u));
   __syncwarp();
   if (__any_sync(0xffffffffu, !(a < INFINITY))) {  // NaN and infinities set no scale
     a = 0.f;
 #pragma unroll 1
-    for (int i = 0; sub + i * RPW < n; ++i) {
+    for (int i = 0; i < mine; ++i) {
       float f[8];
       unpack8(load(i), f);
 #pragma unroll
@@ -152,14 +164,22 @@ __device__ __forceinline__ bool append_page(const AppendFp8Params& p, int h, lon
 #pragma unroll
   for (int o = 1; o < LPR / 2; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   if (RPW > 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
+  if (kTeam > 1) {
+    // two buffers: a warp may begin the team's next page while another still reads this one's
+    float* team_max = exchange + (turn++ & 1) * 2 * kWarps;
+    if (lane % LPR % (LPR / 2) == 0) team_max[2 * warp + is_v] = a;
+    named_bar_sync(1 + warp / kTeam, 32 * kTeam);
+#pragma unroll
+    for (int w = 0; w < kTeam; ++w) a = fmaxf(a, team_max[2 * (warp / kTeam * kTeam + w) + is_v]);
+  }
 
   const float s = fmaxf(s_old, pow2_scale(a));
-  __syncwarp();  // every lane has read the old scale
+  __syncwarp();  // every lane (before the barrier: of every warp) has read the old scale
   if (sub == 0 && unit % (LPR / 2) == 0) *scale = s;
   if (s > s_old && slot0 > 0) {
     const float f0 = __fdiv_rn(s_old, s);
 #pragma unroll 4
-    for (int i = 0; sub + i < slot0; i += RPW) {
+    for (int i = 0; sub + i < slot0; i += RPT) {
       uint2* at = reinterpret_cast<uint2*>(dst + i * p.c_stok);
       float f[8];
       decode8(*at, f);
@@ -170,6 +190,7 @@ __device__ __forceinline__ bool append_page(const AppendFp8Params& p, int h, lon
   }
   const float div = s > 0.f ? s : 1.f;
   dst += slot0 * p.c_stok;
+  const int64_t dst_step = RPT * p.c_stok;
   if ((__float_as_uint(div) & 0x7fffffu) == 0) {
     // s is a power of two (a grown scale is one): x / s is the product with 1 / s
     const float inv = 1.f / div;
@@ -178,38 +199,37 @@ __device__ __forceinline__ bool append_page(const AppendFp8Params& p, int h, lon
       unpack8(u, f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] *= inv;
-      *reinterpret_cast<uint2*>(dst + i * RPW * p.c_stok) = encode8(f);
+      *reinterpret_cast<uint2*>(dst + i * dst_step) = encode8(f);
     };
-#pragma unroll
-    for (int g = 0; g < kHold; g += 4)
-      if (g * RPW < n) {
-#pragma unroll
-        for (int i = g; i < g + 4; ++i)
-          if (sub + i * RPW < n) put(x[i], i);
-      }
-    for (int i = kHold; sub + i * RPW < n; ++i) put(load(i), i);
+#pragma unroll 4
+    for (int i = 0; i < first; ++i) put(hold[32 * i], i);
+    for (int i = first; i < mine; ++i) put(load(i), i);
   } else {
 #pragma unroll 1
-    for (int i = 0; sub + i * RPW < n; ++i) {
+    for (int i = 0; i < mine; ++i) {
       float f[8];
       unpack8(load(i), f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], div);
-      *reinterpret_cast<uint2*>(dst + i * RPW * p.c_stok) = encode8(f);
+      *reinterpret_cast<uint2*>(dst + i * dst_step) = encode8(f);
     }
   }
   return true;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendFp8Params p, int slab) {
+template <int D, int kTeam>
+__global__ void __launch_bounds__(kWarps * 32, 7)
+    append_kernel(const AppendFp8Params p, int slab, int held) {
+  extern __shared__ uint4 hold[];
+  __shared__ float exchange[2 * 2 * kWarps];
   griddep_wait();
-  const int lane = threadIdx.x & 31, P = p.page_size;
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int h = (int)(w % p.Hkv);
-  long long r = w / p.Hkv * slab;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, P = p.page_size;
+  const long long team = ((long long)blockIdx.x * kWarps + warp) / kTeam;
+  const int h = (int)(team % p.Hkv);
+  long long r = team / p.Hkv * slab;
   const long long end = min(r + slab, (long long)p.T);
   if (r >= end) return;
+  int turn = 0;
 
   const long long each = p.cu ? 0 : p.T / p.B;
   int b = p.cu ? request_of(p, r) : (int)(r / each);
@@ -224,7 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendFp8P
     if (r0 < 0) return;
     if (r >= r1) continue;  // an empty request (or padding behind the last one)
     const long long first = (long long)__ldg(p.seq_lens + b) - r1;  // position of row i: first + i
-    r = max(r, -first);  // tokens at negative positions are dropped
+    r = min(max(r, -first), r1);  // tokens at negative positions are dropped
     while (r < end && r < r1) {
       const long long pos = first + r;
       const int slot0 = (int)(pos % P);
@@ -233,7 +253,9 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendFp8P
       if (r == r0 || r == -first || slot0 == 0) {
         const long long pg = pos / P;
         const int blk = pg < p.max_blocks ? __ldg(p.bt + b * p.bt_sb + pg) : -1;
-        if (!append_page<D>(p, h, r, n, blk, slot0) && lane == 0)
+        if (!append_page<D, kTeam>(p, h, r, n, blk, slot0, hold + warp * 32 * held, held,
+                                   exchange, turn) &&
+            lane == 0)
           atomicOr(p.err, pg < p.max_blocks ? DEVERR_BAD_BLOCK : DEVERR_SEQ_TOO_LONG);
       }
       r += n;
@@ -244,21 +266,43 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendFp8P
 
 }  // namespace
 
-cudaError_t launch_gqa_kv_append_fp8(const AppendFp8Params& p, cudaStream_t stream) {
-  // rows a warp walks: 16 once the rows alone give every SM warps enough
+template <int D, int kTeam>
+static cudaError_t launch_t(const AppendFp8Params& p, int most, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e =
+      set_smem_attr_once(append_kernel<D, kTeam>, kWarps * 32 * 16 * kMaxHeld, done);
+  if (e != cudaSuccess) return e;
+  // rows a team walks: up to a page's once single rows give every SM warps enough
   int slab = 1;
-  while (slab < 16 && p.T * p.Hkv / slab > kFullWarps) slab *= 2;
-  const long long warps = (p.T + slab - 1) / slab * p.Hkv;
+  while (slab < most && p.T * p.Hkv * kTeam / slab > kFullWarps) slab *= 2;
+  const long long warps = (p.T + slab - 1) / slab * p.Hkv * kTeam;
+  // 16-byte units a lane holds
+  const int rows = 32 / (2 * D / 8) * kTeam;
+  const int held = std::min((most + rows - 1) / rows, kMaxHeld);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((warps + kWarps - 1) / kWarps));
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kWarps * 32 * 16 * held;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, p.D == 64 ? append_kernel<64> : append_kernel<128>, p, slab);
+  return cudaLaunchKernelEx(&cfg, append_kernel<D, kTeam>, p, slab, held);
+}
+
+cudaError_t launch_gqa_kv_append_fp8(const AppendFp8Params& p, cudaStream_t stream) {
+  // rows that a page receives on average, and a team for about 16 loads a lane of them
+  // (32 for 128 rows of 2 x 128)
+  const int most = (int)std::min<int64_t>(p.page_size, (p.T + p.B - 1) / p.B);
+  if (p.D == 64)
+    return most <= 32   ? launch_t<64, 1>(p, most, stream)
+           : most <= 64 ? launch_t<64, 2>(p, most, stream)
+                        : launch_t<64, 4>(p, most, stream);
+  return most <= 16   ? launch_t<128, 1>(p, most, stream)
+         : most <= 32 ? launch_t<128, 2>(p, most, stream)
+                      : launch_t<128, 4>(p, most, stream);
 }
 
 }  // namespace pkv

@@ -79,6 +79,33 @@ def test_ragged_prompts(D, P):
     check(pr, run(pr))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("P", [32, 64, 128])
+def test_large_pages_in_pieces_held_and_continued(D, P):
+    """Pages whose rows several warps share: whole, begun, continued twice in one batch, with bad
+    pages between good ones of a request."""
+    old = [0, 5, P - 3, 2 * P, 17, 0]
+    new = [3 * P + 7, P, 3, 4 * P, 2 * P - 17, 1]
+    pr = problem(D + 5 * P, old, new, 3, D, P)
+    check(pr, run(pr))
+    pr["bt"][0, 1], pr["bt"][3, 3] = -1, 10 ** 7
+    got = run(pr)
+    with pytest.raises(pkv.PkvError):
+        pkv.check_errors(0)
+    check(pr, got)
+
+
+def test_negative_lengths_take_no_row_of_the_next_request():
+    pr = problem(14, [0, 3, 0], [5, 6, 20], 2, 64, 16)
+    pr["sl"][0], pr["sl"][1] = -3, 2
+    check(pr, run(pr))
+
+
+def test_one_long_prompt_among_single_tokens():
+    pr = problem(15, [9] * 40, [1] * 20 + [300] + [1] * 19, 2, 128, 64)
+    check(pr, run(pr))
+
+
 def test_many_requests_of_one_token_and_of_none():
     g = torch.Generator().manual_seed(3)
     new = torch.randint(0, 3, (500,), generator=g).tolist()
