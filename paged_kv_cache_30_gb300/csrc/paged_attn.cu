@@ -27,7 +27,7 @@
 //    and values become fp16 exactly; the query is scaled to fp16's range by a
 //    power of two for each row (exact but for elements below 2^-29 of the row's
 //    largest).
-//  * One pass with the running maximum m and sum l in 32 bits.  With scales, the
+//  * One pass with a running reference m near the maximum and the sum l in 32 bits.  With scales, the
 //    accumulator holds sum_j 2^(x_j + log2 vs_j - R) code_j under a running
 //    maximum R of its own, so a page of large or small values keeps its
 //    precision: the weights are rounded to fp16 (11 bits) relative to the largest
@@ -46,6 +46,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMergeGroup = 16;
 constexpr int kPairCost = kPagedPairCost;
 constexpr int kSnapTiles = 8;      // a cut this near a pair's border moves there
+constexpr float kSlack = 8.f;      // log2 units: weights stay below 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -544,10 +545,11 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     }
 
     float acc[NB][E][4];
-    float m[NB], l[NB], R[NB];
+    float m[NB], l[NB], R[NB], m_ref[NB], R_ref[NB];  // m_ref: m, or 0 before a key was seen
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       m[nb] = R[nb] = -INFINITY;
+      m_ref[nb] = R_ref[nb] = 0.f;
       l[nb] = 0.f;
 #pragma unroll
       for (int c = 0; c < E; ++c) acc[nb][c][0] = acc[nb][c][1] = acc[nb][c][2] = acc[nb][c][3] = 0.f;
@@ -566,6 +568,19 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         par[U - 1] = took == 2 ? parity : par[0];
         if (took == 2 && ++stage == kStages) stage = 0, parity ^= 1;
       }
+      // the scales of the tiles, before their batch's registers can be turned over
+      float ks[U], lv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        ks[u] = 1.f;
+        lv[u] = 0.f;
+        if (kFp8) {
+          const int k = U == 2 && u >= took ? n : n + u;
+          const bool odd = k & 32;
+          ks[u] = __shfl_sync(0xffffffffu, odd ? sc1.x : sc0.x, k & 31);
+          lv[u] = lg2(__shfl_sync(0xffffffffu, odd ? sc1.y : sc0.y, k & 31));
+        }
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) ok = mbar_wait(bars + 8 * at[u], par[u], p.err) && ok;
       if (!ok) break;
@@ -581,25 +596,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
           ldsm_x4_trans(at_unit(tile + v_base, kUnits + 2 * i), vf[u][i][0], vf[u][i][1],
                         vf[u][i][2], vf[u][i][3]);
       }
-      fence_proxy_async_smem();  // the stages are refilled by TMA
-      __syncwarp();
-      // the scales of the tiles, before their batch's registers can be turned over
-      float ks[U], lv[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        ks[u] = 1.f;
-        lv[u] = 0.f;
-        if (kFp8) {
-          const int k = U == 2 && u >= took ? n : n + u;
-          const bool odd = k & 32;
-          ks[u] = __shfl_sync(0xffffffffu, odd ? sc1.x : sc0.x, k & 31);
-          lv[u] = lg2(__shfl_sync(0xffffffffu, odd ? sc1.y : sc0.y, k & 31));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < took && issued < count) issue(issued++, at[u]);
-
       // ---- S = Q K^T: tokens 0..7 (sa) and 8..15 (sb), kChains sums each ----
       constexpr int kChains = D == 128 ? 2 : 1;
       float sa[U][kChains][4], sb[U][kChains][4];
@@ -628,6 +624,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
           }
         }
       }
+      // The fragments are in registers: the stages are free.  Asking for their next
+      // tiles takes the issuing lane some 150 cycles, which the products above cover.
+      fence_proxy_async_smem();
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < took && issued < count) issue(issued++, at[u]);
+
       // logits in log2 units: tokens 2t, 2t + 1, 2t + 8, 2t + 9
       float x[NB][U][4];
 #pragma unroll
@@ -668,51 +672,45 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         }
       }
 
-      // ---- online softmax ----
-      uint32_t pb[NB][U][2];
+      // ---- online softmax: the references m (of l) and R (of the accumulator) move only
+      // when a logit passes them by more than kSlack, so that most tiles need no
+      // reduction over the row's lanes; any reference gives the same result ----
+      bool pass = false;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float mx = -INFINITY, mu = -INFINITY;  // largest logit; largest with its value's scale
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float(&y)[4] = x[nb][u];
-          float tm = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
-          mx = fmaxf(mx, tm);
-          mu = fmaxf(mu, tm + lv[u]);
+          const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+          pass |= top > m[nb] + kSlack;
+          if (kFp8) pass |= top + lv[u] > R[nb] + kSlack;
         }
-        const float mn = fmaxf(m[nb], mx), mref = mn == -INFINITY ? 0.f : mn;
-        const float alpha = ex2(m[nb] - mref);
-        float sum = 0.f;
+      if (__any_sync(0xffffffffu, pass)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float e[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = ex2(x[nb][u][i] - mref);
-          sum += (e[0] + e[1]) + (e[2] + e[3]);
-          if constexpr (!kFp8) {
-            pb[nb][u][0] = pack_bf16(e[0], e[1]);
-            pb[nb][u][1] = pack_bf16(e[2], e[3]);
-          }
-        }
-        l[nb] = __fmaf_rn(l[nb], alpha, sum);
-        m[nb] = mn;
-        float beta = alpha;
-        if constexpr (kFp8) {
-          const float Rn = fmaxf(R[nb], mu), shift = Rn == -INFINITY ? 0.f : Rn;
-          beta = ex2(R[nb] - shift);
-          R[nb] = Rn;
+        for (int nb = 0; nb < NB; ++nb) {
+          float mx = -INFINITY, mu = -INFINITY;  // largest logit; largest with its value's scale
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const float d = lv[u] - shift;
             const float(&y)[4] = x[nb][u];
-            pb[nb][u][0] = pack_f16(ex2(y[0] + d), ex2(y[1] + d));
-            pb[nb][u][1] = pack_f16(ex2(y[2] + d), ex2(y[3] + d));
+            float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            mx = fmaxf(mx, top);
+            mu = fmaxf(mu, top + lv[u]);
           }
-        }
-        // rows 2t, 2t + 1 are the accumulator's columns; their factors are on lanes 8t, 8t + 4
-        if (__any_sync(0xffffffffu, beta != 1.f)) {
+          const float mn = fmaxf(m[nb], mx);
+          m_ref[nb] = mn == -INFINITY ? 0.f : mn;
+          const float alpha = ex2(m[nb] - m_ref[nb]);
+          l[nb] *= alpha;
+          m[nb] = mn;
+          float beta = alpha;
+          if (kFp8) {
+            const float Rn = fmaxf(R[nb], mu);
+            R_ref[nb] = Rn == -INFINITY ? 0.f : Rn;
+            beta = ex2(R[nb] - R_ref[nb]);
+            R[nb] = Rn;
+          }
+          // rows 2t, 2t + 1 are the accumulator's columns; their factors are on lanes 8t, 8t + 4
           const float b0 = __shfl_sync(0xffffffffu, beta, 8 * t);
           const float b1 = __shfl_sync(0xffffffffu, beta, 8 * t + 4);
 #pragma unroll
@@ -721,6 +719,25 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
           }
         }
       }
+      uint32_t pb[NB][U][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float(&y)[4] = x[nb][u];
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = ex2(y[i] - m_ref[nb]);
+          l[nb] += (e[0] + e[1]) + (e[2] + e[3]);
+          if constexpr (kFp8) {
+            const float d = lv[u] - R_ref[nb];
+            pb[nb][u][0] = pack_f16(ex2(y[0] + d), ex2(y[1] + d));
+            pb[nb][u][1] = pack_f16(ex2(y[2] + d), ex2(y[3] + d));
+          } else {
+            pb[nb][u][0] = pack_bf16(e[0], e[1]);
+            pb[nb][u][1] = pack_bf16(e[2], e[3]);
+          }
+        }
 
       // ---- O^T += V^T P^T ----
 #pragma unroll
