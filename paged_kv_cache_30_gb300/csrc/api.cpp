@@ -1172,7 +1172,18 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   p.grid = int(std::max<int64_t>(
       1, std::min<int64_t>(std::min(ws.num_sms * shape.ctas_per_sm, pkv::kPagedMaxGrid),
                            (cost + pkv::kPagedMinCost - 1) / pkv::kPagedMinCost)));
-  if (int64_t(2) * p.grid * shape.part_floats * 4 > int64_t(ws.partial_bytes))
+  // Cluster mode: every pair has CTAs of its own in one wave, none with more than
+  // kPagedClusterTiles tiles.
+  const int64_t slots = int64_t(ws.num_sms) * shape.ctas_per_sm;
+  if (B * Hkv <= slots) {
+    const int64_t c = std::max<int64_t>(
+        1, std::min({int64_t(pkv::kPagedMaxCluster), slots * 7 / 8 / (B * Hkv), (tiles + 15) / 16}));
+    if ((tiles + c - 1) / c <= pkv::kPagedClusterTiles) {
+      p.cluster = int(c);
+      p.grid = int(B * Hkv * c);
+    }
+  }
+  if (!p.cluster && int64_t(2) * p.grid * shape.part_floats * 4 > int64_t(ws.partial_bytes))
     return fail(PKV_ERR_WORKSPACE, "workspace holds %lld bytes of partials, %lld needed",
                 (long long)ws.partial_bytes, (long long)(int64_t(2) * p.grid * shape.part_floats * 4));
   p.partials = ws.partials;

@@ -32,7 +32,11 @@
 //    maximum R of its own, so a page of large or small values keeps its
 //    precision: the weights are rounded to fp16 (11 bits) relative to the largest
 //    contribution; for the bf16 cache they are rounded to bf16, as V is bf16.
-//  * A request cut between CTAs: each publishes its 32-bit (O, m, l, R); the last
+//  * Cluster mode, for few and short requests (the rule is the caller's): a cluster of
+//    CTAs takes one pair each, a CTA an equal part of its tiles, and the first CTA
+//    merges the parts through distributed shared memory: no scan of the lengths, no
+//    global partials (see launch_paged_attn's caller for what it measured).
+//  * Otherwise, a request cut between CTAs: each publishes its 32-bit (O, m, l, R); the last
 //    CTA of a group of up to 16 (an arrival counter) merges the group in order,
 //    the last group merges the groups.  Results do not depend on timing.
 #include "pkv_internal.h"
@@ -318,7 +322,7 @@ __device__ __forceinline__ void merge_partials(const PagedParams& p, int n, Slot
   }
 }
 
-template <class C>
+template <class C, bool kCluster>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedParams p,
                       const __grid_constant__ CUtensorMap kv_map) {
@@ -342,51 +346,66 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   if (tid == 0) tma_prefetch_desc(&kv_map);
   griddep_wait();  // nothing of the caller's is read before
 
-  // ---- prefix[b]: tiles per kv head before request b ----
-  {
-    const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
-    int mine = 0;
-    for (int b = b0; b < min(b0 + per, B); ++b) {
-      const int len = __ldg(p.seq_lens + b);
-      if (blockIdx.x == 0 && len > p.max_blocks * p.page_size) atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
-      mine += span_of(p, len).tiles;
+  // This CTA's tiles are [f0, f1) of all pairs' (of one pair's in the cluster mode).
+  int f0, f1, chunk = 0, snap = 0;
+  Pair next = {};  // the pair after the current one
+  const int part = kCluster ? (int)blockIdx.x % p.cluster : 0;
+  if constexpr (kCluster) {
+    next.b = (int)blockIdx.x / p.cluster / Hkv;
+    next.kvh = (int)blockIdx.x / p.cluster % Hkv;
+    const int len = __ldg(p.seq_lens + next.b);
+    if (part == 0 && next.kvh == 0 && len > p.max_blocks * p.page_size)
+      atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
+    next.n = span_of(p, len).tiles;
+    f0 = (int)((long long)next.n * part / p.cluster);
+    f1 = (int)((long long)next.n * (part + 1) / p.cluster);
+    griddep_launch_dependents();
+  } else {
+    // ---- prefix[b]: tiles per kv head before request b ----
+    {
+      const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
+      int mine = 0;
+      for (int b = b0; b < min(b0 + per, B); ++b) {
+        const int len = __ldg(p.seq_lens + b);
+        if (blockIdx.x == 0 && len > p.max_blocks * p.page_size) atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
+        mine += span_of(p, len).tiles;
+      }
+      int run = block_scan(mine, misc);
+      for (int b = b0; b < min(b0 + per, B); ++b) {
+        prefix[b] = run;
+        run += span_of(p, __ldg(p.seq_lens + b)).tiles;
+        if (b == B - 1) prefix[B] = run;
+      }
     }
-    int run = block_scan(mine, misc);
-    for (int b = b0; b < min(b0 + per, B); ++b) {
-      prefix[b] = run;
-      run += span_of(p, __ldg(p.seq_lens + b)).tiles;
-      if (b == B - 1) prefix[B] = run;
-    }
-  }
-  __syncthreads();
-  griddep_launch_dependents();
+    __syncthreads();
+    griddep_launch_dependents();
 
-  // requests without a key
-  for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    if (prefix[b + 1] != prefix[b]) continue;
-    for (int i = tid; i < Hkv * p.G * (D / 8); i += kThreads) {
-      const int h = i / (D / 8);
-      *reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + (i % (D / 8)) * 8) =
-          make_uint4(0, 0, 0, 0);
-      if (i % (D / 8) == 0 && p.lse) p.lse[b * p.lse_sb + h * p.lse_sh] = -INFINITY;
+    // requests without a key
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+      if (prefix[b + 1] != prefix[b]) continue;
+      for (int i = tid; i < Hkv * p.G * (D / 8); i += kThreads) {
+        const int h = i / (D / 8);
+        *reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + (i % (D / 8)) * 8) =
+            make_uint4(0, 0, 0, 0);
+        if (i % (D / 8) == 0 && p.lse) p.lse[b * p.lse_sb + h * p.lse_sh] = -INFINITY;
+      }
     }
-  }
 
-  // ---- this CTA's tiles [f0, f1) ----
-  // cuts are placed in the space of costs and turned into places of tiles
-  const int tiles = prefix[B] * Hkv, total = tiles + kPairCost * B * Hkv;
-  const int chunk = max((int)(((uint32_t)total + gridDim.x - 1) / gridDim.x), kPagedMinCost);
-  const int snap = min(kSnapTiles, chunk / 2);
-  int f0, f1;
-  {
-    // lanes 0..15 place this CTA's cut, lanes 16..31 the next one's
-    const long long x = ((long long)blockIdx.x + (lane >> 4)) * chunk;
-    const Pair r = pair_at_group<kPairCost, 16>(prefix, B, Hkv, (int)min(x, (long long)total - 1));
-    const int at = (int)min(x, (long long)total - 1) - r.begin - kPairCost;  // the pair's tiles before the cut
-    int f = prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
-    if (x >= total) f = tiles;
-    f0 = __shfl_sync(0xffffffffu, f, 0);
-    f1 = __shfl_sync(0xffffffffu, f, 16);
+    // ---- this CTA's tiles ----
+    // cuts are placed in the space of costs and turned into places of tiles
+    const int tiles = prefix[B] * Hkv, total = tiles + kPairCost * B * Hkv;
+    chunk = max((int)(((uint32_t)total + gridDim.x - 1) / gridDim.x), kPagedMinCost);
+    snap = min(kSnapTiles, chunk / 2);
+    {
+      // lanes 0..15 place this CTA's cut, lanes 16..31 the next one's
+      const long long x = ((long long)blockIdx.x + (lane >> 4)) * chunk;
+      const Pair r = pair_at_group<kPairCost, 16>(prefix, B, Hkv, (int)min(x, (long long)total - 1));
+      const int at = (int)min(x, (long long)total - 1) - r.begin - kPairCost;  // the pair's tiles before the cut
+      int f = prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
+      if (x >= total) f = tiles;
+      f0 = __shfl_sync(0xffffffffu, f, 0);
+      f1 = __shfl_sync(0xffffffffu, f, 16);
+    }
   }
   // this warp's n-th tile is at place f0 + warp + 4 n
   const int count = f1 - f0 > warp ? (f1 - f0 - warp + kWarps - 1) / kWarps : 0;
@@ -396,12 +415,11 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   int l_blk = 0, l_pos = 0;     // lane's tile of the batch of 32: page; kv head, tile in the page
   int n_blk = 0, n_pos = 0;     // the same of the next batch
   float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;  // (ks, vs) of an even, an odd batch
-  Pair next = {};  // the pair after the current one
   auto look_up = [&](int n) {
     n_blk = n_pos = 0;
     if (n >= count) return;
     const int f = f0 + warp + kWarps * n;
-    const Pair r = f >= next.begin && f < next.begin + next.n
+    const Pair r = kCluster || (f >= next.begin && f < next.begin + next.n)
                        ? next : pair_at_lane<0>(prefix, B, Hkv, f);
     const Span s = span_of(p, __ldg(p.seq_lens + r.b));
     int tau = f - r.begin;
@@ -453,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   };
   int slot = 0;
   if (f0 < f1) {
-    next = pair_at_group<0, 32>(prefix, B, Hkv, f0);
+    if (!kCluster) next = pair_at_group<0, 32>(prefix, B, Hkv, f0);
     load_q(next, 0);
   }
   __syncwarp();  // the ring's barriers are lane 0's
@@ -491,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
 
     // ---- the query rows as the A operand; the next pair's rows are asked for ----
     const uint16_t* q_rows = qbuf + slot * C::kRows * D;
-    if (seg_end < f1) {
+    if (!kCluster && seg_end < f1) {
       next = pair_at_group<0, 32>(prefix, B, Hkv, seg_end);
       if (C::kQSlots == 2) load_q(next, slot ^ 1);
     }
@@ -539,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       }
     }
 
-    if (C::kQSlots == 1 && seg_end < f1) {
+    if (!kCluster && C::kQSlots == 1 && seg_end < f1) {
       __syncthreads();  // every warp has its rows
       load_q(next, 0);
     }
@@ -813,11 +831,26 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       }
     }
 
-    if (f == pr.begin && seg_end == pr.begin + pr.n) {
+    if (kCluster && p.cluster > 1) {
+      // this part's result, where the cluster's first CTA finds it
+      __syncthreads();  // every warp has read wbuf
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float* dst = wbuf + (er + 8 * nb) * D + ed;
+#pragma unroll
+        for (int e = 0; e < E; ++e) dst[e] = o[nb][e];
+        if (ed == 0) {
+          float* st = wbuf + C::kRows * D + er + 8 * nb;
+          st[0] = mc[nb];
+          st[C::kRows] = lc[nb];
+          st[2 * C::kRows] = Rc[nb];
+        }
+      }
+    } else if (kCluster || (f == pr.begin && seg_end == pr.begin + pr.n)) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
         finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
-    } else {
+    } else if constexpr (!kCluster) {
       // Contributors: the CTA whose range holds the first tile (slot 2 c + 1) and the
       // ones whose cuts lie inside (slot 2 c), more than snap tiles from either border.
       const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kPairCost;
@@ -870,24 +903,97 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   // limit) before the shared memory goes to another CTA.
   if (!ok)
     for (; n < issued; ++n) mbar_wait(bars + 8 * (n % kStages), (n / kStages) & 1, p.err);
+
+  if constexpr (kCluster) {
+    if (next.n == 0 && part == 0) {  // no key
+      for (int i = tid; i < p.G * (D / 8); i += kThreads) {
+        const int h = next.kvh * p.G + i / (D / 8);
+        *reinterpret_cast<uint4*>(p.out + next.b * p.o_sb + h * p.o_sh + (i % (D / 8)) * 8) =
+            make_uint4(0, 0, 0, 0);
+        if (i % (D / 8) == 0 && p.lse) p.lse[next.b * p.lse_sb + h * p.lse_sh] = -INFINITY;
+      }
+    }
+    if (p.cluster > 1) {
+      __syncwarp();
+      cluster_sync();  // every part's result is visible
+      if (part == 0 && next.n > 0) {
+        const uint32_t wb = smem_u32(wbuf);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int row = er + 8 * nb;
+          float o[E], ms[kPagedMaxCluster], Rs[kPagedMaxCluster], m = -INFINITY, l = 0.f, R = m;
+          // parts in order; a part without a tile left nothing
+          auto has = [&](int r) {
+            return r < p.cluster && (int)((long long)next.n * r / p.cluster) <
+                                        (int)((long long)next.n * (r + 1) / p.cluster);
+          };
+#pragma unroll
+          for (int r = 0; r < kPagedMaxCluster; ++r) {
+            ms[r] = Rs[r] = -INFINITY;
+            if (!has(r)) continue;
+            const uint32_t st = map_shared_rank(wb + 4u * (C::kRows * D + row), r);
+            ms[r] = ld_cluster_f32(st);
+            Rs[r] = ld_cluster_f32(st + 4u * 2 * C::kRows);
+          }
+#pragma unroll
+          for (int r = 0; r < kPagedMaxCluster; ++r) {
+            m = fmaxf(m, ms[r]);
+            R = fmaxf(R, Rs[r]);
+          }
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+          for (int r = 0; r < kPagedMaxCluster; ++r) {
+            if (!has(r)) continue;
+            const uint32_t at = map_shared_rank(wb, r);
+            l = __fmaf_rn(weight(ms[r], m),
+                          ld_cluster_f32(at + 4u * (C::kRows * D + C::kRows + row)), l);
+            const float w = weight(Rs[r], R);
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+              const float4 v = ld_cluster_f4(at + 4u * (row * D + ed + e));
+              o[e] = __fmaf_rn(w, v.x, o[e]);
+              o[e + 1] = __fmaf_rn(w, v.y, o[e + 1]);
+              o[e + 2] = __fmaf_rn(w, v.z, o[e + 2]);
+              o[e + 3] = __fmaf_rn(w, v.w, o[e + 3]);
+            }
+          }
+          const float sink =
+              p.sinks && row < p.G ? __ldg(p.sinks + next.kvh * p.G + row) * kLog2e : -INFINITY;
+          finalize<C>(p, next.b, next.kvh, row, ed, sink, o, m, l, R);
+        }
+      }
+      __syncwarp();
+      cluster_sync();  // the parts stay until they have been read
+    }
+  }
 }
 
-template <class C>
-cudaError_t launch_t(PagedParams p, const CUtensorMap& map, cudaStream_t stream) {
+template <class C, bool kCluster>
+cudaError_t launch_mode(const PagedParams& p, const CUtensorMap& map, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = set_smem_attr_once(paged_attn_kernel<C>, C::smem_bytes(kPagedMaxBatch), done);
+  cudaError_t e =
+      set_smem_attr_once(paged_attn_kernel<C, kCluster>, C::smem_bytes(kPagedMaxBatch), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::smem_bytes(p.B);
+  cfg.dynamicSmemBytes = C::smem_bytes(kCluster ? 0 : p.B);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster ? p.cluster : 1;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<C>, p, map);
+  cfg.numAttrs = kCluster && p.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<C, kCluster>, p, map);
+}
+
+template <class C>
+cudaError_t launch_t(const PagedParams& p, const CUtensorMap& map, cudaStream_t stream) {
+  return p.cluster ? launch_mode<C, true>(p, map, stream) : launch_mode<C, false>(p, map, stream);
 }
 
 template <typename F>

@@ -250,6 +250,7 @@ struct PagedParams {
   float scale;
   int page_shift;                // log2(page_size)
   int grid;
+  int cluster;                   // > 0: cluster mode, this many CTAs for each pair
   float* partials;               // [2 * grid] slots
   int* slot_counters;            // [2 * grid] arrival counters of merge groups
   int* pair_counters;            // [B * Hkv] arrival counters of the groups
@@ -268,6 +269,8 @@ cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& kv_map, c
 constexpr int kPagedPairCost = 12;
 constexpr int kPagedMinCost = 16;
 constexpr int kPagedMaxGrid = 512;  // 32 merge groups of 16
+constexpr int kPagedMaxCluster = 8;
+constexpr int kPagedClusterTiles = 48;  // most tiles of a CTA in the cluster mode
 
 // ------------------------------------------------ append to an e4m3 cache --
 struct AppendFp8Params {

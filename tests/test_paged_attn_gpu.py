@@ -23,12 +23,14 @@ def _lib():
     pkv.init(0)
 
 
-def problem(seed, lens, Hkv, G, D, P, fp8, window=0, first=0, sinks=False, nhd=False, spread=3.0):
+def problem(seed, lens, Hkv, G, D, P, fp8, window=0, first=0, sinks=False, nhd=False, spread=3.0,
+            wide=False):
     """Seeded CPU tensors.  Every slot that no request sees holds NaN (keys and values), and
     so do the scales of pages that hold no visible key; unused table entries are -1."""
     g = torch.Generator().manual_seed(seed)
     lens = torch.tensor(lens, dtype=torch.int32)
-    B, width = len(lens), max(1, -(-int(lens.max()) // P)) + 1
+    # a wide table (requests could be long) rules out a cluster of blocks for each request
+    B, width = len(lens), max(1, -(-int(lens.max()) // P)) + (9000 if wide else 1)
     see = [plain.visible(int(L), window, first) for L in lens]
     pages = [sorted(set((s // P).tolist())) for s in see]
     pool = sum(map(len, pages)) + 4
@@ -105,8 +107,9 @@ def check(pr, out, lse):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("G,Hkv,P", [(1, 3, 16), (4, 2, 32), (8, 1, 16), (8, 2, 64), (5, 2, 128),
                                      (16, 1, 32), (9, 2, 16)])
-def test_head_layouts_and_edge_lengths(fp8, D, G, Hkv, P):
-    pr = problem(G * 100 + P + D, EDGE_LENS, Hkv, G, D, P, fp8, sinks=(G % 2 == 0))
+@pytest.mark.parametrize("wide", [False, True])
+def test_head_layouts_and_edge_lengths(fp8, D, G, Hkv, P, wide):
+    pr = problem(G * 100 + P + D, EDGE_LENS, Hkv, G, D, P, fp8, sinks=(G % 2 == 0), wide=wide)
     check(pr, *run(pr))
 
 
@@ -116,6 +119,24 @@ def test_head_layouts_and_edge_lengths(fp8, D, G, Hkv, P):
 @pytest.mark.parametrize("P", [16, 32])
 def test_windows_and_first_tokens(fp8, window, first, P):
     pr = problem(window * 7 + first, EDGE_LENS, 2, 8, 128, P, fp8, window, first, sinks=True)
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("window,first,D,G", [(1, 1, 128, 8), (20, 3, 64, 4), (100, 70, 128, 2)])
+def test_windows_of_more_pairs_than_blocks_run_at_once(fp8, window, first, D, G):
+    pr = problem(window, EDGE_LENS * 20, 2, G, D, 16, fp8, window, first, sinks=True)
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("B,L", [(1, 100), (1, 4000), (3, 2000), (40, 600), (57, 500), (100, 300), (228, 40)])
+def test_parts_of_one_to_eight_blocks_a_pair(fp8, B, L):
+    """Batches whose pairs get clusters of every size, lengths from none to the table's width."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, L + 1, (B,), generator=g).tolist()
+    lens[-1] = L
+    pr = problem(B, lens, 1 if B > 60 else 2, 8, 64, 16, fp8, sinks=True)
     check(pr, *run(pr))
 
 
