@@ -30,7 +30,7 @@
  *    pkv_gqa_kv_append_fp8 writes tokens (one each, or whole prompts) into the
  *    e4m3 cache.
  *
- *  - pkv_pages_fork / _release / _reserve / _compact / _copy: the cache's pages,
+ *  - pkv_pages_fork / _release / _trim / _reserve / _compact / _copy: its pages,
  *    kept on the device in block tables, lengths and reference counts.
  *
  *  - pkv_gqa_kv_append / pkv_mla_kv_append: the step before either call,
@@ -503,7 +503,8 @@ PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
  * The pages of a cache, on the device.  State, shared by all layers:
  *   block_table  int32 [rows, W], rows contiguous and apart (rows <= 8192): row
  *                b's logical page j is block_table[b][j].
- *   seq_lens     int32 [rows]: row b owns entries [0, ceil(seq_lens[b] / P)).
+ *   seq_lens     int32 [rows]: row b owns entries [0, ceil(seq_lens[b] / P)); an
+ *                owned entry of -1 is a page given back.
  *   page_refs    int32 [num_pages]: how many owned entries name each page; 0 is
  *                free.  Zeros at the start; the calls below keep it.
  * Pages are taken lowest index first, in the order of the call's list, so a
@@ -533,12 +534,29 @@ PKV_API int pkv_pages_fork(const pkv_tensor* block_table, const pkv_tensor* seq_
  * pkv_pages_release -- row rows[i] keeps its first keep_lens[i] tokens (0 frees
  * the row, a length it does not reach changes nothing): the entries of pages
  * past them become -1 and their counts go down.  A row named several times is
- * released to the smallest length.
+ * released to the smallest length.  A cut inside a page that other rows share
+ * leaves it shared: before tokens are appended to such a row, fork it
+ * (pkv_pages_fork gives the copy a last page of its own) and go on with the copy.
  *   rows, keep_lens  int32 [n].
  */
 PKV_API int pkv_pages_release(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
                               const pkv_tensor* page_refs, const pkv_tensor* rows,
                               const pkv_tensor* keep_lens, int page_size, void* stream);
+
+/*
+ * pkv_pages_trim -- every row gives back the pages that hold no token its next
+ * one will see through a window: entries of pages that begin at or after
+ * first_tokens and end at or before seq_lens - window become -1 and their counts
+ * go down.  Lengths stay; the attention calls with this window (or a smaller
+ * one) and these first tokens never read such entries, and the other page calls
+ * leave them -1.  A row that may be cut back (pkv_pages_release) wants a window
+ * larger by as much.
+ *   window        >= 1.
+ *   first_tokens  >= 0.
+ */
+PKV_API int pkv_pages_trim(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                           const pkv_tensor* page_refs, int page_size, int window,
+                           int first_tokens, void* stream);
 
 /*
  * pkv_pages_reserve -- row rows[i] grows to new_lens[i] tokens: free pages fill

@@ -26,6 +26,7 @@ Names follow the C ABI without its ``pkv_`` prefix:
     pages_fork(block_table, seq_lens, page_refs, parents, children, page_size,
                copy_src, copy_dst, stream=None)
     pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size, stream=None)
+    pages_trim(block_table, seq_lens, page_refs, page_size, window, first_tokens, stream=None)
     pages_reserve(block_table, seq_lens, page_refs, rows, new_lens, page_size, stream=None)
     pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_dst,
                   num_moves, stream=None)
@@ -48,7 +49,7 @@ __all__ = [
     "paged_decode_attn_noalloc",
     "mla_verify_attn", "gqa_kv_append", "mla_kv_append", "num_kv_splits", "check_errors", "check_counters", "shutdown",
     "paged_decode_attn_fp8", "paged_window_attn", "gqa_kv_append_fp8", "pages_fork",
-    "pages_release", "pages_reserve", "pages_compact", "pages_copy",
+    "pages_release", "pages_trim", "pages_reserve", "pages_compact", "pages_copy",
     "version", "last_error",
 ]
 
@@ -83,7 +84,7 @@ _lib = None
 _call = None  # the compiled binding of the calls that come many times a step (csrc/pycall.c)
 _CALLS = ("pkv_paged_decode_attn_fp8", "pkv_paged_window_attn", "pkv_gqa_kv_append_fp8",
           "pkv_pages_fork", "pkv_pages_release", "pkv_pages_reserve", "pkv_pages_compact",
-          "pkv_pages_copy", "pkv_last_error")
+          "pkv_pages_copy", "pkv_pages_trim", "pkv_last_error")
 
 
 def _calls():
@@ -140,6 +141,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.pkv_pages_release.argtypes = [T, T, T, T, T, i32, vp]
         lib.pkv_pages_reserve.argtypes = [T, T, T, T, T, i32, vp]
         lib.pkv_pages_compact.argtypes = [T, T, T, i32, T, T, T, vp]
+        lib.pkv_pages_trim.argtypes = [T, T, T, i32, i32, i32, vp]
         lib.pkv_pages_copy.argtypes = [vp, i32, T, T, vp]
         lib.pkv_num_kv_splits.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_double, i32, i32]
         lib.pkv_check_errors.argtypes = [i32, ctypes.POINTER(ctypes.c_int32)]
@@ -153,7 +155,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                      "pkv_selftest_wait_timeout", "pkv_paged_decode_attn_fp8",
                      "pkv_paged_window_attn", "pkv_gqa_kv_append_fp8", "pkv_pages_fork",
                      "pkv_pages_release", "pkv_pages_reserve", "pkv_pages_compact",
-                     "pkv_pages_copy", "pkv_shutdown", "pkv_version"):
+                     "pkv_pages_copy", "pkv_pages_trim", "pkv_shutdown", "pkv_version"):
             getattr(lib, name).restype = i32
         if path is None:
             _lib = lib
@@ -362,6 +364,13 @@ def pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size, 
     back (C: pkv_pages_release)."""
     (_call or _calls()).pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size,
                                       stream)
+
+
+def pages_trim(block_table, seq_lens, page_refs, page_size, window, first_tokens, stream=None):
+    """Give back every row's pages between its first ``first_tokens`` tokens and
+    its last ``window`` (C: pkv_pages_trim)."""
+    (_call or _calls()).pages_trim(block_table, seq_lens, page_refs, page_size, window, first_tokens,
+                                   stream)
 
 
 def pages_reserve(block_table, seq_lens, page_refs, rows, new_lens, page_size, stream=None):

@@ -1249,7 +1249,7 @@ PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
   if (cu_tokens && (rc = check_tensor(cu_tokens, "cu_tokens", PKV_DTYPE_I32, 1))) return rc;
   const int64_t T = k->shape[0], Hkv = k->shape[1], D = k->shape[2], B = seq_lens->shape[0];
   for (int i = 0; i < 3; ++i)
-    if (v->shape[i] != k->shape[i] || (i < 2 && v->stride[i] != k->stride[i]))
+    if (v->shape[i] != k->shape[i] || (i < 2 && k->shape[i] > 1 && v->stride[i] != k->stride[i]))
       return fail(PKV_ERR_INVALID_ARG, "v must have the shape and strides of k");
   if ((rc = check_paged_cache(kv_cache, kv_scale, true, D, page_size))) return rc;
   if (kv_cache->shape[1] != Hkv)
@@ -1268,7 +1268,7 @@ PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
     return fail(PKV_ERR_INVALID_ARG, "k and v last dims must be contiguous");
   if (k->stride[0] % 8 || k->stride[1] % 8 || !aligned16(k->data) || !aligned16(v->data))
     return fail(PKV_ERR_ALIGNMENT, "k and v rows must be 16-byte aligned");
-  if (T >= (int64_t(1) << 31) || T * Hkv >= (int64_t(1) << 33))
+  if (T * Hkv >= (int64_t(1) << 31))
     return fail(PKV_ERR_UNSUPPORTED, "%lld tokens x %lld heads", (long long)T, (long long)Hkv);
   if ((rc = check_no_overlap({{kv_cache, "kv_cache"}, {kv_scale, "kv_scale"}},
                              {{k, "k"}, {v, "v"}, {block_table, "block_table"},
@@ -1425,6 +1425,28 @@ PKV_API int pkv_pages_release(const pkv_tensor* block_table, const pkv_tensor* s
       pkv::launch_pages_release(t, static_cast<const int32_t*>(rows->data),
                                 static_cast<const int32_t*>(keep_lens->data), int(n), stream);
   if (e != cudaSuccess) return cuda_fail(e, "pages release launch");
+  return PKV_OK;
+}
+
+PKV_API int pkv_pages_trim(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                           const pkv_tensor* page_refs, int page_size, int window,
+                           int first_tokens, void* stream_ptr) {
+  int rc;
+  pkv::PageTables t;
+  if ((rc = page_tables(block_table, seq_lens, page_refs, page_size, &t))) return rc;
+  if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window %d < 1", window);
+  if (first_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "first_tokens %d < 0", first_tokens);
+  if ((rc = check_no_overlap({{block_table, "block_table"}, {seq_lens, "seq_lens"},
+                              {page_refs, "page_refs"}}, {})))
+    return rc;
+  if (t.rows == 0) return PKV_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  DeviceState* st = nullptr;
+  int* scratch = nullptr;
+  if ((rc = page_call(block_table, "block_table", 0, stream, &st, &scratch))) return rc;
+  t.err = st->ws.err;
+  const cudaError_t e = pkv::launch_pages_trim(t, window, first_tokens, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pages trim launch");
   return PKV_OK;
 }
 

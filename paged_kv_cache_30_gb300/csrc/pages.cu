@@ -3,13 +3,15 @@
 //
 // State: block_table [rows, W] (row b's logical page j is block_table[b][j]),
 // seq_lens [rows], and page_refs [num_pages], the number of table entries that
-// name each page (0: free).  Row b owns entries [0, ceil(seq_lens[b] / P)).
+// name each page (0: free).  Row b owns entries [0, ceil(seq_lens[b] / P)); -1 among
+// them is a page given back.
 // New pages are taken lowest index first, in the order of the call's list, so
 // results do not depend on timing.
 //
 //   fork(p -> c)     c's full pages are p's (refs + 1); a partly filled last page
 //                    gets a page of its own, and (source, copy) goes to the list.
 //   release(b, n)    entries past ceil(n / P) go (refs - 1, entry -1), length n.
+//   trim             entries of pages that a window and first tokens hide go (-1).
 //   reserve(b, n)    entries up to ceil(n / P) come (refs = 1), length n.
 //   compact          with n live pages, the k-th live page at or above n moves to
 //                    the k-th free page below n: sources and targets are disjoint,
@@ -98,9 +100,9 @@ __device__ __forceinline__ void apply_fork(const PageTables& t, const int32_t* c
   int src = -1, dst = -1;
   if (L >= 0) {
     const int full = L / t.page_size, child = children[i];
-    const bool part = L % t.page_size != 0;
-    const bool granted = !part || ws[8 + i] < ws[0];
     const int32_t* from = t.bt + parents[i] * t.bt_sb;
+    const bool part = L % t.page_size != 0 && from[full] != -1;
+    const bool granted = !part || ws[8 + i] < ws[0];
     int32_t* to = t.bt + child * t.bt_sb;
     if (part && granted) {
       src = from[full];
@@ -113,7 +115,7 @@ __device__ __forceinline__ void apply_fork(const PageTables& t, const int32_t* c
         page = from[j];
         if (page >= 0 && page < t.num_pages)
           atomicAdd(t.refs + page, 1);
-        else
+        else if (page != -1)  // a page given back
           atomicOr(t.err, DEVERR_BAD_BLOCK);
       } else if (j == full) {
         page = dst;
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         atomicOr(t.err, DEVERR_BAD_ROW);
       } else if (kFork) {
         note = row_len(t, o);
-        need = note % t.page_size != 0;
+        need = note % t.page_size != 0 && t.bt[o * t.bt_sb + note / t.page_size] != -1;
       } else {
         const int L = row_len(t, r);
         if (o > (long long)t.max_blocks * t.page_size)
@@ -236,6 +238,17 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
+// Takes entry j of a row and gives its page back; an entry goes once, whoever takes it.
+__device__ __forceinline__ void give_back(const PageTables& t, int row, int j) {
+  const int page = atomicExch(t.bt + row * t.bt_sb + j, -1);
+  if (page < 0 || page >= t.num_pages) {
+    if (page != -1) atomicOr(t.err, DEVERR_BAD_BLOCK);
+  } else if (atomicSub(t.refs + page, 1) <= 0) {
+    atomicAdd(t.refs + page, 1);
+    atomicOr(t.err, DEVERR_BAD_ROW);
+  }
+}
+
 __global__ void release_kernel(const PageTables t, const int32_t* rows, const int32_t* keep) {
   __shared__ int sL;
   griddep_wait();
@@ -247,17 +260,19 @@ __global__ void release_kernel(const PageTables t, const int32_t* rows, const in
   if (tid == 0) sL = row_len(t, row);
   __syncthreads();
   const int L = sL, k = max(min(keep[i], L), 0);
-  // an entry goes once, whoever takes it
-  for (int j = pages_of(k, t.page_size) + tid; j < pages_of(L, t.page_size); j += blockDim.x) {
-    const int page = atomicExch(t.bt + row * t.bt_sb + j, -1);
-    if (page < 0 || page >= t.num_pages) {
-      if (page != -1) atomicOr(t.err, DEVERR_BAD_BLOCK);
-    } else if (atomicSub(t.refs + page, 1) <= 0) {
-      atomicAdd(t.refs + page, 1);
-      atomicOr(t.err, DEVERR_BAD_ROW);
-    }
-  }
+  for (int j = pages_of(k, t.page_size) + tid; j < pages_of(L, t.page_size); j += blockDim.x)
+    give_back(t, row, j);
   if (tid == 0) atomicMin(t.seq_lens + row, k);
+}
+
+// Row blockIdx.x: the pages that end at or before its window and begin at or after
+// its first tokens.
+__global__ void trim_kernel(const PageTables t, int window, int first) {
+  griddep_wait();
+  const int row = blockIdx.x, L = row_len(t, row), P = t.page_size;
+  const int begin = pages_of(first, P), end = (L > window ? L - window : 0) / P;
+  for (int j = begin + threadIdx.x; j < end; j += blockDim.x)
+    if (t.bt[row * t.bt_sb + j] != -1) give_back(t, row, j);
 }
 
 constexpr int kApplyThreads = 128;
@@ -375,7 +390,7 @@ __global__ void __launch_bounds__(kBlockThreads)
     for (int j = threadIdx.x; j < used; j += kBlockThreads) {
       const int page = bt[j];
       if (page < 0 || page >= t.num_pages) {
-        atomicOr(t.err, DEVERR_BAD_BLOCK);
+        if (page != -1) atomicOr(t.err, DEVERR_BAD_BLOCK);
       } else if (page >= n) {
         // a page with no count is no one's: its entry stays, as the page does
         const int k = ws[blocks + page];
@@ -489,6 +504,10 @@ cudaError_t launch_pages_fork(const PageTables& t, const int32_t* parents, const
 cudaError_t launch_pages_release(const PageTables& t, const int32_t* rows, const int32_t* keep,
                                  int n, cudaStream_t stream) {
   return launch(release_kernel, dim3(n), 64, 0, stream, t, rows, keep);
+}
+
+cudaError_t launch_pages_trim(const PageTables& t, int window, int first, cudaStream_t stream) {
+  return launch(trim_kernel, dim3(t.rows), 128, 0, stream, t, window, first);
 }
 
 cudaError_t launch_pages_reserve(const PageTables& t, const int32_t* rows, const int32_t* lens,

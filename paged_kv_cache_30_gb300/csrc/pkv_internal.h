@@ -326,6 +326,8 @@ cudaError_t launch_pages_fork(const PageTables& t, const int32_t* parents, const
                               cudaStream_t stream);
 cudaError_t launch_pages_release(const PageTables& t, const int32_t* rows, const int32_t* keep,
                                  int n, cudaStream_t stream);
+// window > 0, first >= 0; t.rows > 0
+cudaError_t launch_pages_trim(const PageTables& t, int window, int first, cudaStream_t stream);
 cudaError_t launch_pages_reserve(const PageTables& t, const int32_t* rows, const int32_t* lens,
                                  int n, int* scratch, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PageTables& t, int32_t* copy_src, int32_t* copy_dst, int n,

@@ -23,12 +23,13 @@ typedef int (*fork_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, 
                        const pkv_tensor*, int, const pkv_tensor*, const pkv_tensor*, void*);
 typedef int (*rows_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, const pkv_tensor*,
                        const pkv_tensor*, int, void*);
+typedef int (*trim_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, int, int, int, void*);
 typedef int (*compact_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, int,
                           const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, void*);
 typedef int (*copy_fn)(const pkv_tensor* const*, int, const pkv_tensor*, const pkv_tensor*, void*);
 typedef const char* (*text_fn)(void);
 
-enum { ATTN8, WINDOW, APPEND, FORK, RELEASE, RESERVE, COMPACT, COPY, LAST_ERROR, NUM_FNS };
+enum { ATTN8, WINDOW, APPEND, FORK, RELEASE, RESERVE, COMPACT, COPY, TRIM, LAST_ERROR, NUM_FNS };
 enum { MAX_TENSORS = 66 }; /* 64 page tensors and two lists */
 
 static void* fns[NUM_FNS];
@@ -241,6 +242,19 @@ static PyObject* reserve(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return rows_call(fns[RESERVE], a, n);
 }
 
+/* block_table, seq_lens, page_refs, page_size, window, first_tokens, stream */
+static PyObject* trim(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const int at[3] = {0, 1, 2};
+  pkv_tensor d[3];
+  const pkv_tensor* p[3];
+  int page, window, first;
+  void* s;
+  if (count_args(n, 7) || describe_all(a, at, 3, d, p) || int_of(a[3], &page) ||
+      int_of(a[4], &window) || int_of(a[5], &first) || stream_of(a[6], a[2], &s))
+    return NULL;
+  CALL(((trim_fn)fns[TRIM])(p[0], p[1], p[2], page, window, first, s));
+}
+
 /* block_table, seq_lens, page_refs, page_size, copy_src, copy_dst, num_moves, stream */
 static PyObject* compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   static const int at[6] = {0, 1, 2, 4, 5, 6};
@@ -317,6 +331,7 @@ static PyMethodDef methods[] = {
     METHOD("pages_reserve", reserve),
     METHOD("pages_compact", compact),
     METHOD("pages_copy", copy),
+    METHOD("pages_trim", trim),
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkvcall", NULL, -1, methods};

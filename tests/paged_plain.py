@@ -151,9 +151,17 @@ class Pool:
                 continue
             n = max(min(n, self.lens[r]), 0)
             for j in range(self.pages_of(n), self.pages_of(self.lens[r])):
-                self.refs[self.table[r][j]] -= 1
-                self.table[r][j] = -1
+                if self.table[r][j] != -1:
+                    self.refs[self.table[r][j]] -= 1
+                    self.table[r][j] = -1
             self.lens[r] = n
+
+    def trim(self, window, first):
+        for r, n in enumerate(self.lens):
+            for j in range(self.pages_of(first), max(n - window, 0) // self.P):
+                if self.table[r][j] != -1:
+                    self.refs[self.table[r][j]] -= 1
+                    self.table[r][j] = -1
 
     def fork(self, parents, children):
         free, before, src, dst = self.free(), 0, [], []
@@ -164,14 +172,16 @@ class Pool:
             rows = range(len(lens))
             if p not in rows or c not in rows or c in children[:i] or c in parents or lens[c]:
                 continue
-            full, part = lens[p] // self.P, lens[p] % self.P > 0
+            full = lens[p] // self.P
+            part = lens[p] % self.P > 0 and self.table[p][full] != -1
             if part and before >= len(free):
                 self.table[c] = [-1] * self.width
                 before += 1
                 continue
             self.table[c] = self.table[p][:full] + [-1] * (self.width - full)
             for page in self.table[c][:full]:
-                self.refs[page] += 1
+                if page != -1:
+                    self.refs[page] += 1
             if part:
                 src[i], dst[i] = self.table[p][full], free[before]
                 self.table[c][full] = dst[i]

@@ -145,24 +145,39 @@ def pages(rows=4, W=8, n=3, num=50):
 
 
 def call_pages(lib, what, x):
-    r = {k: ref(t) if k != "P" else t for k, t in x.items()}
+    r = {k: t if k in ("P", "window", "first") else ref(t) for k, t in x.items()}
     if what == "fork":
         return lib.pkv_pages_fork(r["bt"], r["sl"], r["refs"], r["a"], r["b"], r["P"], r["c"], r["d"], None)
+    if what == "trim":
+        return lib.pkv_pages_trim(r["bt"], r["sl"], r["refs"], r["P"], x.get("window", 5), x.get("first", 2), None)
     if what == "compact":
         return lib.pkv_pages_compact(r["bt"], r["sl"], r["refs"], r["P"], r["a"], r["b"], r["one"], None)
     return getattr(lib, "pkv_pages_" + what)(r["bt"], r["sl"], r["refs"], r["a"], r["b"], r["P"], None)
 
 
-@pytest.mark.parametrize("what", ["fork", "release", "reserve", "compact"])
+@pytest.mark.parametrize("what", ["fork", "release", "trim", "reserve", "compact"])
 @pytest.mark.parametrize("change,code", [
     (dict(bt=None), -1), (dict(sl=tensor("sl", [3], I32)), -1), (dict(refs=None), -1),
     (dict(bt=tensor("bt", [4, 8], I32, [4, 1])), -1), (dict(bt=tensor("bt", [4, 8], I32, [8, 2])), -1),
     (dict(bt=tensor("bt", [4, 8], F32)), -1), (dict(P=0), -1),
     (dict(refs=tensor("refs", [0], I32)), -1), (dict(refs=tensor("refs", [50], I32, [2])), -1),
     (dict(refs=tensor("refs", [50], I32, ptr=PTR["bt"])), -1),
+    (dict(bt=tensor("bt", [9000, 8], I32), sl=tensor("sl", [9000], I32)), -2),
+])
+def test_table_refusals(lib, what, change, code):
+    assert call_pages(lib, what, {**pages(), **change}) == code
+
+
+@pytest.mark.parametrize("change", [dict(window=0), dict(window=-3), dict(first=-1)])
+def test_trim_refusals(lib, change):
+    assert call_pages(lib, "trim", {**pages(), **change}) == -1
+    assert call_pages(lib, "trim", pages(rows=0)) == 0
+
+
+@pytest.mark.parametrize("what", ["fork", "release", "reserve", "compact"])
+@pytest.mark.parametrize("change,code", [
     (dict(b=tensor("b", [2], I32)), -1), (dict(a=tensor("a", [3], I32, [2])), -1),
     (dict(a=tensor("a", [3], F32)), -1), (dict(b=tensor("b", [3], I32, ptr=PTR["bt"])), -1),
-    (dict(bt=tensor("bt", [9000, 8], I32), sl=tensor("sl", [9000], I32)), -2),
 ])
 def test_page_call_refusals(lib, what, change, code):
     assert call_pages(lib, what, {**pages(), **change}) == code

@@ -42,6 +42,9 @@ class Device:
     def release(self, rows, keep):
         pkv.pages_release(self.bt, self.sl, self.refs, ints(rows), ints(keep), self.P)
 
+    def trim(self, window, first):
+        pkv.pages_trim(self.bt, self.sl, self.refs, self.P, window, first)
+
     def fork(self, parents, children):
         src, dst = ints([7] * len(parents)), ints([7] * len(parents))
         pkv.pages_fork(self.bt, self.sl, self.refs, ints(parents), ints(children), self.P, src, dst)
@@ -91,6 +94,11 @@ def test_a_long_run_of_page_calls(P, pages, rows):
                 s, t = d.fork(par, kids)
                 assert s.tolist() == src and t.tolist() == dst
         assert d.same(m), f"step {step}"
+        if step % 3 == 2:  # then the row is never cut to where trimmed pages would be seen
+            window, first = rng.randint(1, 9 * P), rng.choice([0, 0, 1, P, 2 * P + 3])
+            m.trim(window, first)
+            d.trim(window, first)
+            assert d.same(m), f"trim after step {step}"
         if step % 5 == 4:
             most = rng.choice([pages // 2, 3, 0])
             src, dst, n = m.compact(most)
@@ -158,6 +166,37 @@ def test_a_row_released_twice_loses_its_pages_once():
         x.release([0, 1, 0, 0], [100, 0, 3, 50])
     assert m.lens[0] == 3
     assert d.same(m)
+    assert pkv.check_errors(0) == 0
+
+
+@pytest.mark.parametrize("window,first", [(1, 0), (16, 0), (17, 5), (40, 16), (100, 33), (5000, 1)])
+def test_trimmed_rows_are_attended_as_before(window, first):
+    """Pages that a window and first tokens hide go back to the pool, are taken by another row and
+    overwritten; the row's attention stays what it was."""
+    P, lens = 16, [200, 161, 160, 15, 0, 113]
+    m = plain.Pool(7, 16, 70, P)
+    d = Device(m)
+    for x in (m, d):
+        x.reserve([0, 1, 2, 3, 4, 5], lens)
+    g = torch.Generator().manual_seed(window)
+    kv = torch.randn(70, 2, P, 128, generator=g).bfloat16().cuda()
+    q = torch.randn(7, 8, 64, generator=g).bfloat16().cuda()
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    pkv.paged_window_attn(q, kv, d.bt, d.sl, None, window, first, 0.125, P, outs[0])
+    held = sum(m.refs)
+    for x in (m, d):
+        x.trim(window, first)
+    assert d.same(m)
+    free = 70 - sum(m.refs)
+    assert free >= 70 - held
+    take = min(free, 16) * P
+    for x in (m, d):
+        x.reserve([6], [take])
+    assert d.same(m)
+    kv[torch.tensor([p for p in m.table[6] if p >= 0]).cuda()] = float("nan")
+    pkv.paged_window_attn(q[:6], kv, d.bt[:6], d.sl[:6], None, window, first, 0.125, P, outs[1][:6])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][:6], outs[1][:6])
     assert pkv.check_errors(0) == 0
 
 
