@@ -296,3 +296,68 @@ def test_captured_graphs_share_the_workspace_and_see_new_lengths():
     torch.cuda.synchronize()
     short = dict(a, sl=torch.tensor([37, 0, 20], dtype=torch.int32))
     check(short, outs[0][0].cpu(), outs[0][1].cpu())
+
+
+def far_cache(fp8):
+    """A cache of more than 2^32 bytes (and scales) of which a few pages, near its end, are used."""
+    P, Hkv, D = 32, 8, 128
+    pool = (5 << 30) // (Hkv * P * 2 * D * (1 if fp8 else 2))
+    pr = problem(21, [300, 77, 310], Hkv, 2, D, P, fp8, sinks=True)
+    n = pr["kv"].shape[0]
+    kv = torch.empty(pool, Hkv, P, 2 * D, dtype=pr["kv"].dtype, device="cuda")
+    kv[-n:] = pr["kv"].cuda()
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) and k != "kv" else v for k, v in pr.items()}
+    d["kv"] = kv
+    d["bt"] = torch.where(d["bt"] >= 0, d["bt"] + (pool - n), d["bt"])
+    if fp8:
+        d["sc"] = torch.zeros(pool, Hkv, 2, device="cuda")
+        d["sc"][-n:] = pr["sc"].cuda()
+    return pr, d, pool, n
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_offsets_past_32_bits(fp8):
+    pr, d, pool, n = far_cache(fp8)
+    out = torch.full_like(d["q"], math.nan)
+    lse = torch.full(d["q"].shape[:2], math.nan, device="cuda")
+    call(d, out, lse)
+    torch.cuda.synchronize()
+    check(pr, out.cpu(), lse.cpu())
+    # pages moved to the front of the pool, and there attended
+    src = torch.arange(pool - n, pool, dtype=torch.int32, device="cuda")
+    dst = torch.arange(n, dtype=torch.int32, device="cuda")
+    pkv.pages_copy([d["kv"], d["sc"]] if fp8 else d["kv"], src, dst)
+    d["bt"] = torch.where(d["bt"] >= 0, d["bt"] - (pool - n), d["bt"])
+    out2 = torch.full_like(out, math.nan)
+    call(d, out2, lse)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2)
+
+
+def test_append_past_32_bits():
+    pr, d, pool, n = far_cache(True)
+    T = 5
+    k, v = (torch.randn(T, 8, 128, device="cuda").bfloat16() for _ in range(2))
+    sl = torch.tensor([2 * T], dtype=torch.int32, device="cuda")
+    d["sc"][-1] = 2.0 ** -9
+    bt = torch.tensor([[pool - 1]], dtype=torch.int32, device="cuda")
+    before = d["kv"][:-1].view(torch.uint8)[::997].clone()
+    pkv.gqa_kv_append_fp8(k, v, d["kv"], d["sc"], bt, sl, None, 32)
+    torch.cuda.synchronize()
+    got = d["kv"][-1, :, T:2 * T].float() * d["sc"][-1][:, None, :].repeat_interleave(128, 2)
+    want = torch.cat([k, v], 2).transpose(0, 1).float()
+    # e4m3 of x / s is within 2^-4 of x, or 2^-10 s where x / s is below 2^-6
+    far = (got - want).abs() - want.abs() * 2.0 ** -4 \
+        - 2.0 ** -10 * d["sc"][-1][:, None, :].repeat_interleave(128, 2)
+    assert (far <= 0).all()
+    assert torch.equal(d["kv"][:-1].view(torch.uint8)[::997], before)
+
+
+def test_host_memory_is_refused():
+    pr = problem(30, [20, 3], 1, 8, 64, 16, True)
+    out = torch.empty_like(pr["q"])
+    with pytest.raises(pkv.PkvError):
+        call(pr, out, None)
+    with pytest.raises(pkv.PkvError) as e:
+        call(pr, out, None, torch.cuda.current_stream())
+    assert e.value.code == -1
