@@ -18,6 +18,12 @@
 // 32-way search of cu_tokens and walks the pages that begin in its rows, loading
 // the rows of a page to shared memory at once (up to 16 16-byte copies a lane)
 // before it reduces, and encoding them from there.
+//
+// Measured (GB300, 8 kv heads of 128, graph replays): 64 single tokens 2.9 us, 1024
+// of them 7.8 us; 12.5 k tokens of ragged prompts (77 MB) 17 us = 4.5 TB/s, 32 k
+// tokens 32.7 us = 6.2 TB/s (91 % of the measured copy bandwidth; pages of 32 and 128
+// tokens 79 and 81 %).  What is left is the chain of dependent reads that a warp
+// begins with (request, length, page, rows): about 4 us, hidden only by other warps.
 #include <algorithm>
 
 #include "pkv_internal.h"
@@ -27,6 +33,8 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4;
+// Single rows a warp until there are this many (one prompt of 16000 tokens: 15.6 us,
+// 17.4 at 16384; ragged prompts of 12.5 k tokens: 17.1 and 16.1).
 constexpr int kFullWarps = 8192;
 constexpr int kMaxHeld = 32;
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100

@@ -17,8 +17,11 @@
 //                    the k-th free page below n: sources and targets are disjoint,
 //                    so the copies need no order.
 //
-// Bound by latency (lists of a few hundred entries) except copying, which is
-// bound by memory.
+// Bound by latency (lists of a few hundred entries: launches and two or three
+// dependent reads each) except copying, which is bound by memory.  Measured (GB300,
+// graph replays): a reservation or fork of a few rows 2.5 to 3 us, a compaction of
+// 16384 pages 7 us (three launches; one CTA took 50), copying 4109 pages of 32 KB
+// 42.9 us = 6.27 TB/s (the same bytes as one contiguous copy: 40.9).
 #include <limits.h>
 
 #include <algorithm>
@@ -30,7 +33,9 @@ namespace pkv {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kOneCtaEntries = 16384;  // table entries that the planning CTA handles itself
+// Table entries that the planning CTA handles itself: one launch less (about 1 us);
+// with more, a CTA for each row is faster (256 forks of 250 entries: 13.8 -> 11.5 us).
+constexpr int kOneCtaEntries = 16384;
 
 // Exclusive scan over the CTA; *total = the sum.
 template <typename T>
@@ -406,7 +411,9 @@ __global__ void __launch_bounds__(kBlockThreads)
   }
 }
 
-// A CTA copies pieces of kCopyPiece bytes of the listed pages of one tensor.
+// A CTA copies pieces of kCopyPiece bytes of the listed pages of one tensor, eight
+// 16-byte loads of a thread in flight (compaction of half of 16384 pages: 53.7 us; with
+// four 58.9).
 constexpr int kCopyThreads = 128;
 constexpr int kCopyLoads = 8;
 constexpr int64_t kCopyPiece = kCopyThreads * kCopyLoads * 16;

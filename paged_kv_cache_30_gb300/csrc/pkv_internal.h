@@ -265,12 +265,15 @@ PagedShape paged_attn_shape(int D, bool fp8, int G);
 // box (a piece, 16 tokens, all pieces, 1, 1), 128-byte swizzle.
 cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
 // A CTA's share of the work is counted in 16-token tiles plus a cost for each
-// (request, kv head) pair, and is no smaller than kPagedMinCost.
+// (request, kv head) pair, and is no smaller than kPagedMinCost.  64 requests of
+// log-uniform lengths, e4m3: 84.2 us at a cost of 4, 53.9 at 8, 52.6 at 12, 52.8 at 16.
 constexpr int kPagedPairCost = 12;
 constexpr int kPagedMinCost = 16;
 constexpr int kPagedMaxGrid = 512;  // 32 merge groups of 16
 constexpr int kPagedMaxCluster = 8;
-constexpr int kPagedClusterTiles = 48;  // most tiles of a CTA in the cluster mode
+// Most tiles of a CTA in the cluster mode (bf16, a window of 1024 on 16 x 8 kv heads,
+// 33 tiles each: 15.4 us in clusters, 17.2 without).
+constexpr int kPagedClusterTiles = 48;
 
 // ------------------------------------------------ append to an e4m3 cache --
 struct AppendFp8Params {
