@@ -49,8 +49,8 @@ struct DeviceState {
   cudaStream_t last_stream = nullptr;
   bool has_last = false;
   // Streams whose last call of the library may have written block tables,
-  // lengths or whole pages (the page calls): the attention kernels read those
-  // before their dependency wait, so the next one there is launched plainly.
+  // lengths or whole pages (the page calls): kernels that read those before
+  // their dependency wait need the call to have ended (settle_pages).
   std::vector<cudaStream_t> pages_written;
 };
 
@@ -149,7 +149,7 @@ int note_pages_written(DeviceState* st, cudaStream_t stream) {
   return PKV_OK;
 }
 
-// Whether it did; a launch that waits for the kernel before it ends the matter.
+// Whether it did, once.
 bool take_pages_written(DeviceState* st, cudaStream_t stream) {
   std::lock_guard<std::mutex> lk(g_mu);
   for (size_t i = 0; i < st->pages_written.size(); ++i)
@@ -158,6 +158,16 @@ bool take_pages_written(DeviceState* st, cudaStream_t stream) {
       return true;
     }
   return false;
+}
+
+// Before a kernel that reads tables, lengths or pages ahead of its dependency
+// wait: if a page call came before on the stream, a memset of an unused (zero)
+// scheduler word between the two.  Programmatic dependence holds between
+// neighbouring kernels alone, so the kernel then starts after the page call ended.
+int settle_pages(DeviceState* st, cudaStream_t stream) {
+  if (!take_pages_written(st, stream)) return PKV_OK;
+  const cudaError_t e = cudaMemsetAsync(st->ws.sched + 48, 0, sizeof(int), stream);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "ordering after a page call");
 }
 
 // ------------------------------------------------------------ validation --
@@ -581,7 +591,7 @@ PKV_API int pkv_paged_decode_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
   p.sched = ws.sched;
   p.err = ws.err;
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  p.plain = take_pages_written(st, stream);
+  if ((rc = settle_pages(st, stream))) return rc;
   const cudaError_t e = pkv::launch_gqa_decode(p, call.map, page_size, shape.grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gqa decode launch");
   return PKV_OK;
@@ -820,7 +830,7 @@ static int mla_verify_impl(const pkv_tensor* q, const pkv_tensor* q8, const pkv_
            units * cap;
   p.err = ws.err;
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  p.plain = take_pages_written(st, stream);
+  if ((rc = settle_pages(st, stream))) return rc;
   const cudaError_t e =
       native ? pkv::launch_mla_verify_native(p, kv_map, int(units * cap), stream)
       : pair ? pkv::launch_mla_verify_pair(p, q_map, kv_map, v_map, int(units * cap), stream)

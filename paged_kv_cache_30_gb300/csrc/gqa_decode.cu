@@ -762,7 +762,7 @@ cudaError_t launch_page(const GqaParams& p, const CUtensorMap& kv_map, int grid,
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = p.plain ? 0 : 1;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = kCluster ? p.cluster : 1;
   attr[1].val.clusterDim.y = 1;

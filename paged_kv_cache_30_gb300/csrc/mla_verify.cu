@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 
 template <typename Kernel, typename... Args>
 cudaError_t launch_pdl(Kernel* fn, int grid, int threads, int smem, cudaStream_t stream,
-                       bool dependent, Args... args) {
+                       Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -750,7 +750,7 @@ cudaError_t launch_pdl(Kernel* fn, int grid, int threads, int smem, cudaStream_t
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fn, args...);
@@ -765,7 +765,7 @@ cudaError_t launch_t(const MlaParams& p, const CUtensorMap& q_map, const CUtenso
   e = launch_mla_plan(p, grid, stream, false);
   if (e != cudaSuccess) return e;
   return launch_pdl(mla_verify_kernel<kFp8>, grid, Cfg<kFp8>::kThreads, Cfg<kFp8>::kSmemBytes,
-                    stream, true, p, q_map, kv_map);
+                    stream, p, q_map, kv_map);
 }
 
 }  // namespace
@@ -776,8 +776,8 @@ cudaError_t launch_mla_plan(const MlaParams& p, int grid, cudaStream_t stream, b
   if (e != cudaSuccess) return e;
   int p2 = 1;
   while (p2 < p.B) p2 <<= 1;
-  return launch_pdl(mla_plan_kernel, 1, kPlanThreads, p.B > kPlanSortMax ? 0 : p2 * 8, stream,
-                    !p.plain, p, grid, pair ? 1 : 0);
+  return launch_pdl(mla_plan_kernel, 1, kPlanThreads, p.B > kPlanSortMax ? 0 : p2 * 8, stream, p,
+                    grid, pair ? 1 : 0);
 }
 
 cudaError_t launch_mla_verify(const MlaParams& p, const CUtensorMap& q_map,

@@ -71,7 +71,6 @@ struct GqaParams {
   int* sched;
   int* err;
   int cluster;         // > 1: cluster mode with this many splits per cluster (see below)
-  int plain;           // host: launch after the kernel before has ended (no dependent launch)
 };
 
 // Launch the GQA decode kernel for page size 16 or 32.  p.cluster <= 1: the
@@ -168,7 +167,6 @@ struct MlaParams {
   int64_t q8_sr, q8_sh;
   const float* q_scale;
   int64_t qs_sr, qs_sh;
-  int plain;                     // host: the planning kernel is no programmatic dependent
 };
 
 // The planning kernel: writes p.plan[0, grid) (one CTA; programmatic dependent

@@ -402,3 +402,43 @@ def test_bf16_decode_right_after_a_page_call():
         torch.cuda.synchronize()
         assert torch.equal(outs[0], outs[1])
     assert pkv.check_errors(0) == 0
+    assert pkv.check_counters(0) == 0
+
+
+def test_bf16_append_and_decode_after_copied_pages_in_a_graph():
+    """A copied page, a token appended to it and the decode that reads it, captured: the decode
+    kernel's early reads see the copy."""
+    P = 16
+    kv = torch.randn(64, 1, P, 256, device="cuda").bfloat16()
+    q = torch.randn(1, 8, 128, device="cuda").bfloat16()
+    k, v = (torch.randn(1, 1, 128, device="cuda").bfloat16() for _ in range(2))
+    bt = torch.arange(32, 64, dtype=torch.int32, device="cuda").view(1, 32)
+    sl = ints([32 * P])
+    src, dst = ints(list(range(32))), ints(list(range(32, 64)))
+    out = torch.zeros_like(q)
+
+    def step():
+        pkv.pages_copy(kv, src, dst)
+        pkv.paged_decode_attn(q, kv, bt, sl, None, 0, 0.09, P, 0, out)
+        pkv.pages_copy(kv, src, dst)
+        pkv.gqa_kv_append(k, v, kv, bt, sl, P)
+        pkv.paged_decode_attn(q, kv, bt, sl, None, 0, 0.09, P, 0, out)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(20):
+        kv[:32] = torch.randn(32, 1, P, 256, device="cuda").bfloat16()
+        kv[32:] = float("nan")
+        graph.replay()
+        want = kv.clone()
+        want[32:] = want[:32]
+        want[63, 0, 15] = torch.cat([k[0, 0], v[0, 0]])
+        ref = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        pkv.paged_decode_attn(q, want, bt, sl, None, 0, 0.09, P, 0, ref)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    assert pkv.check_errors(0) == 0
