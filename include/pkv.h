@@ -437,7 +437,8 @@ PKV_API int pkv_mla_kv_append(const pkv_tensor* latent, const pkv_tensor* latent
  *   lse          fp32 [B, Hq] or NULL.
  *   stream       cudaStream_t.
  * B <= 2048, and B * Hkv * (16-key tiles that a row of block_table, or the window
- * and first tokens, can span + 16) < 2^31.
+ * and first tokens, can span + 16) < 2^31 - 4096.  A small workspace (two partials of
+ * at most 8.4 KB a CTA) makes the call run on fewer CTAs.
  * What masked keys hold (NaN, infinities, stale bytes) reaches no result.
  * Errors as pkv_paged_decode_attn; a bad block-table entry reads as a page of
  * zeros and raises bit 1, a seq_len beyond the table is clamped and raises bit

@@ -1174,7 +1174,7 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   if (window > 0)
     tiles = std::min<int64_t>(width, (int64_t(window) + 14) / 16 + 1 + (int64_t(first_tokens) + 15) / 16);
   if (width * 16 > (int64_t(1) << 31) - 256 ||
-      B * Hkv * (tiles + pkv::kPagedPairCost) >= (int64_t(1) << 31))
+      B * Hkv * (tiles + pkv::kPagedPairCost) >= (int64_t(1) << 31) - 4096)
     return fail(PKV_ERR_UNSUPPORTED, "%lld requests x %lld kv heads of up to %lld tiles of 16 keys",
                 (long long)B, (long long)Hkv, (long long)tiles);
   const pkv::Workspace& ws = st->ws;
@@ -1197,9 +1197,13 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
       p.grid = int(B * Hkv * c);
     }
   }
-  if (!p.cluster && int64_t(2) * p.grid * shape.part_floats * 4 > int64_t(ws.partial_bytes))
-    return fail(PKV_ERR_WORKSPACE, "workspace holds %lld bytes of partials, %lld needed",
-                (long long)ws.partial_bytes, (long long)(int64_t(2) * p.grid * shape.part_floats * 4));
+  if (!p.cluster) {  // two partials for each CTA: a small workspace runs fewer of them
+    const int64_t fit = int64_t(ws.partial_bytes) / (int64_t(2) * shape.part_floats * 4);
+    if (fit < 1)
+      return fail(PKV_ERR_WORKSPACE, "workspace holds %lld bytes of partials, %lld needed",
+                  (long long)ws.partial_bytes, (long long)(int64_t(2) * shape.part_floats * 4));
+    p.grid = int(std::min<int64_t>(p.grid, fit));
+  }
   p.partials = ws.partials;
   p.pair_counters = ws.counters;
   p.slot_counters = ws.counters + pkv::kTopCounters;

@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const Span s = span_of(p, __ldg(p.seq_lens + r.b));
     int tau = f - r.begin;
     if (tau >= s.head) tau += s.gap;
-    const int page = tau >> (pshift - 4);
+    const int page = min(tau >> (pshift - 4), p.max_blocks - 1);  // whatever the lengths do meanwhile
     n_pos = (r.kvh << 3) | (tau & ((1 << (pshift - 4)) - 1));
     n_blk = __ldg(p.bt + r.b * p.bt_sb + page);
   };

@@ -361,3 +361,25 @@ def test_host_memory_is_refused():
     with pytest.raises(pkv.PkvError) as e:
         call(pr, out, None, torch.cuda.current_stream())
     assert e.value.code == -1
+
+
+def test_a_small_workspace_runs_on_fewer_blocks():
+    """Room for partials of a dozen blocks, then for none: the first is slower and right, the
+    second refused; a cluster launch needs none."""
+    pr = problem(31, [3000, 1, 900, 0, 64, 2222], 2, 8, 128, 16, True, sinks=True, wide=True)
+    few = problem(32, [100, 300, 0], 1, 8, 128, 16, True)
+    torch.cuda.synchronize()
+    pkv.shutdown()
+    try:
+        pkv.init(0, 12 * 2 * (8 * 128 + 24) * 4)
+        check(pr, *run(pr))
+        pkv.shutdown()
+        pkv.init(0, 1024)
+        with pytest.raises(pkv.PkvError) as e:
+            run(pr)
+        assert e.value.code == -4
+        check(few, *run(few))
+    finally:
+        pkv.shutdown()
+        pkv.init(0)
+    check(pr, *run(pr))
