@@ -1182,14 +1182,17 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   p.grid = int(std::max<int64_t>(
       1, std::min<int64_t>(std::min(ws.num_sms * shape.ctas_per_sm, pkv::kPagedMaxGrid),
                            (cost + pkv::kPagedMinCost - 1) / pkv::kPagedMinCost)));
-  // Cluster mode: every pair has CTAs of its own in one wave (with an eighth of the
-  // places to spare, as clusters do not fill every GPC), about 16 tiles each and none
-  // more than kPagedClusterTiles.  On / off: four short requests 4.5 / 6.5 us, 256
-  // requests of 200 keys 6.5 / 8.4, 16 x 8 kv heads of 1000 keys 11.1 / 13.7, a
-  // 1001-key window on 33 x 4 kv heads 12.1 / 13.0; without the spare places 64 pairs
-  // in clusters of 7 took 22.5 us instead of 13.2.
+  // Cluster mode: every pair has CTAs of its own, about 16 tiles each and none more than
+  // kPagedClusterTiles; one CTA each for up to two waves of pairs, clusters where they
+  // leave an eighth of the places to spare, as clusters do not fill every GPC.
+  // On / off: four short requests 4.5 / 6.5 us, 256 requests of 200 keys 6.5 / 8.4,
+  // 16 x 8 kv heads of 1000 keys 11.1 / 13.7, a 1001-key window on 33 x 4 kv heads
+  // 12.1 / 13.0, 100 x 8 kv heads of 300 to 700 keys 23.7 / 26.6, a window of 128 on
+  // 64 x 8 kv heads 9.3 / 10.6; without the spare places 64 pairs in clusters of 7 took
+  // 22.5 us instead of 13.2, and without the limit of two waves 1000 x 8 kv heads of up
+  // to 300 keys 83 instead of 70.
   const int64_t slots = int64_t(ws.num_sms) * shape.ctas_per_sm;
-  if (B * Hkv <= slots) {
+  if (B * Hkv <= 2 * slots) {
     const int64_t c = std::max<int64_t>(
         1, std::min({int64_t(pkv::kPagedMaxCluster), slots * 7 / 8 / (B * Hkv), (tiles + 15) / 16}));
     if ((tiles + c - 1) / c <= pkv::kPagedClusterTiles) {

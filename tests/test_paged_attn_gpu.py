@@ -130,6 +130,14 @@ def test_windows_of_more_pairs_than_blocks_run_at_once(fp8, window, first, D, G)
 
 
 @pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("window,first,D,G", [(1, 1, 128, 8), (20, 3, 64, 4), (100, 70, 128, 2),
+                                              (33, 17, 128, 16), (300, 9, 64, 12)])
+def test_windows_of_more_pairs_than_two_waves(fp8, window, first, D, G):
+    pr = problem(window + 3, EDGE_LENS * 40, 2, G, D, 16, fp8, window, first, sinks=True)
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
 @pytest.mark.parametrize("B,L", [(1, 100), (1, 4000), (3, 2000), (40, 600), (57, 500), (100, 300), (228, 40)])
 def test_parts_of_one_to_eight_blocks_a_pair(fp8, B, L):
     """Batches whose pairs get clusters of every size, lengths from none to the table's width."""
