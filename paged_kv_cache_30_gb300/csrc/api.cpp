@@ -1191,20 +1191,31 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   // 64 x 8 kv heads 9.3 / 10.6; without the spare places 64 pairs in clusters of 7 took
   // 22.5 us instead of 13.2, and without the limit of two waves 1000 x 8 kv heads of up
   // to 300 keys 83 instead of 70.
-  const int64_t slots = int64_t(ws.num_sms) * shape.ctas_per_sm;
-  if (B * Hkv <= 2 * slots) {
+  // Warp mode, for more pairs than that of at most kPagedWarpTiles each: what the merge of
+  // a CTA's warps costs a short pair is saved.  On / off, e4m3: 2000 x 8 kv heads of 30 to
+  // 60 keys 55.6 / 113.8 us, 1000 x 8 of up to 300 keys, heads of 64, 45.7 / 70.3, 256 x 8
+  // of 10 to 700 keys 37.5 / 42.9, of 700 to 768 keys 68.8 / 71.3; a bf16 window of 128 on
+  // 512 x 8 kv heads 58.7 / 64.2.  With fewer pairs it loses: 64 requests of up to 32768
+  // keys 62.6 / 51.2.  Its partials are those of four times as many shares.
+  const int64_t slots = int64_t(ws.num_sms) * shape.ctas_per_sm, pairs = B * Hkv;
+  const int64_t part_bytes = int64_t(shape.part_floats) * 4;
+  if (pairs <= 2 * slots) {
     const int64_t c = std::max<int64_t>(
-        1, std::min({int64_t(pkv::kPagedMaxCluster), slots * 7 / 8 / (B * Hkv), (tiles + 15) / 16}));
+        1, std::min({int64_t(pkv::kPagedMaxCluster), slots * 7 / 8 / pairs, (tiles + 15) / 16}));
     if ((tiles + c - 1) / c <= pkv::kPagedClusterTiles) {
+      p.mode = pkv::kPagedCluster;
       p.cluster = int(c);
-      p.grid = int(B * Hkv * c);
+      p.grid = int(pairs * c);
     }
+  } else if (tiles <= pkv::kPagedWarpTiles &&
+             int64_t(ws.partial_bytes) >= 2 * pkv::kPagedWarps * p.grid * part_bytes) {
+    p.mode = pkv::kPagedWarp;
   }
-  if (!p.cluster) {  // two partials for each CTA: a small workspace runs fewer of them
-    const int64_t fit = int64_t(ws.partial_bytes) / (int64_t(2) * shape.part_floats * 4);
+  if (p.mode == pkv::kPagedShares) {  // two partials for each CTA: a small workspace runs fewer of them
+    const int64_t fit = int64_t(ws.partial_bytes) / (2 * part_bytes);
     if (fit < 1)
       return fail(PKV_ERR_WORKSPACE, "workspace holds %lld bytes of partials, %lld needed",
-                  (long long)ws.partial_bytes, (long long)(int64_t(2) * shape.part_floats * 4));
+                  (long long)ws.partial_bytes, (long long)(2 * part_bytes));
     p.grid = int(std::min<int64_t>(p.grid, fit));
   }
   p.partials = ws.partials;

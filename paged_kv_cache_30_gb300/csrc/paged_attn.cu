@@ -36,6 +36,10 @@
 //    CTAs takes one pair each, a CTA an equal part of its tiles, and the first CTA
 //    merges the parts through distributed shared memory: no scan of the lengths, no
 //    global partials (see launch_paged_attn's caller for what it measured).
+//  * Warp mode, for many short requests (again the caller's rule): the shares are the
+//    warps', which write a pair that they hold whole from their accumulators, without a
+//    merge of warps or a barrier.  Of the warps that share a pair the last to arrive
+//    merges the accumulators that all have published, in order.
 //  * Otherwise, a request cut between CTAs: each publishes its 32-bit (O, m, l, R); the last
 //    CTA of a group of up to 16 (an arrival counter) merges the group in order,
 //    the last group merges the groups.  Results do not depend on timing.
@@ -55,13 +59,17 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kPagedWarps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMergeGroup = 16;
 constexpr int kPairCost = kPagedPairCost;
+// The same for a warp in the warp mode: 2000 requests of 1 to 64 keys take 14.1 us at
+// 2, 14.8 at 3; 1000 x 8 of up to 300 keys 47.4 at 2, 45.8 at 3, 47.9 at 5.
+constexpr int kWarpPairCost = 3;
 // A cut this near a pair's border moves there.  Wider costs more than the merges it
 // saves: at 32, 33 requests of a 1001-key window took 16.9 us instead of 13.0.
 constexpr int kSnapTiles = 8;
+constexpr int kWarpSnapTiles = 4;  // in the warp mode; 8: 40.2 us instead of 37.5 for 256 x 8 pairs
 constexpr float kSlack = 8.f;      // log2 units: weights stay below 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -98,6 +106,7 @@ struct Cfg {
   static constexpr int smem_bytes(int B) { return kOffPrefix + (B + 1) * 4 + 1024; }
   static_assert(kOffWb % 1024 == 0 && kOffQ % 16 == 0 && kOffBars % 8 == 0, "shared-memory offsets");
   static_assert(kStages <= 32, "a batch of look-ups covers the ring");
+  static_assert(kWarps * 2 * kRows * D * 2 <= kWarps * kWbFloats * 4, "query rows of the warps");
   static_assert(kCtas * (smem_bytes(kPagedMaxBatch) + 1024) <= 228 * 1024, "CTAs per SM");
 };
 
@@ -338,12 +347,123 @@ __device__ __forceinline__ void merge_partials(const PagedParams& p, int n, Slot
   }
 }
 
-template <class C, bool kCluster>
+// The same three for a warp whose lanes hold the accumulators of the products: lane
+// (g, t) = (lane / 4, lane % 4) has columns 2t and 2t + 1, which are the kv head's query
+// rows 8 nb + 2t and 8 nb + 2t + 1, and the statistics of rows 8 nb + g.
+template <class C>
+__device__ __forceinline__ void warp_store_partial(const PagedParams& p, int slot,
+                                                   const float (&acc)[C::NB][C::D / 16][4],
+                                                   const float (&m)[C::NB], const float (&l)[C::NB],
+                                                   const float (&R)[C::NB]) {
+  const int lane = threadIdx.x & 31;
+  float* dst = p.partials + (int64_t)slot * C::kPartFloats;
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb) {
+#pragma unroll
+    for (int c = 0; c < C::D / 16; ++c)
+      *reinterpret_cast<float4*>(dst + ((nb * (C::D / 16) + c) * 32 + lane) * 4) =
+          make_float4(acc[nb][c][0], acc[nb][c][1], acc[nb][c][2], acc[nb][c][3]);
+    if ((lane & 3) == 0) {
+      float* st = dst + C::kRows * C::D + 8 * nb + (lane >> 2);
+      st[0] = m[nb];
+      st[C::kRows] = l[nb];
+      st[2 * C::kRows] = C::kFp8 ? R[nb] : m[nb];
+    }
+  }
+}
+
+template <class C, typename SlotOf>
+__device__ __forceinline__ void warp_merge_partials(const PagedParams& p, int n, SlotOf slot_of,
+                                                    float (&acc)[C::NB][C::D / 16][4],
+                                                    float (&m)[C::NB], float (&l)[C::NB],
+                                                    float (&R)[C::NB]) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb) {
+    m[nb] = R[nb] = -INFINITY;
+    l[nb] = 0.f;
+#pragma unroll
+    for (int c = 0; c < C::D / 16; ++c)
+      acc[nb][c][0] = acc[nb][c][1] = acc[nb][c][2] = acc[nb][c][3] = 0.f;
+    for (int k = 0; k < n; ++k) {
+      const float* src = p.partials + (int64_t)slot_of(k) * C::kPartFloats;
+      const float* st = src + C::kRows * C::D + 8 * nb + (lane >> 2);
+      const float mk = __ldcg(st), lk = __ldcg(st + C::kRows), Rk = __ldcg(st + 2 * C::kRows);
+      float4 v[C::D / 16];
+#pragma unroll
+      for (int c = 0; c < C::D / 16; ++c)
+        v[c] = ldcg_f4(src + ((nb * (C::D / 16) + c) * 32 + lane) * 4);
+      const float mn = fmaxf(m[nb], mk), Rn = fmaxf(R[nb], Rk);
+      l[nb] = __fmaf_rn(weight(m[nb], mn), l[nb], weight(mk, mn) * lk);
+      const float a = weight(R[nb], Rn), w = weight(Rk, Rn);
+      m[nb] = mn;
+      R[nb] = Rn;
+      const float a0 = __shfl_sync(0xffffffffu, a, 8 * t), a1 = __shfl_sync(0xffffffffu, a, 8 * t + 4);
+      const float w0 = __shfl_sync(0xffffffffu, w, 8 * t), w1 = __shfl_sync(0xffffffffu, w, 8 * t + 4);
+#pragma unroll
+      for (int c = 0; c < C::D / 16; ++c) {
+        acc[nb][c][0] = __fmaf_rn(a0, acc[nb][c][0], w0 * v[c].x);
+        acc[nb][c][1] = __fmaf_rn(a1, acc[nb][c][1], w1 * v[c].y);
+        acc[nb][c][2] = __fmaf_rn(a0, acc[nb][c][2], w0 * v[c].z);
+        acc[nb][c][3] = __fmaf_rn(a1, acc[nb][c][3], w1 * v[c].w);
+      }
+    }
+  }
+}
+
+template <class C>
+__device__ __forceinline__ void warp_finalize(const PagedParams& p, int b, int kvh,
+                                              const float (&sink)[C::NB],
+                                              const float (&acc)[C::NB][C::D / 16][4],
+                                              const float (&m)[C::NB], const float (&l)[C::NB],
+                                              const float (&R)[C::NB]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint16_t* out = p.out + b * p.o_sb + (int64_t)(kvh * p.G) * p.o_sh;
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb) {
+    const int row = 8 * nb + g, r0 = 8 * nb + 2 * t;
+    float f = 0.f;
+    if (l[nb] != 0.f)
+      f = (C::kFp8 ? ex2(R[nb] - m[nb]) : 1.f) / (l[nb] + ex2(sink[nb] - m[nb]));
+    if (t == 0 && p.lse && row < p.G)
+      p.lse[b * p.lse_sb + (kvh * p.G + row) * p.lse_sh] =
+          l[nb] != 0.f ? __fmaf_rn(m[nb], kLn2, logf(l[nb])) : -INFINITY;
+    const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+    for (int c = 0; c < C::D / 16; ++c) {
+      const float(&a)[4] = acc[nb][c];
+      if constexpr (C::kFp8) {  // dims 16 c + 2g and the next of both rows
+        uint16_t* dst = out + 16 * c + 2 * g;
+        if (r0 < p.G)
+          *reinterpret_cast<uint32_t*>(dst + r0 * p.o_sh) = pack_bf16(a[0] * f0, a[2] * f0);
+        if (r0 + 1 < p.G)
+          *reinterpret_cast<uint32_t*>(dst + (r0 + 1) * p.o_sh) = pack_bf16(a[1] * f1, a[3] * f1);
+      } else {
+        // dims 16 c + g and 16 c + 8 + g of both rows: lanes of an even g and the next
+        // trade, so that each has two dims of one row to write
+        const bool odd = g & 1;
+        const float x = __shfl_xor_sync(0xffffffffu, odd ? a[0] * f0 : a[1] * f1, 4);
+        const float y = __shfl_xor_sync(0xffffffffu, odd ? a[2] * f0 : a[3] * f1, 4);
+        uint16_t* dst = out + (r0 + odd) * p.o_sh + 16 * c + (g & ~1);
+        if (r0 + odd < p.G) {
+          *reinterpret_cast<uint32_t*>(dst) =
+              odd ? pack_bf16(x, a[1] * f1) : pack_bf16(a[0] * f0, x);
+          *reinterpret_cast<uint32_t*>(dst + 8) =
+              odd ? pack_bf16(y, a[3] * f1) : pack_bf16(a[2] * f0, y);
+        }
+      }
+    }
+  }
+}
+
+template <class C, int kMode>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedParams p,
                       const __grid_constant__ CUtensorMap kv_map) {
+  constexpr bool kCluster = kMode == kPagedCluster, kPerWarp = kMode == kPagedWarp;
   constexpr int D = C::D, NB = C::NB, U = C::U, kStages = C::kStages, E = D / 16;
   constexpr bool kFp8 = C::kFp8;
+  constexpr int kCost = kPerWarp ? kWarpPairCost : kPairCost;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base_u32 = (raw + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_u32 - raw);
@@ -407,24 +527,29 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       }
     }
 
-    // ---- this CTA's tiles ----
+    // ---- this CTA's (or warp's) tiles ----
     // cuts are placed in the space of costs and turned into places of tiles
-    const int tiles = prefix[B] * Hkv, total = tiles + kPairCost * B * Hkv;
-    chunk = max((int)(((uint32_t)total + gridDim.x - 1) / gridDim.x), kPagedMinCost);
-    snap = min(kSnapTiles, chunk / 2);
+    const int tiles = prefix[B] * Hkv, total = tiles + kCost * B * Hkv;
+    const uint32_t shares = kPerWarp ? gridDim.x * kWarps : gridDim.x;
+    const uint32_t share = kPerWarp ? blockIdx.x * kWarps + warp : blockIdx.x;
+    chunk = max((int)(((uint32_t)total + shares - 1) / shares), kPerWarp ? 1 : kPagedMinCost);
+    snap = min(kPerWarp ? kWarpSnapTiles : kSnapTiles, chunk / 2);
     {
-      // lanes 0..15 place this CTA's cut, lanes 16..31 the next one's
-      const long long x = ((long long)blockIdx.x + (lane >> 4)) * chunk;
-      const Pair r = pair_at_group<kPairCost, 16>(prefix, B, Hkv, (int)min(x, (long long)total - 1));
-      const int at = (int)min(x, (long long)total - 1) - r.begin - kPairCost;  // the pair's tiles before the cut
+      // lanes 0..15 place this share's cut, lanes 16..31 the next one's
+      const long long x = ((long long)share + (lane >> 4)) * chunk;
+      const int y = (int)min(x, (long long)total - 1);
+      const Pair r = pair_at_group<kCost, 16>(prefix, B, Hkv, y);
+      const int at = y - r.begin - kCost;  // the pair's tiles before the cut
       int f = prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
       if (x >= total) f = tiles;
       f0 = __shfl_sync(0xffffffffu, f, 0);
       f1 = __shfl_sync(0xffffffffu, f, 16);
     }
   }
-  // this warp's n-th tile is at place f0 + warp + 4 n
-  const int count = f1 - f0 > warp ? (f1 - f0 - warp + kWarps - 1) / kWarps : 0;
+  // this warp's n-th tile is at place w0 + kStep n
+  constexpr int kStep = kPerWarp ? 1 : kWarps;
+  const int w0 = kPerWarp ? f0 : f0 + warp;
+  const int count = f1 > w0 ? (f1 - w0 + kStep - 1) / kStep : 0;
 
   // ---- the loader ----
   const int pshift = p.page_shift;
@@ -434,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   auto look_up = [&](int n) {
     n_blk = n_pos = 0;
     if (n >= count) return;
-    const int f = f0 + warp + kWarps * n;
+    const int f = w0 + kStep * n;
     const Pair r = kCluster || (f >= next.begin && f < next.begin + next.n)
                        ? next : pair_at_lane<0>(prefix, B, Hkv, f);
     const Span s = span_of(p, __ldg(p.seq_lens + r.b));
@@ -474,11 +599,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                   l_pos >> 3, l_blk);
     }
   };
-  // The 8 (16) query rows of a pair, 16 bytes a thread, rows past the group zero.
-  uint16_t* qbuf = reinterpret_cast<uint16_t*>(base + C::kOffQ);
+  // The 8 (16) query rows of a pair, 16 bytes a thread, rows past the group zero.  A
+  // warp that has pairs of its own keeps their rows where others merge.
+  constexpr int kQSlots = kPerWarp ? 2 : C::kQSlots;
+  uint16_t* qbuf = kPerWarp ? reinterpret_cast<uint16_t*>(wbuf) + warp * 2 * C::kRows * D
+                            : reinterpret_cast<uint16_t*>(base + C::kOffQ);
   auto load_q = [&](const Pair& r, int slot) {
 #pragma unroll
-    for (int i = tid; i < C::kRows * D / 8; i += kThreads) {
+    for (int i = kPerWarp ? lane : tid; i < C::kRows * D / 8; i += kPerWarp ? 32 : kThreads) {
       const int row = i / (D / 8), d = i % (D / 8) * 8;
       const bool in = row < p.G;
       cp_async_16(smem_u32(qbuf + (slot * C::kRows + row) * D + d),
@@ -511,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   constexpr int kUnits = D * (kFp8 ? 1 : 2) / 16;  // 16-byte units of a K (or V) row
 
   const int er = tid >> 4, ed = (tid & 15) * E;  // this thread's part of an output
+  const int sr = kPerWarp ? g : er;  // the row whose sink this thread needs
   float* my_wb = wbuf + warp * C::kWbFloats;
   bool ok = true;
   int n = 0, stage = 0;  // the warp's next tile and its stage
@@ -519,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   for (int f = f0; f < f1;) {
     const Pair pr = next;
     cp_async_wait_all();
-    __syncthreads();  // the query rows are in; wbuf and misc are free
+    if (kPerWarp) __syncwarp(); else __syncthreads();  // the query rows are in; wbuf and misc are free
     const int seg_end = min(pr.begin + pr.n, f1);
     const Span sp = span_of(p, __ldg(p.seq_lens + pr.b));
 
@@ -527,13 +656,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const uint16_t* q_rows = qbuf + slot * C::kRows * D;
     if (!kCluster && seg_end < f1) {
       next = pair_at_group<0, 32>(prefix, B, Hkv, seg_end);
-      if (C::kQSlots == 2) load_q(next, slot ^ 1);
+      if (kQSlots == 2) load_q(next, slot ^ 1);
     }
     float sink[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
-      sink[nb] = p.sinks && er + 8 * nb < p.G
-                     ? __ldg(p.sinks + pr.kvh * p.G + er + 8 * nb) * kLog2e : -INFINITY;
+      sink[nb] = p.sinks && sr + 8 * nb < p.G
+                     ? __ldg(p.sinks + pr.kvh * p.G + sr + 8 * nb) * kLog2e : -INFINITY;
     uint32_t qa[D / 16][2 * NB];
     float row_scale[NB];  // logits of row g (g + 8) in log2 units per unit of S
 #pragma unroll
@@ -573,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       }
     }
 
-    if (!kCluster && C::kQSlots == 1 && seg_end < f1) {
+    if (!kCluster && kQSlots == 1 && seg_end < f1) {
       __syncthreads();  // every warp has its rows
       load_q(next, 0);
     }
@@ -589,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       for (int c = 0; c < E; ++c) acc[nb][c][0] = acc[nb][c][1] = acc[nb][c][2] = acc[nb][c][3] = 0.f;
     }
 
-    const int seg_n = (seg_end - f0 - warp + kWarps - 1) / kWarps;  // this warp's tiles end here
+    const int seg_n = (seg_end - w0 + kStep - 1) / kStep;  // this warp's tiles end here
     for (int took; ok && n < seg_n; n += took) {
       took = min(U, seg_n - n);
       int at[U];  // stages; an absent second tile reads the first again and counts for nothing
@@ -684,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       // ---- visibility ----
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        int tau = f0 + warp - pr.begin + kWarps * (n + u);
+        int tau = w0 - pr.begin + kStep * (n + u);
         if (tau >= sp.head) tau += sp.gap;
         const int tok = tau * 16;
         if (u < took && tok + 16 <= sp.L && (tok >= sp.start || tok + 16 <= sp.first)) continue;
@@ -795,124 +924,150 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         }
     }
 
-    // ---- merge the warps ----
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 1);
       l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 2);
-      float* r0 = my_wb + (8 * nb + 2 * t) * C::kWbRow;
-      float* r1 = r0 + C::kWbRow;
-#pragma unroll
-      for (int c = 0; c < E; ++c) {
-        // rows of the accumulator: dims 16c + 2g and 16c + 2g + 1 (e4m3), 16c + g and + 8 (bf16)
-        const int d0 = 16 * c + (kFp8 ? 2 * g : g), d1 = d0 + (kFp8 ? 1 : 8);
-        r0[d0] = acc[nb][c][0]; r1[d0] = acc[nb][c][1];
-        r0[d1] = acc[nb][c][2]; r1[d1] = acc[nb][c][3];
-      }
-      if (t == 0) {
-        float* st = my_wb + C::kRows * C::kWbRow + 8 * nb + g;
-        st[0] = m[nb];
-        st[C::kRows] = l[nb];
-        st[2 * C::kRows] = kFp8 ? R[nb] : m[nb];
-      }
     }
-    __syncthreads();
-    float o[NB][E], mc[NB], lc[NB], Rc[NB];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const float* st = wbuf + C::kRows * C::kWbRow + er + 8 * nb;
-      mc[nb] = Rc[nb] = -INFINITY;
-      lc[nb] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        mc[nb] = fmaxf(mc[nb], st[w * C::kWbFloats]);
-        Rc[nb] = fmaxf(Rc[nb], st[w * C::kWbFloats + 2 * C::kRows]);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[nb][e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* sw = st + w * C::kWbFloats;
-        lc[nb] = __fmaf_rn(weight(sw[0], mc[nb]), sw[C::kRows], lc[nb]);
-        const float wt = weight(sw[2 * C::kRows], Rc[nb]);
-        const float* ow = wbuf + w * C::kWbFloats + (er + 8 * nb) * C::kWbRow + ed;
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(ow + e);
-          o[nb][e] = __fmaf_rn(wt, a.x, o[nb][e]);
-          o[nb][e + 1] = __fmaf_rn(wt, a.y, o[nb][e + 1]);
-          o[nb][e + 2] = __fmaf_rn(wt, a.z, o[nb][e + 2]);
-          o[nb][e + 3] = __fmaf_rn(wt, a.w, o[nb][e + 3]);
+    if constexpr (kPerWarp) {
+      bool last = true;
+      if (f != pr.begin || seg_end != pr.begin + pr.n) {
+        // Contributors and slots as below, of warps.
+        const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kCost;
+        const int c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
+        const int me = (int)blockIdx.x * kWarps + warp - c0;
+        auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+        warp_store_partial<C>(p, slot_of(me), acc, m, l, R);
+        __syncwarp();
+        int* cnt = p.pair_counters + pr.b * Hkv + pr.kvh;
+        int arrived = 0;
+        if (lane == 0) arrived = atomic_add_acq_rel_gpu(cnt, 1);
+        last = __shfl_sync(0xffffffffu, arrived, 0) == c1 - c0;
+        __syncwarp();
+        if (last) {
+          if (lane == 0) store_relaxed_gpu(cnt, 0);
+          warp_merge_partials<C>(p, c1 - c0 + 1, slot_of, acc, m, l, R);
         }
       }
-    }
-
-    if (kCluster && p.cluster > 1) {
-      // this part's result, where the cluster's first CTA finds it
-      __syncthreads();  // every warp has read wbuf
-#pragma unroll
+      if (last) warp_finalize<C>(p, pr.b, pr.kvh, sink, acc, m, l, R);
+    } else {
+      // ---- merge the warps ----
+  #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float* dst = wbuf + (er + 8 * nb) * D + ed;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dst[e] = o[nb][e];
-        if (ed == 0) {
-          float* st = wbuf + C::kRows * D + er + 8 * nb;
-          st[0] = mc[nb];
-          st[C::kRows] = lc[nb];
-          st[2 * C::kRows] = Rc[nb];
+        float* r0 = my_wb + (8 * nb + 2 * t) * C::kWbRow;
+        float* r1 = r0 + C::kWbRow;
+  #pragma unroll
+        for (int c = 0; c < E; ++c) {
+          // rows of the accumulator: dims 16c + 2g and 16c + 2g + 1 (e4m3), 16c + g and + 8 (bf16)
+          const int d0 = 16 * c + (kFp8 ? 2 * g : g), d1 = d0 + (kFp8 ? 1 : 8);
+          r0[d0] = acc[nb][c][0]; r1[d0] = acc[nb][c][1];
+          r0[d1] = acc[nb][c][2]; r1[d1] = acc[nb][c][3];
+        }
+        if (t == 0) {
+          float* st = my_wb + C::kRows * C::kWbRow + 8 * nb + g;
+          st[0] = m[nb];
+          st[C::kRows] = l[nb];
+          st[2 * C::kRows] = kFp8 ? R[nb] : m[nb];
         }
       }
-    } else if (kCluster || (f == pr.begin && seg_end == pr.begin + pr.n)) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
-    } else if constexpr (!kCluster) {
-      // Contributors: the CTA whose range holds the first tile (slot 2 c + 1) and the
-      // ones whose cuts lie inside (slot 2 c), more than snap tiles from either border.
-      const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kPairCost;
-      const int c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
-      const int parts = c1 - c0 + 1, me = (int)blockIdx.x - c0;
-      auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        store_partial<C>(p, slot_of(me), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-      const int gi = me / kMergeGroup, gfirst = gi * kMergeGroup;
-      const int gsize = min(kMergeGroup, parts - gfirst);
-      const int groups = (parts + kMergeGroup - 1) / kMergeGroup;
-      int* gcnt = p.slot_counters + slot_of(gfirst);
-      int* tcnt = p.pair_counters + pr.b * Hkv + pr.kvh;
       __syncthreads();
-      if (tid == 0) misc[8] = atomic_add_acq_rel_gpu(gcnt, 1);
-      __syncthreads();
-      if (misc[8] == gsize - 1) {
-        if (tid == 0) store_relaxed_gpu(gcnt, 0);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          merge_partials<C>(p, gsize, [&](int k) { return slot_of(gfirst + k); }, er + 8 * nb,
-                            ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-          if (groups == 1)
-            finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
-          else
-            store_partial<C>(p, slot_of(gfirst), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+      float o[NB][E], mc[NB], lc[NB], Rc[NB];
+  #pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float* st = wbuf + C::kRows * C::kWbRow + er + 8 * nb;
+        mc[nb] = Rc[nb] = -INFINITY;
+        lc[nb] = 0.f;
+  #pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          mc[nb] = fmaxf(mc[nb], st[w * C::kWbFloats]);
+          Rc[nb] = fmaxf(Rc[nb], st[w * C::kWbFloats + 2 * C::kRows]);
         }
-        if (groups > 1) {
-          __syncthreads();
-          if (tid == 0) misc[9] = atomic_add_acq_rel_gpu(tcnt, 1);
-          __syncthreads();
-          if (misc[9] == groups - 1) {
-            if (tid == 0) store_relaxed_gpu(tcnt, 0);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              merge_partials<C>(p, groups, [&](int k) { return slot_of(k * kMergeGroup); },
-                                er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+  #pragma unroll
+        for (int e = 0; e < E; ++e) o[nb][e] = 0.f;
+  #pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float* sw = st + w * C::kWbFloats;
+          lc[nb] = __fmaf_rn(weight(sw[0], mc[nb]), sw[C::kRows], lc[nb]);
+          const float wt = weight(sw[2 * C::kRows], Rc[nb]);
+          const float* ow = wbuf + w * C::kWbFloats + (er + 8 * nb) * C::kWbRow + ed;
+  #pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(ow + e);
+            o[nb][e] = __fmaf_rn(wt, a.x, o[nb][e]);
+            o[nb][e + 1] = __fmaf_rn(wt, a.y, o[nb][e + 1]);
+            o[nb][e + 2] = __fmaf_rn(wt, a.z, o[nb][e + 2]);
+            o[nb][e + 3] = __fmaf_rn(wt, a.w, o[nb][e + 3]);
+          }
+        }
+      }
+
+      if (kCluster && p.cluster > 1) {
+        // this part's result, where the cluster's first CTA finds it
+        __syncthreads();  // every warp has read wbuf
+  #pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float* dst = wbuf + (er + 8 * nb) * D + ed;
+  #pragma unroll
+          for (int e = 0; e < E; ++e) dst[e] = o[nb][e];
+          if (ed == 0) {
+            float* st = wbuf + C::kRows * D + er + 8 * nb;
+            st[0] = mc[nb];
+            st[C::kRows] = lc[nb];
+            st[2 * C::kRows] = Rc[nb];
+          }
+        }
+      } else if (kCluster || (f == pr.begin && seg_end == pr.begin + pr.n)) {
+  #pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
+      } else if constexpr (!kCluster) {
+        // Contributors: the CTA whose range holds the first tile (slot 2 c + 1) and the
+        // ones whose cuts lie inside (slot 2 c), more than snap tiles from either border.
+        const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kPairCost;
+        const int c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
+        const int parts = c1 - c0 + 1, me = (int)blockIdx.x - c0;
+        auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+  #pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          store_partial<C>(p, slot_of(me), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+        const int gi = me / kMergeGroup, gfirst = gi * kMergeGroup;
+        const int gsize = min(kMergeGroup, parts - gfirst);
+        const int groups = (parts + kMergeGroup - 1) / kMergeGroup;
+        int* gcnt = p.slot_counters + slot_of(gfirst);
+        int* tcnt = p.pair_counters + pr.b * Hkv + pr.kvh;
+        __syncthreads();
+        if (tid == 0) misc[8] = atomic_add_acq_rel_gpu(gcnt, 1);
+        __syncthreads();
+        if (misc[8] == gsize - 1) {
+          if (tid == 0) store_relaxed_gpu(gcnt, 0);
+  #pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            merge_partials<C>(p, gsize, [&](int k) { return slot_of(gfirst + k); }, er + 8 * nb,
+                              ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+            if (groups == 1)
               finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
+            else
+              store_partial<C>(p, slot_of(gfirst), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+          }
+          if (groups > 1) {
+            __syncthreads();
+            if (tid == 0) misc[9] = atomic_add_acq_rel_gpu(tcnt, 1);
+            __syncthreads();
+            if (misc[9] == groups - 1) {
+              if (tid == 0) store_relaxed_gpu(tcnt, 0);
+  #pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                merge_partials<C>(p, groups, [&](int k) { return slot_of(k * kMergeGroup); },
+                                  er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+                finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
+              }
             }
           }
         }
       }
     }
     f = seg_end;
-    slot ^= C::kQSlots - 1;
+    slot ^= kQSlots - 1;
   }
 
   // A wait that gave up leaves copies in flight: wait for them (again with a
@@ -985,11 +1140,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   }
 }
 
-template <class C, bool kCluster>
+template <class C, int kMode>
 cudaError_t launch_mode(const PagedParams& p, const CUtensorMap& map, cudaStream_t stream) {
+  constexpr bool kCluster = kMode == kPagedCluster;
   static std::atomic<uint64_t> done{0};
   cudaError_t e =
-      set_smem_attr_once(paged_attn_kernel<C, kCluster>, C::smem_bytes(kPagedMaxBatch), done);
+      set_smem_attr_once(paged_attn_kernel<C, kMode>, C::smem_bytes(kPagedMaxBatch), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
@@ -1004,12 +1160,14 @@ cudaError_t launch_mode(const PagedParams& p, const CUtensorMap& map, cudaStream
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kCluster && p.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<C, kCluster>, p, map);
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<C, kMode>, p, map);
 }
 
 template <class C>
 cudaError_t launch_t(const PagedParams& p, const CUtensorMap& map, cudaStream_t stream) {
-  return p.cluster ? launch_mode<C, true>(p, map, stream) : launch_mode<C, false>(p, map, stream);
+  return p.mode == kPagedCluster ? launch_mode<C, kPagedCluster>(p, map, stream)
+         : p.mode == kPagedWarp ? launch_mode<C, kPagedWarp>(p, map, stream)
+                                 : launch_mode<C, kPagedShares>(p, map, stream);
 }
 
 template <typename F>

@@ -223,6 +223,12 @@ cudaError_t launch_wait_selftest(int* err, cudaStream_t stream);
 cudaError_t launch_mla_kv_append(const AppendParams& p, cudaStream_t stream);
 
 // ----------------------------------- decode with a window and first tokens --
+enum : int {
+  kPagedShares = 0,   // CTAs take equal shares of all tiles
+  kPagedCluster = 1,  // a cluster of CTAs for each (request, kv head) pair
+  kPagedWarp = 2,     // warps take equal shares of all tiles
+};
+constexpr int kPagedWarps = 4;      // of a CTA
 constexpr int kPagedMaxGroup = 16;  // query heads per kv head
 constexpr int kPagedMaxBatch = 2048;
 
@@ -248,10 +254,11 @@ struct PagedParams {
   float scale;
   int page_shift;                // log2(page_size)
   int grid;
-  int cluster;                   // > 0: cluster mode, this many CTAs for each pair
-  float* partials;               // [2 * grid] slots
+  int mode;                      // kPagedShares, kPagedCluster, kPagedWarp
+  int cluster;                   // cluster mode: CTAs for each pair
+  float* partials;               // two slots for each CTA (each warp in the warp mode)
   int* slot_counters;            // [2 * grid] arrival counters of merge groups
-  int* pair_counters;            // [B * Hkv] arrival counters of the groups
+  int* pair_counters;            // [B * Hkv] arrival counters of the groups (of the warps)
   int* err;
 };
 struct PagedShape {
@@ -272,6 +279,10 @@ constexpr int kPagedMaxCluster = 8;
 // Most tiles of a CTA in the cluster mode (bf16, a window of 1024 on 16 x 8 kv heads,
 // 33 tiles each: 15.4 us in clusters, 17.2 without).
 constexpr int kPagedClusterTiles = 48;
+// Most tiles of a pair in the warp mode, in which one warp merges a pair's parts: 150 x 8
+// kv heads of up to 2000 keys took 57.0 us in equal shares of CTAs, 55.8 in the warp mode,
+// but a batch with one such request among very short ones gives it dozens of parts.
+constexpr int kPagedWarpTiles = 64;
 
 // ------------------------------------------------ append to an e4m3 cache --
 struct AppendFp8Params {

@@ -163,6 +163,100 @@ def test_many_short_requests(fp8):
     check(pr, *run(pr))
 
 
+MANY = [n for i in range(27) for n in EDGE_LENS]  # with 3 kv heads more pairs than two waves
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,P", [(1, 16), (5, 32), (8, 128), (16, 64)])
+def test_head_layouts_of_many_requests(fp8, D, G, P):
+    pr = problem(G + P, MANY, 3, G, D, P, fp8, sinks=(G % 2 == 0))
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("D,G", [(128, 8), (64, 16)])
+def test_long_requests_among_many_of_one_key(fp8, D, G):
+    """The long ones are cut into dozens of parts, which one warp merges."""
+    lens = [1] * 400 + [1000, 0, 990] + [1, 2] * 100 + [1008] + [1] * 100
+    pr = problem(23, lens, 2, G, D, 16, fp8, sinks=True)
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_many_requests_strided_and_without_lse(fp8):
+    pr = problem(24, MANY, 3, 5, 128, 16, fp8, nhd=True)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in pr.items()}
+    B, Hq, D = pr["q"].shape
+    hold = torch.full((B, Hq + 1, D + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, 2 * Hq), 7.0, device="cuda")
+    call(d, hold[:, :Hq, :D], lse[:, ::2])
+    torch.cuda.synchronize()
+    check(pr, hold[:, :Hq, :D].cpu(), lse[:, ::2].cpu())
+    assert (hold[:, Hq:] == 7).all() and (hold[:, :, D:] == 7).all() and (lse[:, 1::2] == 7).all()
+    first = hold[:, :Hq, :D].clone()
+    hold.fill_(7.0)
+    call(d, hold[:, :Hq, :D], None)
+    torch.cuda.synchronize()
+    assert torch.equal(hold[:, :Hq, :D], first)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_many_requests_replayed_beside_eager_calls(fp8):
+    """Every run gives the same bits, a captured one with new lengths gives theirs, and the
+    counters that the parts of a request share are back at zero."""
+    pr = problem(25, MANY, 3, 8, 64, 16, fp8, sinks=True)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in pr.items()}
+    want = run(pr, d=d)
+    check(pr, *want)
+    out, lse = torch.empty_like(d["q"]), torch.empty(d["q"].shape[:2], device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(d, out, lse, torch.cuda.current_stream())
+    for _ in range(10):
+        out.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+        again = run(pr, d=d)
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+    pr["sl"] = pr["sl"] // 2
+    d["sl"].copy_(pr["sl"])
+    graph.replay()
+    torch.cuda.synchronize()
+    check(pr, out.cpu(), lse.cpu())
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_bad_entries_among_many_requests(fp8):
+    pr = problem(26, MANY, 3, 4, 128, 16, fp8, sinks=True)
+    want = run(pr)
+    rows = [b for b, n in enumerate(MANY) if n >= 300][::5]
+    for i, b in enumerate(rows):
+        pr["bt"][b, 3] = pr["kv"].shape[0] if i % 2 else -7
+    out, lse = run(pr)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.check_errors(0)
+    assert e.value.code == -7
+    check(pr, out, lse)
+    rest = [b for b in range(len(MANY)) if b not in rows]
+    assert torch.equal(out[rest], want[0][rest]) and torch.equal(lse[rest], want[1][rest])
+
+
+def test_many_requests_in_a_small_workspace():
+    """No room for the partials of every warp: blocks share the work, in fewer places."""
+    pr = problem(27, MANY, 3, 8, 128, 16, True, sinks=True)
+    torch.cuda.synchronize()
+    pkv.shutdown()
+    try:
+        pkv.init(0, 100 * 2 * (8 * 128 + 24) * 4)
+        check(pr, *run(pr))
+    finally:
+        pkv.shutdown()
+        pkv.init(0)
+    check(pr, *run(pr))
+
+
 def test_largest_batch_and_one_request_of_no_key():
     pr = problem(2, [1 + i % 3 for i in range(2048)], 1, 1, 64, 16, True)
     check(pr, *run(pr))
