@@ -1186,8 +1186,8 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   // kPagedClusterTiles; one CTA each for up to two waves of pairs, clusters where they
   // leave an eighth of the places to spare, as clusters do not fill every GPC.
   // On / off: four short requests 4.5 / 6.5 us, 256 requests of 200 keys 6.5 / 8.4,
-  // 16 x 8 kv heads of 1000 keys 11.1 / 13.7, a 1001-key window on 33 x 4 kv heads
-  // 12.1 / 13.0, 100 x 8 kv heads of 300 to 700 keys 23.7 / 26.6, a window of 128 on
+  // 16 x 8 kv heads of 1000 keys 10.8 / 13.7, a 1001-key window on 33 x 4 kv heads
+  // 10.1 / 13.0, 100 x 8 kv heads of 300 to 700 keys 23.7 / 26.6, a window of 128 on
   // 64 x 8 kv heads 9.3 / 10.6; without the spare places 64 pairs in clusters of 7 took
   // 22.5 us instead of 13.2, and without the limit of two waves 1000 x 8 kv heads of up
   // to 300 keys 83 instead of 70.
