@@ -42,16 +42,18 @@
 //    merge of warps or a barrier.  Of the warps that share a pair the last to arrive
 //    merges the accumulators that all have published, in order.
 //  * Otherwise, a request cut between CTAs: each publishes its 32-bit (O, m, l, R); the last
-//    CTA of a group of up to 16 (an arrival counter) merges the group in order,
-//    the last group merges the groups.  Results do not depend on timing.
+//    CTA of a group of up to kMergeGroup (an arrival counter) merges the group, the last
+//    group merges the groups: each warp a fourth of the parts in order, then the warps'
+//    results (one thread per output going through all parts took 18.4 us instead of 15.1
+//    for one request of 16000 keys).  Results do not depend on timing.
 //
 // Measured (GB300, graph replays; the copy bandwidth is 6786 GB/s): e4m3, 8 requests
-// of 131072 keys, 8 kv heads of 128: 317 us = 6.79 TB/s; 64 requests of up to 32768
-// keys (272 MB): 51.2 us = 5.3 TB/s, of which 4 us pass before the first tile arrives
-// (lengths, table, tile: three dependent reads) and the CTAs end between 41 and 52;
+// of 131072 keys, 8 kv heads of 128: 316 us = 6.81 TB/s; 64 requests of up to 32768
+// keys (272 MB): 49.8 us = 5.5 TB/s, of which 4 us pass before the first tile arrives
+// (lengths, table, tile: three dependent reads) and the CTAs end over the last 10;
 // bf16, a window of 4096 + 64 on 32 requests: 83 us = 6.4 TB/s; four short requests:
 // 4.5 us.  1 GB of e4m3 heads of 128 reads at 97 % (up to 8 query heads per kv head)
-// and 93 % (16), of 64 at 93 and 78 % (bound by instructions: 12 warps an SM, 2.1
+// and 93 % (16), of 64 at 91 and 79 % (bound by instructions: 12 warps an SM, 2.1
 // instructions a cycle); bf16 at 95 to 99 %.  A tile's way through a warp is about
 // 700 (bf16) to 1200 (e4m3) cycles, of which the 16 products of S take 150 to 250.
 #include "pkv_internal.h"
@@ -62,7 +64,9 @@ namespace {
 
 constexpr int kWarps = kPagedWarps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMergeGroup = 16;
+// One request of 131072 keys and one kv head: 17.6 us at 16, 18.3 at 12, 19.4 at 8; of 16000
+// keys and 8 kv heads: 15.2, 15.1, 14.8; 4 requests of up to 16000: 13.9, 13.2, 13.3.
+constexpr int kMergeGroup = 12;
 constexpr int kPairCost = kPagedPairCost;
 // The same for a warp in the warp mode: 2000 requests of 1 to 64 keys take 14.1 us at
 // 2, 14.8 at 3; 1000 x 8 of up to 300 keys 47.4 at 2, 45.8 at 3, 47.9 at 5.
@@ -305,50 +309,96 @@ __device__ __forceinline__ void store_partial(const PagedParams& p, int slot, in
   }
 }
 
-// Merge partials k = 0 .. n - 1 at slots slot_of(k), in order, for this thread's
-// row and dims: the loads of four partials are in flight at once.
-template <class C, typename SlotOf>
-__device__ __forceinline__ void merge_partials(const PagedParams& p, int n, SlotOf slot_of, int er,
-                                               int ed, float (&o)[C::D / 16], float& m, float& l,
-                                               float& R) {
+// The four warps' (O, m, l, R) in shared memory merged, for rows er and er + 8, dims
+// [ed, ed + E).
+template <class C>
+__device__ __forceinline__ void combine_warps(const float* wbuf, int er, int ed,
+                                              float (&o)[C::NB][C::D / 16], float (&mc)[C::NB],
+                                              float (&lc)[C::NB], float (&Rc)[C::NB]) {
   constexpr int E = C::D / 16;
-  m = R = -INFINITY;
-  l = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 4) {
-    float mk[4], lk[4], Rk[4];
-    float4 ok[4][E / 4];
+  for (int nb = 0; nb < C::NB; ++nb) {
+    const float* st = wbuf + C::kRows * C::kWbRow + er + 8 * nb;
+    mc[nb] = Rc[nb] = -INFINITY;
+    lc[nb] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float* src = p.partials + (int64_t)slot_of(min(k0 + i, n - 1)) * C::kPartFloats;
-      const float* st = src + C::kRows * C::D + er;
-      mk[i] = __ldcg(st);
-      lk[i] = __ldcg(st + C::kRows);
-      Rk[i] = __ldcg(st + 2 * C::kRows);
-#pragma unroll
-      for (int e = 0; e < E / 4; ++e) ok[i][e] = ldcg_f4(src + er * C::D + ed + 4 * e);
+    for (int w = 0; w < kWarps; ++w) {
+      mc[nb] = fmaxf(mc[nb], st[w * C::kWbFloats]);
+      Rc[nb] = fmaxf(Rc[nb], st[w * C::kWbFloats + 2 * C::kRows]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (k0 + i >= n) break;
-      const float mn = fmaxf(m, mk[i]), Rn = fmaxf(R, Rk[i]);
-      l = __fmaf_rn(weight(m, mn), l, weight(mk[i], mn) * lk[i]);
-      const float a = weight(R, Rn), w = weight(Rk[i], Rn);
-      m = mn;
-      R = Rn;
+    for (int e = 0; e < E; ++e) o[nb][e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E / 4; ++e) {
-        o[4 * e] = __fmaf_rn(a, o[4 * e], w * ok[i][e].x);
-        o[4 * e + 1] = __fmaf_rn(a, o[4 * e + 1], w * ok[i][e].y);
-        o[4 * e + 2] = __fmaf_rn(a, o[4 * e + 2], w * ok[i][e].z);
-        o[4 * e + 3] = __fmaf_rn(a, o[4 * e + 3], w * ok[i][e].w);
+    for (int w = 0; w < kWarps; ++w) {
+      const float* sw = st + w * C::kWbFloats;
+      lc[nb] = __fmaf_rn(weight(sw[0], mc[nb]), sw[C::kRows], lc[nb]);
+      const float wt = weight(sw[2 * C::kRows], Rc[nb]);
+      const float* ow = wbuf + w * C::kWbFloats + (er + 8 * nb) * C::kWbRow + ed;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(ow + e);
+        o[nb][e] = __fmaf_rn(wt, a.x, o[nb][e]);
+        o[nb][e + 1] = __fmaf_rn(wt, a.y, o[nb][e + 1]);
+        o[nb][e + 2] = __fmaf_rn(wt, a.z, o[nb][e + 2]);
+        o[nb][e + 3] = __fmaf_rn(wt, a.w, o[nb][e + 3]);
       }
     }
   }
 }
 
-// The same three for a warp whose lanes hold the accumulators of the products: lane
+// Slot of a pair's part i, whose first part is CTA (warp) c0's.
+__device__ __forceinline__ int part_slot(int c0, int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); }
+
+// The warp's part of merging a pair's parts first, first + step, .. before end: every
+// fourth, in order, into its own (O, m, l, R) in shared memory.  A lane has floats
+// 128 u + 4 lane .. + 3 of the partial, and the statistics of row `lane`.  A call, as its
+// registers would cost the loop over tiles some of its own (e4m3 heads of 64 on 1 GB: 91 %
+// of the copy bandwidth, 90 inlined).
+template <class C>
+__device__ __noinline__ void gather_partials(const float* partials, int c0, int first, int step,
+                                             int end, float* wb) {
+  constexpr int kUnits = C::kRows * C::D / 128;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m = -INFINITY, l = 0.f, R = -INFINITY;
+  float4 a[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = first + warp * step; i < end; i += kWarps * step) {
+    const float* src = partials + (int64_t)part_slot(c0, i) * C::kPartFloats;
+    const float* st = src + C::kRows * C::D + min(lane, C::kRows - 1);
+    const float mk = __ldcg(st), lk = __ldcg(st + C::kRows), Rk = __ldcg(st + 2 * C::kRows);
+    float4 v[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) v[u] = ldcg_f4(src + 128 * u + 4 * lane);
+    const float mn = fmaxf(m, mk), Rn = fmaxf(R, Rk);
+    l = __fmaf_rn(weight(m, mn), l, weight(mk, mn) * lk);
+    const float keep = weight(R, Rn), add = weight(Rk, Rn);
+    m = mn;
+    R = Rn;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int row = (128 * u + 4 * lane) / C::D;
+      const float x = __shfl_sync(0xffffffffu, keep, row), y = __shfl_sync(0xffffffffu, add, row);
+      a[u].x = __fmaf_rn(x, a[u].x, y * v[u].x);
+      a[u].y = __fmaf_rn(x, a[u].y, y * v[u].y);
+      a[u].z = __fmaf_rn(x, a[u].z, y * v[u].z);
+      a[u].w = __fmaf_rn(x, a[u].w, y * v[u].w);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int i = 128 * u + 4 * lane;
+    *reinterpret_cast<float4*>(wb + i / C::D * C::kWbRow + i % C::D) = a[u];
+  }
+  if (lane < C::kRows) {
+    float* st = wb + C::kRows * C::kWbRow + lane;
+    st[0] = m;
+    st[C::kRows] = l;
+    st[2 * C::kRows] = R;
+  }
+}
+
+// The same for a warp whose lanes hold the accumulators of the products: lane
 // (g, t) = (lane / 4, lane % 4) has columns 2t and 2t + 1, which are the kv head's query
 // rows 8 nb + 2t and 8 nb + 2t + 1, and the statistics of rows 8 nb + g.
 template <class C>
@@ -373,8 +423,8 @@ __device__ __forceinline__ void warp_store_partial(const PagedParams& p, int slo
   }
 }
 
-template <class C, typename SlotOf>
-__device__ __forceinline__ void warp_merge_partials(const PagedParams& p, int n, SlotOf slot_of,
+template <class C>
+__device__ __forceinline__ void warp_merge_partials(const PagedParams& p, int c0, int n,
                                                     float (&acc)[C::NB][C::D / 16][4],
                                                     float (&m)[C::NB], float (&l)[C::NB],
                                                     float (&R)[C::NB]) {
@@ -387,7 +437,7 @@ __device__ __forceinline__ void warp_merge_partials(const PagedParams& p, int n,
     for (int c = 0; c < C::D / 16; ++c)
       acc[nb][c][0] = acc[nb][c][1] = acc[nb][c][2] = acc[nb][c][3] = 0.f;
     for (int k = 0; k < n; ++k) {
-      const float* src = p.partials + (int64_t)slot_of(k) * C::kPartFloats;
+      const float* src = p.partials + (int64_t)part_slot(c0, k) * C::kPartFloats;
       const float* st = src + C::kRows * C::D + 8 * nb + (lane >> 2);
       const float mk = __ldcg(st), lk = __ldcg(st + C::kRows), Rk = __ldcg(st + 2 * C::kRows);
       float4 v[C::D / 16];
@@ -937,8 +987,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kCost;
         const int c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
         const int me = (int)blockIdx.x * kWarps + warp - c0;
-        auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
-        warp_store_partial<C>(p, slot_of(me), acc, m, l, R);
+        warp_store_partial<C>(p, part_slot(c0, me), acc, m, l, R);
         __syncwarp();
         int* cnt = p.pair_counters + pr.b * Hkv + pr.kvh;
         int arrived = 0;
@@ -947,17 +996,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         __syncwarp();
         if (last) {
           if (lane == 0) store_relaxed_gpu(cnt, 0);
-          warp_merge_partials<C>(p, c1 - c0 + 1, slot_of, acc, m, l, R);
+          warp_merge_partials<C>(p, c0, c1 - c0 + 1, acc, m, l, R);
         }
       }
       if (last) warp_finalize<C>(p, pr.b, pr.kvh, sink, acc, m, l, R);
     } else {
       // ---- merge the warps ----
-  #pragma unroll
+#pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float* r0 = my_wb + (8 * nb + 2 * t) * C::kWbRow;
         float* r1 = r0 + C::kWbRow;
-  #pragma unroll
+#pragma unroll
         for (int c = 0; c < E; ++c) {
           // rows of the accumulator: dims 16c + 2g and 16c + 2g + 1 (e4m3), 16c + g and + 8 (bf16)
           const int d0 = 16 * c + (kFp8 ? 2 * g : g), d1 = d0 + (kFp8 ? 1 : 8);
@@ -973,42 +1022,15 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
       }
       __syncthreads();
       float o[NB][E], mc[NB], lc[NB], Rc[NB];
-  #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const float* st = wbuf + C::kRows * C::kWbRow + er + 8 * nb;
-        mc[nb] = Rc[nb] = -INFINITY;
-        lc[nb] = 0.f;
-  #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          mc[nb] = fmaxf(mc[nb], st[w * C::kWbFloats]);
-          Rc[nb] = fmaxf(Rc[nb], st[w * C::kWbFloats + 2 * C::kRows]);
-        }
-  #pragma unroll
-        for (int e = 0; e < E; ++e) o[nb][e] = 0.f;
-  #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float* sw = st + w * C::kWbFloats;
-          lc[nb] = __fmaf_rn(weight(sw[0], mc[nb]), sw[C::kRows], lc[nb]);
-          const float wt = weight(sw[2 * C::kRows], Rc[nb]);
-          const float* ow = wbuf + w * C::kWbFloats + (er + 8 * nb) * C::kWbRow + ed;
-  #pragma unroll
-          for (int e = 0; e < E; e += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(ow + e);
-            o[nb][e] = __fmaf_rn(wt, a.x, o[nb][e]);
-            o[nb][e + 1] = __fmaf_rn(wt, a.y, o[nb][e + 1]);
-            o[nb][e + 2] = __fmaf_rn(wt, a.z, o[nb][e + 2]);
-            o[nb][e + 3] = __fmaf_rn(wt, a.w, o[nb][e + 3]);
-          }
-        }
-      }
+      combine_warps<C>(wbuf, er, ed, o, mc, lc, Rc);
 
       if (kCluster && p.cluster > 1) {
-        // this part's result, where the cluster's first CTA finds it
+        // this part's result, where the cluster's other CTAs find it
         __syncthreads();  // every warp has read wbuf
-  #pragma unroll
+#pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float* dst = wbuf + (er + 8 * nb) * D + ed;
-  #pragma unroll
+#pragma unroll
           for (int e = 0; e < E; ++e) dst[e] = o[nb][e];
           if (ed == 0) {
             float* st = wbuf + C::kRows * D + er + 8 * nb;
@@ -1018,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
           }
         }
       } else if (kCluster || (f == pr.begin && seg_end == pr.begin + pr.n)) {
-  #pragma unroll
+#pragma unroll
         for (int nb = 0; nb < NB; ++nb)
           finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
       } else if constexpr (!kCluster) {
@@ -1027,42 +1049,42 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kPairCost;
         const int c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
         const int parts = c1 - c0 + 1, me = (int)blockIdx.x - c0;
-        auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
-  #pragma unroll
+#pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-          store_partial<C>(p, slot_of(me), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+          store_partial<C>(p, part_slot(c0, me), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
         const int gi = me / kMergeGroup, gfirst = gi * kMergeGroup;
         const int gsize = min(kMergeGroup, parts - gfirst);
         const int groups = (parts + kMergeGroup - 1) / kMergeGroup;
-        int* gcnt = p.slot_counters + slot_of(gfirst);
+        int* gcnt = p.slot_counters + part_slot(c0, gfirst);
         int* tcnt = p.pair_counters + pr.b * Hkv + pr.kvh;
         __syncthreads();
         if (tid == 0) misc[8] = atomic_add_acq_rel_gpu(gcnt, 1);
         __syncthreads();
         if (misc[8] == gsize - 1) {
           if (tid == 0) store_relaxed_gpu(gcnt, 0);
-  #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            merge_partials<C>(p, gsize, [&](int k) { return slot_of(gfirst + k); }, er + 8 * nb,
-                              ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-            if (groups == 1)
-              finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
-            else
-              store_partial<C>(p, slot_of(gfirst), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-          }
-          if (groups > 1) {
+          gather_partials<C>(p.partials, c0, gfirst, 1, gfirst + gsize, my_wb);
+          __syncthreads();
+          combine_warps<C>(wbuf, er, ed, o, mc, lc, Rc);
+          bool whole = groups == 1;
+          if (!whole) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              store_partial<C>(p, part_slot(c0, gfirst), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
             __syncthreads();
             if (tid == 0) misc[9] = atomic_add_acq_rel_gpu(tcnt, 1);
             __syncthreads();
             if (misc[9] == groups - 1) {
               if (tid == 0) store_relaxed_gpu(tcnt, 0);
-  #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                merge_partials<C>(p, groups, [&](int k) { return slot_of(k * kMergeGroup); },
-                                  er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-                finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
-              }
+              gather_partials<C>(p.partials, c0, 0, kMergeGroup, parts, my_wb);
+              __syncthreads();
+              combine_warps<C>(wbuf, er, ed, o, mc, lc, Rc);
+              whole = true;
             }
+          }
+          if (whole) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
           }
         }
       }
