@@ -19,9 +19,9 @@
 // the rows of a page to shared memory at once (up to 16 16-byte copies a lane)
 // before it reduces, and encoding them from there.
 //
-// Measured (GB300, 8 kv heads of 128, graph replays): 64 single tokens 2.9 us, 1024
-// of them 7.8 us; 12.5 k tokens of ragged prompts (77 MB) 17 us = 4.5 TB/s, 32 k
-// tokens 32.7 us = 6.2 TB/s (91 % of the measured copy bandwidth; pages of 32 and 128
+// Measured (GB300, 8 kv heads of 128, graph replays): 64 single tokens 2.8 us, 1024
+// of them 7.7 us; 12.5 k tokens of ragged prompts (77 MB) 16.6 us = 4.6 TB/s, 32 k
+// tokens 32.3 us = 6.2 TB/s (92 % of the measured copy bandwidth; pages of 32 and 128
 // tokens 79 and 81 %).  What is left is the chain of dependent reads that a warp
 // begins with (request, length, page, rows): about 4 us, hidden only by other warps.
 #include <algorithm>
@@ -98,20 +98,38 @@ __device__ __forceinline__ void decode8(const uint2& u, float (&f)[8]) {
   }
 }
 
+// A request's rows [r0, r1) of the new ones and its length.
+struct Request {
+  int r0, r1, len;
+};
+__device__ __forceinline__ Request request_at(const AppendFp8Params& p, int b) {
+  return {__ldg(p.cu + b), __ldg(p.cu + b + 1), __ldg(p.seq_lens + b)};
+}
+
 // The last request that begins at or before row r (-1: none), 32 requests at a time.
-__device__ __forceinline__ int request_of(const AppendFp8Params& p, long long r) {
+// The last step reads all that is asked of a request, so that nothing waits for a read
+// after it.
+__device__ __forceinline__ int request_of(const AppendFp8Params& p, long long r, Request& q) {
   const int lane = threadIdx.x & 31;
   int lo = 0, len = p.B;  // among requests [lo, lo + len); an earlier one begins before r
   int found = -1;
+  bool all = true;  // q holds all of request `found`
   while (len > 0) {
     const int step = (len + 31) >> 5, at = lo + lane * step;
-    const bool yes = lane * step < len && __ldg(p.cu + at) <= r;
+    const bool in = lane * step < len;
+    const Request mine = !in ? Request{} : step == 1 ? request_at(p, at) : Request{__ldg(p.cu + at)};
+    const bool yes = in && mine.r0 <= r;
     const int cnt = __popc(__ballot_sync(0xffffffffu, yes));
     if (cnt == 0) break;
+    all = step == 1;
+    q.r0 = __shfl_sync(0xffffffffu, mine.r0, cnt - 1);
+    q.r1 = __shfl_sync(0xffffffffu, mine.r1, cnt - 1);
+    q.len = __shfl_sync(0xffffffffu, mine.len, cnt - 1);
     found = lo + (cnt - 1) * step;
     len = min(step - 1, lo + len - found - 1);
     lo = found + 1;
   }
+  if (!all) q = request_at(p, found);
   return found;
 }
 
@@ -239,36 +257,45 @@ __global__ void __launch_bounds__(kWarps * 32, 7)
   if (r >= end) return;
   int turn = 0;
 
-  const long long each = p.cu ? 0 : p.T / p.B;
-  int b = p.cu ? request_of(p, r) : (int)(r / each);
-  if (b < 0) {  // rows before the first request are padding
-    b = 0;
-    r = __ldg(p.cu);
-    if (r < 0) return;
-  }
-  for (; r < end && b < p.B; ++b) {
-    const long long r0 = p.cu ? __ldg(p.cu + b) : b * each;
-    const long long r1 = p.cu ? min((long long)__ldg(p.cu + b + 1), (long long)p.T) : r0 + each;
-    if (r0 < 0) return;
-    if (r >= r1) continue;  // an empty request (or padding behind the last one)
-    const long long first = (long long)__ldg(p.seq_lens + b) - r1;  // position of row i: first + i
-    r = min(max(r, -first), r1);  // tokens at negative positions are dropped
-    while (r < end && r < r1) {
-      const long long pos = first + r;
-      const int slot0 = (int)(pos % P);
-      const int n = (int)min((long long)(P - slot0), r1 - r);
-      // a page belongs to the warp of its first new row
-      if (r == r0 || r == -first || slot0 == 0) {
-        const long long pg = pos / P;
-        const int blk = pg < p.max_blocks ? __ldg(p.bt + b * p.bt_sb + pg) : -1;
-        if (!append_page<D, kTeam>(p, h, r, n, blk, slot0, hold + warp * 32 * held, held,
-                                   exchange, turn) &&
-            lane == 0)
-          atomicOr(p.err, pg < p.max_blocks ? DEVERR_BAD_BLOCK : DEVERR_SEQ_TOO_LONG);
-      }
-      r += n;
+  const int each = p.cu ? 0 : (int)(p.T / p.B);
+  Request q;
+  int b;
+  if (p.cu) {
+    b = request_of(p, r, q);
+    if (b < 0) {  // rows before the first request are padding
+      b = 0;
+      q = request_at(p, 0);
+      r = q.r0;
     }
-    if (r < r1) return;
+  } else {
+    b = (int)(r / each);
+    q = {b * each, (b + 1) * each, __ldg(p.seq_lens + b)};
+  }
+  for (;;) {
+    const long long r0 = q.r0, r1 = min((long long)q.r1, (long long)p.T);
+    if (r0 < 0) return;
+    if (r < r1) {  // else an empty request, or padding behind the last one
+      const long long first = (long long)q.len - r1;  // position of row i: first + i
+      r = min(max(r, -first), r1);  // tokens at negative positions are dropped
+      while (r < end && r < r1) {
+        const long long pos = first + r;
+        const int slot0 = (int)(pos % P);
+        const int n = (int)min((long long)(P - slot0), r1 - r);
+        // a page belongs to the warp of its first new row
+        if (r == r0 || r == -first || slot0 == 0) {
+          const long long pg = pos / P;
+          const int blk = pg < p.max_blocks ? __ldg(p.bt + b * p.bt_sb + pg) : -1;
+          if (!append_page<D, kTeam>(p, h, r, n, blk, slot0, hold + warp * 32 * held, held,
+                                     exchange, turn) &&
+              lane == 0)
+            atomicOr(p.err, pg < p.max_blocks ? DEVERR_BAD_BLOCK : DEVERR_SEQ_TOO_LONG);
+        }
+        r += n;
+      }
+      if (r < r1) return;
+    }
+    if (r >= end || ++b >= p.B) return;
+    q = p.cu ? request_at(p, b) : Request{q.r1, q.r1 + each, __ldg(p.seq_lens + b)};
   }
 }
 
