@@ -1183,14 +1183,16 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
       1, std::min<int64_t>(std::min(ws.num_sms * shape.ctas_per_sm, pkv::kPagedMaxGrid),
                            (cost + pkv::kPagedMinCost - 1) / pkv::kPagedMinCost)));
   // Cluster mode: every pair has CTAs of its own, about 16 tiles each and none more than
-  // kPagedClusterTiles; one CTA each for up to two waves of pairs, clusters where they
-  // leave an eighth of the places to spare, as clusters do not fill every GPC.
+  // kPagedClusterTiles, or twice that for one CTA a pair in waves that are two thirds full;
+  // one CTA each for up to two waves of pairs, clusters where they leave an eighth of the
+  // places to spare, as clusters do not fill every GPC.
   // On / off: four short requests 4.5 / 6.5 us, 256 requests of 200 keys 6.5 / 8.4,
   // 16 x 8 kv heads of 1000 keys 10.8 / 13.7, a 1001-key window on 33 x 4 kv heads
-  // 10.1 / 13.0, 100 x 8 kv heads of 300 to 700 keys 23.7 / 26.6, a window of 128 on
-  // 64 x 8 kv heads 9.3 / 10.6; without the spare places 64 pairs in clusters of 7 took
-  // 22.5 us instead of 13.2, and without the limit of two waves 1000 x 8 kv heads of up
-  // to 300 keys 83 instead of 70.
+  // 10.1 / 13.0, 100 x 8 kv heads of 300 to 700 keys 23.7 / 26.6, 48 x 8 of 800 to 1000
+  // 18.4 / 23.2, 56 x 8 of 1500 29.6 / 35.3, a window of 1024 on 64 x 8 38.5 / 42.5.
+  // Without the spare places 64 pairs in clusters of 7 took 22.5 us instead of 13.2, without
+  // the limit of two waves 1000 x 8 kv heads of up to 300 keys 83 instead of 70, and in
+  // waves that are 56 % full 64 x 8 of up to 1500 keys 38.5 instead of 34.1.
   // Warp mode, for more pairs than that of at most kPagedWarpTiles each: what the merge of
   // a CTA's warps costs a short pair is saved.  On / off, e4m3: 2000 x 8 kv heads of 30 to
   // 60 keys 55.6 / 113.8 us, 1000 x 8 of up to 300 keys, heads of 64, 45.7 / 70.3, 256 x 8
@@ -1202,7 +1204,8 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   if (pairs <= 2 * slots) {
     const int64_t c = std::max<int64_t>(
         1, std::min({int64_t(pkv::kPagedMaxCluster), slots * 7 / 8 / pairs, (tiles + 15) / 16}));
-    if ((tiles + c - 1) / c <= pkv::kPagedClusterTiles) {
+    const bool full = c == 1 && 3 * pairs >= 2 * ((pairs + slots - 1) / slots * slots);
+    if ((tiles + c - 1) / c <= (full ? 2 : 1) * pkv::kPagedClusterTiles) {
       p.mode = pkv::kPagedCluster;
       p.cluster = int(c);
       p.grid = int(pairs * c);

@@ -276,7 +276,7 @@ constexpr int kPagedPairCost = 12;
 constexpr int kPagedMinCost = 16;
 constexpr int kPagedMaxGrid = 512;
 constexpr int kPagedMaxCluster = 8;
-// Most tiles of a CTA in the cluster mode (bf16, a window of 1024 on 16 x 8 kv heads,
+// Most tiles of a CTA in the cluster mode, but for full waves (bf16, a window of 1024 on 16 x 8 kv heads,
 // 33 tiles each: 15.4 us in clusters, 17.2 without).
 constexpr int kPagedClusterTiles = 48;
 // Most tiles of a pair in the warp mode, in which one warp merges a pair's parts: 150 x 8
