@@ -438,7 +438,10 @@ PKV_API int pkv_mla_kv_append(const pkv_tensor* latent, const pkv_tensor* latent
  *   stream       cudaStream_t.
  * B <= 2048, and B * Hkv * (16-key tiles that a row of block_table, or the window
  * and first tokens, can span + 16) < 2^31 - 4096.  A small workspace (two partials of
- * at most 8.4 KB a CTA) makes the call run on fewer CTAs.
+ * at most 8.4 KB a CTA) makes the call run on fewer CTAs.  Few and short requests are
+ * fastest when the table is no wider than the longest one needs (a view of its first
+ * columns will do), as the launch is chosen by the width: four of 300 keys take 4.6 us,
+ * with a table for 65536 keys 6.4.
  * What masked keys hold (NaN, infinities, stale bytes) reaches no result.
  * Errors as pkv_paged_decode_attn; a bad block-table entry reads as a page of
  * zeros and raises bit 1, a seq_len beyond the table is clamped and raises bit

@@ -1193,12 +1193,6 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   // Without the spare places 64 pairs in clusters of 7 took 22.5 us instead of 13.2, without
   // the limit of two waves 1000 x 8 kv heads of up to 300 keys 83 instead of 70, and in
   // waves that are 56 % full 64 x 8 of up to 1500 keys 38.5 instead of 34.1.
-  // Warp mode, for more pairs than that of at most kPagedWarpTiles each: what the merge of
-  // a CTA's warps costs a short pair is saved.  On / off, e4m3: 2000 x 8 kv heads of 30 to
-  // 60 keys 55.6 / 113.8 us, 1000 x 8 of up to 300 keys, heads of 64, 45.7 / 70.3, 256 x 8
-  // of 10 to 700 keys 37.5 / 42.9, of 700 to 768 keys 68.8 / 71.3; a bf16 window of 128 on
-  // 512 x 8 kv heads 58.7 / 64.2.  With fewer pairs it loses: 64 requests of up to 32768
-  // keys 62.6 / 51.2.  Its partials are those of four times as many shares.
   const int64_t slots = int64_t(ws.num_sms) * shape.ctas_per_sm, pairs = B * Hkv;
   const int64_t part_bytes = int64_t(shape.part_floats) * 4;
   if (pairs <= 2 * slots) {
@@ -1206,20 +1200,17 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
         1, std::min({int64_t(pkv::kPagedMaxCluster), slots * 7 / 8 / pairs, (tiles + 15) / 16}));
     const bool full = c == 1 && 3 * pairs >= 2 * ((pairs + slots - 1) / slots * slots);
     if ((tiles + c - 1) / c <= (full ? 2 : 1) * pkv::kPagedClusterTiles) {
-      p.mode = pkv::kPagedCluster;
       p.cluster = int(c);
       p.grid = int(pairs * c);
     }
-  } else if (tiles <= pkv::kPagedWarpTiles &&
-             int64_t(ws.partial_bytes) >= 2 * pkv::kPagedWarps * p.grid * part_bytes) {
-    p.mode = pkv::kPagedWarp;
   }
-  if (p.mode == pkv::kPagedShares) {  // two partials for each CTA: a small workspace runs fewer of them
+  if (!p.cluster) {  // two partials for each CTA (each warp): a small workspace runs fewer of them
     const int64_t fit = int64_t(ws.partial_bytes) / (2 * part_bytes);
     if (fit < 1)
       return fail(PKV_ERR_WORKSPACE, "workspace holds %lld bytes of partials, %lld needed",
                   (long long)ws.partial_bytes, (long long)(2 * part_bytes));
     p.grid = int(std::min<int64_t>(p.grid, fit));
+    p.warps = fit >= pkv::kPagedWarps * p.grid;
   }
   p.partials = ws.partials;
   p.pair_counters = ws.counters;

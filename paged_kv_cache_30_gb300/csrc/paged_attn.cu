@@ -37,10 +37,12 @@
 //    merge the parts through distributed shared memory (a 1001-key window on 33 x 4 kv
 //    heads 10.1 us; 12.1 where the first CTA merged alone): no scan of the lengths, no
 //    global partials (see launch_paged_attn's caller for what it measured).
-//  * Warp mode, for many short requests (again the caller's rule): the shares are the
-//    warps', which write a pair that they hold whole from their accumulators, without a
-//    merge of warps or a barrier.  Of the warps that share a pair the last to arrive
-//    merges the accumulators that all have published, in order.
+//  * Without clusters the kernel chooses by the lengths that it reads.  Warp mode, for
+//    many short requests: the shares are the warps', which write a pair that they hold
+//    whole from their accumulators, without a merge of warps or a barrier; of the warps
+//    that share a pair the last to arrive merges the accumulators that all have
+//    published, in order.  Whole pairs, an equal number for each CTA, where that ends no
+//    later than equal shares with their merges.
 //  * Otherwise, a request cut between CTAs: each publishes its 32-bit (O, m, l, R); the last
 //    CTA of a group of up to kMergeGroup (an arrival counter) merges the group, the last
 //    group merges the groups: each warp a fourth of the parts in order, then the warps'
@@ -63,6 +65,11 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = kPagedWarps;
+enum : int {
+  kPagedShares,   // CTAs take equal shares of all tiles
+  kPagedCluster,  // a cluster of CTAs takes a (request, kv head) pair
+  kPagedWarp,     // warps take equal shares of all tiles
+};
 constexpr int kThreads = kWarps * 32;
 // One request of 131072 keys and one kv head: 17.6 us at 16, 18.3 at 12, 19.4 at 8; of 16000
 // keys and 8 kv heads: 15.2, 15.1, 14.8; 4 requests of up to 16000: 13.9, 13.2, 13.3.
@@ -71,6 +78,11 @@ constexpr int kPairCost = kPagedPairCost;
 // The same for a warp in the warp mode: 2000 requests of 1 to 64 keys take 14.1 us at
 // 2, 14.8 at 3; 1000 x 8 of up to 300 keys 47.4 at 2, 45.8 at 3, 47.9 at 5.
 constexpr int kWarpPairCost = 3;
+// What cuts inside pairs cost a CTA, in tiles: whole pairs (up to two a CTA) where the
+// longest ones end no later.  Tables as wide as for 65536 keys, on / off: 48 x 8 kv heads
+// of 800 to 1000 keys 20.6 / 23.3 us, 56 x 8 of 1500 31.6 / 35.5, 400 of 10 to 500 keys
+// 12.0 / 13.2; 110 x 8 of 10 to 1000, which the rule leaves, 33.1 / 28.0.
+constexpr uint32_t kEndCost = 24;
 // A cut this near a pair's border moves there.  Wider costs more than the merges it
 // saves: at 32, 33 requests of a 1001-key window took 16.9 us instead of 13.0.
 constexpr int kSnapTiles = 8;
@@ -507,95 +519,54 @@ __device__ __forceinline__ void warp_finalize(const PagedParams& p, int b, int k
   }
 }
 
+// The CTA's work, after the prologue below.  next: the pair in the cluster mode; whole:
+// equal numbers of pairs for the CTAs instead of equal shares of tiles.
 template <class C, int kMode>
-__global__ void __launch_bounds__(kThreads, C::kCtas)
-    paged_attn_kernel(const __grid_constant__ PagedParams p,
-                      const __grid_constant__ CUtensorMap kv_map) {
+__device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& kv_map,
+                                       uint8_t* base, uint32_t base_u32, Pair next, bool whole) {
   constexpr bool kCluster = kMode == kPagedCluster, kPerWarp = kMode == kPagedWarp;
   constexpr int D = C::D, NB = C::NB, U = C::U, kStages = C::kStages, E = D / 16;
   constexpr bool kFp8 = C::kFp8;
   constexpr int kCost = kPerWarp ? kWarpPairCost : kPairCost;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw), base_u32 = (raw + 1023u) & ~1023u;
-  uint8_t* base = smem_raw + (base_u32 - raw);
   float* wbuf = reinterpret_cast<float*>(base + C::kOffWb);
   int* misc = reinterpret_cast<int*>(base + C::kOffMisc);
-  int* prefix = reinterpret_cast<int*>(base + C::kOffPrefix);
+  const int* prefix = reinterpret_cast<const int*>(base + C::kOffPrefix);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = base_u32 + warp * kStages * C::kTileBytes;
   const uint32_t bars = base_u32 + C::kOffBars + warp * kStages * 8;
   const int B = p.B, Hkv = p.Hkv;
 
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
-    fence_barrier_init();
-  }
-  if (tid == 0) tma_prefetch_desc(&kv_map);
-  griddep_wait();  // nothing of the caller's is read before
-
-  // This CTA's tiles are [f0, f1) of all pairs' (of one pair's in the cluster mode).
+  // This CTA's tiles (the warp's in the warp mode) are [f0, f1) of all pairs' (of one
+  // pair's in the cluster mode).
   int f0, f1, chunk = 0, snap = 0;
-  Pair next = {};  // the pair after the current one
   const int part = kCluster ? (int)blockIdx.x % p.cluster : 0;
   if constexpr (kCluster) {
-    next.b = (int)blockIdx.x / p.cluster / Hkv;
-    next.kvh = (int)blockIdx.x / p.cluster % Hkv;
-    const int len = __ldg(p.seq_lens + next.b);
-    if (part == 0 && next.kvh == 0 && len > p.max_blocks * p.page_size)
-      atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
-    next.n = span_of(p, len).tiles;
     f0 = (int)((long long)next.n * part / p.cluster);
     f1 = (int)((long long)next.n * (part + 1) / p.cluster);
-    griddep_launch_dependents();
+  } else if (whole) {
+    auto place = [&](uint32_t cta) {  // of the first tile of its first pair
+      const int i = (int)((long long)B * Hkv * cta / gridDim.x), b = i / Hkv;
+      return b == B ? prefix[B] * Hkv
+                    : prefix[b] * Hkv + i % Hkv * (prefix[b + 1] - prefix[b]);
+    };
+    f0 = place(blockIdx.x);
+    f1 = place(blockIdx.x + 1);
   } else {
-    // ---- prefix[b]: tiles per kv head before request b ----
-    {
-      const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
-      int mine = 0;
-      for (int b = b0; b < min(b0 + per, B); ++b) {
-        const int len = __ldg(p.seq_lens + b);
-        if (blockIdx.x == 0 && len > p.max_blocks * p.page_size) atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
-        mine += span_of(p, len).tiles;
-      }
-      int run = block_scan(mine, misc);
-      for (int b = b0; b < min(b0 + per, B); ++b) {
-        prefix[b] = run;
-        run += span_of(p, __ldg(p.seq_lens + b)).tiles;
-        if (b == B - 1) prefix[B] = run;
-      }
-    }
-    __syncthreads();
-    griddep_launch_dependents();
-
-    // requests without a key
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-      if (prefix[b + 1] != prefix[b]) continue;
-      for (int i = tid; i < Hkv * p.G * (D / 8); i += kThreads) {
-        const int h = i / (D / 8);
-        *reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + (i % (D / 8)) * 8) =
-            make_uint4(0, 0, 0, 0);
-        if (i % (D / 8) == 0 && p.lse) p.lse[b * p.lse_sb + h * p.lse_sh] = -INFINITY;
-      }
-    }
-
-    // ---- this CTA's (or warp's) tiles ----
     // cuts are placed in the space of costs and turned into places of tiles
     const int tiles = prefix[B] * Hkv, total = tiles + kCost * B * Hkv;
     const uint32_t shares = kPerWarp ? gridDim.x * kWarps : gridDim.x;
     const uint32_t share = kPerWarp ? blockIdx.x * kWarps + warp : blockIdx.x;
     chunk = max((int)(((uint32_t)total + shares - 1) / shares), kPerWarp ? 1 : kPagedMinCost);
     snap = min(kPerWarp ? kWarpSnapTiles : kSnapTiles, chunk / 2);
-    {
-      // lanes 0..15 place this share's cut, lanes 16..31 the next one's
-      const long long x = ((long long)share + (lane >> 4)) * chunk;
-      const int y = (int)min(x, (long long)total - 1);
-      const Pair r = pair_at_group<kCost, 16>(prefix, B, Hkv, y);
-      const int at = y - r.begin - kCost;  // the pair's tiles before the cut
-      int f = prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
-      if (x >= total) f = tiles;
-      f0 = __shfl_sync(0xffffffffu, f, 0);
-      f1 = __shfl_sync(0xffffffffu, f, 16);
-    }
+    // lanes 0..15 place this share's cut, lanes 16..31 the next one's
+    const long long x = ((long long)share + (lane >> 4)) * chunk;
+    const int y = (int)min(x, (long long)total - 1);
+    const Pair r = pair_at_group<kCost, 16>(prefix, B, Hkv, y);
+    const int at = y - r.begin - kCost;  // the pair's tiles before the cut
+    int f = prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
+    if (x >= total) f = tiles;
+    f0 = __shfl_sync(0xffffffffu, f, 0);
+    f1 = __shfl_sync(0xffffffffu, f, 16);
   }
   // this warp's n-th tile is at place w0 + kStep n
   constexpr int kStep = kPerWarp ? 1 : kWarps;
@@ -1157,12 +1128,99 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
   }
 }
 
-template <class C, int kMode>
+template <class C, bool kCluster>
+__global__ void __launch_bounds__(kThreads, C::kCtas)
+    paged_attn_kernel(const __grid_constant__ PagedParams p,
+                      const __grid_constant__ CUtensorMap kv_map) {
+  constexpr int D = C::D;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base_u32 = (raw + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_u32 - raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = p.B, Hkv = p.Hkv;
+
+  if (lane == 0) {
+    const uint32_t bars = base_u32 + C::kOffBars + warp * C::kStages * 8;
+    for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8 * s, 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) tma_prefetch_desc(&kv_map);
+  griddep_wait();  // nothing of the caller's is read before
+
+  if constexpr (kCluster) {
+    Pair pair = {};
+    pair.b = (int)blockIdx.x / p.cluster / Hkv;
+    pair.kvh = (int)blockIdx.x / p.cluster % Hkv;
+    const int len = __ldg(p.seq_lens + pair.b);
+    if (blockIdx.x % p.cluster == 0 && pair.kvh == 0 && len > p.max_blocks * p.page_size)
+      atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
+    pair.n = span_of(p, len).tiles;
+    griddep_launch_dependents();
+    attend<C, kPagedCluster>(p, kv_map, base, base_u32, pair, false);
+  } else {
+    int* misc = reinterpret_cast<int*>(base + C::kOffMisc);
+    int* prefix = reinterpret_cast<int*>(base + C::kOffPrefix);
+    // ---- prefix[b]: tiles per kv head before request b; the most of a request ----
+    int most = 0;
+    {
+      const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
+      int mine = 0;
+      for (int b = b0; b < min(b0 + per, B); ++b) {
+        const int len = __ldg(p.seq_lens + b);
+        if (blockIdx.x == 0 && len > p.max_blocks * p.page_size) atomicOr(p.err, DEVERR_SEQ_TOO_LONG);
+        const int tiles = span_of(p, len).tiles;
+        mine += tiles;
+        most = max(most, tiles);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) misc[kWarps + warp] = most;
+      int run = block_scan(mine, misc);
+      for (int b = b0; b < min(b0 + per, B); ++b) {
+        prefix[b] = run;
+        run += span_of(p, __ldg(p.seq_lens + b)).tiles;
+        if (b == B - 1) prefix[B] = run;
+      }
+    }
+    __syncthreads();
+    griddep_launch_dependents();
+
+    // requests without a key
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+      if (prefix[b + 1] != prefix[b]) continue;
+      for (int i = tid; i < Hkv * p.G * (D / 8); i += kThreads) {
+        const int h = i / (D / 8);
+        *reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + (i % (D / 8)) * 8) =
+            make_uint4(0, 0, 0, 0);
+        if (i % (D / 8) == 0 && p.lse) p.lse[b * p.lse_sb + h * p.lse_sh] = -INFINITY;
+      }
+    }
+
+    // ---- how the work is cut, by what the lengths turn out to be ----
+    // Whole pairs save a CTA the merges at its two ends, which cost about kEndCost.
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) most = max(most, misc[kWarps + w]);
+    const uint32_t pairs = B * Hkv, waves = (pairs + gridDim.x - 1) / gridDim.x;
+    // Warp mode: what the merge of a CTA's warps costs a short pair is saved, where there
+    // are pairs enough for the warps.  On / off, e4m3: 2000 x 8 kv heads of 30 to 60 keys
+    // 55.6 / 113.8 us, 1000 x 8 of up to 300 keys, heads of 64, 45.7 / 70.3, 256 x 8 of 10
+    // to 700 keys 38.5 / 42.9, of 700 to 768 keys 69.3 / 71.3; a bf16 window of 128 on
+    // 512 x 8 kv heads 58.7 / 64.2.  64 x 8 of up to 32768 keys lose, 62.6 / 51.2.
+    if (p.warps && waves > 2 && most <= kPagedWarpTiles) {
+      attend<C, kPagedWarp>(p, kv_map, base, base_u32, Pair{}, false);
+    } else {
+      const uint32_t share = max(((uint32_t)prefix[B] * Hkv + kPairCost * pairs) / gridDim.x,
+                                 (uint32_t)kPagedMinCost);
+      attend<C, kPagedShares>(p, kv_map, base, base_u32, Pair{},
+                              waves <= 2 && waves * (most + kPairCost) <= share + kEndCost);
+    }
+  }
+}
+
+template <class C, bool kCluster>
 cudaError_t launch_mode(const PagedParams& p, const CUtensorMap& map, cudaStream_t stream) {
-  constexpr bool kCluster = kMode == kPagedCluster;
   static std::atomic<uint64_t> done{0};
   cudaError_t e =
-      set_smem_attr_once(paged_attn_kernel<C, kMode>, C::smem_bytes(kPagedMaxBatch), done);
+      set_smem_attr_once(paged_attn_kernel<C, kCluster>, C::smem_bytes(kPagedMaxBatch), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
@@ -1177,14 +1235,12 @@ cudaError_t launch_mode(const PagedParams& p, const CUtensorMap& map, cudaStream
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kCluster && p.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<C, kMode>, p, map);
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<C, kCluster>, p, map);
 }
 
 template <class C>
 cudaError_t launch_t(const PagedParams& p, const CUtensorMap& map, cudaStream_t stream) {
-  return p.mode == kPagedCluster ? launch_mode<C, kPagedCluster>(p, map, stream)
-         : p.mode == kPagedWarp ? launch_mode<C, kPagedWarp>(p, map, stream)
-                                 : launch_mode<C, kPagedShares>(p, map, stream);
+  return p.cluster ? launch_mode<C, true>(p, map, stream) : launch_mode<C, false>(p, map, stream);
 }
 
 template <typename F>

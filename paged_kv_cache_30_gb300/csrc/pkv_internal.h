@@ -223,11 +223,6 @@ cudaError_t launch_wait_selftest(int* err, cudaStream_t stream);
 cudaError_t launch_mla_kv_append(const AppendParams& p, cudaStream_t stream);
 
 // ----------------------------------- decode with a window and first tokens --
-enum : int {
-  kPagedShares = 0,   // CTAs take equal shares of all tiles
-  kPagedCluster = 1,  // a cluster of CTAs for each (request, kv head) pair
-  kPagedWarp = 2,     // warps take equal shares of all tiles
-};
 constexpr int kPagedWarps = 4;      // of a CTA
 constexpr int kPagedMaxGroup = 16;  // query heads per kv head
 constexpr int kPagedMaxBatch = 2048;
@@ -254,8 +249,8 @@ struct PagedParams {
   float scale;
   int page_shift;                // log2(page_size)
   int grid;
-  int mode;                      // kPagedShares, kPagedCluster, kPagedWarp
-  int cluster;                   // cluster mode: CTAs for each pair
+  int cluster;                   // > 0: cluster mode, this many CTAs for each pair
+  bool warps;                    // there are partials for shares of warps
   float* partials;               // two slots for each CTA (each warp in the warp mode)
   int* slot_counters;            // [2 * grid] arrival counters of merge groups
   int* pair_counters;            // [B * Hkv] arrival counters of the groups (of the warps)

@@ -175,6 +175,19 @@ def test_head_layouts_of_many_requests(fp8, D, G, P):
 
 
 @pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("D,G", [(128, 8), (64, 12)])
+@pytest.mark.parametrize("lens,Hkv", [
+    (MANY, 3),                                                     # more than two waves
+    ([180 + i % 21 for i in range(300)], 1),                       # whole pairs, one a block
+    ([180 + i % 21 if i % 50 else 0 for i in range(300)], 2),      # two a block, some of no key
+    ([3000] + [200] * 299, 1)])                                    # one that is cut
+def test_tables_wider_than_the_lengths(fp8, D, G, lens, Hkv):
+    """The lengths, not the width of the table, choose how the work is cut."""
+    pr = problem(28, lens, Hkv, G, D, 16, fp8, sinks=True, wide=True)
+    check(pr, *run(pr))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
 @pytest.mark.parametrize("D,G", [(128, 8), (64, 16)])
 def test_long_requests_among_many_of_one_key(fp8, D, G):
     """The long ones are cut into dozens of parts, which one warp merges."""
