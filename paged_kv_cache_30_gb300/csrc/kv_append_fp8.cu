@@ -12,17 +12,17 @@
 // but for codes that leave e4m3's normal range (below 2^-6 of the new scale).
 //
 // Bound by memory for prompts (bf16 read once, codes written once), by latency
-// for single tokens.  A team of warps (1, 2 or 4, so that a page's rows are about
-// 16 loads a lane) takes one kv head of `slab` consecutive rows (1 when there are
+// for single tokens.  A team of warps (1, 2 or 4, so that a page's rows are 16 to
+// 32 loads a lane) takes one kv head of `slab` consecutive rows (1 when there are
 // few, a page's when there are many): it finds the first row's request with a
 // 32-way search of cu_tokens and walks the pages that begin in its rows, loading
-// the rows of a page to shared memory at once (up to 16 16-byte copies a lane)
+// the rows of a page to shared memory at once (up to 32 16-byte copies a lane)
 // before it reduces, and encoding them from there.
 //
-// Measured (GB300, 8 kv heads of 128, graph replays): 64 single tokens 2.8 us, 1024
-// of them 7.7 us; 12.5 k tokens of ragged prompts (77 MB) 16.6 us = 4.6 TB/s, 32 k
-// tokens 32.3 us = 6.2 TB/s (92 % of the measured copy bandwidth; pages of 32 and 128
-// tokens 79 and 81 %).  What is left is the chain of dependent reads that a warp
+// Measured (GB300, 8 kv heads of 128, graph replays): 64 single tokens 2.9 us, 1024
+// of them 7.6 us; 12.5 k tokens of ragged prompts (77 MB) 16.3 us = 4.7 TB/s, 32 k
+// tokens 31.6 us = 6.4 TB/s (94 % of the measured copy bandwidth; pages of 32 and 128
+// tokens 88 and 82 %).  What is left is the chain of dependent reads that a warp
 // begins with (request, length, page, rows): about 4 us, hidden only by other warps.
 #include <algorithm>
 
@@ -32,10 +32,16 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 4;
-// Single rows a warp until there are this many (one prompt of 16000 tokens: 15.6 us,
-// 17.4 at 16384; ragged prompts of 12.5 k tokens: 17.1 and 16.1).
-constexpr int kFullWarps = 8192;
+constexpr int kWarps = 4;  // of a CTA at most
+// Single warps with more than this many rows of a page are CTAs of their own, so that a
+// place is free again when one warp is done (16 k tokens, pages of 32, heads of 128: 14.6
+// us, 15.9 in CTAs of two, 17.5 of four); with fewer the launch of so many CTAs costs more
+// (1024 single tokens, 8 kv heads: 8.4 us, 7.7 in CTAs of four).
+constexpr int kAlone = 8;
+// Single rows a warp until there are this many.  16 requests of up to 2000 tokens, 2 kv
+// heads: 6.6 us, 8.2 at 4096 and 8.9 at 8192 (pages of 32, heads of 128); 100 of up to 160,
+// 4 kv heads, pages of 128: 9.9 us, 12.2 at 2048.
+constexpr int kFullWarps = 3200;
 constexpr int kMaxHeld = 32;
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
 
@@ -145,7 +151,8 @@ __device__ __forceinline__ void cp_async_wait_all() {
 // RPW = 32 / (2D/8) rows at once, a team of kTeam warps kTeam times as many.  `hold`
 // keeps the first `held` 16-byte units of each lane in shared memory
 // (hold[32 i + lane] is read by the lane that asked for it); later ones are read
-// twice.  exchange: 2 x 2 floats per warp, turn: pages of the team so far.  False: the page is not in the cache.
+// twice.  exchange: 2 x 2 floats per warp, turn: pages of the team so far.  False: the
+// page is not in the cache.
 template <int D, int kTeam>
 __device__ __forceinline__ bool append_page(const AppendFp8Params& p, int h, long long r, int n,
                                             int blk, int slot0, uint4* hold, int held,
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32, 7)
   __shared__ float exchange[2 * 2 * kWarps];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, P = p.page_size;
-  const long long team = ((long long)blockIdx.x * kWarps + warp) / kTeam;
+  const long long team = ((long long)blockIdx.x * (blockDim.x >> 5) + warp) / kTeam;
   const int h = (int)(team % p.Hkv);
   long long r = team / p.Hkv * slab;
   const long long end = min(r + slab, (long long)p.T);
@@ -315,9 +322,10 @@ static cudaError_t launch_t(const AppendFp8Params& p, int most, cudaStream_t str
   const int rows = 32 / (2 * D / 8) * kTeam;
   const int held = std::min((most + rows - 1) / rows, kMaxHeld);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((warps + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = kWarps * 32 * 16 * held;
+  const int cta = kTeam == 1 && most > kAlone ? 1 : kWarps;
+  cfg.gridDim = dim3((unsigned)((warps + cta - 1) / cta));
+  cfg.blockDim = dim3(cta * 32);
+  cfg.dynamicSmemBytes = cta * 32 * 16 * held;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -328,16 +336,14 @@ static cudaError_t launch_t(const AppendFp8Params& p, int most, cudaStream_t str
 }
 
 cudaError_t launch_gqa_kv_append_fp8(const AppendFp8Params& p, cudaStream_t stream) {
-  // rows that a page receives on average, and a team for about 16 loads a lane of them
-  // (32 for 128 rows of 2 x 128)
+  // rows that a page receives on average, and a team for 16 to 32 loads a lane of them
+  // (two warps for 32 rows of 2 x 128 took 18.1 us for 16 k tokens, one takes 14.6)
   const int most = (int)std::min<int64_t>(p.page_size, (p.T + p.B - 1) / p.B);
   if (p.D == 64)
     return most <= 32   ? launch_t<64, 1>(p, most, stream)
            : most <= 64 ? launch_t<64, 2>(p, most, stream)
                         : launch_t<64, 4>(p, most, stream);
-  return most <= 16   ? launch_t<128, 1>(p, most, stream)
-         : most <= 32 ? launch_t<128, 2>(p, most, stream)
-                      : launch_t<128, 4>(p, most, stream);
+  return most <= 32 ? launch_t<128, 1>(p, most, stream) : launch_t<128, 4>(p, most, stream);
 }
 
 }  // namespace pkv
