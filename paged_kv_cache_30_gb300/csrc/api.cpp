@@ -1178,10 +1178,10 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
     return fail(PKV_ERR_UNSUPPORTED, "%lld requests x %lld kv heads of up to %lld tiles of 16 keys",
                 (long long)B, (long long)Hkv, (long long)tiles);
   const pkv::Workspace& ws = st->ws;
-  const int64_t cost = B * Hkv * (tiles + pkv::kPagedPairCost);
+  const int64_t slots = int64_t(ws.num_sms) * shape.ctas_per_sm, pairs = B * Hkv;
+  const int64_t cost = pairs * (tiles + pkv::kPagedPairCost);
   p.grid = int(std::max<int64_t>(
-      1, std::min<int64_t>(std::min(ws.num_sms * shape.ctas_per_sm, pkv::kPagedMaxGrid),
-                           (cost + pkv::kPagedMinCost - 1) / pkv::kPagedMinCost)));
+      1, std::min<int64_t>(slots, (cost + pkv::kPagedMinCost - 1) / pkv::kPagedMinCost)));
   // Cluster mode: every pair has CTAs of its own, about 16 tiles each and none more than
   // kPagedClusterTiles, or twice that for one CTA a pair in waves that are two thirds full;
   // one CTA each for up to two waves of pairs, clusters where they leave an eighth of the
@@ -1193,7 +1193,6 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   // Without the spare places 64 pairs in clusters of 7 took 22.5 us instead of 13.2, without
   // the limit of two waves 1000 x 8 kv heads of up to 300 keys 83 instead of 70, and in
   // waves that are 56 % full 64 x 8 of up to 1500 keys 38.5 instead of 34.1.
-  const int64_t slots = int64_t(ws.num_sms) * shape.ctas_per_sm, pairs = B * Hkv;
   const int64_t part_bytes = int64_t(shape.part_floats) * 4;
   if (pairs <= 2 * slots) {
     const int64_t c = std::max<int64_t>(

@@ -269,7 +269,6 @@ cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& kv_map, c
 // log-uniform lengths, e4m3: 84.2 us at a cost of 4, 53.9 at 8, 52.6 at 12, 52.8 at 16.
 constexpr int kPagedPairCost = 12;
 constexpr int kPagedMinCost = 16;
-constexpr int kPagedMaxGrid = 512;
 constexpr int kPagedMaxCluster = 8;
 // Most tiles of a CTA in the cluster mode, but for full waves (bf16, a window of 1024 on 16 x 8 kv heads,
 // 33 tiles each: 15.4 us in clusters, 17.2 without).
