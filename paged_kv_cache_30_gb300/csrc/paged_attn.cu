@@ -27,9 +27,9 @@
 //    and values become fp16 exactly; the query is scaled to fp16's range by a
 //    power of two for each row (exact but for elements below 2^-29 of the row's
 //    largest).
-//  * One pass with a running reference m near the maximum and the sum l in 32 bits.  With scales, the
-//    accumulator holds sum_j 2^(x_j + log2 vs_j - R) code_j under a running
-//    maximum R of its own, so a page of large or small values keeps its
+//  * One pass with a running reference m near the maximum and the sum l in 32 bits.
+//    With scales, the accumulator holds sum_j 2^(x_j + log2 vs_j - R) code_j under a
+//    running maximum R of its own, so a page of large or small values keeps its
 //    precision: the weights are rounded to fp16 (11 bits) relative to the largest
 //    contribution; for the bf16 cache they are rounded to bf16, as V is bf16.
 //  * Cluster mode, for few and short requests (the rule is the caller's): a cluster of
@@ -51,12 +51,12 @@
 //
 // Measured (GB300, graph replays; the copy bandwidth is 6786 GB/s): e4m3, 8 requests
 // of 131072 keys, 8 kv heads of 128: 316 us = 6.81 TB/s; 64 requests of up to 32768
-// keys (272 MB): 49.8 us = 5.5 TB/s, of which 4 us pass before the first tile arrives
+// keys (272 MB): 50.1 us = 5.4 TB/s, of which 4 us pass before the first tile arrives
 // (lengths, table, tile: three dependent reads) and the CTAs end over the last 10;
 // bf16, a window of 4096 + 64 on 32 requests: 83 us = 6.4 TB/s; four short requests:
 // 4.5 us.  1 GB of e4m3 heads of 128 reads at 97 % (up to 8 query heads per kv head)
-// and 93 % (16), of 64 at 91 and 79 % (bound by instructions: 12 warps an SM, 2.1
-// instructions a cycle); bf16 at 95 to 99 %.  A tile's way through a warp is about
+// and 93 % (16), of 64 at 92 and 79 % (bound by instructions: 12 warps an SM, 2.1
+// instructions a cycle); bf16 at 96 to 99 %.  A tile's way through a warp is about
 // 700 (bf16) to 1200 (e4m3) cycles, of which the 16 products of S take 150 to 250.
 #include "pkv_internal.h"
 #include "ptx.cuh"
