@@ -23,15 +23,20 @@
 //    across the borders of requests.  Block-table entries (and scales) are read
 //    32 tiles ahead, one lane each.
 //  * S[rows x 16 tokens] = Q K^T and O^T[dims x rows] += V^T P^T on
-//    mma.m16n8k16, rows = the G query heads (one or two blocks of 8).  e4m3 keys
-//    and values become fp16 exactly; the query is scaled to fp16's range by a
-//    power of two for each row (exact but for elements below 2^-29 of the row's
-//    largest).
+//    mma.m16n8k16, rows = the G query heads (one or two blocks of 8); the second
+//    on mma.m16n8k8 in tf32 for e4m3.  e4m3 keys become fp16 and values tf32
+//    exactly; the query is scaled to fp16's range by a power of two for each row
+//    (exact but for elements below 2^-29 of the row's largest).
 //  * One pass with a running reference m near the maximum and the sum l in 32 bits.
 //    With scales, the accumulator holds sum_j 2^(x_j + log2 vs_j - R) code_j under a
 //    running maximum R of its own, so a page of large or small values keeps its
-//    precision: the weights are rounded to fp16 (11 bits) relative to the largest
-//    contribution; for the bf16 cache they are rounded to bf16, as V is bf16.
+//    precision.  Each weight is rounded once, to tf32: by 2^-11 of itself, down to 2^-126
+//    of the largest.  The largest may be a first token's, or of a page with large
+//    values, and have next to nothing to add, so the others need their bits however small
+//    they are beside it.  fp16 weights lose them below 2^-14 and all below 2^-25 of it (16
+//    nats under a first token without a value, 6000 keys were off by half); they take
+//    1 to 2 % less time for heads of 128, 10 to 15 % less for heads of 64 and for 16 rows.
+//    For the bf16 cache the weights are rounded to bf16, as V is bf16.
 //  * Cluster mode, for few and short requests (the rule is the caller's): a cluster of
 //    CTAs takes one pair each, a CTA an equal part of its tiles, and the threads of all
 //    merge the parts through distributed shared memory (a 1001-key window on 33 x 4 kv
@@ -50,13 +55,13 @@
 //    for one request of 16000 keys).  Results do not depend on timing.
 //
 // Measured (GB300, graph replays; the copy bandwidth is 6786 GB/s): e4m3, 8 requests
-// of 131072 keys, 8 kv heads of 128: 316 us = 6.81 TB/s; 64 requests of up to 32768
-// keys (272 MB): 50.1 us = 5.4 TB/s, of which 4 us pass before the first tile arrives
+// of 131072 keys, 8 kv heads of 128: 314 us = 6.85 TB/s; 64 requests of up to 32768
+// keys (272 MB): 51.4 us = 5.3 TB/s, of which 4 us pass before the first tile arrives
 // (lengths, table, tile: three dependent reads) and the CTAs end over the last 10;
 // bf16, a window of 4096 + 64 on 32 requests: 83 us = 6.4 TB/s; four short requests:
-// 4.5 us.  1 GB of e4m3 heads of 128 reads at 97 % (up to 8 query heads per kv head)
-// and 93 % (16), of 64 at 92 and 79 % (bound by instructions: 12 warps an SM, 2.1
-// instructions a cycle); bf16 at 96 to 99 %.  A tile's way through a warp is about
+// 5.0 us.  1 GB of e4m3 heads of 128 reads at 96 % (up to 8 query heads per kv head)
+// and 80 % (16), of 64 at 83 and 68 % (bound by instructions and, more than with fp16
+// weights, by the matrix pipe); bf16 at 96 to 99 %.  A tile's way through a warp is about
 // 700 (bf16) to 1200 (e4m3) cycles, of which the 16 products of S take 150 to 250.
 #include "pkv_internal.h"
 #include "ptx.cuh"
@@ -97,8 +102,8 @@ struct Cfg {
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kRows = 8 * NB;
   // tiles of a step: two of 2 KB share a step's waits and checks (1 GB of e4m3 heads of
-  // 64: 88 % of the copy bandwidth, 85 % with one; 16 heads per kv head 72 and 66 %)
-  static constexpr int U = D == 64 && kFp8 ? 2 : 1;
+  // 64: 178 us, 185 with one), but for 16 rows (222 us, 216 with one)
+  static constexpr int U = D == 64 && kFp8 && NB == 1 ? 2 : 1;
   static constexpr int kChunks = 2 * D * (kFp8 ? 1 : 2) / 128;  // 128-byte pieces of a [K | V] row
   static constexpr int kTileBytes = 16 * 128 * kChunks;
   // CTAs per SM, as many as the registers of the loop allow without spilling (four for
@@ -277,6 +282,28 @@ __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, ui
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// D += A B over 8 tokens in tf32: 11 significant bits and the exponents of 32-bit values.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)),
+        "r"(__float_as_uint(a3)), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float x) {  // to nearest
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_f32(uint32_t w) {
+  float2 f;
+  asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}"
+      : "=f"(f.x), "=f"(f.y) : "r"(w));
+  return f;
 }
 
 // This thread's part of the output: row er (a query head of the kv head), dims
@@ -904,7 +931,7 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
           }
         }
       }
-      uint32_t pb[NB][U][2];
+      uint32_t pb[NB][U][kFp8 ? 4 : 2];  // tf32; bf16 pairs
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -916,8 +943,8 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
           l[nb] += (e[0] + e[1]) + (e[2] + e[3]);
           if constexpr (kFp8) {
             const float d = lv[u] - R_ref[nb];
-            pb[nb][u][0] = pack_f16(ex2(y[0] + d), ex2(y[1] + d));
-            pb[nb][u][1] = pack_f16(ex2(y[2] + d), ex2(y[3] + d));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pb[nb][u][i] = to_tf32(ex2(y[i] + d));
           } else {
             pb[nb][u][0] = pack_bf16(e[0], e[1]);
             pb[nb][u][1] = pack_bf16(e[2], e[3]);
@@ -925,25 +952,33 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
         }
 
       // ---- O^T += V^T P^T ----
+      if constexpr (kFp8) {
+        // A register of codes holds (token 2t: dims 2g, 2g + 1; token 2t + 1: the same), the
+        // next one tokens 2t + 8 and 2t + 9: as k = t and t + 4 of two products, which are
+        // E apart as the second adds to the first.
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int c = 0; c < E; ++c) {
-          uint32_t a0, a1, a2, a3;
-          if constexpr (kFp8) {
-            // a register holds (token 2t: dims 2g, 2g + 1; token 2t + 1: the same)
-            const uint32_t lo = vf[u][c / 2][2 * (c & 1)], hi = vf[u][c / 2][2 * (c & 1) + 1];
-            const uint32_t lp = __byte_perm(lo, 0, 0x3120), hp = __byte_perm(hi, 0, 0x3120);
-            a0 = e4m3x2_f16(lp); a1 = e4m3x2_f16_hi(lp);
-            a2 = e4m3x2_f16(hp); a3 = e4m3x2_f16_hi(hp);
-          } else {
-            // units 2c and 2c + 1 of V: dims 16c + g and 16c + 8 + g
-            a0 = vf[u][c][0]; a1 = vf[u][c][2]; a2 = vf[u][c][1]; a3 = vf[u][c][3];
-          }
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma<kFp8>(acc[nb][c], a0, a1, a2, a3, pb[nb][u][0], pb[nb][u][1]);
-        }
+            for (int c = 0; c < E; ++c) {
+              const uint32_t w = __byte_perm(vf[u][c / 2][2 * (c & 1) + h], 0, 0x3120);
+              const float2 r0 = f16x2_f32(e4m3x2_f16(w)), r1 = f16x2_f32(e4m3x2_f16_hi(w));
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma_tf32(acc[nb][c], r0.x, r1.x, r0.y, r1.y, pb[nb][u][2 * h], pb[nb][u][2 * h + 1]);
+            }
+      } else {
+        // units 2c and 2c + 1 of V: dims 16c + g and 16c + 8 + g
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int c = 0; c < E; ++c)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma<false>(acc[nb][c], vf[u][c][0], vf[u][c][2], vf[u][c][1], vf[u][c][3],
+                         pb[nb][u][0], pb[nb][u][1]);
+      }
     }
 
 #pragma unroll
