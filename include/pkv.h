@@ -79,7 +79,8 @@
  *    pkv_paged_decode_attn_fp8 and pkv_paged_window_attn read nothing before
  *    the wait.  The pkv_pages_* calls write tables, lengths and pages: the first
  *    attention call after one on its stream waits for it to end (the library
- *    puts a 4-byte memset between them), so no care is needed there.
+ *    puts a 4-byte memset between them, in streams and in captures
+ *    apart), so no care is needed there.
  *  - The launch shape depends only on the device and the batch size, never on
  *    the sequence lengths or the block table, which the kernels read on the
  *    device: a captured graph stays valid when seq_lens and block_table change.

@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
 SOURCES = ["api.cpp", "gqa_decode.cu", "gqa_noalloc.cu", "mla_verify.cu", "mla_verify_native.cu",
            "mla_verify_pair.cu", "kv_append.cu", "paged_attn.cu", "kv_append_fp8.cu", "pages.cu"]
-HEADERS = ["pkv_internal.h", "ptx.cuh", "tcgen05.cuh", "mla_common.cuh"]
+HEADERS = ["pkv_internal.h", "page_order.h", "ptx.cuh", "tcgen05.cuh", "mla_common.cuh"]
 PYCALL = os.path.join(BUILD, "_pkvcall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",

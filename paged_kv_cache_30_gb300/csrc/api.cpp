@@ -16,8 +16,8 @@
 #include <initializer_list>
 #include <string>
 #include <utility>
-#include <vector>
 
+#include "page_order.h"
 #include "pkv_internal.h"
 
 namespace {
@@ -48,14 +48,13 @@ struct DeviceState {
   cudaEvent_t order_event = nullptr;
   cudaStream_t last_stream = nullptr;
   bool has_last = false;
-  // Streams whose last call of the library may have written block tables,
-  // lengths or whole pages (the page calls): kernels that read those before
-  // their dependency wait need the call to have ended (settle_pages).
-  std::vector<cudaStream_t> pages_written;
+  pkv::PageOrder pages;  // under g_pages_mu
 };
 
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
+// Held while a page call or an attention call goes into a stream of the device.
+std::mutex g_pages_mu[kMaxDevices];
 
 // ------------------------------------------------------------ workspace --
 int init_locked(int device, size_t partial_bytes) {
@@ -136,38 +135,35 @@ int order_streams(DeviceState* st, cudaStream_t stream, bool capturing) {
   return PKV_OK;
 }
 
-// Remembers that `stream`'s last kernel wrote tables, lengths or pages.
-int note_pages_written(DeviceState* st, cudaStream_t stream) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  for (cudaStream_t s : st->pages_written)
-    if (s == stream) return PKV_OK;
-  try {
-    st->pages_written.push_back(stream);
-  } catch (...) {
-    return fail(PKV_ERR_INVALID_ARG, "host allocation failed");
-  }
+// The id of the capture that `stream` is in, 0 for none.
+int capture_of(cudaStream_t stream, bool capturing, unsigned long long* id) {
+  *id = 0;
+  if (!capturing) return PKV_OK;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamGetCaptureInfo(stream, &cs, id);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetCaptureInfo");
+  if (cs != cudaStreamCaptureStatusActive) *id = 0;
   return PKV_OK;
 }
 
-// Whether it did, once.
-bool take_pages_written(DeviceState* st, cudaStream_t stream) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  for (size_t i = 0; i < st->pages_written.size(); ++i)
-    if (st->pages_written[i] == stream) {
-      st->pages_written.erase(st->pages_written.begin() + i);
-      return true;
-    }
-  return false;
-}
-
-// Before a kernel that reads tables, lengths or pages ahead of its dependency
-// wait: if a page call came before on the stream, a memset of an unused (zero)
-// scheduler word between the two.  Programmatic dependence holds between
-// neighbouring kernels alone, so the kernel then starts after the page call ended.
-int settle_pages(DeviceState* st, cudaStream_t stream) {
-  if (!take_pages_written(st, stream)) return PKV_OK;
+// What makes the next kernel of `stream` start after the one before it has ended: a memset of
+// an unused (zero) scheduler word.
+int order_after_pages(DeviceState* st, cudaStream_t stream) {
   const cudaError_t e = cudaMemsetAsync(st->ws.sched + 48, 0, sizeof(int), stream);
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "ordering after a page call");
+}
+
+// An attention call's way into its stream, behind any page call there: `early` for kernels
+// that read tables, lengths or pages ahead of their dependency wait.  *lock is held until the
+// launch is in.
+int settle_pages(DeviceState* st, int device, cudaStream_t stream, bool capturing, bool early,
+                 std::unique_lock<std::mutex>* lock) {
+  unsigned long long capture = 0;
+  const int rc = capture_of(stream, capturing, &capture);
+  if (rc != PKV_OK) return rc;
+  *lock = std::unique_lock<std::mutex>(g_pages_mu[device]);
+  const bool need = st->pages.settle(stream, capture);
+  return early && need ? order_after_pages(st, stream) : PKV_OK;
 }
 
 // ------------------------------------------------------------ validation --
@@ -591,7 +587,8 @@ PKV_API int pkv_paged_decode_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
   p.sched = ws.sched;
   p.err = ws.err;
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  if ((rc = settle_pages(st, stream))) return rc;
+  std::unique_lock<std::mutex> lock;
+  if ((rc = settle_pages(st, call.device, stream, capturing, true, &lock))) return rc;
   const cudaError_t e = pkv::launch_gqa_decode(p, call.map, page_size, shape.grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gqa decode launch");
   return PKV_OK;
@@ -830,7 +827,8 @@ static int mla_verify_impl(const pkv_tensor* q, const pkv_tensor* q8, const pkv_
            units * cap;
   p.err = ws.err;
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  if ((rc = settle_pages(st, stream))) return rc;
+  std::unique_lock<std::mutex> lock;
+  if ((rc = settle_pages(st, dev, stream, capturing, true, &lock))) return rc;
   const cudaError_t e =
       native ? pkv::launch_mla_verify_native(p, kv_map, int(units * cap), stream)
       : pair ? pkv::launch_mla_verify_pair(p, q_map, kv_map, v_map, int(units * cap), stream)
@@ -1236,7 +1234,8 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
                   (int)cr);
   }
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  take_pages_written(st, stream);
+  std::unique_lock<std::mutex> lock;
+  if ((rc = settle_pages(st, dev, stream, capturing, false, &lock))) return rc;
   const cudaError_t e = pkv::launch_paged_attn(p, map, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return PKV_OK;
@@ -1377,20 +1376,35 @@ static int check_list(const pkv_tensor* t, const char* name, int64_t n) {
   return PKV_OK;
 }
 
-// Device, workspace and `ints` of scratch of a page call.
-static int page_call(const pkv_tensor* first, const char* name, int64_t ints, cudaStream_t stream,
-                     DeviceState** st, int** scratch) {
-  int rc, dev = 0;
-  bool capturing = false;
-  if ((rc = device_of(first, name, stream, &dev))) return rc;
-  if ((rc = workspace_for(dev, stream, st, &capturing))) return rc;
-  if (ints * 4 > int64_t((*st)->ws.partial_bytes))
-    return fail(PKV_ERR_WORKSPACE, "workspace holds %lld ints, %lld needed",
-                (long long)((*st)->ws.partial_bytes / 4), (long long)ints);
-  *scratch = reinterpret_cast<int*>((*st)->ws.partials);
-  if ((rc = order_streams(*st, stream, capturing))) return rc;
-  return note_pages_written(*st, stream);
-}
+// A page call on its way into the stream: device, workspace and `ints` of scratch.
+struct PageCall {
+  cudaStream_t stream;
+  DeviceState* st = nullptr;
+  int* scratch = nullptr;
+  unsigned long long capture = 0;
+  std::unique_lock<std::mutex> lock;  // until the call's kernels are in the stream and noted
+
+  int begin(const pkv_tensor* first, const char* name, int64_t ints) {
+    int rc, dev = 0;
+    bool capturing = false;
+    if ((rc = device_of(first, name, stream, &dev))) return rc;
+    if ((rc = workspace_for(dev, stream, &st, &capturing))) return rc;
+    if (ints * 4 > int64_t(st->ws.partial_bytes))
+      return fail(PKV_ERR_WORKSPACE, "workspace holds %lld ints, %lld needed",
+                  (long long)(st->ws.partial_bytes / 4), (long long)ints);
+    scratch = reinterpret_cast<int*>(st->ws.partials);
+    if ((rc = order_streams(st, stream, capturing))) return rc;
+    if ((rc = capture_of(stream, capturing, &capture))) return rc;
+    lock = std::unique_lock<std::mutex>(g_pages_mu[dev]);
+    return PKV_OK;
+  }
+
+  // After the launches, failed ones too: the first of several may be in the stream.
+  int end(cudaError_t e, const char* what) {
+    const int rc = st->pages.wrote(stream, capture) ? order_after_pages(st, stream) : PKV_OK;
+    return e != cudaSuccess ? cuda_fail(e, what) : rc;
+  }
+};
 
 PKV_API int pkv_pages_fork(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
                            const pkv_tensor* page_refs, const pkv_tensor* parents,
@@ -1412,19 +1426,15 @@ PKV_API int pkv_pages_fork(const pkv_tensor* block_table, const pkv_tensor* seq_
                              {{parents, "parents"}, {children, "children"}})))
     return rc;
   if (n == 0) return PKV_OK;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  DeviceState* st = nullptr;
-  int* scratch = nullptr;
-  if ((rc = page_call(block_table, "block_table", pkv::pages_scratch_ints(n, t.num_pages), stream,
-                      &st, &scratch)))
+  PageCall call{static_cast<cudaStream_t>(stream_ptr)};
+  if ((rc = call.begin(block_table, "block_table", pkv::pages_scratch_ints(n, t.num_pages))))
     return rc;
-  t.err = st->ws.err;
+  t.err = call.st->ws.err;
   const cudaError_t e = pkv::launch_pages_fork(
       t, static_cast<const int32_t*>(parents->data), static_cast<const int32_t*>(children->data),
-      int(n), static_cast<int32_t*>(copy_src->data), static_cast<int32_t*>(copy_dst->data), scratch,
-      stream);
-  if (e != cudaSuccess) return cuda_fail(e, "pages fork launch");
-  return PKV_OK;
+      int(n), static_cast<int32_t*>(copy_src->data), static_cast<int32_t*>(copy_dst->data),
+      call.scratch, call.stream);
+  return call.end(e, "pages fork launch");
 }
 
 PKV_API int pkv_pages_release(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
@@ -1441,16 +1451,13 @@ PKV_API int pkv_pages_release(const pkv_tensor* block_table, const pkv_tensor* s
                              {{rows, "rows"}, {keep_lens, "keep_lens"}})))
     return rc;
   if (n == 0) return PKV_OK;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  DeviceState* st = nullptr;
-  int* scratch = nullptr;
-  if ((rc = page_call(block_table, "block_table", 0, stream, &st, &scratch))) return rc;
-  t.err = st->ws.err;
+  PageCall call{static_cast<cudaStream_t>(stream_ptr)};
+  if ((rc = call.begin(block_table, "block_table", 0))) return rc;
+  t.err = call.st->ws.err;
   const cudaError_t e =
       pkv::launch_pages_release(t, static_cast<const int32_t*>(rows->data),
-                                static_cast<const int32_t*>(keep_lens->data), int(n), stream);
-  if (e != cudaSuccess) return cuda_fail(e, "pages release launch");
-  return PKV_OK;
+                                static_cast<const int32_t*>(keep_lens->data), int(n), call.stream);
+  return call.end(e, "pages release launch");
 }
 
 PKV_API int pkv_pages_trim(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
@@ -1465,14 +1472,11 @@ PKV_API int pkv_pages_trim(const pkv_tensor* block_table, const pkv_tensor* seq_
                               {page_refs, "page_refs"}}, {})))
     return rc;
   if (t.rows == 0) return PKV_OK;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  DeviceState* st = nullptr;
-  int* scratch = nullptr;
-  if ((rc = page_call(block_table, "block_table", 0, stream, &st, &scratch))) return rc;
-  t.err = st->ws.err;
-  const cudaError_t e = pkv::launch_pages_trim(t, window, first_tokens, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "pages trim launch");
-  return PKV_OK;
+  PageCall call{static_cast<cudaStream_t>(stream_ptr)};
+  if ((rc = call.begin(block_table, "block_table", 0))) return rc;
+  t.err = call.st->ws.err;
+  const cudaError_t e = pkv::launch_pages_trim(t, window, first_tokens, call.stream);
+  return call.end(e, "pages trim launch");
 }
 
 PKV_API int pkv_pages_reserve(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
@@ -1491,18 +1495,15 @@ PKV_API int pkv_pages_reserve(const pkv_tensor* block_table, const pkv_tensor* s
                              {{rows, "rows"}, {new_lens, "new_lens"}})))
     return rc;
   if (n == 0) return PKV_OK;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  DeviceState* st = nullptr;
-  int* scratch = nullptr;
-  if ((rc = page_call(block_table, "block_table", pkv::pages_scratch_ints(n, t.num_pages), stream,
-                      &st, &scratch)))
+  PageCall call{static_cast<cudaStream_t>(stream_ptr)};
+  if ((rc = call.begin(block_table, "block_table", pkv::pages_scratch_ints(n, t.num_pages))))
     return rc;
-  t.err = st->ws.err;
+  t.err = call.st->ws.err;
   const cudaError_t e =
       pkv::launch_pages_reserve(t, static_cast<const int32_t*>(rows->data),
-                                static_cast<const int32_t*>(new_lens->data), int(n), scratch, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "pages reserve launch");
-  return PKV_OK;
+                                static_cast<const int32_t*>(new_lens->data), int(n), call.scratch,
+                                call.stream);
+  return call.end(e, "pages reserve launch");
 }
 
 PKV_API int pkv_pages_compact(const pkv_tensor* block_table, const pkv_tensor* seq_lens,
@@ -1521,16 +1522,13 @@ PKV_API int pkv_pages_compact(const pkv_tensor* block_table, const pkv_tensor* s
                               {copy_dst, "copy_dst"}, {num_moves, "num_moves"}},
                              {})))
     return rc;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  DeviceState* st = nullptr;
-  int* scratch = nullptr;
-  if ((rc = page_call(page_refs, "page_refs", pkv::pages_compact_ints(t.num_pages), stream, &st, &scratch))) return rc;
-  t.err = st->ws.err;
+  PageCall call{static_cast<cudaStream_t>(stream_ptr)};
+  if ((rc = call.begin(page_refs, "page_refs", pkv::pages_compact_ints(t.num_pages)))) return rc;
+  t.err = call.st->ws.err;
   const cudaError_t e = pkv::launch_pages_compact(
       t, static_cast<int32_t*>(copy_src->data), static_cast<int32_t*>(copy_dst->data), int(n),
-      static_cast<int32_t*>(num_moves->data), scratch, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "pages compact launch");
-  return PKV_OK;
+      static_cast<int32_t*>(num_moves->data), call.scratch, call.stream);
+  return call.end(e, "pages compact launch");
 }
 
 PKV_API int pkv_pages_copy(const pkv_tensor* const* pages, int num_tensors,
@@ -1583,14 +1581,11 @@ PKV_API int pkv_pages_copy(const pkv_tensor* const* pages, int num_tensors,
   p.src = static_cast<const int32_t*>(copy_src->data);
   p.dst = static_cast<const int32_t*>(copy_dst->data);
   p.n = int(n);
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  DeviceState* st = nullptr;
-  int* scratch = nullptr;
-  if ((rc = page_call(pages[0], "pages[0]", 0, stream, &st, &scratch))) return rc;
-  p.err = st->ws.err;
-  const cudaError_t e = pkv::launch_pages_copy(p, st->ws.num_sms, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "pages copy launch");
-  return PKV_OK;
+  PageCall call{static_cast<cudaStream_t>(stream_ptr)};
+  if ((rc = call.begin(pages[0], "pages[0]", 0))) return rc;
+  p.err = call.st->ws.err;
+  const cudaError_t e = pkv::launch_pages_copy(p, call.st->ws.num_sms, call.stream);
+  return call.end(e, "pages copy launch");
 }
 
 }  // extern "C"
