@@ -600,7 +600,8 @@ PKV_API int pkv_pages_compact(const pkv_tensor* block_table, const pkv_tensor* s
  * but the target of one only, and no target may be a source (the lists of
  * pkv_pages_fork and pkv_pages_compact are so); otherwise what the pages in
  * question hold is unspecified.
- *   pages      num_tensors (1 to 64) descriptors [num_pages, ...] of any dtype:
+ *   pages      num_tensors (1 to 64) descriptors [num_pages, ...] of the PKV_DTYPE
+ *              types (others can be described as one of them of their bytes):
  *              a page's elements are dense, the page stride is any; 4-byte
  *              aligned.
  */

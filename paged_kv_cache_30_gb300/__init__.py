@@ -391,8 +391,8 @@ def pages_compact(block_table, seq_lens, page_refs, page_size, copy_src, copy_ds
 
 def pages_copy(pages, copy_src, copy_dst, stream=None):
     """Copy page copy_src[i] to page copy_dst[i] in each cache of ``pages`` (a
-    tensor [num_pages, ...] or up to 64 of them), skipping negative entries (C:
-    pkv_pages_copy)."""
+    tensor [num_pages, ...] or up to 64 of them: bf16, fp32, int32, e4m3, or
+    views as one of these), skipping negative entries (C: pkv_pages_copy)."""
     (_call or _calls()).pages_copy([pages] if hasattr(pages, "data_ptr") else pages, copy_src,
                                    copy_dst, stream)
 

@@ -1549,6 +1549,8 @@ PKV_API int pkv_pages_copy(const pkv_tensor* const* pages, int num_tensors,
     if (!t) return fail(PKV_ERR_INVALID_ARG, "pages[%d] is NULL", i);
     if (t->ndim < 1 || t->ndim > 5)
       return fail(PKV_ERR_INVALID_ARG, "pages[%d] has %d dims", i, t->ndim);
+    if (t->dtype < PKV_DTYPE_BF16 || t->dtype > PKV_DTYPE_FP8_E4M3)
+      return fail(PKV_ERR_INVALID_ARG, "pages[%d] has dtype %d, which is not a PKV_DTYPE", i, t->dtype);
     if ((rc = check_tensor(t, "a page tensor", t->dtype, t->ndim))) return rc;
     int64_t count = 1, span = 1;
     for (int d = 1; d < t->ndim; ++d) {
