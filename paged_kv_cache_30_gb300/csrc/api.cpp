@@ -1559,7 +1559,10 @@ PKV_API int pkv_pages_copy(const pkv_tensor* const* pages, int num_tensors,
     }
     if (t->shape[0] < 1 || t->shape[0] >= (int64_t(1) << 30) || count < 1)
       return fail(PKV_ERR_INVALID_ARG, "pages[%d] has no page, or too many", i);
-    if (span != count)
+    // dense: as many elements as the span has, and none of them twice
+    pkv_tensor page = *t;
+    page.shape[0] = 1;
+    if (span != count || check_distinct_rows(&page, "a page") != PKV_OK)
       return fail(PKV_ERR_INVALID_ARG, "the pages of pages[%d] are not dense", i);
     if (t->shape[0] > 1 && t->stride[0] < span)
       return fail(PKV_ERR_INVALID_ARG, "the pages of pages[%d] overlap", i);

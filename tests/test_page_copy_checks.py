@@ -37,3 +37,12 @@ def test_other_torch_dtypes_are_refused():
     for dtype in (torch.float16, torch.uint8, torch.int64):
         with pytest.raises(pkv.PkvError, match="dtype"):
             pkv.pages_copy(torch.zeros(4, 8, dtype=dtype), *lists)
+
+
+@pytest.mark.parametrize("shape,stride,code", [
+    ([8, 4, 4], [16, 1, 4], 0), ([8, 3, 1, 2], [6, 2, 99, 1], 0), ([8, 2, 3], [8, 1, 2], 0),
+    ([8, 3, 3], [20, 2, 2], -1),        # as many elements as the span has, but not all of them
+    ([8, 2, 2, 2], [20, 1, 1, 5], -1), ([8, 4, 2], [8, 0, 7], -1), ([8, 5, 3], [40, 3, 1], 0),
+])
+def test_pages_with_gaps_and_repeats_are_refused(lib, shape, stride, code):
+    assert copy(lib, _t(shape, pkv.DTYPE_F32, stride, 0x10000000)) == code
