@@ -60,7 +60,8 @@
  *    the new stream first waits for the previous one: the library records an
  *    event on the previous call's stream at that moment, so that stream must
  *    still exist (destroy a stream only after another call on the device has
- *    been made from a live stream, or after pkv_shutdown()).  No event is
+ *    been made from a live stream, or after pkv_shutdown()).  Threads may make
+ *    such calls at once: each is put in order and launched as one step.  No event is
  *    recorded between calls on one stream, which keeps consecutive launches
  *    overlapping (programmatic dependent launch).
  *  - Programmatic dependent launch: the attention kernels launch as dependents

@@ -48,13 +48,15 @@ struct DeviceState {
   cudaEvent_t order_event = nullptr;
   cudaStream_t last_stream = nullptr;
   bool has_last = false;
-  pkv::PageOrder pages;  // under g_pages_mu
+  pkv::PageOrder pages;  // under g_launch_mu
 };
 
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
-// Held while a page call or an attention call goes into a stream of the device.
-std::mutex g_pages_mu[kMaxDevices];
+// Held while a call that uses the device's workspace goes into its stream, from the ordering
+// behind the calls before it to its last launch: two threads on two streams must not both
+// order themselves and launch afterwards.  (Taken before g_mu.)
+std::mutex g_launch_mu[kMaxDevices];
 
 // ------------------------------------------------------------ workspace --
 int init_locked(int device, size_t partial_bytes) {
@@ -154,14 +156,11 @@ int order_after_pages(DeviceState* st, cudaStream_t stream) {
 }
 
 // An attention call's way into its stream, behind any page call there: `early` for kernels
-// that read tables, lengths or pages ahead of their dependency wait.  *lock is held until the
-// launch is in.
-int settle_pages(DeviceState* st, int device, cudaStream_t stream, bool capturing, bool early,
-                 std::unique_lock<std::mutex>* lock) {
+// that read tables, lengths or pages ahead of their dependency wait.
+int settle_pages(DeviceState* st, cudaStream_t stream, bool capturing, bool early) {
   unsigned long long capture = 0;
   const int rc = capture_of(stream, capturing, &capture);
   if (rc != PKV_OK) return rc;
-  *lock = std::unique_lock<std::mutex>(g_pages_mu[device]);
   const bool need = st->pages.settle(stream, capture);
   return early && need ? order_after_pages(st, stream) : PKV_OK;
 }
@@ -586,9 +585,9 @@ PKV_API int pkv_paged_decode_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
   p.group_counters = ws.counters + pkv::kTopCounters;
   p.sched = ws.sched;
   p.err = ws.err;
+  std::lock_guard<std::mutex> lock(g_launch_mu[call.device]);
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  std::unique_lock<std::mutex> lock;
-  if ((rc = settle_pages(st, call.device, stream, capturing, true, &lock))) return rc;
+  if ((rc = settle_pages(st, stream, capturing, true))) return rc;
   const cudaError_t e = pkv::launch_gqa_decode(p, call.map, page_size, shape.grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gqa decode launch");
   return PKV_OK;
@@ -826,9 +825,9 @@ static int mla_verify_impl(const pkv_tensor* q, const pkv_tensor* q8, const pkv_
   p.plan = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ws.partials) + ws.partial_bytes) -
            units * cap;
   p.err = ws.err;
+  std::lock_guard<std::mutex> lock(g_launch_mu[dev]);
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  std::unique_lock<std::mutex> lock;
-  if ((rc = settle_pages(st, dev, stream, capturing, true, &lock))) return rc;
+  if ((rc = settle_pages(st, stream, capturing, true))) return rc;
   const cudaError_t e =
       native ? pkv::launch_mla_verify_native(p, kv_map, int(units * cap), stream)
       : pair ? pkv::launch_mla_verify_pair(p, q_map, kv_map, v_map, int(units * cap), stream)
@@ -898,6 +897,7 @@ PKV_API int pkv_mla_quantize_q(const pkv_tensor* q, const pkv_tensor* q8,
   p.qs_sr = q_scale->stride[0];
   p.R = int(R);
   p.H = int(H);
+  std::lock_guard<std::mutex> lock(g_launch_mu[dev]);
   if ((rc = order_streams(st, stream, capturing))) return rc;
   const cudaError_t e = pkv::launch_mla_quantize_q(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "mla quantize launch");
@@ -1233,9 +1233,9 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
       return fail(PKV_ERR_INVALID_ARG, "cuTensorMapEncodeTiled rejected the kv_cache layout (%d)",
                   (int)cr);
   }
+  std::lock_guard<std::mutex> lock(g_launch_mu[dev]);
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  std::unique_lock<std::mutex> lock;
-  if ((rc = settle_pages(st, dev, stream, capturing, false, &lock))) return rc;
+  if ((rc = settle_pages(st, stream, capturing, false))) return rc;
   const cudaError_t e = pkv::launch_paged_attn(p, map, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return PKV_OK;
@@ -1393,10 +1393,9 @@ struct PageCall {
       return fail(PKV_ERR_WORKSPACE, "workspace holds %lld ints, %lld needed",
                   (long long)(st->ws.partial_bytes / 4), (long long)ints);
     scratch = reinterpret_cast<int*>(st->ws.partials);
-    if ((rc = order_streams(st, stream, capturing))) return rc;
     if ((rc = capture_of(stream, capturing, &capture))) return rc;
-    lock = std::unique_lock<std::mutex>(g_pages_mu[dev]);
-    return PKV_OK;
+    lock = std::unique_lock<std::mutex>(g_launch_mu[dev]);
+    return order_streams(st, stream, capturing);
   }
 
   // After the launches, failed ones too: the first of several may be in the stream.
