@@ -442,9 +442,10 @@ PKV_API int pkv_mla_kv_append(const pkv_tensor* latent, const pkv_tensor* latent
  * and first tokens, can span + 16) < 2^31 - 4096.  A small workspace (two partials of
  * at most 8.4 KB a CTA) makes the call run on fewer CTAs.  Few and short requests are
  * fastest when the table is no wider than the longest one needs (a view of its first
- * columns will do), as the launch is chosen by the width: four of 300 keys take 4.6 us,
- * with a table for 65536 keys 6.4.
- * What masked keys hold (NaN, infinities, stale bytes) reaches no result.
+ * columns will do), as the launch is chosen by the width: four of up to 300 keys take 5.0
+ * us, with a table for 65536 keys 6.7.
+ * What masked keys hold (NaN, infinities, stale bytes) reaches no result.  The weights
+ * (times their page's scale) are rounded by 2^-11 of themselves, whatever the largest.
  * Errors as pkv_paged_decode_attn; a bad block-table entry reads as a page of
  * zeros and raises bit 1, a seq_len beyond the table is clamped and raises bit
  * 2 of the device error word.
@@ -461,7 +462,7 @@ PKV_API int pkv_paged_decode_attn_fp8(const pkv_tensor* q, const pkv_tensor* kv_
  * Next to pkv_paged_decode_attn it takes first_tokens, 1 to 16 query heads per
  * kv head, head_dim 64, pages of 64 and 128 tokens and any token stride.
  *   kv_cache     bf16 [num_blocks, Hkv, P, 2D]; strides multiples of 8.
- *   other arguments as pkv_paged_decode_attn_fp8.
+ *   other arguments as pkv_paged_decode_attn_fp8; the weights are rounded to bf16.
  */
 PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cache,
                                   const pkv_tensor* block_table, const pkv_tensor* seq_lens,
@@ -520,7 +521,7 @@ PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
  * the table, bit 32 (PKV_ERR_NO_PAGES) the pool ran out, bit 64
  * (PKV_ERR_BAD_BLOCK_TABLE) a list entry that was refused (a row outside the
  * table, a row named twice) or a count that would fall below zero.  An entry
- * that raises bit 32 or 64 changes nothing.
+ * that raises bit 32 or 64 changes no length, count or owned entry.
  *
  * pkv_pages_fork -- row children[i] becomes a copy of row parents[i]: its full
  * pages are shared (their counts go up), a partly filled last page gets a page
@@ -528,7 +529,7 @@ PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
  * (both -1 where nothing is to be copied), for pkv_pages_copy on every layer's
  * cache.  Children must be empty (seq_lens 0), each named once, and nobody's
  * parent in the call; a parent may have several.  The child's entries past its
- * pages become -1.  A child without a page (bit 32) stays empty.
+ * pages become -1.  A child without a page (bit 32) stays empty (all of its entries -1).
  *   parents, children, copy_src, copy_dst  int32 [n], n <= 8192.
  */
 PKV_API int pkv_pages_fork(const pkv_tensor* block_table, const pkv_tensor* seq_lens,

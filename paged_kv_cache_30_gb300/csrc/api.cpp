@@ -1184,13 +1184,14 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   // kPagedClusterTiles, or twice that for one CTA a pair in waves that are two thirds full;
   // one CTA each for up to two waves of pairs, clusters where they leave an eighth of the
   // places to spare, as clusters do not fill every GPC.
-  // On / off: four short requests 4.5 / 6.5 us, 256 requests of 200 keys 6.5 / 8.4,
-  // 16 x 8 kv heads of 1000 keys 10.8 / 13.7, a 1001-key window on 33 x 4 kv heads
-  // 10.1 / 13.0, 100 x 8 kv heads of 300 to 700 keys 23.7 / 26.6, 48 x 8 of 800 to 1000
-  // 18.4 / 23.2, 56 x 8 of 1500 29.6 / 35.3, a window of 1024 on 64 x 8 38.5 / 42.5.
-  // Without the spare places 64 pairs in clusters of 7 took 22.5 us instead of 13.2, without
-  // the limit of two waves 1000 x 8 kv heads of up to 300 keys 83 instead of 70, and in
-  // waves that are 56 % full 64 x 8 of up to 1500 keys 38.5 instead of 34.1.
+  // On / off: four short requests 5.0 / 6.4 us, 256 requests of 200 keys 7.3 / 9.2,
+  // 16 x 8 kv heads of 1000 keys 12.0 / 14.7, a 1001-key window on 33 x 4 kv heads
+  // 10.7 / 13.0, 100 x 8 kv heads of 300 to 700 keys 26.1 / 28.6, 48 x 8 of 800 to 1000
+  // 20.0 / 22.4, 56 x 8 of 1500 29.9 / 32.3, a bf16 window of 1024 on 64 x 8 38.2 / 42.5.
+  // Without the spare places 64 pairs in clusters of 7 take 22.5 us instead of 13.2, without
+  // the limit of two waves 1000 x 8 kv heads of up to 300 keys 87 instead of 50 (in the warp
+  // mode), and in waves that are 56 % full 64 x 8 of up to 1500 keys 29.4 instead of 25.9.
+  // A full wave of very unequal lengths loses: 40 x 8 of 10 to 1500 keys, 23.4 / 19.4.
   const int64_t part_bytes = int64_t(shape.part_floats) * 4;
   if (pairs <= 2 * slots) {
     const int64_t c = std::max<int64_t>(

@@ -40,8 +40,9 @@
 //  * Cluster mode, for few and short requests (the rule is the caller's): a cluster of
 //    CTAs takes one pair each, a CTA an equal part of its tiles, and the threads of all
 //    merge the parts through distributed shared memory (a 1001-key window on 33 x 4 kv
-//    heads 10.1 us; 12.1 where the first CTA merged alone): no scan of the lengths, no
-//    global partials (see launch_paged_attn's caller for what it measured).
+//    heads 10.7 us; with fp16 weights 10.1, and 12.1 where the first CTA merged alone): no
+//    scan of the lengths, no global partials (see launch_paged_attn's caller for what it
+//    measured).
 //  * Without clusters the kernel chooses by the lengths that it reads.  Warp mode, for
 //    many short requests: the shares are the warps', which write a pair that they hold
 //    whole from their accumulators, without a merge of warps or a barrier; of the warps
@@ -51,8 +52,8 @@
 //  * Otherwise, a request cut between CTAs: each publishes its 32-bit (O, m, l, R); the last
 //    CTA of a group of up to kMergeGroup (an arrival counter) merges the group, the last
 //    group merges the groups: each warp a fourth of the parts in order, then the warps'
-//    results (one thread per output going through all parts took 18.4 us instead of 15.1
-//    for one request of 16000 keys).  Results do not depend on timing.
+//    results (one request of 16000 keys: 16.1 us; with fp16 weights 15.1, and 18.4 where one
+//    thread per output went through all parts).  Results do not depend on timing.
 //
 // Measured (GB300, graph replays; the copy bandwidth is 6786 GB/s): e4m3, 8 requests
 // of 131072 keys, 8 kv heads of 128: 314 us = 6.85 TB/s; 64 requests of up to 32768
@@ -60,9 +61,9 @@
 // (lengths, table, tile: three dependent reads) and the CTAs end over the last 10;
 // bf16, a window of 4096 + 64 on 32 requests: 83 us = 6.4 TB/s; four short requests:
 // 5.0 us.  1 GB of e4m3 heads of 128 reads at 96 % (up to 8 query heads per kv head)
-// and 80 % (16), of 64 at 83 and 68 % (bound by instructions and, more than with fp16
-// weights, by the matrix pipe); bf16 at 96 to 99 %.  A tile's way through a warp is about
-// 700 (bf16) to 1200 (e4m3) cycles, of which the 16 products of S take 150 to 250.
+// and 80 % (16), of 64 at 83 and 68 % (bound by the latency of a warp's instructions, 12
+// warps an SM); bf16 at 97 to 100 %.  A tile's way through a warp is about 700 cycles
+// (bf16; e4m3 1200 with fp16 weights), of which the 16 products of S take 150 to 250.
 #include "pkv_internal.h"
 #include "ptx.cuh"
 
@@ -76,22 +77,22 @@ enum : int {
   kPagedWarp,     // warps take equal shares of all tiles
 };
 constexpr int kThreads = kWarps * 32;
-// One request of 131072 keys and one kv head: 17.6 us at 16, 18.3 at 12, 19.4 at 8; of 16000
-// keys and 8 kv heads: 15.2, 15.1, 14.8; 4 requests of up to 16000: 13.9, 13.2, 13.3.
+// One request of 131072 keys and one kv head: 19.0 us at 16, 19.3 at 12, 20.9 at 8; of 16000
+// keys and 8 kv heads: 16.0, 16.2, 15.7; 4 requests of up to 16000: 15.2, 14.4, 14.4.
 constexpr int kMergeGroup = 12;
 constexpr int kPairCost = kPagedPairCost;
 // The same for a warp in the warp mode: 2000 requests of 1 to 64 keys take 14.1 us at
-// 2, 14.8 at 3; 1000 x 8 of up to 300 keys 47.4 at 2, 45.8 at 3, 47.9 at 5.
+// 2, 15.0 at 3, 14.8 at 5; 1000 x 8 of up to 300 keys 51.9, 50.0, 51.0.
 constexpr int kWarpPairCost = 3;
 // What cuts inside pairs cost a CTA, in tiles: whole pairs (up to two a CTA) where the
 // longest ones end no later.  Tables as wide as for 65536 keys, on / off: 48 x 8 kv heads
-// of 800 to 1000 keys 20.6 / 23.3 us, 56 x 8 of 1500 31.6 / 35.5, 400 of 10 to 500 keys
-// 12.0 / 13.2; 110 x 8 of 10 to 1000, which the rule leaves, 33.1 / 28.0.
+// of 800 to 1000 keys 22.3 / 24.2 us, 56 x 8 of 1500 32.2 / 36.9, 400 of 10 to 500 keys
+// 12.9 / 14.3; 110 x 8 of 10 to 1000, which the rule leaves, 36.6 / 30.3.
 constexpr uint32_t kEndCost = 24;
 // A cut this near a pair's border moves there.  Wider costs more than the merges it
-// saves: at 32, 33 requests of a 1001-key window took 16.9 us instead of 13.0.
+// saves: at 32, 33 requests of a 1001-key window take 13.5 us in equal shares, 13.0 at 8.
 constexpr int kSnapTiles = 8;
-constexpr int kWarpSnapTiles = 4;  // in the warp mode; 8: 40.2 us instead of 37.5 for 256 x 8 pairs
+constexpr int kWarpSnapTiles = 4;  // in the warp mode; 8: 45.2 us instead of 40.4 for 256 x 8 pairs
 constexpr float kSlack = 8.f;      // log2 units: weights stay below 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -107,7 +108,7 @@ struct Cfg {
   static constexpr int kChunks = 2 * D * (kFp8 ? 1 : 2) / 128;  // 128-byte pieces of a [K | V] row
   static constexpr int kTileBytes = 16 * 128 * kChunks;
   // CTAs per SM, as many as the registers of the loop allow without spilling (four for
-  // e4m3 heads of 64 spill: 79 % instead of 91 %)
+  // e4m3 heads of 64 spilled, with fp16 weights: 1 GB at 79 % of the copy bandwidth, not 91)
   static constexpr int kCtas = D == 128 ? (NB == 1 && kFp8 ? 3 : 2) : (NB == 1 && !kFp8 ? 4 : 3);
   static constexpr int kWbRow = D + 4;
   static constexpr int kWbFloats = kRows * kWbRow + 3 * kRows;  // O, m, l, R of one warp
@@ -116,9 +117,8 @@ struct Cfg {
   static constexpr int kQSlots = D == 128 && NB == 2 && !kFp8 ? 1 : 2;
   static constexpr int kQBytes = kQSlots * kRows * D * 2;
   // Stages of a warp's ring: 96 to 128 KB asked for per SM.  More is not better: three
-  // stages for e4m3 heads of 128 (144 KB) read 8 x 131072 keys in 332 us, two in 317;
-  // fewer than five for e4m3 heads of 64: 91 % (4), 89 % (3), 83 % (2) of the measured
-  // copy bandwidth on 1 GB against 93 %.
+  // stages for e4m3 heads of 128 (144 KB) read 8 x 131072 keys in 332 us, two in 317 (fp16
+  // weights); fewer than five for e4m3 heads of 64: 1 GB in 182 us (4), 180 (3), against 178.
   static constexpr int kStages = kTileBytes == 2048 ? 5 : kTileBytes == 4096 && kCtas == 2 ? 3 : 2;
   static constexpr int kOffWb = kWarps * kStages * kTileBytes;
   static constexpr int kOffQ = kOffWb + kWarps * kWbFloats * 4;
@@ -391,8 +391,8 @@ __device__ __forceinline__ int part_slot(int c0, int i) { return 2 * (c0 + i) + 
 // The warp's part of merging a pair's parts first, first + step, .. before end: every
 // fourth, in order, into its own (O, m, l, R) in shared memory.  A lane has floats
 // 128 u + 4 lane .. + 3 of the partial, and the statistics of row `lane`.  A call, as its
-// registers would cost the loop over tiles some of its own (e4m3 heads of 64 on 1 GB: 91 %
-// of the copy bandwidth, 90 inlined).
+// registers would cost the loop over tiles some of its own (e4m3 heads of 64 on 1 GB, with
+// fp16 weights: 91 % of the copy bandwidth, 90 inlined).
 template <class C>
 __device__ __noinline__ void gather_partials(const float* partials, int c0, int first, int step,
                                              int end, float* wb) {
@@ -1237,9 +1237,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const uint32_t pairs = B * Hkv, waves = (pairs + gridDim.x - 1) / gridDim.x;
     // Warp mode: what the merge of a CTA's warps costs a short pair is saved, where there
     // are pairs enough for the warps.  On / off, e4m3: 2000 x 8 kv heads of 30 to 60 keys
-    // 55.6 / 113.8 us, 1000 x 8 of up to 300 keys, heads of 64, 45.7 / 70.3, 256 x 8 of 10
-    // to 700 keys 38.5 / 42.9, of 700 to 768 keys 69.3 / 71.3; a bf16 window of 128 on
-    // 512 x 8 kv heads 58.7 / 64.2.  64 x 8 of up to 32768 keys lose, 62.6 / 51.2.
+    // 60.1 / 119.4 us, 1000 x 8 of up to 300 keys, heads of 64, 50.0 / 75.8, 256 x 8 of 10
+    // to 700 keys 40.4 / 47.2, of 700 to 768 keys 69.9 / 76.2; a bf16 window of 128 on
+    // 512 x 8 kv heads 58.3 / 63.9.  64 x 8 of up to 32768 keys lose, 63.5 / 51.5.
     if (p.warps && waves > 2 && most <= kPagedWarpTiles) {
       attend<C, kPagedWarp>(p, kv_map, base, base_u32, Pair{}, false);
     } else {

@@ -266,7 +266,7 @@ PagedShape paged_attn_shape(int D, bool fp8, int G);
 cudaError_t launch_paged_attn(const PagedParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
 // A CTA's share of the work is counted in 16-token tiles plus a cost for each
 // (request, kv head) pair, and is no smaller than kPagedMinCost.  64 requests of
-// log-uniform lengths, e4m3: 84.2 us at a cost of 4, 53.9 at 8, 52.6 at 12, 52.8 at 16.
+// log-uniform lengths, e4m3: 80.5 us at a cost of 4, 54.4 at 8, 51.5 at 12, 52.0 at 16.
 constexpr int kPagedPairCost = 12;
 constexpr int kPagedMinCost = 16;
 constexpr int kPagedMaxCluster = 8;
@@ -274,7 +274,7 @@ constexpr int kPagedMaxCluster = 8;
 // 33 tiles each: 15.4 us in clusters, 17.2 without).
 constexpr int kPagedClusterTiles = 48;
 // Most tiles of a pair in the warp mode, in which one warp merges a pair's parts: 150 x 8
-// kv heads of up to 2000 keys took 57.0 us in equal shares of CTAs, 55.8 in the warp mode,
+// kv heads of up to 2000 keys take 60.4 us in equal shares of CTAs, 57.1 in the warp mode,
 // but a batch with one such request among very short ones gives it dozens of parts.
 constexpr int kPagedWarpTiles = 64;
 
