@@ -155,14 +155,13 @@ int order_after_pages(DeviceState* st, cudaStream_t stream) {
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "ordering after a page call");
 }
 
-// An attention call's way into its stream, behind any page call there: `early` for kernels
-// that read tables, lengths or pages ahead of their dependency wait.
-int settle_pages(DeviceState* st, cudaStream_t stream, bool capturing, bool early) {
+// Before a kernel that reads tables, lengths or pages ahead of its dependency wait.
+int settle_pages(DeviceState* st, cudaStream_t stream, bool capturing) {
   unsigned long long capture = 0;
-  const int rc = capture_of(stream, capturing, &capture);
-  if (rc != PKV_OK) return rc;
-  const bool need = st->pages.settle(stream, capture);
-  return early && need ? order_after_pages(st, stream) : PKV_OK;
+  int rc = capture_of(stream, capturing, &capture);
+  if (rc != PKV_OK || !st->pages.due(stream, capture)) return rc;
+  if ((rc = order_after_pages(st, stream)) == PKV_OK) st->pages.settled(stream, capture);
+  return rc;
 }
 
 // ------------------------------------------------------------ validation --
@@ -587,7 +586,7 @@ PKV_API int pkv_paged_decode_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
   p.err = ws.err;
   std::lock_guard<std::mutex> lock(g_launch_mu[call.device]);
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  if ((rc = settle_pages(st, stream, capturing, true))) return rc;
+  if ((rc = settle_pages(st, stream, capturing))) return rc;
   const cudaError_t e = pkv::launch_gqa_decode(p, call.map, page_size, shape.grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gqa decode launch");
   return PKV_OK;
@@ -827,7 +826,7 @@ static int mla_verify_impl(const pkv_tensor* q, const pkv_tensor* q8, const pkv_
   p.err = ws.err;
   std::lock_guard<std::mutex> lock(g_launch_mu[dev]);
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  if ((rc = settle_pages(st, stream, capturing, true))) return rc;
+  if ((rc = settle_pages(st, stream, capturing))) return rc;
   const cudaError_t e =
       native ? pkv::launch_mla_verify_native(p, kv_map, int(units * cap), stream)
       : pair ? pkv::launch_mla_verify_pair(p, q_map, kv_map, v_map, int(units * cap), stream)
@@ -1236,9 +1235,11 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   }
   std::lock_guard<std::mutex> lock(g_launch_mu[dev]);
   if ((rc = order_streams(st, stream, capturing))) return rc;
-  if ((rc = settle_pages(st, stream, capturing, false))) return rc;
+  unsigned long long capture = 0;
+  if ((rc = capture_of(stream, capturing, &capture))) return rc;
   const cudaError_t e = pkv::launch_paged_attn(p, map, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  st->pages.settled(stream, capture);  // the kernel waits before it reads
   return PKV_OK;
 }
 

@@ -37,27 +37,33 @@ class PageOrder {
     return false;
   }
 
-  // A kernel is about to go into `stream`: whether one that reads ahead of its wait needs the
-  // memset.  Whatever goes in now (the memset, or a kernel that waits before it reads and
-  // before it lets the next one start) settles what was due on the stream.
-  bool settle(const void* stream, unsigned long long capture) {
+  // Whether a kernel that reads ahead of its wait needs the memset when it goes into `stream`.
+  bool due(const void* stream, unsigned long long capture) const {
     if (per_thread(stream)) return false;
     stream = base(stream);
     bool need = false;
     for (int i = 0; i < n_; ++i) {
-      Entry& e = entries_[i];
-      if (e.capture != capture) continue;
-      if (e.stream != stream) {
-        need |= capture != 0;
-      } else {
-        need |= e.due;
-        e.due = false;
-        if (capture == 0) {
-          e = entries_[--n_];
-          break;
-        }
-      }
+      const Entry& e = entries_[i];
+      if (e.capture == capture) need |= e.stream == stream ? e.due : capture != 0;
     }
+    return need;
+  }
+
+  // The memset is in `stream`, or a kernel that waits before it reads and before it lets the
+  // next one start: nothing is due on the stream any more.
+  void settled(const void* stream, unsigned long long capture) {
+    stream = base(stream);
+    for (int i = 0; i < n_; ++i)
+      if (entries_[i].stream == stream && entries_[i].capture == capture) {
+        entries_[i].due = false;
+        if (capture == 0) entries_[i] = entries_[--n_];
+        return;
+      }
+  }
+
+  bool settle(const void* stream, unsigned long long capture) {
+    const bool need = due(stream, capture);
+    settled(stream, capture);
     return need;
   }
 

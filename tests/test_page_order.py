@@ -14,6 +14,8 @@ static pkv::PageOrder* o = nullptr;
 extern "C" void fresh() { delete o; o = new pkv::PageOrder(); }
 extern "C" int wrote(long s, unsigned long long c) { return o->wrote((const void*)s, c); }
 extern "C" int settle(long s, unsigned long long c) { return o->settle((const void*)s, c); }
+extern "C" int due(long s, unsigned long long c) { return o->due((const void*)s, c); }
+extern "C" void settled(long s, unsigned long long c) { o->settled((const void*)s, c); }
 extern "C" int size() { return o->size(); }
 """
 S, T = 0x1000, 0x2000  # streams
@@ -26,7 +28,7 @@ def built(tmp_path_factory):
     subprocess.run([shutil.which("g++") or "c++", "-std=c++17", "-shared", "-fPIC", "-I", pkv_build.CSRC,
                     str(d / "t.cpp"), "-o", str(d / "t.so")], check=True)
     lib = ctypes.CDLL(str(d / "t.so"))
-    for f in (lib.wrote, lib.settle):
+    for f in (lib.wrote, lib.settle, lib.due, lib.settled):
         f.argtypes = [ctypes.c_long, ctypes.c_ulonglong]
     return lib
 
@@ -98,3 +100,17 @@ def test_the_default_streams_handles(o):
     assert not o.wrote(0, 0) and o.settle(1, 0)  # two names of one stream
     assert not o.wrote(1, 0) and o.settle(0, 0)
     assert o.wrote(2, 0) and not o.settle(2, 0)  # one name of a stream for each thread
+
+
+@pytest.mark.parametrize("c", [0, 7])
+def test_a_call_that_fails_settles_nothing(o, c):
+    """It asks what is due; only what is in the stream settles it."""
+    assert not o.wrote(S, c)
+    assert o.due(S, c) and o.due(S, c)
+    o.settled(T, c)
+    o.settled(S, 9)
+    assert o.due(S, c)
+    o.settled(S, c)
+    assert not o.due(S, c)
+    o.settled(S, c)
+    assert not o.wrote(S, c) and o.due(S, c)
