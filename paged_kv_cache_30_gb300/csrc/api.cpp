@@ -123,13 +123,18 @@ int workspace_for(int dev, cudaStream_t stream, DeviceState** out, bool* capturi
 }
 
 // Launches sharing a workspace must be ordered: a call on a new stream first
-// waits for the stream of the previous call (outside graph capture).
+// waits for the stream of the previous call, when neither is being captured (an
+// event recorded in a capture would take the new stream into it).
 int order_streams(DeviceState* st, cudaStream_t stream, bool capturing) {
   if (capturing) return PKV_OK;
   std::lock_guard<std::mutex> lk(g_mu);
   if (st->has_last && st->last_stream != stream) {
-    cudaError_t e = cudaEventRecord(st->order_event, st->last_stream);
-    if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, st->order_event, 0);
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st->last_stream, &cs);
+    if (e == cudaSuccess && cs == cudaStreamCaptureStatusNone) {
+      e = cudaEventRecord(st->order_event, st->last_stream);
+      if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, st->order_event, 0);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "cross-stream ordering");
   }
   st->last_stream = stream;

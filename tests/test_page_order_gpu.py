@@ -122,3 +122,28 @@ def test_a_stream_for_each_page_call():
     for h in handles:
         assert int(cudart.cudaStreamDestroy(h.value)) == 0
     assert pkv.check_errors(0) == 0
+
+
+def test_a_call_on_another_stream_while_the_last_one_is_captured():
+    """The capture of the last call's stream records nothing of it: it runs at once."""
+    s = state()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        change(s, ints([700, 900]))
+        torch.cuda.synchronize()
+    last, other = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(last):
+        attend(s, s["outs"][0])
+        torch.cuda.synchronize()
+        graph.capture_begin(capture_error_mode="relaxed")
+        attend(s, s["outs"][2])
+        with torch.cuda.stream(other):
+            attend(s, s["outs"][1])
+        other.synchronize()
+        graph.capture_end()
+    assert torch.equal(s["outs"][0], s["outs"][1])
+    assert not s["outs"][2].any()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(s["outs"][0], s["outs"][2])
+    assert pkv.check_errors(0) == 0
