@@ -30,6 +30,9 @@
  *    pkv_gqa_kv_append_fp8 writes tokens (one each, or whole prompts) into the
  *    e4m3 cache.
  *
+ *  - pkv_qk_norm_rope, pkv_gqa_rope_append: norms of query and key heads and their
+ *    rotation by position, to memory or, with the values, into the bf16 cache.
+ *
  *  - pkv_pages_fork / _release / _trim / _reserve / _compact / _copy: its pages,
  *    kept on the device in block tables, lengths and reference counts.
  *
@@ -505,6 +508,92 @@ PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
                                   const pkv_tensor* kv_cache, const pkv_tensor* kv_scale,
                                   const pkv_tensor* block_table, const pkv_tensor* seq_lens,
                                   const pkv_tensor* cu_tokens, int page_size, void* stream);
+
+/*
+ * pkv_rope_table -- the frequencies of a rotation, for pkv_qk_norm_rope and
+ * pkv_gqa_rope_append (host only: copy the table to the device once).
+ *   inv_freq      [rot_dim / 2] radians per position (any finite values), or NULL
+ *                 for base^(-2i / rot_dim).
+ *   rot_dim       rotated dims of a head: a multiple of 16, at most 128.
+ *   base          > 0.
+ *   factor        > 0; other than 1 it stretches the positions for contexts longer
+ *                 than the model was trained on.  With original_len = 0 every
+ *                 frequency is divided by it.  With original_len > 0 one that
+ *                 makes r turns over original_len positions becomes
+ *                 f (g + (1 - g) / factor), g = (r - low) / (high - low) kept within
+ *                 [0, 1]: slow pairs are stretched, fast ones kept.
+ *   low, high     low < high.
+ *   table         int32 [rot_dim / 2, 2]: turns per position in units of 2^-64 (lower,
+ *                 upper word); whole turns are dropped.
+ */
+PKV_API int pkv_rope_table(const double* inv_freq, int rot_dim, double base, double factor,
+                           double original_len, double low, double high, int32_t* table);
+
+/*
+ * pkv_qk_norm_rope -- RMS norm of each query and key head, and the rotation by the
+ * tokens' positions, in one pass.
+ *   y      = x w / sqrt(mean(x^2) + eps) over a head's D elements (y = x without w)
+ *   (a, b) = c (y_i cos t - y_j sin t), c (y_j cos t + y_i sin t),  t = position f_p
+ * for pair p = (i, j) of the first rot_dim elements, (p, p + rot_dim / 2) or, if
+ * interleaved, (2p, 2p + 1); the others are normed alone.  In 32 bits, the angle
+ * reduced exactly for any position, rounded once to bf16.
+ *
+ *   q            bf16 [T, Hq, D], D 64 or 128; last dim contiguous; strides multiples
+ *                of 8; 16-byte aligned.  A view of part of a wider row will do: the
+ *                last 64 of 576 elements of an MLA query or latent row, heads of a
+ *                fused projection.
+ *   k            bf16 [T, Hkv, D] likewise, or NULL.
+ *   q_weight, k_weight  bf16 or fp32 [D], contiguous, or NULL: no norm.
+ *   eps          >= 0 (of the norms).
+ *   positions    int32 [T]; a token of a negative one is padding, of which nothing
+ *                is written.  May be NULL without rope.
+ *   rope         int32 [rot_dim / 2, 2] of pkv_rope_table, contiguous, 8-byte aligned,
+ *                rot_dim <= D; NULL: no rotation.
+ *   rope_factor  c, a scale of cosines and sines.
+ *   interleaved  0: pairs (p, p + rot_dim / 2); else (2p, 2p + 1).
+ *   q_out, k_out bf16, shapes of q and k, any strides as above.  They may be q and k
+ *                themselves, the same view; otherwise they share no memory with any
+ *                input or with each other (views side by side in one row share none).
+ *   stream       cudaStream_t.
+ * One launch; nothing of the workspace is used.  T == 0 is a no-op.
+ */
+PKV_API int pkv_qk_norm_rope(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* q_weight,
+                             const pkv_tensor* k_weight, float eps, const pkv_tensor* positions,
+                             const pkv_tensor* rope, float rope_factor, int interleaved,
+                             const pkv_tensor* q_out, const pkv_tensor* k_out, void* stream);
+
+/*
+ * pkv_gqa_rope_append -- pkv_qk_norm_rope on the way into a paged bf16 cache: one
+ * token each (decode), or whole prompts; the rotated keys and the values go to the
+ * cache, the queries to q_out.
+ *   q, k, q_weight, k_weight, eps, rope, rope_factor, interleaved, q_out  as
+ *                 pkv_qk_norm_rope (k not NULL).
+ *   v             bf16 [T, Hkv, D], aligned as k; copied.
+ *   positions     int32 [T], what the tokens are rotated by (negative: nothing of the
+ *                 token is written), or NULL: their positions in their requests.
+ *   kv_cache      bf16 [num_blocks, Hkv, P, 2D], pages of 16 to 128 tokens, as
+ *                 pkv_paged_window_attn.  Written in place; it shares no memory with an
+ *                 input.
+ *   block_table   int32 [B, max_blocks].
+ *   seq_lens      int32 [B], lengths including the new tokens: the n new tokens of
+ *                 request b go to positions seq_lens[b] - n .. seq_lens[b] - 1; nothing
+ *                 of those at negative positions is written.
+ *   cu_tokens     int32 [B + 1], non-decreasing: request b's tokens are rows
+ *                 [cu_tokens[b], cu_tokens[b + 1]); rows outside [cu_tokens[0],
+ *                 cu_tokens[B]) are padding and are not written.  NULL: T / B tokens each
+ *                 (T % B must be 0).
+ *   page_size     P.
+ * A token whose page entry lies beyond max_blocks or outside [0, num_blocks) gets its
+ * q_out alone, and raises bit 2 or bit 1 of the device error word.  Attention calls after
+ * it on its stream may follow at once.  Errors as pkv_gqa_kv_append.
+ */
+PKV_API int pkv_gqa_rope_append(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* v,
+                                const pkv_tensor* q_weight, const pkv_tensor* k_weight, float eps,
+                                const pkv_tensor* positions, const pkv_tensor* rope,
+                                float rope_factor, int interleaved, const pkv_tensor* kv_cache,
+                                const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                                const pkv_tensor* cu_tokens, int page_size,
+                                const pkv_tensor* q_out, void* stream);
 
 /*
  * The pages of a cache, on the device.  State, shared by all layers:

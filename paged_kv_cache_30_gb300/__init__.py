@@ -23,6 +23,13 @@ Names follow the C ABI without its ``pkv_`` prefix:
                       scale, page_size, out, lse=None, stream=None)
     gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens,
                       page_size, stream=None)
+    rope_table(rot_dim, base=10000.0, factor=1.0, original_len=0, low=1.0, high=4.0,
+               inv_freq=None, device="cuda")
+    qk_norm_rope(q, k, q_weight, k_weight, eps, positions, rope, rope_factor, interleaved,
+                 q_out, k_out, stream=None)
+    gqa_rope_append(q, k, v, q_weight, k_weight, eps, positions, rope, rope_factor,
+                    interleaved, kv_cache, block_table, seq_lens, cu_tokens, page_size,
+                    q_out, stream=None)
     pages_fork(block_table, seq_lens, page_refs, parents, children, page_size,
                copy_src, copy_dst, stream=None)
     pages_release(block_table, seq_lens, page_refs, rows, keep_lens, page_size, stream=None)
@@ -50,6 +57,7 @@ __all__ = [
     "mla_verify_attn", "gqa_kv_append", "mla_kv_append", "num_kv_splits", "check_errors", "check_counters", "shutdown",
     "paged_decode_attn_fp8", "paged_window_attn", "gqa_kv_append_fp8", "pages_fork",
     "pages_release", "pages_trim", "pages_reserve", "pages_compact", "pages_copy",
+    "rope_table", "qk_norm_rope", "gqa_rope_append",
     "version", "last_error",
 ]
 
@@ -84,7 +92,8 @@ _lib = None
 _call = None  # the compiled binding of the calls that come many times a step (csrc/pycall.c)
 _CALLS = ("pkv_paged_decode_attn_fp8", "pkv_paged_window_attn", "pkv_gqa_kv_append_fp8",
           "pkv_pages_fork", "pkv_pages_release", "pkv_pages_reserve", "pkv_pages_compact",
-          "pkv_pages_copy", "pkv_pages_trim", "pkv_last_error")
+          "pkv_pages_copy", "pkv_pages_trim", "pkv_qk_norm_rope", "pkv_gqa_rope_append",
+          "pkv_last_error")
 
 
 def _calls():
@@ -143,6 +152,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.pkv_pages_compact.argtypes = [T, T, T, i32, T, T, T, vp]
         lib.pkv_pages_trim.argtypes = [T, T, T, i32, i32, i32, vp]
         lib.pkv_pages_copy.argtypes = [vp, i32, T, T, vp]
+        f64 = ctypes.c_double
+        lib.pkv_rope_table.argtypes = [ctypes.POINTER(f64), i32, f64, f64, f64, f64, f64,
+                                       ctypes.POINTER(ctypes.c_int32)]
+        lib.pkv_qk_norm_rope.argtypes = [T, T, T, T, f32, T, T, f32, i32, T, T, vp]
+        lib.pkv_gqa_rope_append.argtypes = [T, T, T, T, T, f32, T, T, f32, i32, T, T, T, T, i32, T, vp]
         lib.pkv_num_kv_splits.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_double, i32, i32]
         lib.pkv_check_errors.argtypes = [i32, ctypes.POINTER(ctypes.c_int32)]
         lib.pkv_check_counters.argtypes = [i32, ctypes.POINTER(ctypes.c_int64)]
@@ -155,7 +169,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                      "pkv_selftest_wait_timeout", "pkv_paged_decode_attn_fp8",
                      "pkv_paged_window_attn", "pkv_gqa_kv_append_fp8", "pkv_pages_fork",
                      "pkv_pages_release", "pkv_pages_reserve", "pkv_pages_compact",
-                     "pkv_pages_copy", "pkv_pages_trim", "pkv_shutdown", "pkv_version"):
+                     "pkv_pages_copy", "pkv_pages_trim", "pkv_rope_table", "pkv_qk_norm_rope",
+                     "pkv_gqa_rope_append", "pkv_shutdown", "pkv_version"):
             getattr(lib, name).restype = i32
         if path is None:
             _lib = lib
@@ -348,6 +363,53 @@ def gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens
     (_call or _calls()).gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens,
                                           page_size, stream)
     return kv_cache
+
+
+def rope_table(rot_dim, base=10000.0, factor=1.0, original_len=0, low=1.0, high=4.0,
+               inv_freq=None, device="cuda"):
+    """The rotation's frequencies (C: pkv_rope_table) as an int32 tensor [rot_dim / 2, 2] for
+    qk_norm_rope and gqa_rope_append, made once: base^(-2i / rot_dim) radians a position, or
+    ``inv_freq`` (a sequence of rot_dim / 2).  A ``factor`` other than 1 divides all of them,
+    or, with ``original_len``, those that turn less than ``low`` times over that many
+    positions, none that turn more than ``high`` times, and mixes the ones between."""
+    import torch
+    n = int(rot_dim) // 2
+    freq = None
+    if inv_freq is not None:
+        values = [float(x) for x in inv_freq]
+        if len(values) != n:
+            raise PkvError(-1, f"inv_freq must have {n} entries")
+        freq = (ctypes.c_double * max(n, 1))(*values)
+    table = torch.empty(max(n, 1), 2, dtype=torch.int32)
+    _check(load_library().pkv_rope_table(
+        freq, int(rot_dim), float(base), float(factor), float(original_len), float(low),
+        float(high), ctypes.cast(table.data_ptr(), ctypes.POINTER(ctypes.c_int32))))
+    return table.to(device)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, eps, positions, rope, rope_factor, interleaved, q_out,
+                 k_out, stream=None):
+    """RMS norm of each head of ``q`` and ``k`` (weights [D], or None for no norm), then the
+    rotation of the first dims by ``positions`` (``rope`` from rope_table, or None for none;
+    cosines and sines times ``rope_factor``), into ``q_out`` and ``k_out``, which may be ``q``
+    and ``k`` (C: pkv_qk_norm_rope).  ``k`` and ``k_out`` may be None.  Tokens of a negative
+    position are not written.  Returns ``(q_out, k_out)``."""
+    (_call or _calls()).qk_norm_rope(q, k, q_weight, k_weight, eps, positions, rope, rope_factor,
+                                     interleaved, q_out, k_out, stream)
+    return q_out, k_out
+
+
+def gqa_rope_append(q, k, v, q_weight, k_weight, eps, positions, rope, rope_factor, interleaved,
+                    kv_cache, block_table, seq_lens, cu_tokens, page_size, q_out, stream=None):
+    """qk_norm_rope on the way into a bf16 cache: the rotated keys and the values of all
+    requests' new tokens (request b's are rows cu_tokens[b] .. cu_tokens[b + 1]; None: T / B
+    each) go to positions ending at seq_lens[b] - 1, the queries to ``q_out`` (C:
+    pkv_gqa_rope_append).  ``positions`` None: rotated by those positions.  Returns
+    ``(q_out, kv_cache)``."""
+    (_call or _calls()).gqa_rope_append(q, k, v, q_weight, k_weight, eps, positions, rope,
+                                        rope_factor, interleaved, kv_cache, block_table, seq_lens,
+                                        cu_tokens, page_size, q_out, stream)
+    return q_out, kv_cache
 
 
 def pages_fork(block_table, seq_lens, page_refs, parents, children, page_size, copy_src,

@@ -232,6 +232,30 @@ int check_no_overlap(std::initializer_list<std::pair<const pkv_tensor*, const ch
   return PKV_OK;
 }
 
+// Whether two views of tokens (dim 0) share no byte although their spans may cross, as
+// queries, keys and values that lie side by side in a projection's output do: with one
+// stride, tokens of one fit between those of the other.
+bool apart(const pkv_tensor* a, const pkv_tensor* b) {
+  if (!overlaps(a, b)) return true;
+  const int64_t step = a->stride[0] * elem_bytes(a->dtype);
+  if (step != b->stride[0] * elem_bytes(b->dtype) || step <= 0) return false;
+  auto extent = [](const pkv_tensor* t) {
+    int64_t last = 0;
+    for (int i = 1; i < t->ndim; ++i) last += (t->shape[i] - 1) * t->stride[i];
+    return (last + 1) * elem_bytes(t->dtype);
+  };
+  const intptr_t off = reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data);
+  const int64_t d = (off % step + step) % step;
+  return d >= extent(a) && d + extent(b) <= step;
+}
+
+bool same_view(const pkv_tensor* a, const pkv_tensor* b) {
+  if (a->data != b->data || a->dtype != b->dtype || a->ndim != b->ndim) return false;
+  for (int i = 0; i < a->ndim; ++i)
+    if (a->shape[i] != b->shape[i] || (a->shape[i] > 1 && a->stride[i] != b->stride[i])) return false;
+  return true;
+}
+
 // Requests hold at most max_blocks x page_size keys; the kernels keep that
 // product in 32-bit integers.
 int check_table_width(const pkv_tensor* block_table, int page_size) {
@@ -1340,6 +1364,255 @@ PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,
   const cudaError_t e = pkv::launch_gqa_kv_append_fp8(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gqa fp8 kv append launch");
   return PKV_OK;
+}
+
+// ----------------------------------------- head norms and rotation of q and k --
+PKV_API int pkv_rope_table(const double* inv_freq, int rot_dim, double base, double factor,
+                           double original_len, double low, double high, int32_t* table) {
+  if (!table) return fail(PKV_ERR_INVALID_ARG, "table is NULL");
+  if (rot_dim < 16 || rot_dim % 16 || rot_dim > 128)
+    return fail(PKV_ERR_UNSUPPORTED, "rot_dim %d (multiples of 16 up to 128 are built)", rot_dim);
+  if (!inv_freq && !(std::isfinite(base) && base > 0))
+    return fail(PKV_ERR_INVALID_ARG, "base %g", base);
+  if (!(std::isfinite(factor) && factor > 0)) return fail(PKV_ERR_INVALID_ARG, "factor %g", factor);
+  if (!(std::isfinite(original_len) && original_len >= 0))
+    return fail(PKV_ERR_INVALID_ARG, "original_len %g", original_len);
+  if (factor != 1 && original_len > 0 && !(std::isfinite(low) && std::isfinite(high) && low < high))
+    return fail(PKV_ERR_INVALID_ARG, "low %g must be below high %g", low, high);
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double turns = (inv_freq ? inv_freq[i] : std::pow(base, -2.0 * i / rot_dim)) / kTwoPi;
+    if (!std::isfinite(turns)) return fail(PKV_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
+    if (factor != 1) {
+      double keep = 0;
+      if (original_len > 0)
+        keep = std::min(1.0, std::max(0.0, (original_len * std::fabs(turns) - low) / (high - low)));
+      turns = turns * (keep + (1 - keep) / factor);
+    }
+    // the fraction of a turn in units of 2^-64, in two exact steps
+    const double upper = (turns - std::floor(turns)) * 4294967296.0, whole = std::floor(upper);
+    const uint32_t hi = uint32_t(uint64_t(whole));
+    const uint32_t lo = uint32_t(uint64_t((upper - whole) * 4294967296.0));
+    std::memcpy(table + 2 * i, &lo, 4);
+    std::memcpy(table + 2 * i + 1, &hi, 4);
+  }
+  return PKV_OK;
+}
+
+// What qk_norm_rope and gqa_rope_append have in common: q, k, weights, positions, the table
+// and q_out.
+static int check_rope(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* q_weight,
+                      const pkv_tensor* k_weight, float eps, const pkv_tensor* positions,
+                      const pkv_tensor* rope, float rope_factor, const pkv_tensor* q_out,
+                      pkv::RopeParams* p) {
+  int rc;
+  if ((rc = check_tensor(q, "q", PKV_DTYPE_BF16, 3))) return rc;
+  if (k && (rc = check_tensor(k, "k", PKV_DTYPE_BF16, 3))) return rc;
+  if ((rc = check_tensor(q_out, "q_out", PKV_DTYPE_BF16, 3))) return rc;
+  if (positions && (rc = check_tensor(positions, "positions", PKV_DTYPE_I32, 1))) return rc;
+  if (rope && (rc = check_tensor(rope, "rope", PKV_DTYPE_I32, 2))) return rc;
+  const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2];
+  if (D != 64 && D != 128)
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %lld (64 and 128 are built)", (long long)D);
+  if (Hq < 1 || Hq > 65535 || (k && (k->shape[1] < 1 || k->shape[1] > 65535)))
+    return fail(PKV_ERR_INVALID_ARG, "%lld query heads", (long long)Hq);
+  if (k && (k->shape[0] != T || k->shape[2] != D))
+    return fail(PKV_ERR_INVALID_ARG, "k must be [%lld, Hkv, %lld]", (long long)T, (long long)D);
+  if (T >= (int64_t(1) << 31)) return fail(PKV_ERR_UNSUPPORTED, "%lld tokens", (long long)T);
+  for (int i = 0; i < 3; ++i)
+    if (q_out->shape[i] != q->shape[i])
+      return fail(PKV_ERR_INVALID_ARG, "q_out must have the shape of q");
+  if (positions && (positions->shape[0] != T || (T > 1 && positions->stride[0] != 1)))
+    return fail(PKV_ERR_INVALID_ARG, "positions must be a contiguous [%lld]", (long long)T);
+  struct {
+    const pkv_tensor* w;
+    const char* name;
+    const void** data;
+    int* f32;
+  } weights[2] = {{q_weight, "q_weight", &p->qw, &p->qw_f32}, {k_weight, "k_weight", &p->kw, &p->kw_f32}};
+  for (auto& w : weights) {
+    if (!w.w) continue;
+    const bool f32 = w.w->dtype == PKV_DTYPE_F32;
+    if ((rc = check_tensor(w.w, w.name, f32 ? PKV_DTYPE_F32 : PKV_DTYPE_BF16, 1))) return rc;
+    if (w.w->shape[0] != D || w.w->stride[0] != 1)
+      return fail(PKV_ERR_INVALID_ARG, "%s must be a contiguous [%lld]", w.name, (long long)D);
+    if (reinterpret_cast<uintptr_t>(w.w->data) % (f32 ? 4 : 2))
+      return fail(PKV_ERR_ALIGNMENT, "%s is not aligned to its elements", w.name);
+    *w.data = w.w->data;
+    *w.f32 = f32;
+  }
+  if (k_weight && !k) return fail(PKV_ERR_INVALID_ARG, "k_weight without k");
+  if ((q_weight || k_weight) && !(std::isfinite(eps) && eps >= 0))
+    return fail(PKV_ERR_INVALID_ARG, "eps %g", double(eps));
+  if (rope) {
+    const int64_t rot = 2 * rope->shape[0];
+    if (rope->shape[1] != 2 || rope->stride[1] != 1 || rope->stride[0] != 2)
+      return fail(PKV_ERR_INVALID_ARG, "rope must be a contiguous [rot_dim / 2, 2] of pkv_rope_table");
+    if (rot < 16 || rot % 16 || rot > D)
+      return fail(PKV_ERR_UNSUPPORTED, "rot_dim %lld (multiples of 16 up to %lld are built)",
+                  (long long)rot, (long long)D);
+    if (reinterpret_cast<uintptr_t>(rope->data) % 8)
+      return fail(PKV_ERR_ALIGNMENT, "rope must be 8-byte aligned");
+    if (!std::isfinite(rope_factor)) return fail(PKV_ERR_INVALID_ARG, "rope_factor is not finite");
+    p->turns = static_cast<const uint2*>(rope->data);
+    p->rot = int(rot);
+  }
+  for (const pkv_tensor* x : {q, k, q_out}) {
+    if (!x) continue;
+    if (x->stride[2] != 1)
+      return fail(PKV_ERR_INVALID_ARG, "q, k and q_out last dims must be contiguous");
+    if (x->stride[0] % 8 || x->stride[1] % 8 || !aligned16(x->data))
+      return fail(PKV_ERR_ALIGNMENT, "q, k and q_out rows must be 16-byte aligned");
+  }
+  if ((rc = check_distinct_rows(q_out, "q_out"))) return rc;
+  if (!same_view(q_out, q) && !apart(q_out, q))
+    return fail(PKV_ERR_INVALID_ARG, "q_out overlaps q (it may be q itself)");
+  if (k && !apart(q_out, k)) return fail(PKV_ERR_INVALID_ARG, "q_out overlaps k");
+  if ((rc = check_no_overlap({{q_out, "q_out"}}, {{q_weight, "q_weight"}, {k_weight, "k_weight"},
+                                                  {positions, "positions"}, {rope, "rope"}})))
+    return rc;
+  p->q = static_cast<const uint16_t*>(q->data);
+  p->q_st = q->stride[0];
+  p->q_sh = q->stride[1];
+  p->q_out = static_cast<uint16_t*>(q_out->data);
+  p->qo_st = q_out->stride[0];
+  p->qo_sh = q_out->stride[1];
+  if (k) {
+    p->k = static_cast<const uint16_t*>(k->data);
+    p->k_st = k->stride[0];
+    p->k_sh = k->stride[1];
+  }
+  p->eps = eps;
+  p->positions = positions ? static_cast<const int32_t*>(positions->data) : nullptr;
+  p->factor = rope_factor;
+  p->T = T;
+  p->Hq = int(Hq);
+  p->Hkv = k ? int(k->shape[1]) : 0;
+  p->D = int(D);
+  return PKV_OK;
+}
+
+PKV_API int pkv_qk_norm_rope(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* q_weight,
+                             const pkv_tensor* k_weight, float eps, const pkv_tensor* positions,
+                             const pkv_tensor* rope, float rope_factor, int interleaved,
+                             const pkv_tensor* q_out, const pkv_tensor* k_out, void* stream_ptr) {
+  int rc;
+  pkv::RopeParams p;
+  std::memset(&p, 0, sizeof p);
+  if ((rc = check_rope(q, k, q_weight, k_weight, eps, positions, rope, rope_factor, q_out, &p)))
+    return rc;
+  if (!k != !k_out) return fail(PKV_ERR_INVALID_ARG, "k and k_out go together");
+  if (rope && !positions) return fail(PKV_ERR_INVALID_ARG, "positions is NULL");
+  if (k_out) {
+    if ((rc = check_tensor(k_out, "k_out", PKV_DTYPE_BF16, 3))) return rc;
+    for (int i = 0; i < 3; ++i)
+      if (k_out->shape[i] != k->shape[i])
+        return fail(PKV_ERR_INVALID_ARG, "k_out must have the shape of k");
+    if (k_out->stride[2] != 1)
+      return fail(PKV_ERR_INVALID_ARG, "k_out last dim must be contiguous");
+    if (k_out->stride[0] % 8 || k_out->stride[1] % 8 || !aligned16(k_out->data))
+      return fail(PKV_ERR_ALIGNMENT, "k_out rows must be 16-byte aligned");
+    if ((rc = check_distinct_rows(k_out, "k_out"))) return rc;
+    if (!same_view(k_out, k) && !apart(k_out, k))
+      return fail(PKV_ERR_INVALID_ARG, "k_out overlaps k (it may be k itself)");
+    if (!apart(k_out, q)) return fail(PKV_ERR_INVALID_ARG, "k_out overlaps q");
+    if (!apart(k_out, q_out)) return fail(PKV_ERR_INVALID_ARG, "k_out overlaps q_out");
+    if ((rc = check_no_overlap({{k_out, "k_out"}}, {{q_weight, "q_weight"}, {k_weight, "k_weight"},
+                                                    {positions, "positions"}, {rope, "rope"}})))
+      return rc;
+    p.k_out = static_cast<uint16_t*>(k_out->data);
+    p.ko_st = k_out->stride[0];
+    p.ko_sh = k_out->stride[1];
+  }
+  p.interleaved = interleaved != 0;
+  if (p.T == 0) return PKV_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  int dev = 0, sms = 0;
+  if ((rc = device_of(q, "q", stream, &dev))) return rc;
+  cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = pkv::launch_rope(p, sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "qk norm and rotation launch");
+  return PKV_OK;
+}
+
+PKV_API int pkv_gqa_rope_append(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* v,
+                                const pkv_tensor* q_weight, const pkv_tensor* k_weight, float eps,
+                                const pkv_tensor* positions, const pkv_tensor* rope,
+                                float rope_factor, int interleaved, const pkv_tensor* kv_cache,
+                                const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                                const pkv_tensor* cu_tokens, int page_size,
+                                const pkv_tensor* q_out, void* stream_ptr) {
+  int rc;
+  pkv::RopeParams p;
+  std::memset(&p, 0, sizeof p);
+  if (!k) return fail(PKV_ERR_INVALID_ARG, "k is NULL");
+  if ((rc = check_rope(q, k, q_weight, k_weight, eps, positions, rope, rope_factor, q_out, &p)))
+    return rc;
+  if ((rc = check_tensor(v, "v", PKV_DTYPE_BF16, 3))) return rc;
+  if ((rc = check_tensor(kv_cache, "kv_cache", PKV_DTYPE_BF16, 4))) return rc;
+  if ((rc = check_tensor(block_table, "block_table", PKV_DTYPE_I32, 2))) return rc;
+  if ((rc = check_tensor(seq_lens, "seq_lens", PKV_DTYPE_I32, 1))) return rc;
+  if (cu_tokens && (rc = check_tensor(cu_tokens, "cu_tokens", PKV_DTYPE_I32, 1))) return rc;
+  const int64_t T = p.T, D = p.D, B = seq_lens->shape[0];
+  for (int i = 0; i < 3; ++i)
+    if (v->shape[i] != k->shape[i]) return fail(PKV_ERR_INVALID_ARG, "v must have the shape of k");
+  if (v->stride[2] != 1) return fail(PKV_ERR_INVALID_ARG, "v last dim must be contiguous");
+  if (v->stride[0] % 8 || v->stride[1] % 8 || !aligned16(v->data))
+    return fail(PKV_ERR_ALIGNMENT, "v rows must be 16-byte aligned");
+  if ((rc = check_paged_cache(kv_cache, nullptr, false, D, page_size))) return rc;
+  if (kv_cache->shape[1] != p.Hkv)
+    return fail(PKV_ERR_INVALID_ARG, "k has %d heads, kv_cache %lld", p.Hkv,
+                (long long)kv_cache->shape[1]);
+  if ((rc = check_distinct_rows(kv_cache, "kv_cache"))) return rc;
+  if ((rc = check_requests(block_table, seq_lens, B, page_size))) return rc;
+  if (B >= (int64_t(1) << 31)) return fail(PKV_ERR_UNSUPPORTED, "%lld requests", (long long)B);
+  if (cu_tokens && (cu_tokens->shape[0] != B + 1 || (B > 0 && cu_tokens->stride[0] != 1)))
+    return fail(PKV_ERR_INVALID_ARG, "cu_tokens must be a contiguous [B + 1]");
+  if (!cu_tokens && (B == 0 ? T != 0 : T % B != 0))
+    return fail(PKV_ERR_INVALID_ARG, "%lld tokens do not divide among %lld requests (cu_tokens)",
+                (long long)T, (long long)B);
+  if (!apart(q_out, v)) return fail(PKV_ERR_INVALID_ARG, "q_out overlaps v");
+  if ((rc = check_no_overlap({{q_out, "q_out"}, {kv_cache, "kv_cache"}},
+                             {{block_table, "block_table"}, {seq_lens, "seq_lens"},
+                              {cu_tokens, "cu_tokens"}})) ||
+      (rc = check_no_overlap({{kv_cache, "kv_cache"}},
+                             {{q, "q"}, {k, "k"}, {v, "v"}, {q_weight, "q_weight"},
+                              {k_weight, "k_weight"}, {positions, "positions"}, {rope, "rope"}})))
+    return rc;
+  if (B == 0 || T == 0) return PKV_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  int dev = 0;
+  if ((rc = device_of(q, "q", stream, &dev))) return rc;
+  DeviceState* st = nullptr;
+  bool capturing = false;
+  if ((rc = workspace_for(dev, stream, &st, &capturing))) return rc;
+  p.interleaved = interleaved != 0;
+  p.v = static_cast<const uint16_t*>(v->data);
+  p.v_st = v->stride[0];
+  p.v_sh = v->stride[1];
+  p.cache = static_cast<uint16_t*>(kv_cache->data);
+  p.c_sblk = kv_cache->stride[0];
+  p.c_sh = kv_cache->stride[1];
+  p.c_stok = kv_cache->stride[2];
+  p.bt = static_cast<const int32_t*>(block_table->data);
+  p.bt_sb = block_table->stride[0];
+  p.max_blocks = int(block_table->shape[1]);
+  p.num_blocks = int(kv_cache->shape[0]);
+  p.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  p.cu = cu_tokens ? static_cast<const int32_t*>(cu_tokens->data) : nullptr;
+  p.B = int(B);
+  p.page_size = page_size;
+  p.err = st->ws.err;
+  unsigned long long capture = 0;
+  if ((rc = capture_of(stream, capturing, &capture))) return rc;
+  std::lock_guard<std::mutex> lock(g_launch_mu[dev]);
+  const cudaError_t e = pkv::launch_rope(p, st->ws.num_sms, stream);
+  // Several tokens of a request can lie on pages that the next attention call reads ahead of
+  // its wait (a single token's page it does not): ordered as after the page calls.
+  if ((cu_tokens || T != B) && st->pages.wrote(stream, capture) &&
+      (rc = order_after_pages(st, stream)))
+    return rc;
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "norm, rotation and append launch");
 }
 
 // ------------------------------------------------------------ cache pages --

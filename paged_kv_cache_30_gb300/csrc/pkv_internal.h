@@ -297,6 +297,34 @@ struct AppendFp8Params {
 };
 cudaError_t launch_gqa_kv_append_fp8(const AppendFp8Params& p, cudaStream_t stream);
 
+// ---------------------------------------- head norms and rotation of q and k --
+// cache != null: keys and values go into the paged cache, else keys go to k_out.
+struct RopeParams {
+  const uint16_t *q, *k, *v;     // bf16 [T, Hq, D], [T, Hkv, D]; v with the cache alone
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;  // strides (elements): token, head
+  const void *qw, *kw;           // [D] weights of the norms, or null
+  int qw_f32, kw_f32;            // fp32 (else bf16)
+  float eps;
+  const int32_t* positions;      // [T] or null (cache: a token's place in its request)
+  const uint2* turns;            // [rot / 2]: turns per position, units of 2^-64
+  float factor;                  // of cosines and sines
+  int rot, interleaved;          // rot 0: no rotation
+  uint16_t *q_out, *k_out;
+  int64_t qo_st, qo_sh, ko_st, ko_sh;
+  int64_t T;
+  int Hq, Hkv, D;
+  uint16_t* cache;               // bf16 [num_blocks, Hkv, P, 2D] or null
+  int64_t c_sblk, c_sh, c_stok;  // elements
+  const int32_t* bt;
+  int64_t bt_sb;
+  int max_blocks, num_blocks;
+  const int32_t* seq_lens;
+  const int32_t* cu;             // [B + 1] or null (T / B tokens each)
+  int B, page_size;
+  int* err;
+};
+cudaError_t launch_rope(const RopeParams& p, int num_sms, cudaStream_t stream);
+
 // ---------------------------------------------------------- cache pages --
 constexpr int kPagesMaxRows = 8192;    // rows of a block table that a page call works on
 constexpr int kPagesMaxTensors = 64;   // tensors of one pages_copy call

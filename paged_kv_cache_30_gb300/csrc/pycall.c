@@ -1,4 +1,4 @@
-/* pycall.c -- the binding of the 8-bit cache, window and page calls, on the CPython C API.
+/* pycall.c -- the binding of the 8-bit cache, window, rotation and page calls, on the CPython C API.
  *
  * It does what a ctypes call does (tensors to pkv_tensor descriptors, the current stream, an
  * exception for a negative status) in compiled code: these calls come many times a step and take
@@ -27,9 +27,17 @@ typedef int (*trim_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, 
 typedef int (*compact_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, int,
                           const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, void*);
 typedef int (*copy_fn)(const pkv_tensor* const*, int, const pkv_tensor*, const pkv_tensor*, void*);
+typedef int (*rope_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, const pkv_tensor*,
+                       float, const pkv_tensor*, const pkv_tensor*, float, int, const pkv_tensor*,
+                       const pkv_tensor*, void*);
+typedef int (*rope_append_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*,
+                              const pkv_tensor*, const pkv_tensor*, float, const pkv_tensor*,
+                              const pkv_tensor*, float, int, const pkv_tensor*, const pkv_tensor*,
+                              const pkv_tensor*, const pkv_tensor*, int, const pkv_tensor*, void*);
 typedef const char* (*text_fn)(void);
 
-enum { ATTN8, WINDOW, APPEND, FORK, RELEASE, RESERVE, COMPACT, COPY, TRIM, LAST_ERROR, NUM_FNS };
+enum { ATTN8, WINDOW, APPEND, FORK, RELEASE, RESERVE, COMPACT, COPY, TRIM, ROPE, ROPE_APPEND,
+       LAST_ERROR, NUM_FNS };
 enum { MAX_TENSORS = 66 }; /* 64 page tensors and two lists */
 
 static void* fns[NUM_FNS];
@@ -295,6 +303,37 @@ static PyObject* copy(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return bad ? NULL : status(rc);
 }
 
+/* q, k, q_weight, k_weight, eps, positions, rope, rope_factor, interleaved, q_out, k_out, stream */
+static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const int at[8] = {0, 1, 2, 3, 5, 6, 9, 10};
+  pkv_tensor d[8];
+  const pkv_tensor* p[8];
+  int pairs;
+  float eps, factor;
+  void* s;
+  if (count_args(n, 12) || describe_all(a, at, 8, d, p) || float_of(a[4], &eps) ||
+      float_of(a[7], &factor) || int_of(a[8], &pairs) || stream_of(a[11], a[0], &s))
+    return NULL;
+  CALL(((rope_fn)fns[ROPE])(p[0], p[1], p[2], p[3], eps, p[4], p[5], factor, pairs, p[6], p[7], s));
+}
+
+/* q, k, v, q_weight, k_weight, eps, positions, rope, rope_factor, interleaved, kv_cache,
+ * block_table, seq_lens, cu_tokens, page_size, q_out, stream */
+static PyObject* rope_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const int at[12] = {0, 1, 2, 3, 4, 6, 7, 10, 11, 12, 13, 15};
+  pkv_tensor d[12];
+  const pkv_tensor* p[12];
+  int pairs, page;
+  float eps, factor;
+  void* s;
+  if (count_args(n, 17) || describe_all(a, at, 12, d, p) || float_of(a[5], &eps) ||
+      float_of(a[8], &factor) || int_of(a[9], &pairs) || int_of(a[14], &page) ||
+      stream_of(a[16], a[0], &s))
+    return NULL;
+  CALL(((rope_append_fn)fns[ROPE_APPEND])(p[0], p[1], p[2], p[3], p[4], eps, p[5], p[6], factor,
+                                          pairs, p[7], p[8], p[9], p[10], page, p[11], s));
+}
+
 /* bind(addresses in the order of the enum, torch dtypes of codes 1..4, current stream of a
  * device index, exception type) */
 static PyObject* bind(PyObject* self, PyObject* args) {
@@ -332,6 +371,8 @@ static PyMethodDef methods[] = {
     METHOD("pages_compact", compact),
     METHOD("pages_copy", copy),
     METHOD("pages_trim", trim),
+    METHOD("qk_norm_rope", rope),
+    METHOD("gqa_rope_append", rope_append),
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkvcall", NULL, -1, methods};
