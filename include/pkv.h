@@ -30,6 +30,9 @@
  *    pkv_gqa_kv_append_fp8 writes tokens (one each, or whole prompts) into the
  *    e4m3 cache.
  *
+ *  - pkv_paged_prefix_attn / _fp8: the same decode where groups of requests share
+ *    their first tokens, which are read once for a group.
+ *
  *  - pkv_qk_norm_rope, pkv_gqa_rope_append: norms of query and key heads and their
  *    rotation by position, to memory or, with the values, into the bf16 cache.
  *
@@ -84,7 +87,7 @@
  *    the wait.  The pkv_pages_* calls write tables, lengths and pages: the first
  *    attention call after one on its stream waits for it to end (the library
  *    puts a 4-byte memset between them, in streams and in captures
- *    apart), so no care is needed there.
+ *    apart), so no care is needed there, nor after pkv_gqa_rope_append.
  *  - The launch shape depends only on the device and the batch size, never on
  *    the sequence lengths or the block table, which the kernels read on the
  *    device: a captured graph stays valid when seq_lens and block_table change.
@@ -472,6 +475,50 @@ PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
                                   const pkv_tensor* sinks, int window, int first_tokens, float scale,
                                   int page_size, const pkv_tensor* out, const pkv_tensor* lse,
                                   void* stream);
+
+/*
+ * pkv_paged_prefix_attn -- pkv_paged_window_attn without a window, where groups of
+ * requests hold the same first tokens (a forked prompt, a common system prompt):
+ * those keys and values are read once for all query rows of a group, as one matrix
+ * product, and each request's own tokens after them.
+ *   q, kv_cache, sinks, scale, page_size, out, lse  as pkv_paged_window_attn.
+ *   block_table, seq_lens  as there: whole rows and lengths, shared tokens included.
+ *   cu_groups    int32 [groups + 1], non-decreasing, within [0, B]: group g is requests
+ *                [cu_groups[g], cu_groups[g + 1]) (none if equal; one alone shares with
+ *                nobody).  Requests outside [cu_groups[0], cu_groups[groups]) are padding
+ *                and are not written.
+ *   shared_lens  int32 [groups]: tokens [0, shared_lens[g]) are the same in every request
+ *                of the group; they are read through the table row of its first request
+ *                that is not empty.  0: nothing is shared.
+ * out and lse are those of pkv_paged_window_attn on the same rows.  A request of length 0
+ * writes zeros and lse = -inf and is otherwise ignored; one that is shorter than
+ * shared_lens[g] cuts what its group shares to its own length.  What is shared is counted
+ * in whole 16-token boxes.  groups <= 2048; offsets that decrease or leave [0, B] raise bit
+ * 64 of the device error word, and all requests are then attended to on their own.
+ * The workspace holds 2 B x 16 + (B Hq + 256 SMs) (4 D + 8) bytes of it next to what
+ * pkv_paged_window_attn needs (PKV_ERR_WORKSPACE).
+ * The weights are rounded to bf16 (2^-9 of themselves).  Two launches; nothing is read
+ * before the dependency wait.  Errors as pkv_paged_decode_attn_fp8.
+ */
+PKV_API int pkv_paged_prefix_attn(const pkv_tensor* q, const pkv_tensor* kv_cache,
+                                  const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                                  const pkv_tensor* cu_groups, const pkv_tensor* shared_lens,
+                                  const pkv_tensor* sinks, float scale, int page_size,
+                                  const pkv_tensor* out, const pkv_tensor* lse, void* stream);
+
+/*
+ * pkv_paged_prefix_attn_fp8 -- the same over an e4m3 cache with a scale for K and one
+ * for V per (page, kv head).
+ *   kv_cache, kv_scale  as pkv_paged_decode_attn_fp8.
+ * The weights of shared tokens, times their values' scale, are rounded to bf16; those of
+ * a request's own tokens as in pkv_paged_decode_attn_fp8.
+ */
+PKV_API int pkv_paged_prefix_attn_fp8(const pkv_tensor* q, const pkv_tensor* kv_cache,
+                                      const pkv_tensor* kv_scale, const pkv_tensor* block_table,
+                                      const pkv_tensor* seq_lens, const pkv_tensor* cu_groups,
+                                      const pkv_tensor* shared_lens, const pkv_tensor* sinks,
+                                      float scale, int page_size, const pkv_tensor* out,
+                                      const pkv_tensor* lse, void* stream);
 
 /*
  * pkv_gqa_kv_append_fp8 -- write new tokens into an e4m3 cache with a scale for

@@ -21,6 +21,10 @@ Names follow the C ABI without its ``pkv_`` prefix:
                           first_tokens, scale, page_size, out, lse=None, stream=None)
     paged_window_attn(q, kv_cache, block_table, seq_lens, sinks, window, first_tokens,
                       scale, page_size, out, lse=None, stream=None)
+    paged_prefix_attn(q, kv_cache, block_table, seq_lens, cu_groups, shared_lens, sinks,
+                      scale, page_size, out, lse=None, stream=None)
+    paged_prefix_attn_fp8(q, kv_cache, kv_scale, block_table, seq_lens, cu_groups,
+                          shared_lens, sinks, scale, page_size, out, lse=None, stream=None)
     gqa_kv_append_fp8(k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens,
                       page_size, stream=None)
     rope_table(rot_dim, base=10000.0, factor=1.0, original_len=0, low=1.0, high=4.0,
@@ -57,7 +61,7 @@ __all__ = [
     "mla_verify_attn", "gqa_kv_append", "mla_kv_append", "num_kv_splits", "check_errors", "check_counters", "shutdown",
     "paged_decode_attn_fp8", "paged_window_attn", "gqa_kv_append_fp8", "pages_fork",
     "pages_release", "pages_trim", "pages_reserve", "pages_compact", "pages_copy",
-    "rope_table", "qk_norm_rope", "gqa_rope_append",
+    "rope_table", "qk_norm_rope", "gqa_rope_append", "paged_prefix_attn", "paged_prefix_attn_fp8",
     "version", "last_error",
 ]
 
@@ -93,7 +97,7 @@ _call = None  # the compiled binding of the calls that come many times a step (c
 _CALLS = ("pkv_paged_decode_attn_fp8", "pkv_paged_window_attn", "pkv_gqa_kv_append_fp8",
           "pkv_pages_fork", "pkv_pages_release", "pkv_pages_reserve", "pkv_pages_compact",
           "pkv_pages_copy", "pkv_pages_trim", "pkv_qk_norm_rope", "pkv_gqa_rope_append",
-          "pkv_last_error")
+          "pkv_paged_prefix_attn_fp8", "pkv_paged_prefix_attn", "pkv_last_error")
 
 
 def _calls():
@@ -156,6 +160,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.pkv_rope_table.argtypes = [ctypes.POINTER(f64), i32, f64, f64, f64, f64, f64,
                                        ctypes.POINTER(ctypes.c_int32)]
         lib.pkv_qk_norm_rope.argtypes = [T, T, T, T, f32, T, T, f32, i32, T, T, vp]
+        lib.pkv_paged_prefix_attn_fp8.argtypes = [T, T, T, T, T, T, T, T, f32, i32, T, T, vp]
+        lib.pkv_paged_prefix_attn.argtypes = [T, T, T, T, T, T, T, f32, i32, T, T, vp]
         lib.pkv_gqa_rope_append.argtypes = [T, T, T, T, T, f32, T, T, f32, i32, T, T, T, T, i32, T, vp]
         lib.pkv_num_kv_splits.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_double, i32, i32]
         lib.pkv_check_errors.argtypes = [i32, ctypes.POINTER(ctypes.c_int32)]
@@ -170,7 +176,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                      "pkv_paged_window_attn", "pkv_gqa_kv_append_fp8", "pkv_pages_fork",
                      "pkv_pages_release", "pkv_pages_reserve", "pkv_pages_compact",
                      "pkv_pages_copy", "pkv_pages_trim", "pkv_rope_table", "pkv_qk_norm_rope",
-                     "pkv_gqa_rope_append", "pkv_shutdown", "pkv_version"):
+                     "pkv_gqa_rope_append", "pkv_paged_prefix_attn",
+                     "pkv_paged_prefix_attn_fp8", "pkv_shutdown", "pkv_version"):
             getattr(lib, name).restype = i32
         if path is None:
             _lib = lib
@@ -351,6 +358,26 @@ def paged_window_attn(q, kv_cache, block_table, seq_lens, sinks, window, first_t
     (and ``lse`` if given) in place and returns ``out``."""
     (_call or _calls()).paged_window_attn(q, kv_cache, block_table, seq_lens, sinks, window,
                                           first_tokens, scale, page_size, out, lse, stream)
+    return out
+
+
+def paged_prefix_attn(q, kv_cache, block_table, seq_lens, cu_groups, shared_lens, sinks, scale,
+                      page_size, out, lse=None, stream=None):
+    """GQA paged decode attention over a bf16 cache where requests cu_groups[g] ..
+    cu_groups[g + 1] - 1 hold the same first shared_lens[g] tokens (as after pages_fork):
+    those are read once for all of them (C: pkv_paged_prefix_attn).  Writes ``out`` (and
+    ``lse`` if given) in place and returns ``out``."""
+    (_call or _calls()).paged_prefix_attn(q, kv_cache, block_table, seq_lens, cu_groups, shared_lens,
+                                          sinks, scale, page_size, out, lse, stream)
+    return out
+
+
+def paged_prefix_attn_fp8(q, kv_cache, kv_scale, block_table, seq_lens, cu_groups, shared_lens,
+                          sinks, scale, page_size, out, lse=None, stream=None):
+    """paged_prefix_attn over an e4m3 cache with fp32 scales ``kv_scale`` [num_blocks, Hkv, 2]
+    (K, V) per page and kv head (C: pkv_paged_prefix_attn_fp8)."""
+    (_call or _calls()).paged_prefix_attn_fp8(q, kv_cache, kv_scale, block_table, seq_lens, cu_groups,
+                                              shared_lens, sinks, scale, page_size, out, lse, stream)
     return out
 
 

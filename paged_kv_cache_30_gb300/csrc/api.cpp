@@ -1105,11 +1105,36 @@ PKV_API int pkv_mla_kv_append(const pkv_tensor* latent, const pkv_tensor* latent
 
 // ------------------------------------- decode with a window and first tokens --
 // Both entry points: kv_scale == nullptr is the bf16 cache.
+// The cache as a tensor map of boxes of 16 tokens: `pieces` pieces of `elems` elements a row.
+static int encode_paged_map(EncodeTiledFn encode, const pkv_tensor* kv_cache, bool fp8, int page_size,
+                            int64_t elems, int64_t pieces, int64_t box_pieces, bool swizzle,
+                            CUtensorMap* map) {
+  const cuuint64_t esz = fp8 ? 1 : 2;
+  const cuuint64_t gdim[5] = {cuuint64_t(elems), cuuint64_t(page_size), cuuint64_t(pieces),
+                              cuuint64_t(kv_cache->shape[1]), cuuint64_t(kv_cache->shape[0])};
+  const cuuint64_t gstride[4] = {cuuint64_t(kv_cache->stride[2]) * esz, cuuint64_t(elems) * esz,
+                                 cuuint64_t(kv_cache->stride[1]) * esz,
+                                 cuuint64_t(kv_cache->stride[0]) * esz};
+  const cuuint32_t box[5] = {cuuint32_t(elems), 16, cuuint32_t(box_pieces), 1, 1};
+  const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+  const CUresult cr = encode(
+      map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, kv_cache->data,
+      gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (cr != CUDA_SUCCESS)
+    return fail(PKV_ERR_INVALID_ARG, "cuTensorMapEncodeTiled rejected the kv_cache layout (%d)", (int)cr);
+  return PKV_OK;
+}
+
+// cu_groups (with shared_lens): the calls for groups of requests with shared tokens.
 static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool fp8,
                            const pkv_tensor* kv_scale, const pkv_tensor* block_table,
                            const pkv_tensor* seq_lens, const pkv_tensor* sinks, int window,
                            int first_tokens, float scale, int page_size, const pkv_tensor* out,
-                           const pkv_tensor* lse, void* stream_ptr) {
+                           const pkv_tensor* lse, void* stream_ptr, bool grouped = false,
+                           const pkv_tensor* cu_groups = nullptr,
+                           const pkv_tensor* shared_lens = nullptr) {
   int rc;
   if ((rc = check_tensor(q, "q", PKV_DTYPE_BF16, 3))) return rc;
   if ((rc = check_tensor(kv_cache, "kv_cache", fp8 ? PKV_DTYPE_FP8_E4M3 : PKV_DTYPE_BF16, 4)))
@@ -1120,8 +1145,16 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   if (sinks && (rc = check_tensor(sinks, "sinks", PKV_DTYPE_F32, 1))) return rc;
   if ((rc = check_tensor(out, "out", PKV_DTYPE_BF16, 3))) return rc;
   if (lse && (rc = check_tensor(lse, "lse", PKV_DTYPE_F32, 2))) return rc;
+  if (grouped && (rc = check_tensor(cu_groups, "cu_groups", PKV_DTYPE_I32, 1))) return rc;
+  if (grouped && (rc = check_tensor(shared_lens, "shared_lens", PKV_DTYPE_I32, 1))) return rc;
   const int64_t B = q->shape[0], Hq = q->shape[1], D = q->shape[2], Hkv = kv_cache->shape[1];
+  const int64_t groups = grouped ? shared_lens->shape[0] : 0;
   if ((rc = check_paged_cache(kv_cache, kv_scale, fp8, D, page_size))) return rc;
+  if (grouped && (groups > pkv::kPagedMaxBatch || cu_groups->shape[0] != groups + 1 ||
+                  cu_groups->stride[0] != 1 || (groups > 1 && shared_lens->stride[0] != 1)))
+    return fail(PKV_ERR_INVALID_ARG,
+                "cu_groups must be a contiguous [groups + 1], shared_lens a contiguous [groups], "
+                "groups at most %d", pkv::kPagedMaxBatch);
   if (Hq < 1 || Hq % Hkv)
     return fail(PKV_ERR_INVALID_ARG, "num_q_heads %lld is no multiple of num_kv_heads %lld",
                 (long long)Hq, (long long)Hkv);
@@ -1151,9 +1184,10 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   if ((rc = check_no_overlap({{out, "out"}, {lse, "lse"}},
                              {{q, "q"}, {kv_cache, "kv_cache"}, {kv_scale, "kv_scale"},
                               {block_table, "block_table"}, {seq_lens, "seq_lens"},
-                              {sinks, "sinks"}})))
+                              {sinks, "sinks"}, {cu_groups, "cu_groups"},
+                              {shared_lens, "shared_lens"}})))
     return rc;
-  if (B == 0) return PKV_OK;
+  if (B == 0 || (grouped && groups == 0)) return PKV_OK;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   int dev = 0;
   if ((rc = device_of(q, "q", stream, &dev))) return rc;
@@ -1204,6 +1238,30 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
     return fail(PKV_ERR_UNSUPPORTED, "%lld requests x %lld kv heads of up to %lld tiles of 16 keys",
                 (long long)B, (long long)Hkv, (long long)tiles);
   const pkv::Workspace& ws = st->ws;
+  // The parts of the shared tokens come first in the workspace.
+  pkv::PrefixParams x;
+  std::memset(&x, 0, sizeof x);
+  int64_t prefix_bytes = 0;
+  if (grouped) {
+    // units: a group of n requests has (n G + 255) / 256 for each kv head, if n > 1
+    const int64_t units = Hkv * (B * p.G / pkv::kPrefixRows + std::min(groups, B / 2));
+    if (units * (width + pkv::kPrefixUnitCost) >= (int64_t(1) << 31) - 4096)
+      return fail(PKV_ERR_UNSUPPORTED, "%lld units of up to %lld boxes of 16 keys", (long long)units,
+                  (long long)width);
+    x.cu_groups = static_cast<const int32_t*>(cu_groups->data);
+    x.shared_lens = static_cast<const int32_t*>(shared_lens->data);
+    x.groups = int(groups);
+    x.grid = ws.num_sms;
+    prefix_bytes = (pkv::prefix_workspace_bytes(B, Hq, D, x.grid) + 255) / 256 * 256;
+    const int64_t rows = B * Hq, rest = int64_t(x.grid) * pkv::kPrefixRows;
+    uint8_t* at = reinterpret_cast<uint8_t*>(ws.partials);
+    x.info = reinterpret_cast<int4*>(at);
+    x.first_o = reinterpret_cast<float4*>(at += 2 * B * 16);
+    x.rest_o = reinterpret_cast<float4*>(at += rows * D * 4);
+    x.first_ml = reinterpret_cast<float2*>(at += rest * D * 4);
+    x.rest_ml = reinterpret_cast<float2*>(at += rows * 8);
+  }
+  const int64_t free_bytes = int64_t(ws.partial_bytes) - prefix_bytes;
   const int64_t slots = int64_t(ws.num_sms) * shape.ctas_per_sm, pairs = B * Hkv;
   const int64_t cost = pairs * (tiles + pkv::kPagedPairCost);
   p.grid = int(std::max<int64_t>(
@@ -1221,7 +1279,7 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   // mode), and in waves that are 56 % full 64 x 8 of up to 1500 keys 29.4 instead of 25.9.
   // A full wave of very unequal lengths loses: 40 x 8 of 10 to 1500 keys, 23.4 / 19.4.
   const int64_t part_bytes = int64_t(shape.part_floats) * 4;
-  if (pairs <= 2 * slots) {
+  if (!grouped && pairs <= 2 * slots) {
     const int64_t c = std::max<int64_t>(
         1, std::min({int64_t(pkv::kPagedMaxCluster), slots * 7 / 8 / pairs, (tiles + 15) / 16}));
     const bool full = c == 1 && 3 * pairs >= 2 * ((pairs + slots - 1) / slots * slots);
@@ -1231,44 +1289,37 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
     }
   }
   if (!p.cluster) {  // two partials for each CTA (each warp): a small workspace runs fewer of them
-    const int64_t fit = int64_t(ws.partial_bytes) / (2 * part_bytes);
+    const int64_t fit = free_bytes / (2 * part_bytes);
     if (fit < 1)
       return fail(PKV_ERR_WORKSPACE, "workspace holds %lld bytes of partials, %lld needed",
-                  (long long)ws.partial_bytes, (long long)(2 * part_bytes));
+                  (long long)ws.partial_bytes, (long long)(prefix_bytes + 2 * part_bytes));
     p.grid = int(std::min<int64_t>(p.grid, fit));
     p.warps = fit >= pkv::kPagedWarps * p.grid;
   }
-  p.partials = ws.partials;
+  p.partials = ws.partials + prefix_bytes / 4;
   p.pair_counters = ws.counters;
   p.slot_counters = ws.counters + pkv::kTopCounters;
-  CUtensorMap map;
+  CUtensorMap map, group_map;
   EncodeTiledFn encode = nullptr;
   if ((rc = get_encoder(&encode))) return rc;
-  {
-    const cuuint64_t esz = fp8 ? 1 : 2, piece = 128 / esz;
-    const cuuint64_t gdim[5] = {piece, cuuint64_t(page_size), cuuint64_t(shape.chunks),
-                                cuuint64_t(Hkv), cuuint64_t(kv_cache->shape[0])};
-    const cuuint64_t gstride[4] = {cuuint64_t(kv_cache->stride[2]) * esz, 128,
-                                   cuuint64_t(kv_cache->stride[1]) * esz,
-                                   cuuint64_t(kv_cache->stride[0]) * esz};
-    const cuuint32_t box[5] = {cuuint32_t(piece), 16, cuuint32_t(shape.chunks), 1, 1};
-    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
-    const CUresult cr = encode(
-        &map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
-        kv_cache->data, gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (cr != CUDA_SUCCESS)
-      return fail(PKV_ERR_INVALID_ARG, "cuTensorMapEncodeTiled rejected the kv_cache layout (%d)",
-                  (int)cr);
-  }
+  if ((rc = encode_paged_map(encode, kv_cache, fp8, page_size, fp8 ? 128 : 64, shape.chunks,
+                             shape.chunks, true, &map)) ||
+      (grouped && (rc = encode_paged_map(encode, kv_cache, fp8, page_size, fp8 ? D : 64,
+                                         fp8 ? 2 : 2 * D / 64, 1, !fp8, &group_map))))
+    return rc;
   std::lock_guard<std::mutex> lock(g_launch_mu[dev]);
   if ((rc = order_streams(st, stream, capturing))) return rc;
   unsigned long long capture = 0;
   if ((rc = capture_of(stream, capturing, &capture))) return rc;
-  const cudaError_t e = pkv::launch_paged_attn(p, map, stream);
+  cudaError_t e = cudaSuccess;
+  if (grouped) {
+    e = pkv::launch_prefix_attn(p, x, group_map, stream);
+    if (e == cudaSuccess) e = pkv::launch_paged_behind(p, x, map, stream);
+  } else {
+    e = pkv::launch_paged_attn(p, map, stream);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
-  st->pages.settled(stream, capture);  // the kernel waits before it reads
+  st->pages.settled(stream, capture);  // the (first) kernel waits before it reads
   return PKV_OK;
 }
 
@@ -1288,6 +1339,25 @@ PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
                                   void* stream) {
   return paged_attn_impl(q, kv_cache, false, nullptr, block_table, seq_lens, sinks, window,
                          first_tokens, scale, page_size, out, lse, stream);
+}
+
+PKV_API int pkv_paged_prefix_attn(const pkv_tensor* q, const pkv_tensor* kv_cache,
+                                  const pkv_tensor* block_table, const pkv_tensor* seq_lens,
+                                  const pkv_tensor* cu_groups, const pkv_tensor* shared_lens,
+                                  const pkv_tensor* sinks, float scale, int page_size,
+                                  const pkv_tensor* out, const pkv_tensor* lse, void* stream) {
+  return paged_attn_impl(q, kv_cache, false, nullptr, block_table, seq_lens, sinks, 0, 0, scale,
+                         page_size, out, lse, stream, true, cu_groups, shared_lens);
+}
+
+PKV_API int pkv_paged_prefix_attn_fp8(const pkv_tensor* q, const pkv_tensor* kv_cache,
+                                      const pkv_tensor* kv_scale, const pkv_tensor* block_table,
+                                      const pkv_tensor* seq_lens, const pkv_tensor* cu_groups,
+                                      const pkv_tensor* shared_lens, const pkv_tensor* sinks,
+                                      float scale, int page_size, const pkv_tensor* out,
+                                      const pkv_tensor* lse, void* stream) {
+  return paged_attn_impl(q, kv_cache, true, kv_scale, block_table, seq_lens, sinks, 0, 0, scale,
+                         page_size, out, lse, stream, true, cu_groups, shared_lens);
 }
 
 PKV_API int pkv_gqa_kv_append_fp8(const pkv_tensor* k, const pkv_tensor* v,

@@ -278,6 +278,42 @@ constexpr int kPagedClusterTiles = 48;
 // but a batch with one such request among very short ones gives it dozens of parts.
 constexpr int kPagedWarpTiles = 64;
 
+// ------------------------------------- decode of groups with shared tokens --
+// Requests [cu_groups[g], cu_groups[g + 1]) share their first shared_lens[g] tokens.  One
+// grid (prefix_attn.cu) attends to what is shared, once for all rows of a group, and leaves
+// 32-bit (O, m, l) parts; the next (paged_attn.cuh) attends to each request's own tokens
+// and adds the parts.
+constexpr int kPrefixRows = 256;     // query rows of a unit: two tiles of 128
+constexpr int kPrefixTileKeys = 128; // keys of a step
+// A CTA's share is counted in 16-key boxes plus a cost for each unit, and is no smaller than
+// kPrefixMinShare (a multiple of a tile's boxes, so that every CTA of a cut unit has a tile).
+constexpr int kPrefixUnitCost = 24;
+constexpr int kPrefixMinShare = 32;
+struct PrefixParams {
+  const int32_t* cu_groups;      // [groups + 1]
+  const int32_t* shared_lens;    // [groups]
+  int groups, grid;
+  // per request: {first request, place of the group's first unit, shared boxes, share}, {row
+  // blocks of a kv head, -, -, -}
+  int4* info;                    // [2 B]
+  // the part of a unit's first CTA: rows b G + h of each kv head
+  float4* first_o;               // [Hkv][D / 4][B G]
+  float2* first_ml;              // [Hkv][B G]
+  // the part of a CTA whose range begins inside a unit
+  float4* rest_o;                // [grid][D / 4][kPrefixRows]
+  float2* rest_ml;               // [grid][kPrefixRows]
+};
+inline int64_t prefix_workspace_bytes(int64_t B, int64_t Hq, int64_t D, int64_t grid) {
+  return 2 * B * 16 + (B * Hq + grid * kPrefixRows) * (D * 4 + 8);
+}
+// kv_map: the cache as (64 dims, token, piece, kv head, page), box (64, 16, 1, 1, 1), 128-byte
+// swizzle; e4m3: (D, token, K | V, kv head, page), box (D, 16, 1, 1, 1), no swizzle.
+cudaError_t launch_prefix_attn(const PagedParams& p, const PrefixParams& x, const CUtensorMap& kv_map,
+                               cudaStream_t stream);
+// The grid after it; kv_map as launch_paged_attn's.
+cudaError_t launch_paged_behind(const PagedParams& p, const PrefixParams& x,
+                                const CUtensorMap& kv_map, cudaStream_t stream);
+
 // ------------------------------------------------ append to an e4m3 cache --
 struct AppendFp8Params {
   const uint16_t *k, *v;         // bf16 [T, Hkv, D]

@@ -34,10 +34,17 @@ typedef int (*rope_append_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_te
                               const pkv_tensor*, const pkv_tensor*, float, const pkv_tensor*,
                               const pkv_tensor*, float, int, const pkv_tensor*, const pkv_tensor*,
                               const pkv_tensor*, const pkv_tensor*, int, const pkv_tensor*, void*);
+typedef int (*prefix8_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*,
+                          const pkv_tensor*, const pkv_tensor*, const pkv_tensor*,
+                          const pkv_tensor*, const pkv_tensor*, float, int, const pkv_tensor*,
+                          const pkv_tensor*, void*);
+typedef int (*prefix_fn)(const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, const pkv_tensor*,
+                         const pkv_tensor*, const pkv_tensor*, const pkv_tensor*, float, int,
+                         const pkv_tensor*, const pkv_tensor*, void*);
 typedef const char* (*text_fn)(void);
 
 enum { ATTN8, WINDOW, APPEND, FORK, RELEASE, RESERVE, COMPACT, COPY, TRIM, ROPE, ROPE_APPEND,
-       LAST_ERROR, NUM_FNS };
+       PREFIX8, PREFIX, LAST_ERROR, NUM_FNS };
 enum { MAX_TENSORS = 66 }; /* 64 page tensors and two lists */
 
 static void* fns[NUM_FNS];
@@ -203,6 +210,37 @@ static PyObject* window_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return NULL;
   CALL(((window_fn)fns[WINDOW])(p[0], p[1], p[2], p[3], p[4], window, first, scale, page, p[5],
                                 p[6], s));
+}
+
+/* q, kv_cache, kv_scale, block_table, seq_lens, cu_groups, shared_lens, sinks, scale, page_size,
+ * out, lse, stream */
+static PyObject* prefix8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const int at[10] = {0, 1, 2, 3, 4, 5, 6, 7, 10, 11};
+  pkv_tensor d[10];
+  const pkv_tensor* p[10];
+  int page;
+  float scale;
+  void* s;
+  if (count_args(n, 13) || describe_all(a, at, 10, d, p) || float_of(a[8], &scale) ||
+      int_of(a[9], &page) || stream_of(a[12], a[0], &s))
+    return NULL;
+  CALL(((prefix8_fn)fns[PREFIX8])(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], scale, page, p[8],
+                                  p[9], s));
+}
+
+/* q, kv_cache, block_table, seq_lens, cu_groups, shared_lens, sinks, scale, page_size, out, lse,
+ * stream */
+static PyObject* prefix(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  static const int at[9] = {0, 1, 2, 3, 4, 5, 6, 9, 10};
+  pkv_tensor d[9];
+  const pkv_tensor* p[9];
+  int page;
+  float scale;
+  void* s;
+  if (count_args(n, 12) || describe_all(a, at, 9, d, p) || float_of(a[7], &scale) ||
+      int_of(a[8], &page) || stream_of(a[11], a[0], &s))
+    return NULL;
+  CALL(((prefix_fn)fns[PREFIX])(p[0], p[1], p[2], p[3], p[4], p[5], p[6], scale, page, p[7], p[8], s));
 }
 
 /* k, v, kv_cache, kv_scale, block_table, seq_lens, cu_tokens, page_size, stream */
@@ -371,6 +409,8 @@ static PyMethodDef methods[] = {
     METHOD("pages_compact", compact),
     METHOD("pages_copy", copy),
     METHOD("pages_trim", trim),
+    METHOD("paged_prefix_attn_fp8", prefix8),
+    METHOD("paged_prefix_attn", prefix),
     METHOD("qk_norm_rope", rope),
     METHOD("gqa_rope_append", rope_append),
     {NULL, NULL, 0, NULL}};
