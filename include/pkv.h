@@ -495,9 +495,9 @@ PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
  * shared_lens[g] cuts what its group shares to its own length.  What is shared is counted
  * in whole 16-token boxes.  groups <= 2048; offsets that decrease or leave [0, B] raise bit
  * 64 of the device error word, and all requests are then attended to on their own.
- * The workspace holds 2 B x 16 + (B Hq + 256 SMs) (4 D + 8) bytes of it next to what
+ * The workspace holds 16 B + B Hq (8 D + 24) + 256 SMs (4 D + 8) bytes of it next to what
  * pkv_paged_window_attn needs (PKV_ERR_WORKSPACE).
- * The weights are rounded to bf16 (2^-9 of themselves).  Two launches; nothing is read
+ * The weights are rounded to bf16 (2^-9 of themselves).  Three launches; nothing is read
  * before the dependency wait.  Errors as pkv_paged_decode_attn_fp8.
  */
 PKV_API int pkv_paged_prefix_attn(const pkv_tensor* q, const pkv_tensor* kv_cache,

@@ -18,7 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
 SOURCES = ["api.cpp", "gqa_decode.cu", "gqa_noalloc.cu", "mla_verify.cu", "mla_verify_native.cu",
            "mla_verify_pair.cu", "kv_append.cu", "paged_attn.cu", "kv_append_fp8.cu", "pages.cu",
-           "rope.cu", "prefix_attn.cu", "paged_behind.cu"]
+           "rope.cu", "prefix_attn.cu", "prefix_own.cu",
+           "prefix_combine.cu"]
 HEADERS = ["pkv_internal.h", "page_order.h", "ptx.cuh", "tcgen05.cuh", "mla_common.cuh",
            "paged_attn.cuh", "prefix_common.cuh"]
 PYCALL = os.path.join(BUILD, "_pkvcall.so")

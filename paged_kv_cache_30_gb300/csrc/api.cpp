@@ -1256,7 +1256,9 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
     const int64_t rows = B * Hq, rest = int64_t(x.grid) * pkv::kPrefixRows;
     uint8_t* at = reinterpret_cast<uint8_t*>(ws.partials);
     x.info = reinterpret_cast<int4*>(at);
-    x.first_o = reinterpret_cast<float4*>(at += 2 * B * 16);
+    x.own_o = reinterpret_cast<float4*>(at += B * 16);
+    x.own_ml = reinterpret_cast<float4*>(at += rows * D * 4);
+    x.first_o = reinterpret_cast<float4*>(at += rows * 16);
     x.rest_o = reinterpret_cast<float4*>(at += rows * D * 4);
     x.first_ml = reinterpret_cast<float2*>(at += rest * D * 4);
     x.rest_ml = reinterpret_cast<float2*>(at += rows * 8);
@@ -1314,7 +1316,8 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   cudaError_t e = cudaSuccess;
   if (grouped) {
     e = pkv::launch_prefix_attn(p, x, group_map, stream);
-    if (e == cudaSuccess) e = pkv::launch_paged_behind(p, x, map, stream);
+    if (e == cudaSuccess) e = pkv::launch_prefix_own(p, x, map, stream);
+    if (e == cudaSuccess) e = pkv::launch_prefix_combine(p, x, stream);
   } else {
     e = pkv::launch_paged_attn(p, map, stream);
   }

@@ -559,85 +559,44 @@ __device__ __forceinline__ void warp_finalize(const PagedParams& p, int b, int k
   }
 }
 
-// The shared tokens' parts (prefix_attn.cu) of row er of request b, dims [ed, ed + N),
-// merged into (o, m, l, R), in order.  A call, for the registers of the loop over tiles.
+// What a request's own tokens add up to, for prefix_combine.cu: row er, dims [ed, ed + N).
 template <class C, int N>
-__device__ __noinline__ void add_shared(const PagedParams& p, const PrefixParams& x, int b, int kvh,
-                                        int er, int ed, float (&o)[N], float& m, float& l, float& R) {
-  griddep_wait();  // the parts are another grid's
+__device__ __forceinline__ void store_own(const PagedParams& p, const PrefixParams& x, int b, int kvh,
+                                          int er, int ed, const float (&o)[N], float m, float l,
+                                          float R) {
   if (er >= p.G) return;
-  const SharedParts parts = shared_parts<C::D>(p, x, b, kvh, er);
-  if (parts.n == 0) return;
-  float mn = m;
-  for (int i = 0; i < parts.n; ++i) mn = fmaxf(mn, __ldcg(parts.ml(i)).x);
-  const float Rn = fmaxf(R, mn), keep = weight(R, Rn);
-  l *= weight(m, mn);
+  const int64_t rows = (int64_t)p.B * p.G, row = (int64_t)b * p.G + er;
+  float4* dst = x.own_o + (kvh * (C::D / 4) + ed / 4) * rows + row;
 #pragma unroll
-  for (int e = 0; e < N; ++e) o[e] *= keep;
-#pragma unroll 4
-  for (int i = 0; i < parts.n; ++i) {
-    const float2 ml = __ldcg(parts.ml(i));
-    float4 v[N / 4];
-#pragma unroll
-    for (int e = 0; e < N / 4; ++e) v[e] = __ldcg(parts.o(i, ed / 4 + e));
-    l = __fmaf_rn(weight(ml.x, mn), ml.y, l);
-    const float w = weight(ml.x, Rn);
-#pragma unroll
-    for (int e = 0; e < N / 4; ++e) {
-      o[4 * e] = __fmaf_rn(w, v[e].x, o[4 * e]);
-      o[4 * e + 1] = __fmaf_rn(w, v[e].y, o[4 * e + 1]);
-      o[4 * e + 2] = __fmaf_rn(w, v[e].z, o[4 * e + 2]);
-      o[4 * e + 3] = __fmaf_rn(w, v[e].w, o[4 * e + 3]);
-    }
-  }
-  m = mn;
-  R = Rn;
+  for (int e = 0; e < N; e += 4) dst[e / 4 * rows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+  if (ed == 0) x.own_ml[kvh * rows + row] = make_float4(m, l, C::kFp8 ? R : m, 0.f);
 }
 
 // The same for a warp whose lanes hold the accumulators of the products.
 template <class C>
-__device__ __noinline__ void warp_add_shared(const PagedParams& p, const PrefixParams& x, int b,
-                                             int kvh, float (&acc)[C::NB][C::D / 16][4],
-                                             float (&m)[C::NB], float (&l)[C::NB],
-                                             float (&R)[C::NB]) {
-  griddep_wait();
+__device__ __forceinline__ void warp_store_own(const PagedParams& p, const PrefixParams& x, int b,
+                                               int kvh, const float (&acc)[C::NB][C::D / 16][4],
+                                               const float (&m)[C::NB], const float (&l)[C::NB],
+                                               const float (&R)[C::NB]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t rows = (int64_t)p.B * p.G, row0 = (int64_t)b * p.G;
+  float* o = reinterpret_cast<float*>(x.own_o + kvh * (C::D / 4) * rows);
 #pragma unroll
   for (int nb = 0; nb < C::NB; ++nb) {
-    // statistics of row 8 nb + g; the accumulator's columns are rows 8 nb + 2t and the next
-    const SharedParts mine = shared_parts<C::D>(p, x, b, kvh, min(8 * nb + g, p.G - 1));
-    const int r0 = min(8 * nb + 2 * t, p.G - 1), r1 = min(8 * nb + 2 * t + 1, p.G - 1);
-    const SharedParts pa = shared_parts<C::D>(p, x, b, kvh, r0), pb = shared_parts<C::D>(p, x, b, kvh, r1);
-    float mn = m[nb];
-    for (int i = 0; i < mine.n; ++i) mn = fmaxf(mn, __ldcg(mine.ml(i)).x);
-    const float was = C::kFp8 ? R[nb] : m[nb], Rn = C::kFp8 ? fmaxf(was, mn) : mn;
-    const float keep = weight(was, Rn);
-    const float k0 = __shfl_sync(0xffffffffu, keep, 8 * t), k1 = __shfl_sync(0xffffffffu, keep, 8 * t + 4);
-    const float R0 = __shfl_sync(0xffffffffu, Rn, 8 * t), R1 = __shfl_sync(0xffffffffu, Rn, 8 * t + 4);
-    l[nb] *= weight(m[nb], mn);
-    for (int i = 0; i < mine.n; ++i) {
-      const float2 ml = __ldcg(mine.ml(i));
-      l[nb] = __fmaf_rn(weight(ml.x, mn), ml.y, l[nb]);
-    }
+    if (t == 0 && 8 * nb + g < p.G)
+      x.own_ml[kvh * rows + row0 + 8 * nb + g] =
+          make_float4(m[nb], l[nb], C::kFp8 ? R[nb] : m[nb], 0.f);
 #pragma unroll
-    for (int c = 0; c < C::D / 16; ++c) {
-      acc[nb][c][0] *= k0; acc[nb][c][1] *= k1; acc[nb][c][2] *= k0; acc[nb][c][3] *= k1;
-    }
-    auto add = [&](const SharedParts& s, float ref, int e) {
-      for (int i = 0; i < s.n; ++i) {
-        const float w = weight(__ldcg(s.ml(i)).x, ref);
+    for (int r = 0; r < 2; ++r) {
+      const int row = 8 * nb + 2 * t + r;
+      if (row >= p.G) continue;
 #pragma unroll
-        for (int c = 0; c < C::D / 16; ++c) {
-          const int d0 = 16 * c + (C::kFp8 ? 2 * g : g), d1 = d0 + (C::kFp8 ? 1 : 8);
-          acc[nb][c][e] = __fmaf_rn(w, __ldcg(s.at(i, d0)), acc[nb][c][e]);
-          acc[nb][c][2 + e] = __fmaf_rn(w, __ldcg(s.at(i, d1)), acc[nb][c][2 + e]);
-        }
+      for (int c = 0; c < C::D / 16; ++c) {
+        const int d0 = 16 * c + (C::kFp8 ? 2 * g : g), d1 = d0 + (C::kFp8 ? 1 : 8);
+        o[((d0 >> 2) * rows + row0 + row) * 4 + (d0 & 3)] = acc[nb][c][r];
+        o[((d1 >> 2) * rows + row0 + row) * 4 + (d1 & 3)] = acc[nb][c][2 + r];
       }
-    };
-    add(pa, R0, 0);
-    add(pb, R1, 1);
-    m[nb] = mn;
-    R[nb] = Rn;
+    }
   }
 }
 
@@ -1103,8 +1062,8 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
           warp_merge_partials<C>(p, c0, c1 - c0 + 1, acc, m, l, R);
         }
       }
-      if (kShared && last) warp_add_shared<C>(p, *x, pr.b, pr.kvh, acc, m, l, R);
-      if (last) warp_finalize<C>(p, pr.b, pr.kvh, sink, acc, m, l, R);
+      if (kShared && last) warp_store_own<C>(p, *x, pr.b, pr.kvh, acc, m, l, R);
+      if (!kShared && last) warp_finalize<C>(p, pr.b, pr.kvh, sink, acc, m, l, R);
     } else {
       // ---- merge the warps ----
 #pragma unroll
@@ -1147,8 +1106,10 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
       } else if (kCluster || (f == pr.begin && seg_end == pr.begin + pr.n)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          if (kShared) add_shared<C>(p, *x, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-          finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
+          if (kShared)
+            store_own<C>(p, *x, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+          else
+            finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
         }
       } else if constexpr (!kCluster) {
         // Contributors: the CTA whose range holds the first tile (slot 2 c + 1) and the
@@ -1192,8 +1153,9 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               if (kShared)
-                add_shared<C>(p, *x, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
-              finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
+                store_own<C>(p, *x, pr.b, pr.kvh, er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
+              else
+                finalize<C>(p, pr.b, pr.kvh, er + 8 * nb, ed, sink[nb], o[nb], mc[nb], lc[nb], Rc[nb]);
             }
           }
         }
@@ -1302,15 +1264,11 @@ __device__ __forceinline__ void paged_attn(const PagedParams& p, const CUtensorM
     int* prefix = reinterpret_cast<int*>(base + C::kOffPrefix);
     // ---- prefix[b]: tiles per kv head before request b; the most of a request ----
     int most = 0;
+    GroupPlan plan = {};  // kShared: behind prefix
     {
       const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
-      // the plan of the groups lies where the rings come later
-      GroupPlan plan = {};
-      if constexpr (kShared) {
-        static_assert(kWarps * C::kStages * C::kTileBytes >= 3 * 4 * (kPagedMaxBatch + 1),
-                      "room for the plan");
-        plan = plan_groups<kThreads>(p, *x, reinterpret_cast<int*>(base), false);
-      }
+      if constexpr (kShared)
+        plan = plan_groups<kThreads, false>(p, *x, prefix + B + 1, nullptr, misc, false);
       int group = kShared ? plan.find(b0) : 0;
       auto tiles_of = [&](int b) {
         const int len = __ldg(p.seq_lens + b);
@@ -1338,19 +1296,26 @@ __device__ __forceinline__ void paged_attn(const PagedParams& p, const CUtensorM
         run += tiles_of(b);
         if (b == B - 1) prefix[B] = run;
       }
-      if constexpr (kShared) {
-        if (tid == 0) misc[10] = plan.first(), misc[11] = plan.end();
-        fence_proxy_async_smem();  // the rings are filled by the async proxy
-      }
     }
     __syncthreads();
     griddep_launch_dependents();
 
+    if constexpr (kShared) {  // for prefix_combine.cu
+      if (blockIdx.x == 0) {
+        for (int b = tid; b < B; b += kThreads) {
+          const int g = plan.groups ? plan.find(b) : -1;
+          const bool mine = b >= plan.first() && b < plan.end();
+          int4 at = make_int4(0, 0, mine ? 0 : -1, plan.share);
+          if (mine && g >= 0) at = make_int4(plan.cu[g] | blocks_of(p, plan, g) << 16, plan.places[g],
+                                             plan.boxes[g], plan.share);
+          x->info[b] = at;
+        }
+      }
+    }
+
     // requests without a key
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+    for (int b = blockIdx.x; !kShared && b < B; b += gridDim.x) {
       if (prefix[b + 1] != prefix[b]) continue;
-      // rows outside of the groups are not the call's
-      if (kShared && (b < misc[10] || b >= misc[11])) continue;
       for (int i = tid; i < Hkv * p.G * (D / 8); i += kThreads) {
         const int h = i / (D / 8);
         *reinterpret_cast<uint4*>(p.out + b * p.o_sb + h * p.o_sh + (i % (D / 8)) * 8) =
@@ -1377,7 +1342,7 @@ __device__ __forceinline__ void paged_attn(const PagedParams& p, const CUtensorM
       attend<C, kPagedShares, kShared>(p, kv_map, base, base_u32, Pair{},
                                        waves <= 2 && waves * (most + kPairCost) <= share + kEndCost, x);
     }
-    if (kShared) griddep_wait();  // a grid ends after the one before it
+    if (kShared) griddep_wait();  // this grid ends after the one before it
   }
 }
 
@@ -1390,9 +1355,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
-    paged_behind_kernel(const __grid_constant__ PagedParams p,
-                        const __grid_constant__ CUtensorMap kv_map,
-                        const __grid_constant__ PrefixParams x) {
+    paged_own_kernel(const __grid_constant__ PagedParams p,
+                     const __grid_constant__ CUtensorMap kv_map,
+                     const __grid_constant__ PrefixParams x) {
   paged_attn<C, false, true>(p, kv_map, &x);
 }
 

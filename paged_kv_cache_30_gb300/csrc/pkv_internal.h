@@ -280,9 +280,9 @@ constexpr int kPagedWarpTiles = 64;
 
 // ------------------------------------- decode of groups with shared tokens --
 // Requests [cu_groups[g], cu_groups[g + 1]) share their first shared_lens[g] tokens.  One
-// grid (prefix_attn.cu) attends to what is shared, once for all rows of a group, and leaves
-// 32-bit (O, m, l) parts; the next (paged_attn.cuh) attends to each request's own tokens
-// and adds the parts.
+// grid (prefix_attn.cu) attends to what is shared, once for all rows of a group, the next
+// (paged_attn.cuh) to each request's own tokens; both leave 32-bit (O, m, l) parts, which
+// the third (prefix_combine.cu) adds up.
 constexpr int kPrefixRows = 256;     // query rows of a unit: two tiles of 128
 constexpr int kPrefixTileKeys = 128; // keys of a step
 // A CTA's share is counted in 16-key boxes plus a cost for each unit, and is no smaller than
@@ -293,9 +293,12 @@ struct PrefixParams {
   const int32_t* cu_groups;      // [groups + 1]
   const int32_t* shared_lens;    // [groups]
   int groups, grid;
-  // per request: {first request, place of the group's first unit, shared boxes, share}, {row
-  // blocks of a kv head, -, -, -}
-  int4* info;                    // [2 B]
+  // per request: {first request of its group | row blocks of a kv head << 16, place of the
+  // group's first unit, shared boxes (-1: padding), share of a CTA}
+  int4* info;                    // [B]
+  // of a request's own tokens; {m, l, reference of O, -}
+  float4* own_o;                 // [Hkv][D / 4][B G]
+  float4* own_ml;                // [Hkv][B G]
   // the part of a unit's first CTA: rows b G + h of each kv head
   float4* first_o;               // [Hkv][D / 4][B G]
   float2* first_ml;              // [Hkv][B G]
@@ -304,15 +307,16 @@ struct PrefixParams {
   float2* rest_ml;               // [grid][kPrefixRows]
 };
 inline int64_t prefix_workspace_bytes(int64_t B, int64_t Hq, int64_t D, int64_t grid) {
-  return 2 * B * 16 + (B * Hq + grid * kPrefixRows) * (D * 4 + 8);
+  return B * 16 + B * Hq * (2 * D * 4 + 24) + grid * kPrefixRows * (D * 4 + 8);
 }
 // kv_map: the cache as (64 dims, token, piece, kv head, page), box (64, 16, 1, 1, 1), 128-byte
 // swizzle; e4m3: (D, token, K | V, kv head, page), box (D, 16, 1, 1, 1), no swizzle.
 cudaError_t launch_prefix_attn(const PagedParams& p, const PrefixParams& x, const CUtensorMap& kv_map,
                                cudaStream_t stream);
-// The grid after it; kv_map as launch_paged_attn's.
-cudaError_t launch_paged_behind(const PagedParams& p, const PrefixParams& x,
-                                const CUtensorMap& kv_map, cudaStream_t stream);
+// The grids after it; kv_map as launch_paged_attn's.
+cudaError_t launch_prefix_own(const PagedParams& p, const PrefixParams& x, const CUtensorMap& kv_map,
+                              cudaStream_t stream);
+cudaError_t launch_prefix_combine(const PagedParams& p, const PrefixParams& x, cudaStream_t stream);
 
 // ------------------------------------------------ append to an e4m3 cache --
 struct AppendFp8Params {

@@ -8,7 +8,7 @@
 //   x_j = scale ks(page of j) q . k_j,   m = max_j x_j
 //   O = sum_j e^(x_j - m) vs(page of j) v_j,   l = sum_j e^(x_j - m)
 // O, m and l go to the workspace in 32 bits; the grid after this one (paged_attn.cuh)
-// attends to each request's own keys, adds these parts and divides.
+// attends to each request's own keys, the third (prefix_combine.cu) adds up all parts.
 //
 // Bound by the tensor cores and the exponentials of many rows (a key of 512 bytes is
 // multiplied with 512 rows, say), by memory of few.
@@ -49,6 +49,13 @@ constexpr int kSlotThreads = 128;
 constexpr int kScaleTiles = 8;  // tiles whose scales are kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;   // log2 units
+constexpr float kTiny = 1e-37f;  // times any score that is finite: no change of its weight
+
+// barriers
+enum {
+  kOpFull = 0, kOpEmpty = 8, kRawFull = 16, kRawEmpty = 22, kSFull = 28, kPReady = 30, kODone = 32,
+  kQFull = 34, kQFree = 35, kPHalf = 36, kScaleFull = 38, kNumBars = kScaleFull + kScaleTiles,
+};
 
 template <int D_, bool kFp8_>
 struct PrefixCfg {
@@ -56,6 +63,9 @@ struct PrefixCfg {
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kThreads = kFp8 ? 512 : 384;  // e4m3: warps 2, 3, 12..15 convert
   static constexpr int kConverters = 192;
+  static constexpr int kFewRegs = kFp8 ? 72 : 88, kManyRegs = kFp8 ? 184 : 208;
+  static_assert((kThreads - 256) * kFewRegs + 256 * kManyRegs <= kThreads * (kFp8 ? 128 : 168),
+                "registers of the launch");
   static constexpr int kChunks = D / 64;            // 128-byte pieces of an operand's row
   static constexpr int kChunkBytes = kTile * 128;   // 16 KB
   static constexpr int kOpBytes = kChunks * kChunkBytes;
@@ -67,23 +77,24 @@ struct PrefixCfg {
   static constexpr int kOffScale = kOffRaw + (kFp8 ? kRaws * kRawBytes : 0);
   static constexpr int kOffMl = kOffScale + kScaleTiles * kTileBoxes * 8;
   static constexpr int kOffBars = kOffMl + kSlotThreads * 8;
-  static constexpr int kOffMisc = kOffBars + 64 * 8;
+  static constexpr int kOffMisc = kOffBars + kNumBars * 8;
   static constexpr int kOffPlaces = kOffMisc + 128;
-  static constexpr int smem_bytes(int groups) { return kOffPlaces + (groups + 1) * 4 + 1024; }
+  static constexpr int smem_bytes(int groups) { return kOffPlaces + (groups + 1) * 8 + 1024; }
   static_assert(smem_bytes(kPagedMaxBatch) <= 227 * 1024, "shared memory");
-  static_assert(3 * 4 * (kPagedMaxBatch + 1) <= kOffScale, "room for the plan of the groups");
+  static_assert(4 * 4 * (kPagedMaxBatch + 1) <= kOffScale, "room for the plan of the groups");
 };
 
-// barriers
-enum {
-  kOpFull = 0, kOpEmpty = 8, kRawFull = 16, kRawEmpty = 22, kSFull = 28, kPReady = 30, kODone = 32,
-  kQFull = 34, kQFree = 35, kScaleFull = 36, kNumBars = kScaleFull + kScaleTiles,
-};
-static_assert(kNumBars <= 64, "barriers");
+// A read that stays where it is: eight scales held over a step cost registers.
+__device__ __forceinline__ float lds_f32(const void* at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(smem_u32(at)));
+  return v;
+}
 
 // A CTA's part of a unit.
 struct Part {
-  int first, rows;      // the group's first request and its rows in the block
+  int first, lead;      // the group's first request, and its first that is not empty
+  int rows;             // of the block
   int row0;             // of the block within the group
   int kvh;
   int boxes, t0, t1;    // shared boxes; tiles of this part
@@ -100,13 +111,15 @@ struct Part {
 __device__ __forceinline__ Part part_at(const PagedParams& p, const PrefixParams& x,
                                         const int* places, int f, int to) {
   Part r;
+  const int* at = places + x.groups + 1;
   int lo = 0, hi = x.groups - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (places[mid] <= f) lo = mid; else hi = mid - 1;
   }
-  r.first = __ldg(x.cu_groups + lo);
-  const int rows = (__ldg(x.cu_groups + lo + 1) - r.first) * p.G;
+  r.first = at[lo] & 0xffff;
+  r.lead = at[lo] >> 16;
+  const int rows = ((at[lo + 1] & 0xffff) - r.first) * p.G;
   const int blocks = (rows + kPrefixRows - 1) / kPrefixRows;
   const int per = (places[lo + 1] - places[lo]) / (p.Hkv * blocks);
   const int unit = (f - places[lo]) / per, begin = places[lo] + unit * per;
@@ -141,7 +154,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool slot = i == kPReady || i == kPReady + 1;
+      const bool slot = (i & ~1) == kPReady || (i & ~1) == kPHalf;
       mbar_init(bar(i), slot ? kSlotThreads : i == kQFull ? 2 * kSlotThreads : 1);
     }
     fence_barrier_init();
@@ -157,48 +170,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   griddep_launch_dependents();
 
   // ---- places of the groups' units ----
+  // what stays of the plan: places, and per group the first request and the first that is
+  // not empty
+  int* rows = places + x.groups + 1;
   int total, share;
   {
+    int* mem = reinterpret_cast<int*>(base);
+    int* lead = mem + plan_ints(x.groups);
     const GroupPlan plan =
-        plan_groups<C::kThreads>(p, x, reinterpret_cast<int*>(base), blockIdx.x == 0);
-    const int n = x.groups, per = (n + C::kThreads - 1) / C::kThreads, g0 = tid * per;
-    auto cost = [&](int g) {
-      const int boxes = plan.groups ? plan.boxes[g] : 0;
-      if (boxes == 0) return 0;
-      const int blocks = ((plan.cu[g + 1] - plan.cu[g]) * p.G + kPrefixRows - 1) / kPrefixRows;
-      return p.Hkv * blocks * (boxes + kPrefixUnitCost);
-    };
-    int mine = 0;
-    for (int g = g0; g < min(g0 + per, n); ++g) mine += cost(g);
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) misc[warp] = incl;
-    __syncthreads();
-    int run = incl - mine;
-    total = 0;
-    for (int w = 0; w < C::kThreads / 32; ++w) {
-      run += w < warp ? misc[w] : 0;
-      total += misc[w];
-    }
-    share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kPrefixMinShare);
-    for (int g = g0; g < min(g0 + per, n); ++g) {
-      places[g] = run;
-      run += cost(g);
-    }
-    if (tid == 0) places[n] = total;
-    __syncthreads();
-    if (blockIdx.x == 0) {  // where the grid after this one finds the parts
-      for (int b = tid; b < p.B; b += C::kThreads) {
-        const int g = plan.groups ? plan.find(b) : -1;
-        const bool in = g >= 0 && b < plan.cu[plan.groups];
-        const int first = in ? plan.cu[g] : 0, rows = in ? (plan.cu[g + 1] - first) * p.G : 0;
-        x.info[2 * b] = make_int4(first, in ? places[g] : 0, in ? plan.boxes[g] : 0, share);
-        x.info[2 * b + 1] = make_int4((rows + kPrefixRows - 1) / kPrefixRows, 0, 0, 0);
-      }
+        plan_groups<C::kThreads, true>(p, x, mem, lead, misc, blockIdx.x == 0);
+    total = plan.groups ? plan.places[plan.groups] : 0;
+    share = plan.share;
+    for (int i = tid; i <= plan.groups; i += C::kThreads) {
+      places[i] = plan.places[i];
+      rows[i] = plan.cu[i] | (i < plan.groups ? min(lead[i], p.B - 1) : 0) << 16;
     }
     fence_proxy_async_smem();  // the plan lies where tiles come
   }
@@ -210,6 +195,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const int to = min(from + share, total);
   const uint32_t ops = base_u32 + C::kOffOps;
 
+  // Registers: the softmax warpgroups take what the others give back (at launch 512 x 128, or
+  // 384 x 168).
+  if (warp < kSlotWarp0 || warp >= kSlotWarp0 + 8) setmaxnreg_dec<C::kFewRegs>();
   if (warp == 0) {
     // ============================ TMA producer ============================
     int op = 0, tiles = 0;  // operands and tiles asked for
@@ -217,17 +205,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const Part u = part_at(p, x, places, f, to);
       f = u.next;
       if (u.tiles() <= 0) continue;
-      // the group's first request that is not empty: its table
-      int b = u.first;
-      for (const int end = __ldg(x.cu_groups + x.groups); b < end; b += 32) {
-        const uint32_t live =
-            __ballot_sync(0xffffffffu, b + lane < end && __ldg(p.seq_lens + b + lane) > 0);
-        if (live) {
-          b += __ffs(live) - 1;
-          break;
-        }
-      }
-      const int32_t* table = p.bt + (int64_t)min(b, p.B - 1) * p.bt_sb;
+      const int32_t* table = p.bt + (int64_t)u.lead * p.bt_sb;
       int blk = 0, off = 0;
       float2 scale = make_float2(0.f, 0.f);
       for (int t = u.t0; t < u.t1; ++t, ++tiles) {
@@ -311,17 +289,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       };
       auto values = [&](int j) {
         const int slot = j & 1, op = op0 + 2 * u.tile(j) + 1, e = op % C::kOps;
-        mbar_wait(bar(kPReady + slot), ready[slot] & 1, p.err);
-        ++ready[slot];
         mbar_wait(bar(kOpFull + e), (op / C::kOps) & 1, p.err);
+        mbar_wait(bar(kPHalf + slot), ready[slot] & 1, p.err);
         tc::fence_after_sync();
         const uint32_t b = ops + e * C::kOpBytes;
 #pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
+        for (int ks = 0; ks < kTile / 16; ++ks) {
+          if (ks == kTile / 32) {
+            mbar_wait(bar(kPReady + slot), ready[slot] & 1, p.err);
+            tc::fence_after_sync();
+          }
           tc::mma_bf16_ts_elect(
               tmem + 2 * kTile + slot * D, tmem + slot * kTile + ks * 8,
               tc::smem_desc(b + ks * 2048, C::kChunkBytes, 1024, tc::kSwizzle128), kIdPv,
               j > 1 || ks > 0);
+        }
+        ++ready[slot];
         if (!dual || slot == 1) tc::commit_elect(bar(kOpEmpty + e));
         if (j + 2 >= steps) tc::commit_elect(bar(kODone + slot));
       };
@@ -336,10 +319,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
   } else if (warp >= kSlotWarp0 && warp < kSlotWarp0 + 8) {
     // ======================= softmax, one thread per row ===================
+    setmaxnreg_inc<C::kManyRegs>();
     const int slot = (warp - kSlotWarp0) >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + slot * kTile, tO = tmem + lanes + 2 * kTile + slot * D;
-    const float c2 = fabsf(p.scale) * kLog2e;
+    const float c2 = fmaxf(fabsf(p.scale) * kLog2e, kTiny);
     const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;  // of the query's signs
     float2* other_ml = reinterpret_cast<float2*>(base + C::kOffMl);
     int units = 0, tiles = 0;
@@ -353,20 +337,31 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       // ---- query rows: 128 each, or half of one tile each; rows past the block are zero ----
       if (units > 0) mbar_wait(bar(kQFree), (units - 1) & 1, p.err);
       {
-        constexpr int kUnits = D / 8;  // 16-byte units of a row
-        const int n = dual ? 128 : 64, r0 = dual ? 0 : 64 * slot, t0 = dual ? slot : 0;
-#pragma unroll 4
-        for (int i = row; i < n * kUnits; i += kSlotThreads) {
-          const int r = r0 + i / kUnits, k = i % kUnits, at = t0 * 128 + r;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (at < u.rows) {
-            const int b = u.first + (u.row0 + at) / p.G, h = (u.row0 + at) % p.G;
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + b * p.q_sb + (u.kvh * p.G + h) * p.q_sh) + k);
-            v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-          }
-          *reinterpret_cast<uint4*>(base + t0 * C::kOpBytes + (k >> 3) * C::kChunkBytes + r * 128 +
-                                    (((k & 7) ^ (r & 7)) * 16)) = v;
+        // 16-byte units; a thread's are kStep rows apart, so its unit k and swizzle stay
+        constexpr int kUnits = D / 8, kStep = kSlotThreads / kUnits, kMine = 128 / kStep;
+        const int n = dual ? kMine : kMine / 2, tile = dual ? slot : 0;
+        const int r0 = (dual ? 0 : 64 * slot) + row / kUnits, k = row % kUnits;
+        int at = u.row0 + 128 * tile + r0, b = u.first + at / p.G, h = at % p.G;
+        const int db = kStep / p.G, dh = kStep % p.G, end = u.row0 + u.rows;
+        uint4 v[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (i < n && at < end)
+            v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + b * p.q_sb + (u.kvh * p.G + h) * p.q_sh) + k);
+          at += kStep;
+          b += db;
+          h += dh;
+          if (h >= p.G) h -= p.G, ++b;
         }
+        uint8_t* dst = base + tile * C::kOpBytes + (k >> 3) * C::kChunkBytes + r0 * 128 +
+                       (((k & 7) ^ (r0 & 7)) * 16);
+        static_assert(kStep % 8 == 0, "the swizzle of a thread's rows");
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          if (i < n)
+            *reinterpret_cast<uint4*>(dst + i * kStep * 128) =
+                make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
@@ -384,20 +379,34 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int valid = min(u.boxes - (u.t0 + t) * kTileBoxes, kTileBoxes);  // boxes
           const float2* sc = reinterpret_cast<const float2*>(base + C::kOffScale) +
                              (at % kScaleTiles) * kTileBoxes;
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(tS + 32 * c, s[c]);
+          // log2 units of a score of box h (never 0: no infinity times 0)
+          auto unit = [&](int h) { return kFp8 ? fmaxf(c2 * lds_f32(sc + h), kTiny) : c2; };
+          tc::wait_ld();
+          if (valid < kTileBoxes) {
+#pragma unroll
+            for (int h = 0; h < kTileBoxes; ++h)
+              if (h >= valid)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[h / 2][16 * (h & 1) + i] = 0xff800000u;  // -inf
+          }
           float top = -INFINITY;
+          {
+            float a[kTileBoxes];
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) {
-            uint32_t s[32];
-            tc::ld_32x32b_x32(tS + 32 * c, s);
-            tc::wait_ld();
+            for (int h = 0; h < kTileBoxes; ++h) {
+              const uint32_t* y = s[h / 2] + 16 * (h & 1);
+              a[h] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (2 * c + h >= valid) continue;
-              float a = __uint_as_float(s[16 * h]);
-#pragma unroll
-              for (int i = 1; i < 16; ++i) a = fmaxf(a, __uint_as_float(s[16 * h + i]));
-              top = fmaxf(top, a * (kFp8 ? c2 * sc[2 * c + h].x : c2));
+              for (int i = 2; i < 16; i += 2)
+                a[h] = fmaxf(fmaxf(a[h], __uint_as_float(y[i])), __uint_as_float(y[i + 1]));
+              if (kFp8) a[h] *= unit(h);
             }
+#pragma unroll
+            for (int h = 0; h < kTileBoxes; h += 2) top = fmaxf(fmaxf(top, a[h]), a[h + 1]);
+            if (!kFp8) top *= c2;
           }
           const bool move = top > m + kSlack || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, move)) {
@@ -405,43 +414,50 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const float keep = m == -INFINITY ? 0.f : ex2(m - mn);
             if (j > 1) {
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tc::ld_32x32b_x32(tO + 32 * c, o);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tc::ld_32x32b_x16(tO + 16 * c, o);
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                tc::st_32x32b_x32(tO + 32 * c, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                tc::st_32x32b_x16(tO + 16 * c, o);
               }
             }
             l *= keep;
             m = mn;
           }
-          const float ref = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float ref = m == -INFINITY ? 0.f : -m;
+          float2 sum[2] = {};
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) {
-            uint32_t s[32], w[16];
-            tc::ld_32x32b_x32(tS + 32 * c, s);
-            tc::wait_ld();
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const bool in = 2 * c + h < valid;
-              const float ks = kFp8 ? c2 * sc[2 * c + h].x : c2, vs = kFp8 ? sc[2 * c + h].y : 1.f;
+              const int box = 2 * c + h;
+              const float ks = unit(box), vs = kFp8 ? lds_f32(&sc[box].y) : 1.f;
+              const float2 k2 = make_float2(ks, ks), r2 = make_float2(ref, ref);
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
-                float e0 = ex2(__fmaf_rn(__uint_as_float(s[16 * h + i]), ks, -ref));
-                float e1 = ex2(__fmaf_rn(__uint_as_float(s[16 * h + i + 1]), ks, -ref));
-                if (!in) e0 = e1 = 0.f;
-                sum[i & 2] += e0;
-                sum[(i & 2) + 1] += e1;
-                w[8 * h + i / 2] = kFp8 ? pack_bf16(e0 * vs, e1 * vs) : pack_bf16(e0, e1);
+                const float2 y = fma2(make_float2(__uint_as_float(s[c][16 * h + i]),
+                                                  __uint_as_float(s[c][16 * h + i + 1])), k2, r2);
+                float2 e = make_float2(ex2(y.x), ex2(y.y));
+                sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+                if (kFp8) e = mul2(e, make_float2(vs, vs));
+                w[8 * h + i / 2] = pack_bf16(e.x, e.y);
               }
             }
             tc::st_32x32b_x16(tS + 16 * c, w);
+            if (c == 1) {  // the first half's product can begin
+              tc::wait_st();
+              tc::fence_before_sync();
+              mbar_arrive(bar(kPHalf + slot));
+            }
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          sum[0] = add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
           tc::wait_st();
+        } else {
+          mbar_arrive(bar(kPHalf + slot));
         }
         tc::fence_before_sync();
         mbar_arrive(bar(kPReady + slot));
@@ -527,11 +543,25 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         mbar_wait(bar(kOpEmpty + eo), ((op / C::kOps) & 1) ^ 1u, p.err);
         const uint8_t* src = base + C::kOffRaw + er * C::kRawBytes;
         uint8_t* dst = base + C::kOffOps + eo * C::kOpBytes;
-        constexpr int kUnits = D / 16;  // 16 codes each
-        for (int k = ct; k < kTile * kUnits; k += C::kConverters) {
-          const int r = k / kUnits, q = k % kUnits;
-          const uint4 w = *reinterpret_cast<const uint4*>(src + k * 16);
-          const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+        // 16 codes each; a thread's are kStep rows apart, which keeps the unit and the swizzle
+        constexpr int kUnits = D / 16, kStep = C::kConverters / kUnits;
+        constexpr int kMine = (kTile + kStep - 1) / kStep;
+        static_assert(C::kConverters % kUnits == 0 && kStep % 8 == 0, "converters");
+        const int r0 = ct / kUnits, q = ct % kUnits, odd = (q >> 2) & 1;
+        // dims 16 q .. + 15: units 2 q' and 2 q' + 1 of piece q / 4, which begin with different
+        // units, for the banks
+        const uint32_t at = (q >> 2) * C::kChunkBytes + r0 * 128;
+        const uint32_t a0 = at + ((2 * (q & 3) + odd) ^ (r0 & 7)) * 16;
+        const uint32_t a1 = at + ((2 * (q & 3) + 1 - odd) ^ (r0 & 7)) * 16;
+        uint4 w[kMine];
+#pragma unroll
+        for (int k = 0; k < kMine; ++k)
+          if (r0 + k * kStep < kTile)
+            w[k] = *reinterpret_cast<const uint4*>(src + (ct + k * C::kConverters) * 16);
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+          if (r0 + k * kStep >= kTile) break;
+          const uint32_t wv[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
           uint32_t o[8];
 #pragma unroll
           for (int h = 0; h < 8; ++h) {
@@ -540,13 +570,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
             o[h] = pack_bf16(fv.x, fv.y);
           }
-          // dims 16 q .. + 15: units 2 q' and 2 q' + 1 of piece q / 4
-          uint8_t* at = dst + (q >> 2) * C::kChunkBytes + r * 128;
-          const int u0 = 2 * (q & 3), sw = r & 7, odd = (q >> 2) & 1;
-          // pieces begin with different units, for the banks
           const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-          *reinterpret_cast<uint4*>(at + (((u0 + odd) ^ sw) * 16)) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(at + (((u0 + 1 - odd) ^ sw) * 16)) = odd ? lo : hi;
+          *reinterpret_cast<uint4*>(dst + a0 + k * kStep * 128) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + a1 + k * kStep * 128) = odd ? lo : hi;
         }
         fence_proxy_async_smem();  // the MMA reads through the async proxy
         __syncwarp();

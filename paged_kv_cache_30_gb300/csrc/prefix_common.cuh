@@ -1,6 +1,7 @@
-// prefix_common.cuh -- what the two grids of a decode call with shared tokens agree on:
-// how many of a group's tokens are read once for all of its rows, and where the parts of
-// a row lie.
+// prefix_common.cuh -- what the grids of a decode call with shared tokens agree on: how many
+// of a group's tokens are read once for all of its rows, and which CTAs take them.  Each CTA
+// of prefix_attn.cu and prefix_own.cu works it out for itself from offsets and lengths, as a grid
+// for it alone would cost more than the few dependent reads.
 #pragma once
 #include <limits.h>
 
@@ -12,8 +13,9 @@ namespace pkv {
 // Groups in shared memory, from plan_groups.
 struct GroupPlan {
   const int *cu, *boxes;  // [groups + 1]; shared 16-key boxes [groups]
+  const int* places;      // [groups + 1]: place of the group's first unit
   int groups;             // 0: none (all requests are on their own)
-  int B;
+  int B, share;           // requests; places of a CTA of the first grid
 
   __device__ __forceinline__ int first() const { return groups ? cu[0] : 0; }
   __device__ __forceinline__ int end() const { return groups ? cu[groups] : B; }
@@ -38,109 +40,106 @@ struct GroupPlan {
   }
 };
 
+// Row blocks of group g's units for a kv head.
+__device__ __forceinline__ int blocks_of(const PagedParams& p, const GroupPlan& plan, int g) {
+  return ((plan.cu[g + 1] - plan.cu[g]) * p.G + kPrefixRows - 1) / kPrefixRows;
+}
+
+constexpr int plan_ints(int groups) { return 3 * (groups + 1); }
+
 // Shared tokens are counted in whole boxes of 16, at most one token less than the group's
 // shortest request that is not empty (so every row sees all of them, and has at least one
 // token behind them), and 0 for a group with fewer than two such requests.
-// scratch: 3 (groups + 1) ints.  All kThreads threads call it.  Offsets that decrease or
-// leave [0, B] raise DEVERR_BAD_ROW (report: by this CTA) and no group counts.
-template <int kThreads>
-__device__ __forceinline__ GroupPlan plan_groups(const PagedParams& p, const PrefixParams& x,
-                                                 int* scratch, bool report) {
-  const int tid = threadIdx.x, B = p.B, n = x.groups;
-  int *cu = scratch, *least = cu + n + 1, *live = least + n + 1;
+//
+// Units (a group's blocks of kPrefixRows rows of a kv head) are laid end to end in the space
+// of costs: kPrefixUnitCost and the shared boxes each.  CTA c of the first grid takes places
+// [c share, (c + 1) share): whole tiles whose first box lies in them.
+//
+// mem: plan_ints(groups) ints that stay; scratch: groups + 1 ints, and with kLead as many that
+// stay and get each group's first request that is not empty; sums: one int per warp.  All
+// kThreads threads call it.  Offsets that decrease or leave [0, B] raise DEVERR_BAD_ROW
+// (report: by this CTA) and no group counts.
+template <int kThreads, bool kLead>
+__device__ __forceinline__ GroupPlan plan_groups(const PagedParams& p, const PrefixParams& x, int* mem,
+                                                 int* scratch, int* sums, bool report) {
+  const int tid = threadIdx.x, lane = tid & 31, B = p.B, n = x.groups;
+  int *cu = mem, *least = cu + n + 1, *places = least + n + 1;
+  int *live = places, *lead = scratch;
+  const int per = (B + kThreads - 1) / kThreads, b0 = tid * per, b1 = min(b0 + per, B);
+  // asked for together
+  const int len0 = b0 < B ? __ldg(p.seq_lens + b0) : 0;
+  const int shared0 = tid < n ? __ldg(x.shared_lens + tid) : 0;
   bool bad = false;
   for (int i = tid; i <= n; i += kThreads) {
     const int c = __ldg(x.cu_groups + i);
     bad |= c < 0 || c > B || (i < n && __ldg(x.cu_groups + i + 1) < c);
     cu[i] = c;
-    if (i < n) {
-      least[i] = INT_MAX;
-      live[i] = 0;
-    }
+    least[i] = INT_MAX;
+    live[i] = 0;
+    if (kLead) lead[i] = INT_MAX;
   }
   if (__syncthreads_or(bad)) {
     if (report && tid == 0) atomicOr(p.err, DEVERR_BAD_ROW);
-    return {cu, least, 0, B};
+    return {cu, least, places, 0, B, kPrefixMinShare};
   }
-  GroupPlan plan = {cu, least, n, B};
+  GroupPlan plan = {cu, least, places, n, B, kPrefixMinShare};
   // a thread's requests are neighbours: one step a group for each
-  const int per = (B + kThreads - 1) / kThreads, b0 = tid * per, b1 = min(b0 + per, B);
-  int g = plan.find(b0), lo = INT_MAX, cnt = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int to = plan.next(g, b);
-    if (to != g && cnt) {
+  int g = plan.find(b0), lo = INT_MAX, cnt = 0, one = 0;
+  auto note = [&] {
+    if (cnt) {
       atomicMin(least + g, lo);
       atomicAdd(live + g, cnt);
+      if (kLead) atomicMin(lead + g, one);
     }
-    if (to != g) lo = INT_MAX, cnt = 0;
+    lo = INT_MAX;
+    cnt = 0;
+  };
+  for (int b = b0; b < b1; ++b) {
+    const int to = plan.next(g, b);
+    if (to != g) note();
     g = to;
-    const int L = min(__ldg(p.seq_lens + b), p.max_blocks * p.page_size);
+    const int L = min(b == b0 ? len0 : __ldg(p.seq_lens + b), p.max_blocks * p.page_size);
     if (g < 0 || b >= cu[n] || L <= 0) continue;
     lo = min(lo, L);
-    ++cnt;
+    if (cnt++ == 0) one = b;
   }
-  if (cnt) {
-    atomicMin(least + g, lo);
-    atomicAdd(live + g, cnt);
-  }
+  note();
   __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
-    const int tokens = live[i] < 2 ? 0 : min(max(__ldg(x.shared_lens + i), 0), least[i] - 1);
-    least[i] = tokens >> 4;
+    const int S = i == tid ? shared0 : __ldg(x.shared_lens + i);
+    least[i] = (live[i] < 2 ? 0 : min(max(S, 0), least[i] - 1)) >> 4;
   }
   __syncthreads();
+  // ---- places: a scan of the groups' costs ----
+  const int each = (n + kThreads - 1) / kThreads, g0 = min(tid * each, n), g1 = min(g0 + each, n);
+  auto cost = [&](int i) {
+    if (least[i] == 0) return 0;
+    return p.Hkv * blocks_of(p, plan, i) * (least[i] + kPrefixUnitCost);
+  };
+  int mine = 0;
+  for (int i = g0; i < g1; ++i) mine += cost(i);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sums[tid >> 5] = incl;
+  __syncthreads();
+  int run = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    run += w < tid >> 5 ? sums[w] : 0;
+    total += sums[w];
+  }
+  for (int i = g0; i < g1; ++i) {
+    places[i] = run;
+    run += cost(i);
+  }
+  if (tid == 0) places[n] = total;
+  plan.share = max((total + x.grid - 1) / x.grid, kPrefixMinShare);
+  __syncthreads();
   return plan;
-}
-
-// A row's parts, first to last.  Units of a group are laid end to end in the space of costs:
-// kPrefixUnitCost and its boxes each; CTA c takes places [c share, (c + 1) share), whole
-// tiles whose first box lies in them, so a unit's parts are those of the CTAs from the one
-// that holds the end of its first tile to the one that holds its end.
-struct SharedParts {
-  const float4 *first_o, *rest_o;    // of row quad 0
-  const float2 *first_ml, *rest_ml;
-  int64_t first_step, rest_cta;      // from quad to quad; from CTA to CTA
-  int n;
-
-  __device__ __forceinline__ const float2* ml(int i) const {
-    return i == 0 ? first_ml : rest_ml + (int64_t)i * kPrefixRows;
-  }
-  __device__ __forceinline__ const float4* o(int i, int quad) const {
-    return i == 0 ? first_o + quad * first_step
-                  : rest_o + i * rest_cta + (int64_t)quad * kPrefixRows;
-  }
-  __device__ __forceinline__ const float* at(int i, int d) const {
-    return reinterpret_cast<const float*>(o(i, d >> 2)) + (d & 3);
-  }
-};
-
-// begin: the unit's place; the CTAs that have a part of it
-__device__ __forceinline__ int first_cta(int begin, int boxes, int share) {
-  return (begin + kPrefixUnitCost + min(boxes, kPrefixTileKeys / 16) - 1) / share;
-}
-__device__ __forceinline__ int last_cta(int begin, int boxes, int share) {
-  return (begin + kPrefixUnitCost + boxes - 1) / share;
-}
-
-template <int D>
-__device__ __forceinline__ SharedParts shared_parts(const PagedParams& p, const PrefixParams& x,
-                                                    int b, int kvh, int h) {
-  SharedParts s = {};
-  const int4 at = __ldcg(x.info + 2 * b);
-  if (at.z == 0) return s;
-  const int blocks = __ldcg(x.info + 2 * b + 1).x;
-  const int row = (b - at.x) * p.G + h, block = row / kPrefixRows;
-  const int begin = at.y + (kvh * blocks + block) * (kPrefixUnitCost + at.z);
-  const int c0 = first_cta(begin, at.z, at.w);
-  const int64_t rows = (int64_t)p.B * p.G, mine = (int64_t)b * p.G + h;
-  s.n = last_cta(begin, at.z, at.w) - c0 + 1;
-  s.first_o = x.first_o + kvh * (D / 4) * rows + mine;
-  s.first_ml = x.first_ml + kvh * rows + mine;
-  s.first_step = rows;
-  s.rest_cta = (int64_t)(D / 4) * kPrefixRows;
-  s.rest_o = x.rest_o + c0 * s.rest_cta + row % kPrefixRows;
-  s.rest_ml = x.rest_ml + (int64_t)c0 * kPrefixRows + row % kPrefixRows;
-  return s;
 }
 
 }  // namespace pkv

@@ -330,7 +330,7 @@ def test_offsets_past_32_bits(fp8):
 def test_a_small_workspace():
     pr = plain.problem(31, [(3000, [3001, 3002, 4000, 3100])], 2, 8, 128, 16, True, sinks=True)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    need = 2 * 4 * 16 + (4 * 16 + sms * 256) * (128 * 4 + 8)
+    need = 4 * 16 + 4 * 16 * (2 * 128 * 4 + 24) + sms * 256 * (128 * 4 + 8)
     torch.cuda.synchronize()
     pkv.shutdown()
     try:
