@@ -23,9 +23,11 @@
 //    the other's row of tensor memory).  While one slot's threads are at their
 //    exponentials, the tensor cores work for the other.
 //  * warp 0 asks for K and V of a tile by TMA, lane l for 16-key box l, into a ring of
-//    operands; warp 1 issues S = Q K^T (M 128, N 128 keys, K D) and O += P V (M 128, N D,
-//    K 128), P read from tensor memory, where it overlays S.  e4m3 tiles land in a ring of
-//    their own, and six warps rewrite them as bf16 (exact).
+//    operands; warps 1 and 2 issue S = Q K^T (M 128, N 128 keys, K D) and O += P V (M 128, N
+//    D, K 128) of a slot each, P read from tensor memory, where it overlays S.  (One warp for
+//    both took 1740 cycles a step of 1024 cycles of products, the rest its waits and
+//    commits.)  e4m3 tiles land in a ring of their own, and four warps rewrite them as bf16
+//    (exact).
 //  * The reference m of a row moves when a score passes it by more than 2^8, and O is
 //    rescaled in tensor memory then; the scores of a step are there only after O of the
 //    steps before is, so that needs no wait.  P, times its value's scale, is rounded once to
@@ -54,16 +56,16 @@ constexpr float kTiny = 1e-37f;  // times any score that is finite: no change of
 // barriers
 enum {
   kOpFull = 0, kOpEmpty = 8, kRawFull = 16, kRawEmpty = 22, kSFull = 28, kPReady = 30, kODone = 32,
-  kQFull = 34, kQFree = 35, kPHalf = 36, kScaleFull = 38, kNumBars = kScaleFull + kScaleTiles,
+  kQFull = 34, kQFree = 35, kPHalf = 36, kTurn = 38, kScaleFull = 40, kNumBars = kScaleFull + kScaleTiles,
 };
 
 template <int D_, bool kFp8_>
 struct PrefixCfg {
   static constexpr int D = D_;
   static constexpr bool kFp8 = kFp8_;
-  static constexpr int kThreads = kFp8 ? 512 : 384;  // e4m3: warps 2, 3, 12..15 convert
-  static constexpr int kConverters = 192;
-  static constexpr int kFewRegs = kFp8 ? 72 : 88, kManyRegs = kFp8 ? 184 : 208;
+  static constexpr int kThreads = kFp8 ? 512 : 384;  // e4m3: warps 12..15 convert
+  static constexpr int kConverters = 128;
+  static constexpr int kFewRegs = kFp8 ? 80 : 120, kManyRegs = kFp8 ? 176 : 192;
   static_assert((kThreads - 256) * kFewRegs + 256 * kManyRegs <= kThreads * (kFp8 ? 128 : 168),
                 "registers of the launch");
   static constexpr int kChunks = D / 64;            // 128-byte pieces of an operand's row
@@ -71,6 +73,9 @@ struct PrefixCfg {
   static constexpr int kOpBytes = kChunks * kChunkBytes;
   static constexpr int kRawBytes = kTile * D;       // an e4m3 operand
   static constexpr int kOps = D == 64 ? (kFp8 ? 6 : 8) : (kFp8 ? 3 : 4);
+  // A unit of one query tile has an operand more, in the other tile's place, where there are
+  // three: with three, the next step's keys wait for the products of this step's values.
+  static constexpr bool kExtraOp = kOps == 3;
   static constexpr int kRaws = D == 64 ? 6 : 3;
   static constexpr int kOffOps = 2 * kOpBytes;  // behind two query tiles
   static constexpr int kOffRaw = kOffOps + kOps * kOpBytes;
@@ -78,17 +83,44 @@ struct PrefixCfg {
   static constexpr int kOffMl = kOffScale + kScaleTiles * kTileBoxes * 8;
   static constexpr int kOffBars = kOffMl + kSlotThreads * 8;
   static constexpr int kOffMisc = kOffBars + kNumBars * 8;
-  static constexpr int kOffPlaces = kOffMisc + 128;
+  static constexpr int kOffPlaces = kOffMisc + 80;
   static constexpr int smem_bytes(int groups) { return kOffPlaces + (groups + 1) * 8 + 1024; }
   static_assert(smem_bytes(kPagedMaxBatch) <= 227 * 1024, "shared memory");
   static_assert(4 * 4 * (kPagedMaxBatch + 1) <= kOffScale, "room for the plan of the groups");
 };
 
-// A read that stays where it is: eight scales held over a step cost registers.
-__device__ __forceinline__ float lds_f32(const void* at) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(smem_u32(at)));
-  return v;
+// Operands of a unit in the ring, for one of the roles that go through them: operand n's
+// place, and the phase of its barriers.
+template <class C>
+struct OpRing {
+  uint32_t base = 0;  // phases of the places at the unit's start
+  int mod = C::kOps;
+
+  __device__ __forceinline__ void begin(bool dual) {
+    if (C::kExtraOp) mod = dual ? C::kOps : C::kOps + 1;
+  }
+  __device__ __forceinline__ int uses(int n) const {  // n / mod
+    return !C::kExtraOp ? n / C::kOps : mod == C::kOps ? n / C::kOps : n / (C::kOps + 1);
+  }
+  __device__ __forceinline__ int place(int n) const { return n - uses(n) * mod; }
+  __device__ __forceinline__ uint32_t phase(int n) const {
+    return ((base >> place(n)) ^ (uint32_t)uses(n)) & 1u;
+  }
+  __device__ __forceinline__ void end(int n) {  // of a unit of n operands
+    const int all = uses(n), left = place(n);
+    // places below `left` were used once more
+    const uint32_t low = (1u << left) - 1u, places = (1u << mod) - 1u;
+    base ^= all & 1 ? places & ~low : low;
+  }
+  static __device__ __forceinline__ uint32_t offset(int place) {  // in shared memory
+    return C::kExtraOp && place == C::kOps ? C::kOpBytes : C::kOffOps + place * C::kOpBytes;
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {  // RNE, lo in bits 0..15
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // A CTA's part of a unit.
@@ -155,13 +187,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       const bool slot = (i & ~1) == kPReady || (i & ~1) == kPHalf;
-      mbar_init(bar(i), slot ? kSlotThreads : i == kQFull ? 2 * kSlotThreads : 1);
+      const bool both = i == kQFree || (i >= kOpEmpty && i < kRawFull);  // of the MMA issuers
+      mbar_init(bar(i), slot ? kSlotThreads : i == kQFull ? 2 * kSlotThreads : both ? 2 : 1);
     }
     fence_barrier_init();
     tma_prefetch_desc(&kv_map);
   }
   if (warp == 1) {
-    tc::tmem_alloc(smem_u32(misc + 24), 512);
+    tc::tmem_alloc(smem_u32(misc + 16), 512);
     tc::tmem_relinquish();
   }
   // The grid after this one reads ahead of its own wait, which is sound as every CTA of
@@ -190,22 +223,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc + 24);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc + 16);
   const int from = min((long long)blockIdx.x * share, (long long)total);
   const int to = min(from + share, total);
-  const uint32_t ops = base_u32 + C::kOffOps;
 
   // Registers: the softmax warpgroups take what the others give back (at launch 512 x 128, or
   // 384 x 168).
   if (warp < kSlotWarp0 || warp >= kSlotWarp0 + 8) setmaxnreg_dec<C::kFewRegs>();
   if (warp == 0) {
     // ============================ TMA producer ============================
-    int op = 0, tiles = 0;  // operands and tiles asked for
+    int op = 0, tiles = 0;  // raw operands and tiles asked for
+    OpRing<C> ring;
     for (int f = from; f < to;) {
       const Part u = part_at(p, x, places, f, to);
       f = u.next;
       if (u.tiles() <= 0) continue;
       const int32_t* table = p.bt + (int64_t)u.lead * p.bt_sb;
+      ring.begin(u.dual());
       int blk = 0, off = 0;
       float2 scale = make_float2(0.f, 0.f);
       for (int t = u.t0; t < u.t1; ++t, ++tiles) {
@@ -230,9 +264,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int box = lane % kTileBoxes;
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++op) {
-          constexpr int kRing = kFp8 ? C::kRaws : C::kOps;
-          const int e = op % kRing, full = (kFp8 ? kRawFull : kOpFull) + e;
-          mbar_wait(bar((kFp8 ? kRawEmpty : kOpEmpty) + e), ((op / kRing) & 1) ^ 1u, p.err);
+          const int n = 2 * (t - u.t0) + kv, e = kFp8 ? op % C::kRaws : ring.place(n);
+          const int full = (kFp8 ? kRawFull : kOpFull) + e;
+          const uint32_t phase = kFp8 ? op / C::kRaws : ring.phase(n);
+          mbar_wait(bar((kFp8 ? kRawEmpty : kOpEmpty) + e), (phase & 1) ^ 1u, p.err);
           if (lane == 0) mbar_arrive_expect_tx(bar(full), kFp8 ? C::kRawBytes : C::kOpBytes);
           if (kFp8 && kv == 0) {  // the scales' place is free: see kScaleTiles
             if (mine)
@@ -249,72 +284,101 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             } else {
 #pragma unroll
               for (int c = 0; c < C::kChunks; ++c)
-                tma_load_5d(ops + e * C::kOpBytes + c * C::kChunkBytes + box * 2048, &kv_map, bar(full),
+                tma_load_5d(base_u32 + ring.offset(e) + c * C::kChunkBytes + box * 2048, &kv_map, bar(full),
                             0, off, kv * C::kChunks + c, u.kvh, blk);
             }
           }
         }
       }
+      ring.end(2 * u.tiles());
     }
-  } else if (warp == 1) {
-    // ============================= MMA issuer =============================
-    constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, kTile, false, false);
+  } else if (warp == 1 || warp == 2) {
+    // ===================== MMA issuers, one for each slot =====================
+    constexpr uint32_t kIdS = kFp8 ? tc::idesc_f16_f32(128, kTile) : tc::idesc_bf16_f32(128, kTile, false, false);
     constexpr uint32_t kIdPv = tc::idesc_bf16_f32(128, D, false, true);
-    int op0 = 0, units = 0;
-    uint32_t ready[2] = {0, 0};  // phases of P
+    const int slot = warp - 1;
+    const uint32_t tS = tmem + slot * kTile, tO = tmem + 2 * kTile + slot * D;
+    // The slots take turns at the tensor cores, a step's products each: left to themselves they
+    // fall into step, and the tensor cores stand still while both are at their exponentials.
+    int units = 0, before = 0;      // the slot whose turn was the last
+    uint32_t ready = 0, turns = 0;  // phases of P; of this slot's turns
+    OpRing<C> ring;
     for (int f = from; f < to;) {
       const Part u = part_at(p, x, places, f, to);
       f = u.next;
       if (u.tiles() <= 0) continue;
       const int steps = u.steps();
       const bool dual = u.dual();
+      const uint32_t q = base_u32 + (dual ? slot : 0) * C::kOpBytes;
+      ring.begin(dual);
       mbar_wait(bar(kQFull), units & 1, p.err);
-      auto scores = [&](int j) {
-        const int slot = j & 1, op = op0 + 2 * u.tile(j), e = op % C::kOps;
-        mbar_wait(bar(kOpFull + e), (op / C::kOps) & 1, p.err);
-        tc::fence_after_sync();
-        const uint32_t a = base_u32 + (dual ? slot : 0) * C::kOpBytes, b = ops + e * C::kOpBytes;
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc::mma_bf16_elect(
-                tmem + slot * kTile,
-                tc::smem_desc(a + c * C::kChunkBytes + ks * 32, 16, 1024, tc::kSwizzle128),
-                tc::smem_desc(b + c * C::kChunkBytes + ks * 32, 16, 1024, tc::kSwizzle128), kIdS,
-                (c | ks) != 0);
-        tc::commit_elect(bar(kSFull + slot));
-        if (!dual || slot == 1) tc::commit_elect(bar(kOpEmpty + e));
-        if (j == steps - 1) tc::commit_elect(bar(kQFree));
+      // an operand is free when both slots have read it, or one that reads it alone
+      auto release = [&](int n) {
+        const int e = ring.place(n);
+        tc::commit_elect(bar(kOpEmpty + e));
+        if (!dual) tc::commit_elect(bar(kOpEmpty + e));
       };
-      auto values = [&](int j) {
-        const int slot = j & 1, op = op0 + 2 * u.tile(j) + 1, e = op % C::kOps;
-        mbar_wait(bar(kOpFull + e), (op / C::kOps) & 1, p.err);
-        mbar_wait(bar(kPHalf + slot), ready[slot] & 1, p.err);
-        tc::fence_after_sync();
-        const uint32_t b = ops + e * C::kOpBytes;
-#pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks) {
-          if (ks == kTile / 32) {
-            mbar_wait(bar(kPReady + slot), ready[slot] & 1, p.err);
-            tc::fence_after_sync();
-          }
-          tc::mma_bf16_ts_elect(
-              tmem + 2 * kTile + slot * D, tmem + slot * kTile + ks * 8,
-              tc::smem_desc(b + ks * 2048, C::kChunkBytes, 1024, tc::kSwizzle128), kIdPv,
-              j > 1 || ks > 0);
+      auto wait_op = [&](int n) { mbar_wait(bar(kOpFull + ring.place(n)), ring.phase(n), p.err); };
+      if (slot >= steps && lane == 0) mbar_arrive(bar(kQFree));  // a single step is slot 0's
+      // A turn: the values of step j, the scores of step j + 2 (the first turn: of step `slot`).
+      for (int j = slot - 2; j < steps; j += 2) {
+        const int kn = 2 * u.tile(j + 2), vn = 2 * u.tile(j) + 1;
+        const bool first = j < 0, more = j + 2 < steps;
+        if (first && !more) continue;
+        // All that can be waited for is, before the turn.  The next keys of a unit of one
+        // query tile may take the place of these values.
+        if ((dual || first) && more) wait_op(kn);
+        if (!first) {
+          wait_op(vn);
+          mbar_wait(bar(kPHalf + slot), ready & 1, p.err);
         }
-        ++ready[slot];
-        if (!dual || slot == 1) tc::commit_elect(bar(kOpEmpty + e));
-        if (j + 2 >= steps) tc::commit_elect(bar(kODone + slot));
-      };
-      scores(0);
-      if (steps > 1) scores(1);
-      for (int j = 0; j < steps; ++j) {
-        values(j);
-        if (j + 2 < steps) scores(j + 2);
+        if (first ? slot == 1 || before == 1 : steps > 1) {
+          mbar_wait(bar(kTurn + slot), turns & 1, p.err);
+          ++turns;
+        }
+        tc::fence_after_sync();
+        if (!first) {
+          const uint32_t b = base_u32 + ring.offset(ring.place(vn));
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks) {
+            if (ks == kTile / 32) {
+              mbar_wait(bar(kPReady + slot), ready & 1, p.err);
+              tc::fence_after_sync();
+            }
+            tc::mma_bf16_ts_elect(
+                tO, tS + ks * 8,
+                tc::smem_desc(b + ks * 2048, C::kChunkBytes, 1024, tc::kSwizzle128), kIdPv,
+                j > 1 || ks > 0);
+          }
+          ++ready;
+          release(vn);
+          if (!more) tc::commit_elect(bar(kODone + slot));
+          if (!dual && more) wait_op(kn);
+        }
+        if (more) {
+          const uint32_t b = base_u32 + ring.offset(ring.place(kn));
+          tc::fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc::mma_bf16_elect(
+                  tS, tc::smem_desc(q + c * C::kChunkBytes + ks * 32, 16, 1024, tc::kSwizzle128),
+                  tc::smem_desc(b + c * C::kChunkBytes + ks * 32, 16, 1024, tc::kSwizzle128), kIdS,
+                  (c | ks) != 0);
+        }
+        // the other slot's turn: its first after this one's first, else if it has a step left;
+        // the next unit begins with slot 0
+        if ((slot == 1 || (first ? steps > 1 : j + 1 < steps)) && lane == 0)
+          mbar_arrive(bar(kTurn + (slot ^ 1)));
+        if (more) {
+          tc::commit_elect(bar(kSFull + slot));
+          release(kn);
+          if (j + 4 >= steps) tc::commit_elect(bar(kQFree));
+        }
       }
-      op0 += 2 * u.tiles();
+      before = (steps - 1) & 1;
+      ring.end(2 * u.tiles());
       ++units;
     }
   } else if (warp >= kSlotWarp0 && warp < kSlotWarp0 + 8) {
@@ -323,9 +387,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int slot = (warp - kSlotWarp0) >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + slot * kTile, tO = tmem + lanes + 2 * kTile + slot * D;
-    const float c2 = fmaxf(fabsf(p.scale) * kLog2e, kTiny);
+    const float scale2 = fabsf(p.scale) * kLog2e;
+    float c2 = fmaxf(scale2, kTiny);  // log2 units of a score
     const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;  // of the query's signs
-    float2* other_ml = reinterpret_cast<float2*>(base + C::kOffMl);
+    float2* other_ml = reinterpret_cast<float2*>(base + C::kOffMl);  // at a unit's end
+    float* row_scale = reinterpret_cast<float*>(other_ml);           // at its start
     int units = 0, tiles = 0;
     uint32_t got = 0, done[2] = {0, 0};  // phases of S; of O
     for (int f = from; f < to;) {
@@ -358,13 +424,36 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                        (((k & 7) ^ (r0 & 7)) * 16);
         static_assert(kStep % 8 == 0, "the swizzle of a thread's rows");
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
-          if (i < n)
-            *reinterpret_cast<uint4*>(dst + i * kStep * 128) =
-                make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+        for (int i = 0; i < kMine; ++i) {
+          if (i >= n) break;
+          if constexpr (kFp8) {
+            // To fp16, as the keys are: 2^up brings the row's largest element into [2^14,
+            // 2^15); exact but for elements below 2^-29 of it.  0 and non-finite rows stay.
+            uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, big = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              big = max(big, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
+#pragma unroll
+            for (int o = kUnits / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const int ex = (int)(big >> 23);
+            const int up = ex == 0 || ex == 255 ? 0 : max(min(127 + 14 - ex, 126), -126);
+            const float mul = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_f16(__uint_as_float(w[e] << 16) * mul, __uint_as_float(w[e] & 0xffff0000u) * mul);
+            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (k == 0) row_scale[128 * tile + r0 + i * kStep] = __uint_as_float((uint32_t)(127 - up) << 23);
+          }
+          *reinterpret_cast<uint4*>(dst + i * kStep * 128) =
+              make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
+      if (kFp8) {  // each row's scale is another thread's
+        named_bar_sync(1, 2 * kSlotThreads);
+        c2 = fmaxf(scale2 * row_scale[(dual ? 128 * slot : 0) + row], kTiny);
+      }
       const int mine = dual ? min(u.rows - 128 * slot, 128) : u.rows;  // rows of this slot
       const bool live = 32 * (warp & 3) < mine;  // of the warp: else it only keeps step
       float m = -INFINITY, l = 0.f;              // m in log2 units
@@ -379,80 +468,95 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int valid = min(u.boxes - (u.t0 + t) * kTileBoxes, kTileBoxes);  // boxes
           const float2* sc = reinterpret_cast<const float2*>(base + C::kOffScale) +
                              (at % kScaleTiles) * kTileBoxes;
-          uint32_t s[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::ld_32x32b_x32(tS + 32 * c, s[c]);
           // log2 units of a score of box h (never 0: no infinity times 0)
-          auto unit = [&](int h) { return kFp8 ? fmaxf(c2 * lds_f32(sc + h), kTiny) : c2; };
-          tc::wait_ld();
-          if (valid < kTileBoxes) {
+          auto unit = [&](int h) { return kFp8 ? fmaxf(c2 * sc[h].x, kTiny) : c2; };
+          // Half of the row at a time in registers: two pieces of 32 keys, from piece c on.
+          uint32_t s[2][32];
+          auto load = [&](int c) {
+            tc::ld_32x32b_x32(tS + 32 * c, s[0]);
+            tc::ld_32x32b_x32(tS + 32 * c + 32, s[1]);
+            tc::wait_ld();
+            if (valid < 2 * c + 4) {
 #pragma unroll
-            for (int h = 0; h < kTileBoxes; ++h)
-              if (h >= valid)
+              for (int h = 0; h < 4; ++h)
+                if (2 * c + h >= valid)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[h / 2][16 * (h & 1) + i] = 0xff800000u;  // -inf
-          }
-          float top = -INFINITY;
-          {
-            float a[kTileBoxes];
+                  for (int i = 0; i < 16; ++i) s[h / 2][16 * (h & 1) + i] = 0xff800000u;  // -inf
+            }
+          };
+          auto largest = [&](int c) {
+            float a[4];
 #pragma unroll
-            for (int h = 0; h < kTileBoxes; ++h) {
+            for (int h = 0; h < 4; ++h) {
               const uint32_t* y = s[h / 2] + 16 * (h & 1);
-              a[h] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+              a[h] = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
 #pragma unroll
-              for (int i = 2; i < 16; i += 2)
-                a[h] = fmaxf(fmaxf(a[h], __uint_as_float(y[i])), __uint_as_float(y[i + 1]));
-              if (kFp8) a[h] *= unit(h);
+              for (int i = 3; i < 15; i += 2)
+                a[h] = max3(a[h], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+              a[h] = fmaxf(a[h], __uint_as_float(y[15]));
+              if (kFp8) a[h] *= unit(2 * c + h);
             }
-#pragma unroll
-            for (int h = 0; h < kTileBoxes; h += 2) top = fmaxf(fmaxf(top, a[h]), a[h + 1]);
-            if (!kFp8) top *= c2;
-          }
-          const bool move = top > m + kSlack || (m == -INFINITY && top > m);
-          if (__any_sync(0xffffffffu, move)) {
-            const float mn = move ? top : m;
-            const float keep = m == -INFINITY ? 0.f : ex2(m - mn);
-            if (j > 1) {
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tc::ld_32x32b_x16(tO + 16 * c, o);
-                tc::wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                tc::st_32x32b_x16(tO + 16 * c, o);
-              }
-            }
-            l *= keep;
-            m = mn;
-          }
-          const float ref = m == -INFINITY ? 0.f : -m;
+            const float top = fmaxf(max3(a[0], a[1], a[2]), a[3]);
+            return kFp8 ? top : top * c2;
+          };
           float2 sum[2] = {};
+          auto weights = [&](int c, float ref, uint32_t (&w)[2][16]) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int box = 2 * c + h;
-              const float ks = unit(box), vs = kFp8 ? lds_f32(&sc[box].y) : 1.f;
+            for (int h = 0; h < 4; ++h) {
+              const float ks = unit(2 * c + h), vs = kFp8 ? sc[2 * c + h].y : 1.f;
               const float2 k2 = make_float2(ks, ks), r2 = make_float2(ref, ref);
+              const uint32_t* x = s[h / 2] + 16 * (h & 1);
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
-                const float2 y = fma2(make_float2(__uint_as_float(s[c][16 * h + i]),
-                                                  __uint_as_float(s[c][16 * h + i + 1])), k2, r2);
+                const float2 y =
+                    fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), k2, r2);
                 float2 e = make_float2(ex2(y.x), ex2(y.y));
                 sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
                 if (kFp8) e = mul2(e, make_float2(vs, vs));
-                w[8 * h + i / 2] = pack_bf16(e.x, e.y);
+                w[h / 2][8 * (h & 1) + i / 2] = pack_bf16(e.x, e.y);
               }
             }
-            tc::st_32x32b_x16(tS + 16 * c, w);
-            if (c == 1) {  // the first half's product can begin
+          };
+          // The first half's weights are taken with the reference as it stands, and again in the
+          // rare case that a score of the row moves it.  One copy of the code for both halves.
+          uint32_t w[2][16];
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            load(c);
+            top = fmaxf(top, largest(c));
+            if (c == 2) {
+              const bool move = top > m + kSlack || (m == -INFINITY && top > m);
+              if (__any_sync(0xffffffffu, move)) {
+                const float mn = move ? top : m;
+                const float keep = m == -INFINITY ? 0.f : ex2(m - mn);
+                if (j > 1) {
+#pragma unroll 1
+                  for (int d = 0; d < D; d += 16) {
+                    uint32_t o[16];
+                    tc::ld_32x32b_x16(tO + d, o);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                    tc::st_32x32b_x16(tO + d, o);
+                  }
+                }
+                l *= keep;
+                m = mn;
+                sum[0] = sum[1] = make_float2(0.f, 0.f);
+                c = -2;
+                continue;
+              }
+              tc::st_32x32b_x16(tS, w[0]);
+              tc::st_32x32b_x16(tS + 16, w[1]);
               tc::wait_st();
               tc::fence_before_sync();
-              mbar_arrive(bar(kPHalf + slot));
+              mbar_arrive(bar(kPHalf + slot));  // the first half's product can begin
             }
+            weights(c, m == -INFINITY ? 0.f : -m, w);
           }
+          tc::st_32x32b_x16(tS + 32, w[0]);
+          tc::st_32x32b_x16(tS + 48, w[1]);
           sum[0] = add2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
           tc::wait_st();
@@ -530,49 +634,70 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       tiles += u.tiles();
       ++units;
     }
-  } else if (kFp8) {
+  } else if (kFp8 && warp >= kSlotWarp0 + 8) {
     // ============= e4m3 operand -> bf16 operand, swizzled for the MMA =============
-    const int ct = warp < 4 ? tid - 64 : tid - 384 + 64;  // 0 .. 191
-    int op = 0;
+    const int ct = tid - 32 * (kSlotWarp0 + 8);
+    int op = 0, units = 0;
+    bool was_dual = false;
+    OpRing<C> ring;
     for (int f = from; f < to;) {
       const Part u = part_at(p, x, places, f, to);
       f = u.next;
-      for (int i = 0; i < 2 * max(u.tiles(), 0); ++i, ++op) {
-        const int er = op % C::kRaws, eo = op % C::kOps;
+      if (u.tiles() <= 0) continue;
+      ring.begin(u.dual());
+      // the operand in the second query tile's place: its last unit's scores are done
+      if (C::kExtraOp && was_dual && !u.dual()) mbar_wait(bar(kQFree), (units - 1) & 1, p.err);
+      was_dual = u.dual();
+      for (int i = 0; i < 2 * u.tiles(); ++i, ++op) {
+        const int er = op % C::kRaws, eo = ring.place(i);
         mbar_wait(bar(kRawFull + er), (op / C::kRaws) & 1, p.err);
-        mbar_wait(bar(kOpEmpty + eo), ((op / C::kOps) & 1) ^ 1u, p.err);
         const uint8_t* src = base + C::kOffRaw + er * C::kRawBytes;
-        uint8_t* dst = base + C::kOffOps + eo * C::kOpBytes;
+        uint8_t* dst = base + ring.offset(eo);
         // 16 codes each; a thread's are kStep rows apart, which keeps the unit and the swizzle
-        constexpr int kUnits = D / 16, kStep = C::kConverters / kUnits;
-        constexpr int kMine = (kTile + kStep - 1) / kStep;
-        static_assert(C::kConverters % kUnits == 0 && kStep % 8 == 0, "converters");
+        constexpr int kUnits = D / 16, kStep = C::kConverters / kUnits, kMine = kTile / kStep;
+        static_assert(kStep % 8 == 0, "the swizzle of a thread's rows");
         const int r0 = ct / kUnits, q = ct % kUnits, odd = (q >> 2) & 1;
         // dims 16 q .. + 15: units 2 q' and 2 q' + 1 of piece q / 4, which begin with different
         // units, for the banks
         const uint32_t at = (q >> 2) * C::kChunkBytes + r0 * 128;
         const uint32_t a0 = at + ((2 * (q & 3) + odd) ^ (r0 & 7)) * 16;
         const uint32_t a1 = at + ((2 * (q & 3) + 1 - odd) ^ (r0 & 7)) * 16;
-        uint4 w[kMine];
+        constexpr int kBatch = 4;
+        static_assert(kMine % kBatch == 0, "batches");
+#pragma unroll 1
+        for (int k0 = 0; k0 < kMine; k0 += kBatch) {
+          uint4 w[kBatch];
+          uint32_t o[kBatch][8];
 #pragma unroll
-        for (int k = 0; k < kMine; ++k)
-          if (r0 + k * kStep < kTile)
-            w[k] = *reinterpret_cast<const uint4*>(src + (ct + k * C::kConverters) * 16);
+          for (int k = 0; k < kBatch; ++k)
+            w[k] = *reinterpret_cast<const uint4*>(src + (ct + (k0 + k) * C::kConverters) * 16);
 #pragma unroll
-        for (int k = 0; k < kMine; ++k) {
-          if (r0 + k * kStep >= kTile) break;
-          const uint32_t wv[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-          uint32_t o[8];
+          for (int k = 0; k < kBatch; ++k) {
+            const uint32_t wv[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            uint32_t f16x2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f16x2) : "h"((uint16_t)(wv[h / 2] >> (16 * (h & 1)))));
-            const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
-            o[h] = pack_bf16(fv.x, fv.y);
+            for (int h = 0; h < 8; ++h)
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                  : "=r"(o[k][h])
+                  : "h"((uint16_t)(wv[h / 2] >> (16 * (h & 1)))));
           }
-          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-          *reinterpret_cast<uint4*>(dst + a0 + k * kStep * 128) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(dst + a1 + k * kStep * 128) = odd ? lo : hi;
+          if (i & 1) {  // values: to bf16, as P is
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+              for (int h = 0; h < 8; ++h) {
+                const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&o[k][h]));
+                o[k][h] = pack_bf16(fv.x, fv.y);
+              }
+          }
+          // the first batch before the operand's place is free
+          if (k0 == 0) mbar_wait(bar(kOpEmpty + eo), ring.phase(i) ^ 1u, p.err);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const uint4 lo = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+            const uint4 hi = make_uint4(o[k][4], o[k][5], o[k][6], o[k][7]);
+            *reinterpret_cast<uint4*>(dst + a0 + (k0 + k) * kStep * 128) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + a1 + (k0 + k) * kStep * 128) = odd ? lo : hi;
+          }
         }
         fence_proxy_async_smem();  // the MMA reads through the async proxy
         __syncwarp();
@@ -582,6 +707,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           mbar_arrive(bar(kOpFull + eo));
         }
       }
+      ring.end(2 * u.tiles());
+      ++units;
     }
   }
 

@@ -220,6 +220,12 @@ __device__ __forceinline__ float ex2(float x) {  // hardware 2^x
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {  // ignores NaN
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Two 32-bit operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
