@@ -13,11 +13,12 @@
 // position 10^6.
 //
 // Bound by memory for many tokens (each element read and written once), by latency
-// for few.  A lane has 8 neighbouring elements of a row (one 16-byte load), D / 8
-// lanes a row; partners of the half layout are rot / 16 lanes apart.  A CTA takes 1
-// to 8 tokens: its threads fill a table of their sines and cosines, and each warp
-// stays with one token, whose part of the table it keeps in registers over that
-// token's heads.  Few tokens are split among CTAs by heads.
+// for few.  A warp has one token, or some of its heads where tokens are few: it finds
+// the token's place, and each lane the sines and cosines of its own pairs, once for
+// all heads.  A lane has 8 elements of a row, D / 8 lanes a row: both quads of four
+// pairs (half layout: quads p / 4 and (p + rot / 2) / 4; else neighbours), so a
+// rotation needs no other lane, and the norm's weights are folded into its sines and
+// cosines.  Rows of the next batch are asked for before those of this one are used.
 #include <algorithm>
 
 #include "pkv_internal.h"
@@ -26,9 +27,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kMaxTokens = 8;  // of a CTA
-constexpr int kUnroll = 4;     // rows a lane has under way
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kBatch = 4;  // rows a lane has under way
 
 enum : int { kNone, kHalf, kInterleaved };
 
@@ -89,178 +89,217 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, long long t) {
   return r;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 4 weights of a norm from element d on.
+__device__ __forceinline__ void load_weights(const void* w, bool f32, int d, float (&f)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    f[i] = !w    ? 1.f
+           : f32 ? __ldg(static_cast<const float*>(w) + d + i)
+                 : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(w) + d + i) << 16);
 }
 
-// 8 weights of a norm from element d on.
-__device__ __forceinline__ void load_weights(const void* w, bool f32, int d, float (&f)[8]) {
-  if (!w) return;
-  if (f32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __ldg(static_cast<const float*>(w) + d + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      f[i] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(w) + d + i) << 16);
-  }
-}
-
-template <int D, bool kAppend, int kPairs>
+template <int D, bool kAppend, int kPairs, bool kNorm>
 __global__ void __launch_bounds__(kThreads)
-    rope_kernel(const __grid_constant__ RopeParams p, int tokens) {
+    rope_kernel(const __grid_constant__ RopeParams p, int groups) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a warp
-  __shared__ float2 table[kMaxTokens * D / 2];        // (cos, sin) times the factor
-  __shared__ Place places[kMaxTokens];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int mine = warp % tokens;  // this warp's token of the CTA's
-  const long long t0 = (long long)blockIdx.x * tokens, t = t0 + mine;
-  const int d = lane % kLanes * 8;
+  const int lane = threadIdx.x & 31, col = lane % kLanes;
+  const long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  // this warp's groups of kRows rows, of the token's query, key and value heads in turn
+  const int g0 = (int)blockIdx.y * groups, g1 = g0 + groups;
+  // this lane's two quads of elements
+  const int half = p.rot / 2;
+  const bool rotates = kPairs == kHalf ? col < p.rot / 8 : kPairs == kInterleaved && 8 * col < p.rot;
+  const int da = kPairs == kHalf ? (rotates ? 4 * col : p.rot + 8 * (col - p.rot / 8)) : 8 * col;
+  const int db = kPairs == kHalf && rotates ? da + half : da + 4;
   griddep_wait();
   griddep_launch_dependents();
-
-  // Rows of a token: query heads, key heads, and on the way into the cache value heads.
-  const int heads = p.Hq + p.Hkv * (kAppend ? 2 : 1);
-  const int subs = kWarps / tokens * (int)gridDim.y, sub = warp / tokens + kWarps / tokens * blockIdx.y;
-  const int step = subs * kRows;  // from a lane's row to its next
-  int row = sub * kRows + lane / kLanes;
-  auto source = [&](int r) {
-    const uint16_t* s = r < p.Hq ? p.q + t * p.q_st + r * p.q_sh
-                        : r < p.Hq + p.Hkv ? p.k + t * p.k_st + (r - p.Hq) * p.k_sh
-                                           : p.v + t * p.v_st + (r - p.Hq - p.Hkv) * p.v_sh;
-    return reinterpret_cast<const uint4*>(s + d);
-  };
-  uint4 x[kUnroll];
-  auto load = [&](int r) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (t < p.T && r + u * step < heads) x[u] = *source(r + u * step);
-    }
-  };
-  load(row);  // under way while the token's place is found
-
-  float qw[8], kw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) qw[i] = kw[i] = 1.f;
-  load_weights(p.qw, p.qw_f32, d, qw);
-  load_weights(p.kw, p.kw_f32, d, kw);
-
-  if (warp < tokens && t < p.T) {
-    const Place r = place_of<kAppend>(p, t);
-    if (lane == 0) places[warp] = r;
-  }
-  __syncthreads();
-  if constexpr (kPairs != kNone) {
-    const int half = p.rot / 2;
-    for (int i = tid; i < tokens * half; i += kThreads) {
-      const int tok = i / half;
-      if (t0 + tok >= p.T) break;
-      const uint2 f = __ldg(p.turns + i % half);
-      const uint64_t turns = ((uint64_t)f.y << 32 | f.x) * (uint64_t)(uint32_t)places[tok].pos;
-      float s, c;
-      sincospif((float)(int)(turns >> 32) * 0x1p-31f, &s, &c);
-      table[tok * (D / 2) + i % half] = make_float2(c * p.factor, s * p.factor);
-    }
-    __syncthreads();
-  }
   if (t >= p.T) return;
-  const Place place = places[mine];
-  if (place.pos < 0) return;
 
-  // This lane's pairs: 8 of the half layout (as first or as second element), 4 interleaved.
-  const int half = p.rot / 2;
-  const bool rotates = d < p.rot, second = kPairs == kHalf && d >= half;
-  float2 cs[kPairs == kInterleaved ? 4 : 8];
-  if constexpr (kPairs != kNone) {
-    const int at = kPairs == kHalf ? (second ? d - half : d) : d / 2;
+  struct Rows {  // of a kind of heads: where they are, and where they go (null: not there)
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t from, to;  // strides
+    int heads, first;  // first group
+  };
+  uint4 x[kBatch];
+  auto load = [&](const Rows& r, int g, int end) {
 #pragma unroll
-    for (int i = 0; i < (kPairs == kInterleaved ? 4 : 8); ++i)
-      cs[i] = rotates ? table[mine * (D / 2) + at + i] : make_float2(1.f, 0.f);
-    if (kPairs == kHalf && !second)  // y_i cos - y_j sin
-#pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i].y = -cs[i].y;
-  }
-  const int partner = kPairs == kHalf && rotates ? (second ? lane - half / 8 : lane + half / 8) : lane;
-
-  // All lanes go the same number of steps: partners trade elements.
-  for (int first = sub * kRows; first < heads; first += kUnroll * step, row += kUnroll * step) {
-    uint4 now[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) now[u] = x[u];
-    if (first + kUnroll * step < heads) load(row + kUnroll * step);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = row + u * step;
-      if (first + u * step >= heads) break;  // the same for the warp
-      const bool is_q = r < p.Hq, is_v = kAppend && r >= p.Hq + p.Hkv;
-      float y[8];
-      unpack8(now[u], y);
-      if (p.qw || p.kw) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __fmaf_rn(y[i], y[i], ss);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-        if (is_q ? p.qw != nullptr : p.kw != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * (is_q ? qw[i] : kw[i]);
-        }
-      }
-      float z[8];
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = (g + u - r.first) * kRows + lane / kLanes;
+      if (g + u >= end || h >= r.heads) continue;
+      const uint16_t* s = r.src + h * r.from;
       if constexpr (kPairs == kHalf) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float other = __shfl_sync(0xffffffffu, y[i], partner);
-          z[i] = rotates ? __fmaf_rn(y[i], cs[i].x, other * cs[i].y) : y[i];
-        }
-      } else if constexpr (kPairs == kInterleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = y[2 * i], b = y[2 * i + 1];
-          z[2 * i] = rotates ? __fmaf_rn(a, cs[i].x, -(b * cs[i].y)) : a;
-          z[2 * i + 1] = rotates ? __fmaf_rn(b, cs[i].x, a * cs[i].y) : b;
-        }
+        const uint2 a = *reinterpret_cast<const uint2*>(s + da), b = *reinterpret_cast<const uint2*>(s + db);
+        x[u] = make_uint4(a.x, a.y, b.x, b.y);
       } else {
+        x[u] = *reinterpret_cast<const uint4*>(s + da);
+      }
+    }
+  };
+  const int q_groups = (p.Hq + kRows - 1) / kRows, k_groups = (p.Hkv + kRows - 1) / kRows;
+  Rows rows = {p.q + t * p.q_st, p.q_out + t * p.qo_st, p.q_sh, p.qo_sh, p.Hq, 0};
+  if (g0 >= q_groups)
+    rows = {p.k + t * p.k_st, nullptr, p.k_sh, 0, p.Hkv, q_groups};
+  int end = min(g1, g0 >= q_groups ? q_groups + k_groups : q_groups);
+  load(rows, g0, end);  // under way while the token's place is found
+
+  const Place place = place_of<kAppend>(p, t);
+  if (place.pos < 0) return;
+  float cs[4], sn[4];  // of this lane's pairs
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = y[i];
+  for (int i = 0; i < 4; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+    if (kPairs != kNone && rotates) {
+      const uint2 f = __ldg(p.turns + 4 * col + i);
+      const uint64_t turns = ((uint64_t)f.y << 32 | f.x) * (uint64_t)(uint32_t)place.pos;
+      sincospif((float)(int)(turns >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+      cs[i] *= p.factor;
+      sn[i] *= p.factor;
+    }
+  }
+
+  int g = g0;
+#pragma unroll 1
+  for (int kind = g0 >= q_groups; kind < 2; ++kind) {
+    // ---- query heads, key heads ----
+    if (kind == 1) {
+      if (g1 <= q_groups || p.Hkv == 0) return;
+      if (g0 < q_groups) {
+        rows = {p.k + t * p.k_st, nullptr, p.k_sh, 0, p.Hkv, q_groups};
+        end = min(g1, q_groups + k_groups);
+        g = q_groups;
+        load(rows, g, end);
       }
-      if (r >= heads) continue;
-      uint4 out = make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]),
-                             pack_bf16(z[6], z[7]));
-      if (is_v) out = now[u];
-      uint16_t* dst;
-      if (is_q) {
-        dst = p.q_out + t * p.qo_st + r * p.qo_sh + d;
-      } else if constexpr (kAppend) {
-        if (place.at < 0) continue;
-        const int h = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
-        dst = p.cache + place.at + h * p.c_sh + (is_v ? D : 0) + d;
+      if constexpr (kAppend) {
+        if (place.at >= 0) rows.dst = p.cache + place.at, rows.to = p.c_sh;
       } else {
-        dst = p.k_out + t * p.ko_st + (r - p.Hq) * p.ko_sh + d;
+        rows.dst = p.k_out + t * p.ko_st;
+        rows.to = p.ko_sh;
       }
-      *reinterpret_cast<uint4*>(dst) = out;
+    }
+    const void* weights = kind ? p.kw : p.qw;
+    const bool norm = kNorm && weights;
+    // with the weights: (a, b) -> (a ac + b bs, b bc + a as)
+    float2 ac[2], bs[2], bc[2], as[2];
+    {
+      float wa[4], wb[4];
+      load_weights(norm ? weights : nullptr, kind ? p.kw_f32 : p.qw_f32, da, wa);
+      load_weights(norm ? weights : nullptr, kind ? p.kw_f32 : p.qw_f32, db, wb);
+      if (kPairs == kInterleaved) {  // a: even elements, b: odd ones
+        const float v[8] = {wa[0], wa[1], wa[2], wa[3], wb[0], wb[1], wb[2], wb[3]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wa[i] = v[2 * i], wb[i] = v[2 * i + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ac[i] = make_float2(wa[2 * i] * cs[2 * i], wa[2 * i + 1] * cs[2 * i + 1]);
+        bs[i] = make_float2(-wb[2 * i] * sn[2 * i], -wb[2 * i + 1] * sn[2 * i + 1]);
+        bc[i] = make_float2(wb[2 * i] * cs[2 * i], wb[2 * i + 1] * cs[2 * i + 1]);
+        as[i] = make_float2(wa[2 * i] * sn[2 * i], wa[2 * i + 1] * sn[2 * i + 1]);
+      }
+    }
+#pragma unroll 1
+    for (; g < end; g += kBatch) {
+      uint4 now[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) now[u] = x[u];
+      load(rows, g + kBatch, end);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (g + u >= end) break;  // the same for the warp
+        const int h = (g + u - rows.first) * kRows + lane / kLanes;
+        float2 a[2], b[2];
+        if constexpr (kPairs == kInterleaved) {
+          a[0] = make_float2(lo_f32(now[u].x), lo_f32(now[u].y));
+          a[1] = make_float2(lo_f32(now[u].z), lo_f32(now[u].w));
+          b[0] = make_float2(hi_f32(now[u].x), hi_f32(now[u].y));
+          b[1] = make_float2(hi_f32(now[u].z), hi_f32(now[u].w));
+        } else {
+          a[0] = make_float2(lo_f32(now[u].x), hi_f32(now[u].x));
+          a[1] = make_float2(lo_f32(now[u].y), hi_f32(now[u].y));
+          b[0] = make_float2(lo_f32(now[u].z), hi_f32(now[u].z));
+          b[1] = make_float2(lo_f32(now[u].w), hi_f32(now[u].w));
+        }
+        float2 inv = make_float2(1.f, 1.f);
+        if (norm) {
+          float2 ss = mul2(a[0], a[0]);
+          ss = fma2(a[1], a[1], ss);
+          ss = fma2(b[0], b[0], ss);
+          ss = fma2(b[1], b[1], ss);
+          float s = ss.x + ss.y;
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          inv.x = inv.y = rsqrtf(__fmaf_rn(s, 1.f / D, p.eps));
+        }
+        float2 ya[2], yb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ya[i] = mul2(a[i], ac[i]);
+          yb[i] = mul2(b[i], bc[i]);
+          if (rotates) {  // other elements stay apart: an infinity times 0 is none of theirs
+            ya[i] = fma2(b[i], bs[i], ya[i]);
+            yb[i] = fma2(a[i], as[i], yb[i]);
+          }
+          if (norm) {
+            ya[i] = mul2(ya[i], inv);
+            yb[i] = mul2(yb[i], inv);
+          }
+        }
+        if (h >= rows.heads || !rows.dst) continue;
+        uint16_t* d = rows.dst + h * rows.to;
+        if constexpr (kPairs == kInterleaved) {
+          *reinterpret_cast<uint4*>(d + da) =
+              make_uint4(pack_bf16(ya[0].x, yb[0].x), pack_bf16(ya[0].y, yb[0].y),
+                         pack_bf16(ya[1].x, yb[1].x), pack_bf16(ya[1].y, yb[1].y));
+        } else if constexpr (kPairs == kHalf) {
+          *reinterpret_cast<uint2*>(d + da) =
+              make_uint2(pack_bf16(ya[0].x, ya[0].y), pack_bf16(ya[1].x, ya[1].y));
+          *reinterpret_cast<uint2*>(d + db) =
+              make_uint2(pack_bf16(yb[0].x, yb[0].y), pack_bf16(yb[1].x, yb[1].y));
+        } else {
+          *reinterpret_cast<uint4*>(d + da) =
+              make_uint4(pack_bf16(ya[0].x, ya[0].y), pack_bf16(ya[1].x, ya[1].y),
+                         pack_bf16(yb[0].x, yb[0].y), pack_bf16(yb[1].x, yb[1].y));
+        }
+      }
+    }
+  }
+  if constexpr (kAppend) {  // ---- value heads: copied ----
+    if (place.at < 0) return;
+    const int v1 = min(g1, q_groups + 2 * k_groups);
+#pragma unroll 1
+    for (int v = max(g0, q_groups + k_groups); v < v1; v += kBatch) {
+      uint4 y[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int h = (v + u - q_groups - k_groups) * kRows + lane / kLanes;
+        if (v + u < v1 && h < p.Hkv)
+          y[u] = *reinterpret_cast<const uint4*>(p.v + t * p.v_st + h * p.v_sh + 8 * col);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int h = (v + u - q_groups - k_groups) * kRows + lane / kLanes;
+        if (v + u < v1 && h < p.Hkv)
+          *reinterpret_cast<uint4*>(p.cache + place.at + h * p.c_sh + D + 8 * col) = y[u];
+      }
     }
   }
 }
 
-template <int D, bool kAppend, int kPairs>
+template <int D, bool kAppend, int kPairs, bool kNorm>
 cudaError_t launch_t(const RopeParams& p, int num_sms, cudaStream_t stream) {
-  const int heads = p.Hq + p.Hkv * (kAppend ? 2 : 1), rows = 32 / (D / 8);
-  int tokens = 1;
-  while (tokens < 4 && p.T / (2 * tokens) >= 4 * num_sms) tokens *= 2;
-  const int64_t ctas = (p.T + tokens - 1) / tokens;
-  // a CTA for each SM and a row a warp, if there are rows
-  const int most = std::max(1, (heads + rows * kWarps / tokens - 1) / (rows * kWarps / tokens));
-  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, 2 * num_sms / ctas));
+  constexpr int kRows = 32 / (D / 8);
+  const int k_groups = (p.Hkv + kRows - 1) / kRows;
+  const int all = (p.Hq + kRows - 1) / kRows + k_groups * (kAppend ? 2 : 1);
+  // a token to a warp, or to several where that leaves an SM fewer than 8 warps
+  const int64_t parts = std::min<int64_t>(all, std::max<int64_t>(1, 8 * num_sms / p.T));
+  const int groups = (int)((all + parts - 1) / parts);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)parts);
+  cfg.gridDim = dim3((unsigned)((p.T + kWarps - 1) / kWarps), (unsigned)((all + groups - 1) / groups));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -268,14 +307,20 @@ cudaError_t launch_t(const RopeParams& p, int num_sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_kernel<D, kAppend, kPairs>, p, tokens);
+  return cudaLaunchKernelEx(&cfg, rope_kernel<D, kAppend, kPairs, kNorm>, p, groups);
+}
+
+template <int D, bool kAppend, bool kNorm>
+cudaError_t launch_n(const RopeParams& p, int num_sms, cudaStream_t stream) {
+  if (p.rot == 0) return launch_t<D, kAppend, kNone, kNorm>(p, num_sms, stream);
+  return p.interleaved ? launch_t<D, kAppend, kInterleaved, kNorm>(p, num_sms, stream)
+                       : launch_t<D, kAppend, kHalf, kNorm>(p, num_sms, stream);
 }
 
 template <int D, bool kAppend>
 cudaError_t launch_d(const RopeParams& p, int num_sms, cudaStream_t stream) {
-  if (p.rot == 0) return launch_t<D, kAppend, kNone>(p, num_sms, stream);
-  return p.interleaved ? launch_t<D, kAppend, kInterleaved>(p, num_sms, stream)
-                       : launch_t<D, kAppend, kHalf>(p, num_sms, stream);
+  return p.qw || p.kw ? launch_n<D, kAppend, true>(p, num_sms, stream)
+                      : launch_n<D, kAppend, false>(p, num_sms, stream);
 }
 
 }  // namespace
