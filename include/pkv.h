@@ -493,7 +493,7 @@ PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
  * out and lse are those of pkv_paged_window_attn on the same rows.  A request of length 0
  * writes zeros and lse = -inf and is otherwise ignored; one that is shorter than
  * shared_lens[g] cuts what its group shares to its own length.  What is shared is counted
- * in whole 16-token boxes.  groups <= 2048; offsets that decrease or leave [0, B] raise bit
+ * in whole pages.  groups <= 2048; offsets that decrease or leave [0, B] raise bit
  * 64 of the device error word, and all requests are then attended to on their own.
  * The workspace holds 16 B + B Hq (8 D + 24) + 256 SMs (4 D + 8) bytes of it next to what
  * pkv_paged_window_attn needs (PKV_ERR_WORKSPACE).

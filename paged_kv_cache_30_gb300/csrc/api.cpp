@@ -1105,17 +1105,18 @@ PKV_API int pkv_mla_kv_append(const pkv_tensor* latent, const pkv_tensor* latent
 
 // ------------------------------------- decode with a window and first tokens --
 // Both entry points: kv_scale == nullptr is the bf16 cache.
-// The cache as a tensor map of boxes of 16 tokens: `pieces` pieces of `elems` elements a row.
+// The cache as a tensor map of `pieces` pieces of `elems` elements a row, in boxes of some
+// tokens by some pieces.
 static int encode_paged_map(EncodeTiledFn encode, const pkv_tensor* kv_cache, bool fp8, int page_size,
-                            int64_t elems, int64_t pieces, int64_t box_pieces, bool swizzle,
-                            CUtensorMap* map) {
+                            int64_t elems, int64_t pieces, int box_tokens, int64_t box_pieces,
+                            bool swizzle, CUtensorMap* map) {
   const cuuint64_t esz = fp8 ? 1 : 2;
   const cuuint64_t gdim[5] = {cuuint64_t(elems), cuuint64_t(page_size), cuuint64_t(pieces),
                               cuuint64_t(kv_cache->shape[1]), cuuint64_t(kv_cache->shape[0])};
   const cuuint64_t gstride[4] = {cuuint64_t(kv_cache->stride[2]) * esz, cuuint64_t(elems) * esz,
                                  cuuint64_t(kv_cache->stride[1]) * esz,
                                  cuuint64_t(kv_cache->stride[0]) * esz};
-  const cuuint32_t box[5] = {cuuint32_t(elems), 16, cuuint32_t(box_pieces), 1, 1};
+  const cuuint32_t box[5] = {cuuint32_t(elems), cuuint32_t(box_tokens), cuuint32_t(box_pieces), 1, 1};
   const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
   const CUresult cr = encode(
       map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, kv_cache->data,
@@ -1305,9 +1306,10 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
   EncodeTiledFn encode = nullptr;
   if ((rc = get_encoder(&encode))) return rc;
   if ((rc = encode_paged_map(encode, kv_cache, fp8, page_size, fp8 ? 128 : 64, shape.chunks,
-                             shape.chunks, true, &map)) ||
+                             16, shape.chunks, true, &map)) ||
       (grouped && (rc = encode_paged_map(encode, kv_cache, fp8, page_size, fp8 ? D : 64,
-                                         fp8 ? 2 : 2 * D / 64, 1, !fp8, &group_map))))
+                                         fp8 ? 2 : 2 * D / 64, page_size, 1, !fp8,
+                                         &group_map))))
     return rc;
   std::lock_guard<std::mutex> lock(g_launch_mu[dev]);
   if ((rc = order_streams(st, stream, capturing))) return rc;

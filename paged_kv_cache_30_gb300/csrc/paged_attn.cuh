@@ -1268,7 +1268,7 @@ __device__ __forceinline__ void paged_attn(const PagedParams& p, const CUtensorM
     {
       const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
       if constexpr (kShared)
-        plan = plan_groups<kThreads, false>(p, *x, prefix + B + 1, nullptr, misc, false);
+        plan = plan_groups<kThreads, false>(p, *x, prefix + B + 1, nullptr, false);
       int group = kShared ? plan.find(b0) : 0;
       auto tiles_of = [&](int b) {
         const int len = __ldg(p.seq_lens + b);
@@ -1299,19 +1299,6 @@ __device__ __forceinline__ void paged_attn(const PagedParams& p, const CUtensorM
     }
     __syncthreads();
     griddep_launch_dependents();
-
-    if constexpr (kShared) {  // for prefix_combine.cu
-      if (blockIdx.x == 0) {
-        for (int b = tid; b < B; b += kThreads) {
-          const int g = plan.groups ? plan.find(b) : -1;
-          const bool mine = b >= plan.first() && b < plan.end();
-          int4 at = make_int4(0, 0, mine ? 0 : -1, plan.share);
-          if (mine && g >= 0) at = make_int4(plan.cu[g] | blocks_of(p, plan, g) << 16, plan.places[g],
-                                             plan.boxes[g], plan.share);
-          x->info[b] = at;
-        }
-      }
-    }
 
     // requests without a key
     for (int b = blockIdx.x; !kShared && b < B; b += gridDim.x) {

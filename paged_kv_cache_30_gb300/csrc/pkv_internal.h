@@ -286,9 +286,14 @@ constexpr int kPagedWarpTiles = 64;
 constexpr int kPrefixRows = 256;     // query rows of a unit: two tiles of 128
 constexpr int kPrefixTileKeys = 128; // keys of a step
 // A CTA's share is counted in 16-key boxes plus a cost for each unit, and is no smaller than
-// kPrefixMinShare (a multiple of a tile's boxes, so that every CTA of a cut unit has a tile).
+// kPrefixMinShare (a multiple of a tile's boxes, so that every CTA of a cut unit has a tile; 64
+// requests behind 512 tokens take 28 us with 32, 25 with 16, 23.5 with 8, but 4 behind 8192 then
+// 22 for 18.5, as more parts are to be added up).
+// Units (a group's blocks of kPrefixRows rows of a kv head) are laid end to end in the space of
+// costs, and CTA c takes places [c share, (c + 1) share): whole tiles whose first box lies in
+// them.
 constexpr int kPrefixUnitCost = 24;
-constexpr int kPrefixMinShare = 32;
+constexpr int kPrefixMinShare = 16;
 struct PrefixParams {
   const int32_t* cu_groups;      // [groups + 1]
   const int32_t* shared_lens;    // [groups]
@@ -309,8 +314,8 @@ struct PrefixParams {
 inline int64_t prefix_workspace_bytes(int64_t B, int64_t Hq, int64_t D, int64_t grid) {
   return B * 16 + B * Hq * (2 * D * 4 + 24) + grid * kPrefixRows * (D * 4 + 8);
 }
-// kv_map: the cache as (64 dims, token, piece, kv head, page), box (64, 16, 1, 1, 1), 128-byte
-// swizzle; e4m3: (D, token, K | V, kv head, page), box (D, 16, 1, 1, 1), no swizzle.
+// kv_map: the cache as (64 dims, token, piece, kv head, page), box (64, P, 1, 1, 1), 128-byte
+// swizzle; e4m3: (D, token, K | V, kv head, page), box (D, P, 1, 1, 1), no swizzle.
 cudaError_t launch_prefix_attn(const PagedParams& p, const PrefixParams& x, const CUtensorMap& kv_map,
                                cudaStream_t stream);
 // The grids after it; kv_map as launch_paged_attn's.

@@ -22,8 +22,8 @@
 //    s tiles s, s + 2, .., and slot 0 adds up the two at the end (each of its threads reads
 //    the other's row of tensor memory).  While one slot's threads are at their
 //    exponentials, the tensor cores work for the other.
-//  * warp 0 asks for K and V of a tile by TMA, lane l for 16-key box l, into a ring of
-//    operands; warps 1 and 2 issue S = Q K^T (M 128, N 128 keys, K D) and O += P V (M 128, N
+//  * warps 0 and 3 ask for K and V of a tile by TMA, a lane for a page and a warp for half of
+//    them, into a ring of operands; warps 1 and 2 issue S = Q K^T (M 128, N 128 keys, K D) and O += P V (M 128, N
 //    D, K 128) of a slot each, P read from tensor memory, where it overlays S.  (One warp for
 //    both took 1740 cycles a step of 1024 cycles of products, the rest its waits and
 //    commits.)  e4m3 tiles land in a ring of their own, and four warps rewrite them as bf16
@@ -48,7 +48,7 @@ namespace {
 constexpr int kTile = kPrefixTileKeys, kTileBoxes = kTile / 16;
 constexpr int kSlotWarp0 = 4;  // softmax warps: 4..7 slot 0, 8..11 slot 1
 constexpr int kSlotThreads = 128;
-constexpr int kScaleTiles = 8;  // tiles whose scales are kept
+constexpr int kScaleTiles = 8;  // tiles whose scales are kept: more than keys are ahead of the weights
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;   // log2 units
 constexpr float kTiny = 1e-37f;  // times any score that is finite: no change of its weight
@@ -65,7 +65,7 @@ struct PrefixCfg {
   static constexpr bool kFp8 = kFp8_;
   static constexpr int kThreads = kFp8 ? 512 : 384;  // e4m3: warps 12..15 convert
   static constexpr int kConverters = 128;
-  static constexpr int kFewRegs = kFp8 ? 80 : 120, kManyRegs = kFp8 ? 176 : 192;
+  static constexpr int kFewRegs = kFp8 ? 72 : 120, kManyRegs = kFp8 ? 184 : 192;
   static_assert((kThreads - 256) * kFewRegs + 256 * kManyRegs <= kThreads * (kFp8 ? 128 : 168),
                 "registers of the launch");
   static constexpr int kChunks = D / 64;            // 128-byte pieces of an operand's row
@@ -74,7 +74,9 @@ struct PrefixCfg {
   static constexpr int kRawBytes = kTile * D;       // an e4m3 operand
   static constexpr int kOps = D == 64 ? (kFp8 ? 6 : 8) : (kFp8 ? 3 : 4);
   // A unit of one query tile has an operand more, in the other tile's place, where there are
-  // three: with three, the next step's keys wait for the products of this step's values.
+  // three: with three, the next step's keys wait for the products of this step's values.  Free
+  // it is then: the three before it hold among them the last keys of a unit of two tiles, and
+  // a unit's accumulators are done before the next one's queries are written.
   static constexpr bool kExtraOp = kOps == 3;
   static constexpr int kRaws = D == 64 ? 6 : 3;
   static constexpr int kOffOps = 2 * kOpBytes;  // behind two query tiles
@@ -86,7 +88,7 @@ struct PrefixCfg {
   static constexpr int kOffPlaces = kOffMisc + 80;
   static constexpr int smem_bytes(int groups) { return kOffPlaces + (groups + 1) * 8 + 1024; }
   static_assert(smem_bytes(kPagedMaxBatch) <= 227 * 1024, "shared memory");
-  static_assert(4 * 4 * (kPagedMaxBatch + 1) <= kOffScale, "room for the plan of the groups");
+  static_assert(4 * (plan_ints(kPagedMaxBatch) + kPagedMaxBatch + 1) <= kOffScale, "room for the plan of the groups");
 };
 
 // Operands of a unit in the ring, for one of the roles that go through them: operand n's
@@ -124,6 +126,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {  // RNE, lo i
 }
 
 // A CTA's part of a unit.
+template <bool kFp8>
 struct Part {
   int first, lead;      // the group's first request, and its first that is not empty
   int rows;             // of the block
@@ -137,12 +140,30 @@ struct Part {
   // steps of the two slots together: step j is slot j & 1's
   __device__ __forceinline__ int steps() const { return dual() ? 2 * tiles() : tiles(); }
   __device__ __forceinline__ int tile(int j) const { return dual() ? j >> 1 : j; }
+  // Operands come in the order in which the steps use them: K0 V0 K1 V1 .. for two query tiles,
+  // K0 K1 V0 K2 V1 .. for one, whose steps j and j + 1 are at work together.  (Of an e4m3 cache
+  // always as for two, which has less to work out.)
+  __device__ __forceinline__ bool by_tile() const { return kFp8 || dual(); }
+  __device__ __forceinline__ int keys(int t) const { return by_tile() ? 2 * t : max(2 * t - 1, 0); }
+  __device__ __forceinline__ int values(int t) const {
+    return by_tile() || t == tiles() - 1 ? 2 * t + 1 : 2 * t + 2;
+  }
+  __device__ __forceinline__ bool are_values(int n) const {  // operand n
+    return by_tile() ? n & 1 : n == 2 * tiles() - 1 || (n > 0 && !(n & 1));
+  }
+  __device__ __forceinline__ int tile_of(int n) const {
+    return by_tile()                ? n >> 1
+           : n == 2 * tiles() - 1 ? tiles() - 1
+           : n & 1                ? (n + 1) >> 1
+                                  : max((n >> 1) - 1, 0);
+  }
 };
 
 // The unit that holds place f < the CTA's end `to`.
-__device__ __forceinline__ Part part_at(const PagedParams& p, const PrefixParams& x,
-                                        const int* places, int f, int to) {
-  Part r;
+template <bool kFp8>
+__device__ __forceinline__ Part<kFp8> part_at(const PagedParams& p, const PrefixParams& x,
+                                              const int* places, int f, int to) {
+  Part<kFp8> r;
   const int* at = places + x.groups + 1;
   int lo = 0, hi = x.groups - 1;
   while (lo < hi) {
@@ -188,7 +209,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       const bool slot = (i & ~1) == kPReady || (i & ~1) == kPHalf;
       const bool both = i == kQFree || (i >= kOpEmpty && i < kRawFull);  // of the MMA issuers
-      mbar_init(bar(i), slot ? kSlotThreads : i == kQFull ? 2 * kSlotThreads : both ? 2 : 1);
+      const bool op_full = i >= kOpFull && i < kOpEmpty;
+      const bool asked = !kFp8 && op_full;  // of the TMA producers
+      mbar_init(bar(i), slot           ? kSlotThreads
+                        : i == kQFull   ? 2 * kSlotThreads
+                        : both || asked ? 2
+                                        : 1);
     }
     fence_barrier_init();
     tma_prefetch_desc(&kv_map);
@@ -208,15 +234,45 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   int* rows = places + x.groups + 1;
   int total, share;
   {
-    int* mem = reinterpret_cast<int*>(base);
-    int* lead = mem + plan_ints(x.groups);
+    int* lead = reinterpret_cast<int*>(base) + plan_ints(x.groups);
     const GroupPlan plan =
-        plan_groups<C::kThreads, true>(p, x, mem, lead, misc, blockIdx.x == 0);
-    total = plan.groups ? plan.places[plan.groups] : 0;
-    share = plan.share;
-    for (int i = tid; i <= plan.groups; i += C::kThreads) {
-      places[i] = plan.places[i];
-      rows[i] = plan.cu[i] | (i < plan.groups ? min(lead[i], p.B - 1) : 0) << 16;
+        plan_groups<C::kThreads, true>(p, x, reinterpret_cast<int*>(base), lead, blockIdx.x == 0);
+    if (warp == 0) {
+      int run = 0;
+      for (int g0 = 0; g0 < plan.groups; g0 += 32) {
+        const int g = g0 + lane;
+        int cost = 0;
+        if (g < plan.groups && plan.boxes[g] > 0)
+          cost = p.Hkv * blocks_of(p, plan, g) * (plan.boxes[g] + kPrefixUnitCost);
+        int incl = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        if (g < plan.groups) {
+          places[g] = run + incl - cost;
+          rows[g] = plan.cu[g] | min(lead[g], p.B - 1) << 16;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (lane == 0) {
+        places[plan.groups] = run;
+        rows[plan.groups] = plan.groups ? plan.cu[plan.groups] : 0;
+      }
+    }
+    __syncthreads();
+    total = places[plan.groups];
+    share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kPrefixMinShare);
+    if (blockIdx.x == gridDim.x - 1) {  // for prefix_combine.cu
+      for (int b = tid; b < p.B; b += C::kThreads) {
+        const int g = plan.groups ? plan.find(b) : -1;
+        const bool in = b >= plan.first() && b < plan.end();
+        int4 at = make_int4(0, 0, in ? 0 : -1, share);
+        if (in && g >= 0)
+          at = make_int4(plan.cu[g] | blocks_of(p, plan, g) << 16, places[g], plan.boxes[g], share);
+        x.info[b] = at;
+      }
     }
     fence_proxy_async_smem();  // the plan lies where tiles come
   }
@@ -230,66 +286,90 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   // Registers: the softmax warpgroups take what the others give back (at launch 512 x 128, or
   // 384 x 168).
   if (warp < kSlotWarp0 || warp >= kSlotWarp0 + 8) setmaxnreg_dec<C::kFewRegs>();
-  if (warp == 0) {
-    // ============================ TMA producer ============================
-    int op = 0, tiles = 0;  // raw operands and tiles asked for
+  if (warp == 0 || (warp == 3 && !kFp8)) {
+    // ============================ TMA producers ============================
+    // An operation takes its warp some 50 cycles to issue, whatever its size, so two warps ask
+    // for half of each operand's pages.  Both go through all operands in order: a warp that
+    // skipped some would take an old phase of a place's barrier for a new one.
+    // (e4m3 operands are half as large, and come from one warp.)
+    const int half = warp == 3;
+    const int in_tile = 7 - p.page_shift;  // log2 of a tile's pages
+    const int batch = 32 >> in_tile;       // tiles whose pages the lanes look up at once
+    const int sub = lane & ((1 << in_tile) - 1);
+    const bool asks = kFp8 || (in_tile == 0 ? half == 0 : sub >> (in_tile - 1) == half);
+    const uint32_t bytes = kFp8 ? C::kRawBytes : C::kOpBytes >> (in_tile == 0 ? (half ? 31 : 0) : 1);
+    int op = 0, tiles = 0;                 // operands and tiles of units before
     OpRing<C> ring;
     for (int f = from; f < to;) {
-      const Part u = part_at(p, x, places, f, to);
+      const auto u = part_at<kFp8>(p, x, places, f, to);
       f = u.next;
       if (u.tiles() <= 0) continue;
       const int32_t* table = p.bt + (int64_t)u.lead * p.bt_sb;
+      const int end = min(u.boxes, u.t1 * kTileBoxes) * 16;  // tokens
       ring.begin(u.dual());
-      int blk = 0, off = 0;
-      float2 scale = make_float2(0.f, 0.f);
-      for (int t = u.t0; t < u.t1; ++t, ++tiles) {
-        if (((t - u.t0) & 3) == 0) {  // the boxes of four tiles
-          const int box = t * kTileBoxes + lane, tok = box * 16;
-          blk = p.num_blocks;  // past the cache: reads as zeros
-          off = tok & (p.page_size - 1);
-          scale = make_float2(0.f, 0.f);
-          if (box < u.boxes) {
-            const int page = __ldg(table + min(tok >> p.page_shift, p.max_blocks - 1));
-            if (page < 0 || page >= p.num_blocks) {
-              if (box < u.t1 * kTileBoxes) atomicOr(p.err, DEVERR_BAD_BLOCK);
-            } else {
-              blk = page;
-              if (kFp8)
-                scale = __ldg(reinterpret_cast<const float2*>(
-                    p.kv_scale + (int64_t)page * p.s_sblk + u.kvh * p.s_sh));
-            }
+      auto page_of = [&](int t) {  // this lane's page of tiles t ..
+        const int page = ((u.t0 + t) << in_tile) + lane;
+        return page << p.page_shift < end ? __ldg(table + min(page, p.max_blocks - 1)) : INT_MAX;
+      };
+      auto scale_of = [&](int page) {
+        float2 s = make_float2(0.f, 0.f);
+        if (kFp8 && half == 0 && page >= 0 && page < p.num_blocks)
+          s = __ldg(reinterpret_cast<const float2*>(p.kv_scale + (int64_t)page * p.s_sblk +
+                                                    u.kvh * p.s_sh));
+        return s;
+      };
+      // Pages of an even and of an odd batch; those of the next one, and a tile later their
+      // scales, are read ahead.
+      int pages[2] = {page_of(0), 0};
+      float2 scale = scale_of(pages[0]), next_scale = scale;
+      for (int n = 0; n < 2 * u.tiles(); ++n, ++op) {
+        const int t = u.tile_of(n), at = t & (batch - 1);
+        const bool values = u.are_values(n), odd = t & batch;
+        if (!values) {
+          if (at == 0) {
+            scale = next_scale;
+            const int now = odd ? pages[1] : pages[0];
+            if (half == 0 && now != INT_MAX && (now < 0 || now >= p.num_blocks))
+              atomicOr(p.err, DEVERR_BAD_BLOCK);
           }
+          // (the values of the batch before have been asked for)
+          if (at == 1) {
+            const int next = page_of(t - 1 + batch);
+            if (odd) pages[0] = next; else pages[1] = next;
+          }
+          if (kFp8 && at == 2) next_scale = scale_of(odd ? pages[0] : pages[1]);
         }
-        const bool mine = lane / kTileBoxes == ((t - u.t0) & 3);
-        const int box = lane % kTileBoxes;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++op) {
-          const int n = 2 * (t - u.t0) + kv, e = kFp8 ? op % C::kRaws : ring.place(n);
-          const int full = (kFp8 ? kRawFull : kOpFull) + e;
-          const uint32_t phase = kFp8 ? op / C::kRaws : ring.phase(n);
-          mbar_wait(bar((kFp8 ? kRawEmpty : kOpEmpty) + e), (phase & 1) ^ 1u, p.err);
-          if (lane == 0) mbar_arrive_expect_tx(bar(full), kFp8 ? C::kRawBytes : C::kOpBytes);
-          if (kFp8 && kv == 0) {  // the scales' place is free: see kScaleTiles
-            if (mine)
+        int page = odd ? pages[1] : pages[0];
+        if (page < 0 || page >= p.num_blocks) page = p.num_blocks;  // past the cache: zeros
+        const bool mine = lane >> in_tile == at;
+        const int e = kFp8 ? op % C::kRaws : ring.place(n);
+        const int full = (kFp8 ? kRawFull : kOpFull) + e;
+        const uint32_t phase = kFp8 ? op / C::kRaws : ring.phase(n);
+        mbar_wait(bar((kFp8 ? kRawEmpty : kOpEmpty) + e), (phase & 1) ^ 1u, p.err);
+        if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
+        if (kFp8 && half == 0 && !values) {  // the scales' place is free: see kScaleTiles
+          const int place = (tiles + t) % kScaleTiles;
+          if (mine)
+            for (int b = 0; b < 1 << (p.page_shift - 4); ++b)
               *reinterpret_cast<float2*>(base + C::kOffScale +
-                                         ((tiles % kScaleTiles) * kTileBoxes + box) * 8) = scale;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kScaleFull + tiles % kScaleTiles));
-          }
+                                         (place * kTileBoxes + (sub << (p.page_shift - 4)) + b) * 8) = scale;
           __syncwarp();
-          if (mine) {
-            if constexpr (kFp8) {
-              tma_load_5d(base_u32 + C::kOffRaw + e * C::kRawBytes + box * 16 * D, &kv_map, bar(full),
-                          0, off, kv, u.kvh, blk);
-            } else {
+          if (lane == 0) mbar_arrive(bar(kScaleFull + place));
+        }
+        __syncwarp();
+        if (mine && asks) {
+          if constexpr (kFp8) {
+            tma_load_5d(base_u32 + C::kOffRaw + e * C::kRawBytes + (sub << p.page_shift) * D, &kv_map,
+                        bar(full), 0, 0, values, u.kvh, page);
+          } else {
 #pragma unroll
-              for (int c = 0; c < C::kChunks; ++c)
-                tma_load_5d(base_u32 + ring.offset(e) + c * C::kChunkBytes + box * 2048, &kv_map, bar(full),
-                            0, off, kv * C::kChunks + c, u.kvh, blk);
-            }
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_5d(base_u32 + ring.offset(e) + c * C::kChunkBytes + (sub << p.page_shift) * 128,
+                          &kv_map, bar(full), 0, 0, (values ? C::kChunks : 0) + c, u.kvh, page);
           }
         }
       }
+      tiles += u.tiles();
       ring.end(2 * u.tiles());
     }
   } else if (warp == 1 || warp == 2) {
@@ -304,7 +384,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint32_t ready = 0, turns = 0;  // phases of P; of this slot's turns
     OpRing<C> ring;
     for (int f = from; f < to;) {
-      const Part u = part_at(p, x, places, f, to);
+      const auto u = part_at<kFp8>(p, x, places, f, to);
       f = u.next;
       if (u.tiles() <= 0) continue;
       const int steps = u.steps();
@@ -322,12 +402,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if (slot >= steps && lane == 0) mbar_arrive(bar(kQFree));  // a single step is slot 0's
       // A turn: the values of step j, the scores of step j + 2 (the first turn: of step `slot`).
       for (int j = slot - 2; j < steps; j += 2) {
-        const int kn = 2 * u.tile(j + 2), vn = 2 * u.tile(j) + 1;
         const bool first = j < 0, more = j + 2 < steps;
         if (first && !more) continue;
-        // All that can be waited for is, before the turn.  The next keys of a unit of one
-        // query tile may take the place of these values.
-        if ((dual || first) && more) wait_op(kn);
+        const int kn = more ? u.keys(u.tile(j + 2)) : 0, vn = first ? 0 : u.values(u.tile(j));
+        // All that can be waited for is, before the turn.  (The next e4m3 keys of a unit of one
+        // query tile may take the place of these values.)
+        if (more && (!kFp8 || dual || first)) wait_op(kn);
         if (!first) {
           wait_op(vn);
           mbar_wait(bar(kPHalf + slot), ready & 1, p.err);
@@ -353,7 +433,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           ++ready;
           release(vn);
           if (!more) tc::commit_elect(bar(kODone + slot));
-          if (!dual && more) wait_op(kn);
+          if (kFp8 && !dual && more) wait_op(kn);
         }
         if (more) {
           const uint32_t b = base_u32 + ring.offset(ring.place(kn));
@@ -395,7 +475,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     int units = 0, tiles = 0;
     uint32_t got = 0, done[2] = {0, 0};  // phases of S; of O
     for (int f = from; f < to;) {
-      const Part u = part_at(p, x, places, f, to);
+      const auto u = part_at<kFp8>(p, x, places, f, to);
       f = u.next;
       if (u.tiles() <= 0) continue;
       const int steps = u.steps();
@@ -637,17 +717,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   } else if (kFp8 && warp >= kSlotWarp0 + 8) {
     // ============= e4m3 operand -> bf16 operand, swizzled for the MMA =============
     const int ct = tid - 32 * (kSlotWarp0 + 8);
-    int op = 0, units = 0;
-    bool was_dual = false;
+    int op = 0;
     OpRing<C> ring;
     for (int f = from; f < to;) {
-      const Part u = part_at(p, x, places, f, to);
+      const auto u = part_at<kFp8>(p, x, places, f, to);
       f = u.next;
       if (u.tiles() <= 0) continue;
       ring.begin(u.dual());
-      // the operand in the second query tile's place: its last unit's scores are done
-      if (C::kExtraOp && was_dual && !u.dual()) mbar_wait(bar(kQFree), (units - 1) & 1, p.err);
-      was_dual = u.dual();
       for (int i = 0; i < 2 * u.tiles(); ++i, ++op) {
         const int er = op % C::kRaws, eo = ring.place(i);
         mbar_wait(bar(kRawFull + er), (op / C::kRaws) & 1, p.err);
@@ -708,7 +784,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       }
       ring.end(2 * u.tiles());
-      ++units;
     }
   }
 

@@ -13,9 +13,8 @@ namespace pkv {
 // Groups in shared memory, from plan_groups.
 struct GroupPlan {
   const int *cu, *boxes;  // [groups + 1]; shared 16-key boxes [groups]
-  const int* places;      // [groups + 1]: place of the group's first unit
   int groups;             // 0: none (all requests are on their own)
-  int B, share;           // requests; places of a CTA of the first grid
+  int B;
 
   __device__ __forceinline__ int first() const { return groups ? cu[0] : 0; }
   __device__ __forceinline__ int end() const { return groups ? cu[groups] : B; }
@@ -47,24 +46,18 @@ __device__ __forceinline__ int blocks_of(const PagedParams& p, const GroupPlan& 
 
 constexpr int plan_ints(int groups) { return 3 * (groups + 1); }
 
-// Shared tokens are counted in whole boxes of 16, at most one token less than the group's
-// shortest request that is not empty (so every row sees all of them, and has at least one
-// token behind them), and 0 for a group with fewer than two such requests.
+// Shared tokens are counted in whole pages, at most one token less than the group's shortest
+// request that is not empty (so every row sees all of them, and has at least one token behind
+// them), and 0 for a group with fewer than two such requests.  (Boxes are 16 tokens.)
 //
-// Units (a group's blocks of kPrefixRows rows of a kv head) are laid end to end in the space
-// of costs: kPrefixUnitCost and the shared boxes each.  CTA c of the first grid takes places
-// [c share, (c + 1) share): whole tiles whose first box lies in them.
-//
-// mem: plan_ints(groups) ints that stay; scratch: groups + 1 ints, and with kLead as many that
-// stay and get each group's first request that is not empty; sums: one int per warp.  All
-// kThreads threads call it.  Offsets that decrease or leave [0, B] raise DEVERR_BAD_ROW
-// (report: by this CTA) and no group counts.
+// mem: plan_ints(groups) ints; lead, with kLead: groups + 1 ints, which get each group's first
+// request that is not empty.  All kThreads threads call it.  Offsets that decrease or leave
+// [0, B] raise DEVERR_BAD_ROW (report: by this CTA) and no group counts.
 template <int kThreads, bool kLead>
 __device__ __forceinline__ GroupPlan plan_groups(const PagedParams& p, const PrefixParams& x, int* mem,
-                                                 int* scratch, int* sums, bool report) {
-  const int tid = threadIdx.x, lane = tid & 31, B = p.B, n = x.groups;
-  int *cu = mem, *least = cu + n + 1, *places = least + n + 1;
-  int *live = places, *lead = scratch;
+                                                 int* lead, bool report) {
+  const int tid = threadIdx.x, B = p.B, n = x.groups;
+  int *cu = mem, *least = cu + n + 1, *live = least + n + 1;
   const int per = (B + kThreads - 1) / kThreads, b0 = tid * per, b1 = min(b0 + per, B);
   // asked for together
   const int len0 = b0 < B ? __ldg(p.seq_lens + b0) : 0;
@@ -80,9 +73,9 @@ __device__ __forceinline__ GroupPlan plan_groups(const PagedParams& p, const Pre
   }
   if (__syncthreads_or(bad)) {
     if (report && tid == 0) atomicOr(p.err, DEVERR_BAD_ROW);
-    return {cu, least, places, 0, B, kPrefixMinShare};
+    return {cu, least, 0, B};
   }
-  GroupPlan plan = {cu, least, places, n, B, kPrefixMinShare};
+  GroupPlan plan = {cu, least, n, B};
   // a thread's requests are neighbours: one step a group for each
   int g = plan.find(b0), lo = INT_MAX, cnt = 0, one = 0;
   auto note = [&] {
@@ -94,50 +87,23 @@ __device__ __forceinline__ GroupPlan plan_groups(const PagedParams& p, const Pre
     lo = INT_MAX;
     cnt = 0;
   };
-  for (int b = b0; b < b1; ++b) {
-    const int to = plan.next(g, b);
+#pragma unroll 1
+  for (int b = b0; b <= b1; ++b) {
+    const int to = b < b1 ? plan.next(g, b) : n;
     if (to != g) note();
     g = to;
+    if (b == b1) break;
     const int L = min(b == b0 ? len0 : __ldg(p.seq_lens + b), p.max_blocks * p.page_size);
     if (g < 0 || b >= cu[n] || L <= 0) continue;
     lo = min(lo, L);
     if (cnt++ == 0) one = b;
   }
-  note();
   __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
     const int S = i == tid ? shared0 : __ldg(x.shared_lens + i);
-    least[i] = (live[i] < 2 ? 0 : min(max(S, 0), least[i] - 1)) >> 4;
+    const int pages = live[i] < 2 ? 0 : min(max(S, 0), least[i] - 1) >> p.page_shift;
+    least[i] = pages << (p.page_shift - 4);
   }
-  __syncthreads();
-  // ---- places: a scan of the groups' costs ----
-  const int each = (n + kThreads - 1) / kThreads, g0 = min(tid * each, n), g1 = min(g0 + each, n);
-  auto cost = [&](int i) {
-    if (least[i] == 0) return 0;
-    return p.Hkv * blocks_of(p, plan, i) * (least[i] + kPrefixUnitCost);
-  };
-  int mine = 0;
-  for (int i = g0; i < g1; ++i) mine += cost(i);
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) sums[tid >> 5] = incl;
-  __syncthreads();
-  int run = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    run += w < tid >> 5 ? sums[w] : 0;
-    total += sums[w];
-  }
-  for (int i = g0; i < g1; ++i) {
-    places[i] = run;
-    run += cost(i);
-  }
-  if (tid == 0) places[n] = total;
-  plan.share = max((total + x.grid - 1) / x.grid, kPrefixMinShare);
   __syncthreads();
   return plan;
 }

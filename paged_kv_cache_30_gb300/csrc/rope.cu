@@ -28,7 +28,14 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kBatch = 4;  // rows a lane has under way
+// Rows a lane has under way, and CTAs of an SM.  16384 tokens of 36 heads of 128 with norms:
+// 54.2 us, 59.4 without the limit of registers, 61.5 with 2 rows and without it; 5001 of 27
+// heads of 64 with norms: 9.0 us, 9.9 with 4 rows, 10.6 with the limit; 8191 of 48 heads of 64
+// without norms into the cache: 15.7 us, 16.4 with 2 rows.
+template <int D, bool kNorm>
+constexpr int kBatch = D == 128 || !kNorm ? 4 : 2;
+template <int D>
+constexpr int kCtas = D == 128 ? 6 : 1;
 
 enum : int { kNone, kHalf, kInterleaved };
 
@@ -102,8 +109,9 @@ __device__ __forceinline__ void load_weights(const void* w, bool f32, int d, flo
 }
 
 template <int D, bool kAppend, int kPairs, bool kNorm>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas<D>)
     rope_kernel(const __grid_constant__ RopeParams p, int groups) {
+  constexpr int kBatch = pkv::kBatch<D, kNorm>;
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a warp
   const int lane = threadIdx.x & 31, col = lane % kLanes;
   const long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -295,8 +303,11 @@ cudaError_t launch_t(const RopeParams& p, int num_sms, cudaStream_t stream) {
   constexpr int kRows = 32 / (D / 8);
   const int k_groups = (p.Hkv + kRows - 1) / kRows;
   const int all = (p.Hq + kRows - 1) / kRows + k_groups * (kAppend ? 2 : 1);
-  // a token to a warp, or to several where that leaves an SM fewer than 8 warps
-  const int64_t parts = std::min<int64_t>(all, std::max<int64_t>(1, 8 * num_sms / p.T));
+  // A token to a warp, or to several where that leaves an SM fewer than 8 warps (16 on the way
+  // into the cache, where a warp first looks its page up).  64 tokens of 72 heads 2.2 us, 3.0
+  // with 16; of 80 heads into the cache 3.7 us, 4.6 with 8.
+  const int64_t parts =
+      std::min<int64_t>(all, std::max<int64_t>(1, (kAppend ? 16 : 8) * num_sms / p.T));
   const int groups = (int)((all + parts - 1) / parts);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.T + kWarps - 1) / kWarps), (unsigned)((all + groups - 1) / groups));
