@@ -1257,6 +1257,7 @@ static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool
     const int64_t rows = B * Hq, rest = int64_t(x.grid) * pkv::kPrefixRows;
     uint8_t* at = reinterpret_cast<uint8_t*>(ws.partials);
     x.info = reinterpret_cast<int4*>(at);
+    x.queue = reinterpret_cast<uint32_t*>(ws.counters + ws.num_counters - 1);
     x.own_o = reinterpret_cast<float4*>(at += B * 16);
     x.own_ml = reinterpret_cast<float4*>(at += rows * D * 4);
     x.first_o = reinterpret_cast<float4*>(at += rows * 16);

@@ -600,12 +600,42 @@ __device__ __forceinline__ void warp_store_own(const PagedParams& p, const Prefi
   }
 }
 
+// Tiles and pair costs of a CTA's (a warp's) share.
+__device__ __forceinline__ uint32_t chunk_of(uint32_t total, bool warps) {
+  const uint32_t shares = warps ? gridDim.x * kWarps : gridDim.x;
+  return max((total + shares - 1) / shares, warps ? 1u : (uint32_t)kPagedMinCost);
+}
+
+// Shares in turn, with shared tokens: a CTA draws the number of its next one from a counter, as
+// the CTAs do not begin together: on the SMs that prefix_attn.cu leaves at once, on the others when
+// it ends (64 requests behind 512 tokens 25.2 -> 20.8 us).  Parts have a share's place, whoever
+// takes it, so results do not depend on timing.
+// Every CTA draws one too many, and the last of these sets the counter back to 0.
+struct Draw {
+  uint32_t* place;  // in shared memory: two, for the numbers of this share and of the next
+  uint32_t share, shares;
+  int stage;        // of the warp's ring
+  uint32_t parity;
+  bool ok;
+
+  // by one thread
+  __device__ __forceinline__ void next(const PrefixParams* x) { place[0] = atomicAdd(x->queue, 1u); }
+  __device__ __forceinline__ void take() {
+    __syncthreads();
+    share = place[0];
+    place = reinterpret_cast<uint32_t*>(reinterpret_cast<uintptr_t>(place) ^ 4u);
+  }
+  __device__ __forceinline__ void reset(const PrefixParams* x) {
+    if (share == shares + gridDim.x - 1) *x->queue = 0;
+  }
+};
+
 // The CTA's work, after the prologue below.  next: the pair in the cluster mode; whole:
 // equal numbers of pairs for the CTAs instead of equal shares of tiles.
 template <class C, int kMode, bool kShared = false>
 __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& kv_map,
                                        uint8_t* base, uint32_t base_u32, Pair next, bool whole,
-                                       const PrefixParams* x = nullptr) {
+                                       const PrefixParams* x = nullptr, Draw* draw = nullptr) {
   constexpr bool kCluster = kMode == kPagedCluster, kPerWarp = kMode == kPagedWarp;
   constexpr int D = C::D, NB = C::NB, U = C::U, kStages = C::kStages, E = D / 16;
   constexpr bool kFp8 = C::kFp8;
@@ -618,6 +648,8 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
   const uint32_t bars = base_u32 + C::kOffBars + warp * kStages * 8;
   const int B = p.B, Hkv = p.Hkv;
 
+  const uint32_t cta = kShared ? draw->share : blockIdx.x;
+
   // This CTA's tiles (the warp's in the warp mode) are [f0, f1) of all pairs' (of one
   // pair's in the cluster mode).
   int f0, f1, chunk = 0, snap = 0;
@@ -627,26 +659,25 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
     f1 = (int)((long long)next.n * (part + 1) / p.cluster);
   } else if (whole) {
     auto place = [&](uint32_t cta) {  // of the first tile of its first pair
-      const int i = (int)((long long)B * Hkv * cta / gridDim.x), b = i / Hkv;
+      const int i = (int)((long long)B * Hkv * cta / (kShared ? draw->shares : gridDim.x)), b = i / Hkv;
       return b == B ? prefix[B] * Hkv
                     : prefix[b] * Hkv + i % Hkv * (prefix[b + 1] - prefix[b]);
     };
-    f0 = place(blockIdx.x);
-    f1 = place(blockIdx.x + 1);
+    f0 = place(cta);
+    f1 = place(cta + 1);
   } else {
     // cuts are placed in the space of costs and turned into places of tiles
     const int tiles = prefix[B] * Hkv, total = tiles + kCost * B * Hkv;
-    const uint32_t shares = kPerWarp ? gridDim.x * kWarps : gridDim.x;
-    const uint32_t share = kPerWarp ? blockIdx.x * kWarps + warp : blockIdx.x;
-    chunk = max((int)(((uint32_t)total + shares - 1) / shares), kPerWarp ? 1 : kPagedMinCost);
+    const uint32_t share = kPerWarp ? cta * kWarps + warp : cta;
+    chunk = (int)chunk_of((uint32_t)total, kPerWarp);
     snap = min(kPerWarp ? kWarpSnapTiles : kSnapTiles, chunk / 2);
     // lanes 0..15 place this share's cut, lanes 16..31 the next one's
-    const long long x = ((long long)share + (lane >> 4)) * chunk;
-    const int y = (int)min(x, (long long)total - 1);
+    const long long at_cost = ((long long)share + (lane >> 4)) * chunk;
+    const int y = (int)min(at_cost, (long long)total - 1);
     const Pair r = pair_at_group<kCost, 16>(prefix, B, Hkv, y);
     const int at = y - r.begin - kCost;  // the pair's tiles before the cut
     int f = prefix[r.b] * Hkv + r.kvh * r.n + (at <= snap ? 0 : r.n - at <= snap ? r.n : at);
-    if (x >= total) f = tiles;
+    if (at_cost >= total) f = tiles;
     f0 = __shfl_sync(0xffffffffu, f, 0);
     f1 = __shfl_sync(0xffffffffu, f, 16);
   }
@@ -726,7 +757,12 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
   __syncwarp();  // the ring's barriers are lane 0's
   look_up(lane);
   int issued = 0;
-  for (; issued < min(count, kStages); ++issued) issue(issued, issued);
+  // with shares in turn the ring goes on where the share before ended
+  bool ok = !kShared || draw->ok, drawn = false;
+  int n = 0, stage = kShared ? draw->stage : 0;  // the warp's next tile and its stage
+  uint32_t parity = kShared ? draw->parity : 0;
+  for (; ok && issued < min(count, kStages); ++issued)
+    issue(issued, kShared ? (stage + issued) % kStages : issued);
 
   // ---- fragment addresses ----
   // ldmatrix: matrix mi = lane / 8 takes its 8 rows from lanes 8 mi .. 8 mi + 7.
@@ -746,9 +782,6 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
   const int er = tid >> 4, ed = (tid & 15) * E;  // this thread's part of an output
   const int sr = kPerWarp ? g : er;  // the row whose sink this thread needs
   float* my_wb = wbuf + warp * C::kWbFloats;
-  bool ok = true;
-  int n = 0, stage = 0;  // the warp's next tile and its stage
-  uint32_t parity = 0;
 
   for (int f = f0; f < f1;) {
     const Pair pr = next;
@@ -1038,6 +1071,10 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
       }
     }
 
+    if (kShared && tid == 0 && seg_end == f1) {
+      draw->next(x);
+      drawn = true;
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 1);
@@ -1049,7 +1086,7 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
         // Contributors and slots as below, of warps.
         const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kCost;
         const int c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
-        const int me = (int)blockIdx.x * kWarps + warp - c0;
+        const int me = (int)cta * kWarps + warp - c0;
         warp_store_partial<C>(p, part_slot(c0, me), acc, m, l, R);
         __syncwarp();
         int* cnt = p.pair_counters + pr.b * Hkv + pr.kvh;
@@ -1116,7 +1153,7 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
         // ones whose cuts lie inside (slot 2 c), more than snap tiles from either border.
         const int x0 = pr.begin + (pr.b * Hkv + pr.kvh + 1) * kPairCost;
         const int c0 = (x0 + snap) / chunk, c1 = (x0 + pr.n - snap - 1) / chunk;
-        const int parts = c1 - c0 + 1, me = (int)blockIdx.x - c0;
+        const int parts = c1 - c0 + 1, me = (int)cta - c0;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
           store_partial<C>(p, part_slot(c0, me), er + 8 * nb, ed, o[nb], mc[nb], lc[nb], Rc[nb]);
@@ -1167,8 +1204,18 @@ __device__ __forceinline__ void attend(const PagedParams& p, const CUtensorMap& 
 
   // A wait that gave up leaves copies in flight: wait for them (again with a
   // limit) before the shared memory goes to another CTA.
-  if (!ok)
-    for (; n < issued; ++n) mbar_wait(bars + 8 * (n % kStages), (n / kStages) & 1, p.err);
+  if (!ok) {
+    for (; n < issued; ++n) {
+      mbar_wait(bars + 8 * stage, parity, p.err);
+      if (++stage == kStages) stage = 0, parity ^= 1;
+    }
+  }
+  if (kShared) {
+    if (tid == 0 && !drawn) draw->next(x);
+    draw->ok = ok;
+    draw->stage = stage;
+    draw->parity = parity;
+  }
 
   if constexpr (kCluster) {
     if (next.n == 0 && part == 0) {  // no key
@@ -1245,6 +1292,8 @@ __device__ __forceinline__ void paged_attn(const PagedParams& p, const CUtensorM
     fence_barrier_init();
   }
   if (tid == 0) tma_prefetch_desc(&kv_map);
+  Draw draw = {reinterpret_cast<uint32_t*>(base + C::kOffMisc) + 10, 0, 0, 0, 0, true};
+  if (kShared && tid == 0) draw.next(x);
   // Nothing of the caller's is read before the wait; with shared tokens the grid before this
   // one is prefix_attn.cu's, which has waited before it lets this one start.
   if (!kShared) griddep_wait();
@@ -1297,7 +1346,7 @@ __device__ __forceinline__ void paged_attn(const PagedParams& p, const CUtensorM
         if (b == B - 1) prefix[B] = run;
       }
     }
-    __syncthreads();
+    if (kShared) draw.take(); else __syncthreads();
     griddep_launch_dependents();
 
     // requests without a key
@@ -1321,14 +1370,25 @@ __device__ __forceinline__ void paged_attn(const PagedParams& p, const CUtensorM
     // 60.1 / 119.4 us, 1000 x 8 of up to 300 keys, heads of 64, 50.0 / 75.8, 256 x 8 of 10
     // to 700 keys 40.4 / 47.2, of 700 to 768 keys 69.9 / 76.2; a bf16 window of 128 on
     // 512 x 8 kv heads 58.3 / 63.9.  64 x 8 of up to 32768 keys lose, 63.5 / 51.5.
-    if (p.warps && waves > 2 && most <= kPagedWarpTiles) {
-      attend<C, kPagedWarp, kShared>(p, kv_map, base, base_u32, Pair{}, false, x);
-    } else {
-      const uint32_t share = max(((uint32_t)prefix[B] * Hkv + kPairCost * pairs) / gridDim.x,
-                                 (uint32_t)kPagedMinCost);
-      attend<C, kPagedShares, kShared>(p, kv_map, base, base_u32, Pair{},
-                                       waves <= 2 && waves * (most + kPairCost) <= share + kEndCost, x);
+    const bool warps = p.warps && waves > 2 && most <= kPagedWarpTiles;
+    const uint32_t share = max(((uint32_t)prefix[B] * Hkv + kPairCost * pairs) / gridDim.x,
+                               (uint32_t)kPagedMinCost);
+    const bool whole = waves <= 2 && waves * (most + kPairCost) <= share + kEndCost;
+    if (kShared) {
+      const uint32_t total = (uint32_t)prefix[B] * Hkv + (warps ? kWarpPairCost : kPairCost) * pairs;
+      const uint32_t chunk = chunk_of(total, warps);
+      const uint32_t n = (total + chunk - 1) / chunk;
+      draw.shares = !warps && whole ? pairs : warps ? (n + kWarps - 1) / kWarps : n;
     }
+    while (!kShared || draw.share < draw.shares) {
+      if (warps)
+        attend<C, kPagedWarp, kShared>(p, kv_map, base, base_u32, Pair{}, false, x, &draw);
+      else
+        attend<C, kPagedShares, kShared>(p, kv_map, base, base_u32, Pair{}, whole, x, &draw);
+      if (!kShared) break;
+      draw.take();
+    }
+    if (kShared && tid == 0) draw.reset(x);
     if (kShared) griddep_wait();  // this grid ends after the one before it
   }
 }

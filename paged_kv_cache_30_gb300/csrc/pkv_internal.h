@@ -285,14 +285,16 @@ constexpr int kPagedWarpTiles = 64;
 // the third (prefix_combine.cu) adds up.
 constexpr int kPrefixRows = 256;     // query rows of a unit: two tiles of 128
 constexpr int kPrefixTileKeys = 128; // keys of a step
-// A CTA's share is counted in 16-key boxes plus a cost for each unit, and is no smaller than
-// kPrefixMinShare (a multiple of a tile's boxes, so that every CTA of a cut unit has a tile; 64
-// requests behind 512 tokens take 28 us with 32, 25 with 16, 23.5 with 8, but 4 behind 8192 then
-// 22 for 18.5, as more parts are to be added up).
+// A CTA's share is counted in 16-key boxes plus a cost for each unit; it is a multiple of a
+// tile's boxes, so that every CTA of a cut unit has a tile, and no smaller than kPrefixMinShare
+// (64 requests behind 512 tokens take 20 us with 16, 22 with 24, 23 with 32; 4 requests 12.6,
+// 13.4 and 14.4; 4 behind 8192 17.6, 16.4 and 18.3).  At a cost of 24, 64 requests behind 2048
+// tokens take 27.7 us instead of 24.8, 33 e4m3 requests with heads of 64 34.8 instead of 34.1,
+// but 128 requests behind 32768 126 instead of 128.
 // Units (a group's blocks of kPrefixRows rows of a kv head) are laid end to end in the space of
 // costs, and CTA c takes places [c share, (c + 1) share): whole tiles whose first box lies in
 // them.
-constexpr int kPrefixUnitCost = 24;
+constexpr int kPrefixUnitCost = 40;
 constexpr int kPrefixMinShare = 16;
 struct PrefixParams {
   const int32_t* cu_groups;      // [groups + 1]
@@ -301,6 +303,7 @@ struct PrefixParams {
   // per request: {first request of its group | row blocks of a kv head << 16, place of the
   // group's first unit, shared boxes (-1: padding), share of a CTA}
   int4* info;                    // [B]
+  uint32_t* queue;               // the next share of the requests' own tokens; 0 between calls
   // of a request's own tokens; {m, l, reference of O, -}
   float4* own_o;                 // [Hkv][D / 4][B G]
   float4* own_ml;                // [Hkv][B G]

@@ -263,7 +263,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     __syncthreads();
     total = places[plan.groups];
+    // Whole tiles: a CTA with a little less would have as many at most, and the SMs that are
+    // left are the next grid's (64 requests behind 512 tokens 25.3 -> 20.8 us).
     share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kPrefixMinShare);
+    share = (share + kTileBoxes - 1) / kTileBoxes * kTileBoxes;
     if (blockIdx.x == gridDim.x - 1) {  // for prefix_combine.cu
       for (int b = tid; b < p.B; b += C::kThreads) {
         const int g = plan.groups ? plan.find(b) : -1;

@@ -34,6 +34,12 @@ __global__ void __launch_bounds__(kThreads)
   const int4 at = __ldcg(x.info + b);
   const int len = __ldg(p.seq_lens + b);
   const float sink = p.sinks ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
+  // asked for with them; what was not written is not used
+  const float4 ml = __ldcg(x.own_ml + kvh * rows + row);
+  float4 o[kQuads];
+#pragma unroll
+  for (int k = 0; k < kQuads; ++k)
+    o[k] = __ldcg(x.own_o + (kvh * (D / 4) + q0 + 16 * k) * rows + row);
   if (at.z < 0) return;  // padding
   uint16_t* out = p.out + b * p.o_sb + head * p.o_sh;
   float* lse = p.lse ? p.lse + b * p.lse_sb + head * p.lse_sh : nullptr;
@@ -44,11 +50,6 @@ __global__ void __launch_bounds__(kThreads)
     if (lse && q0 == 0) *lse = -INFINITY;
     return;
   }
-  const float4 ml = __ldcg(x.own_ml + kvh * rows + row);
-  float4 o[kQuads];
-#pragma unroll
-  for (int k = 0; k < kQuads; ++k)
-    o[k] = __ldcg(x.own_o + (kvh * (D / 4) + q0 + 16 * k) * rows + row);
   float m = ml.x, l = ml.y, R = ml.z;
 
   // The shared tokens' parts: of the CTAs from the one that holds the end of the unit's first
