@@ -732,29 +732,26 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         mbar_wait(bar(kRawFull + er), (op / C::kRaws) & 1, p.err);
         const uint8_t* src = base + C::kOffRaw + er * C::kRawBytes;
         uint8_t* dst = base + ring.offset(eo);
-        // 16 codes each; a thread's are kStep rows apart, which keeps the unit and the swizzle
-        constexpr int kUnits = D / 16, kStep = C::kConverters / kUnits, kMine = kTile / kStep;
+        // 8 codes each, a 16-byte unit of the operand; a thread's are kStep rows apart, which keeps
+        // the unit and the swizzle
+        constexpr int kUnits = D / 8, kStep = C::kConverters / kUnits, kMine = kTile / kStep;
         static_assert(kStep % 8 == 0, "the swizzle of a thread's rows");
-        const int r0 = ct / kUnits, q = ct % kUnits, odd = (q >> 2) & 1;
-        // dims 16 q .. + 15: units 2 q' and 2 q' + 1 of piece q / 4, which begin with different
-        // units, for the banks
-        const uint32_t at = (q >> 2) * C::kChunkBytes + r0 * 128;
-        const uint32_t a0 = at + ((2 * (q & 3) + odd) ^ (r0 & 7)) * 16;
-        const uint32_t a1 = at + ((2 * (q & 3) + 1 - odd) ^ (r0 & 7)) * 16;
-        constexpr int kBatch = 4;
+        const int r0 = ct / kUnits, q = ct % kUnits;
+        dst += (q >> 3) * C::kChunkBytes + r0 * 128 + ((q & 7) ^ (r0 & 7)) * 16;
+        constexpr int kBatch = 8;
         static_assert(kMine % kBatch == 0, "batches");
 #pragma unroll 1
         for (int k0 = 0; k0 < kMine; k0 += kBatch) {
-          uint4 w[kBatch];
-          uint32_t o[kBatch][8];
+          uint2 w[kBatch];
+          uint32_t o[kBatch][4];
 #pragma unroll
           for (int k = 0; k < kBatch; ++k)
-            w[k] = *reinterpret_cast<const uint4*>(src + (ct + (k0 + k) * C::kConverters) * 16);
+            w[k] = *reinterpret_cast<const uint2*>(src + (ct + (k0 + k) * C::kConverters) * 8);
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            const uint32_t wv[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            const uint32_t wv[2] = {w[k].x, w[k].y};
 #pragma unroll
-            for (int h = 0; h < 8; ++h)
+            for (int h = 0; h < 4; ++h)
               asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
                   : "=r"(o[k][h])
                   : "h"((uint16_t)(wv[h / 2] >> (16 * (h & 1)))));
@@ -763,7 +760,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-              for (int h = 0; h < 8; ++h) {
+              for (int h = 0; h < 4; ++h) {
                 const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&o[k][h]));
                 o[k][h] = pack_bf16(fv.x, fv.y);
               }
@@ -771,12 +768,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           // the first batch before the operand's place is free
           if (k0 == 0) mbar_wait(bar(kOpEmpty + eo), ring.phase(i) ^ 1u, p.err);
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const uint4 lo = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
-            const uint4 hi = make_uint4(o[k][4], o[k][5], o[k][6], o[k][7]);
-            *reinterpret_cast<uint4*>(dst + a0 + (k0 + k) * kStep * 128) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + a1 + (k0 + k) * kStep * 128) = odd ? lo : hi;
-          }
+          for (int k = 0; k < kBatch; ++k)
+            *reinterpret_cast<uint4*>(dst + (k0 + k) * kStep * 128) =
+                make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
         }
         fence_proxy_async_smem();  // the MMA reads through the async proxy
         __syncwarp();
