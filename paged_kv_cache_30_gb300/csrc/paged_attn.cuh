@@ -55,6 +55,10 @@
 //    results (one request of 16000 keys: 16.1 us; with fp16 weights 15.1, and 18.4 where one
 //    thread per output went through all parts).  Results do not depend on timing.
 //
+//  * Behind shared tokens (kShared; prefix_attn.cu has attended to those): a request's tiles
+//    are those after the shared ones, CTAs draw their shares from a counter, and what a pair adds
+//    up to goes to the workspace in 32 bits instead of the output.
+//
 // Measured (GB300, graph replays; the copy bandwidth is 6786 GB/s): e4m3, 8 requests
 // of 131072 keys, 8 kv heads of 128: 314 us = 6.85 TB/s; 64 requests of up to 32768
 // keys (272 MB): 51.4 us = 5.3 TB/s, of which 4 us pass before the first tile arrives

@@ -10,29 +10,38 @@
 // O, m and l go to the workspace in 32 bits; the grid after this one (paged_attn.cuh)
 // attends to each request's own keys, the third (prefix_combine.cu) adds up all parts.
 //
-// Bound by the tensor cores and the exponentials of many rows (a key of 512 bytes is
-// multiplied with 512 rows, say), by memory of few.
+// Bound by the tensor cores, and under them by power, with many rows (a key of 512 bytes is
+// multiplied with 1024 rows, say), by memory with few.
 //
 //  * A unit is (group, kv head, block of 256 rows); units are laid end to end, counted in
 //    16-key boxes plus a cost for each, and CTA c takes an equal share of the whole, whose
-//    cuts fall on 128-key tiles.  One CTA per SM.
+//    cuts fall on 128-key tiles.  One CTA per SM, on as many SMs as the shares need.
 //  * Two slots, each with a score tile S[128 x 128] and an accumulator O[128 x D] in
 //    tensor memory and 128 softmax threads, one per row.  More than 128 rows: slot s has
 //    rows 128 s .. and both go through all tiles.  Fewer: both slots have the same rows, slot
 //    s tiles s, s + 2, .., and slot 0 adds up the two at the end (each of its threads reads
 //    the other's row of tensor memory).  While one slot's threads are at their
 //    exponentials, the tensor cores work for the other.
-//  * warps 0 and 3 ask for K and V of a tile by TMA, a lane for a page and a warp for half of
-//    them, into a ring of operands; warps 1 and 2 issue S = Q K^T (M 128, N 128 keys, K D) and O += P V (M 128, N
-//    D, K 128) of a slot each, P read from tensor memory, where it overlays S.  (One warp for
-//    both took 1740 cycles a step of 1024 cycles of products, the rest its waits and
-//    commits.)  e4m3 tiles land in a ring of their own, and four warps rewrite them as bf16
-//    (exact).
+//  * Warps 0 and 3 ask for K and V of a tile by TMA, a lane for a page and a warp for half of
+//    them, into a ring of operands; warps 1 and 2 issue S = Q K^T (M 128, N 128 keys, K D) and
+//    O += P V (M 128, N D, K 128) of a slot each, P read from tensor memory, where it overlays
+//    S.  (One warp for both took 1740 cycles a step of 1024 cycles of products, the rest its
+//    waits and commits.)  e4m3 tiles land in a ring of their own, and four warps rewrite K as
+//    fp16 and V as bf16 (both exact).
 //  * The reference m of a row moves when a score passes it by more than 2^8, and O is
 //    rescaled in tensor memory then; the scores of a step are there only after O of the
 //    steps before is, so that needs no wait.  P, times its value's scale, is rounded once to
 //    bf16, whose exponents are those of 32-bit values: 2^-9 of each weight, as in the decode
 //    of a bf16 cache.
+//
+// Measured (GB300, whole calls in a graph, 64 query and 8 kv heads of 128; the cuBLAS rate is 1929
+// TFLOP/s, 1759 for seconds on end): 128 requests behind 131072 tokens 406 us = 1.35 PFLOP/s; on inputs
+// that change from call to call, for seconds, 459 us = 1.20, at 1.4 kW and 1.5 to 1.8 GHz.  64
+// requests behind 8192 tokens and up to 2048 of their own 45.5 us, of which this grid has 25: a
+// start of 6 us (three dependent reads), 1 us a step, parts written in 2.  58 forked e4m3 samples
+// behind 500 to 32768 tokens (438 MB) 157 us; the same of bf16 (876 MB) 155 us = 84 % of the copy
+// bandwidth.  e4m3 tiles of few rows are bound by their rewriting, which is latency (8 codes a
+// thread at a time, 8 reads under way; 16 codes and 4 reads: 164 us; none at all: 149).
 #include <algorithm>
 
 #include "pkv_internal.h"
@@ -226,6 +235,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   // The grid after this one reads ahead of its own wait, which is sound as every CTA of
   // this one has waited before it lets it start.
   griddep_wait();
+  if (blockIdx.x == 0) {
+    // it is 0, unless calls that shared the workspace ran at once
+    if (tid == 0) {
+      atomicExch(x.queue, 0u);
+      __threadfence();
+    }
+    __syncthreads();
+  }
   griddep_launch_dependents();
 
   // ---- places of the groups' units ----

