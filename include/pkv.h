@@ -603,7 +603,8 @@ PKV_API int pkv_rope_table(const double* inv_freq, int rot_dim, double base, dou
  *                themselves, the same view; otherwise they share no memory with any
  *                input or with each other (views side by side in one row share none).
  *   stream       cudaStream_t.
- * One launch; nothing of the workspace is used.  T == 0 is a no-op.
+ * One launch; nothing of the workspace is used.  T == 0 is a no-op.  Where k_out lies in
+ * the pages of a cache, the note on dependent launch above applies to the next call.
  */
 PKV_API int pkv_qk_norm_rope(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* q_weight,
                              const pkv_tensor* k_weight, float eps, const pkv_tensor* positions,

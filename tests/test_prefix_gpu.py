@@ -2,6 +2,7 @@
 pkv_paged_prefix_attn_fp8) against the 64-bit definition on each request's own row, element by
 element within the bounds of the kernels' roundings."""
 import math
+import threading
 
 import pytest
 import torch
@@ -310,6 +311,50 @@ def test_same_bits_every_time_back_to_back_and_on_another_stream(fp8):
     torch.cuda.synchronize()
     assert all(torch.equal(o, outs[0]) for o in outs)
     check(pr, outs[0], None)
+
+
+def test_calls_of_three_threads():
+    """Each on a stream of its own, with parts, counters and the counter of shares in the one
+    workspace: every result is what the call gives alone."""
+    jobs = []
+    for seed, fp8, groups in ((41, False, [(5000, [5001 + 7 * i for i in range(20)]), (0, [3000])]),
+                              (42, True, [(700, [710, 900, 3000]), (9000, [9001, 9500])]),
+                              (43, False, [(33, [40] * 50), (128, [129, 4000])])):
+        d = upload(plain.problem(seed, groups, 2, 8, 128, 16, fp8))
+        want = torch.empty_like(d["q"])
+        call(d, want, None)
+        outs = [torch.full_like(d["q"], math.nan) for _ in range(40)]
+        jobs.append((d, want, outs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    failed, start = [], threading.Barrier(len(jobs))
+
+    def work(d, want, outs, stream):
+        try:
+            start.wait()
+            for out in outs:
+                call(d, out, None, stream)
+        except Exception as e:  # noqa: BLE001 (shown below)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for _, want, outs, _ in jobs:
+        assert all(torch.equal(out, want) for out in outs)
+    assert pkv.check_errors(0) == 0
+    assert pkv.check_counters(0) == 0
+
+
+@BOTH
+def test_one_request_of_many_own_tokens_beside_short_ones(fp8):
+    """Own tokens of very unequal length: blocks that begin early take several shares in turn."""
+    pr = plain.problem(44, [(160, [161, 20000, 170, 162]), (64, [65, 66, 6000])], 4, 4, 128, 16, fp8,
+                       sinks=True)
+    check(pr, *run(pr))
 
 
 @BOTH

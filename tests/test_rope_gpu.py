@@ -155,6 +155,29 @@ def test_zeros_infinities_and_nan_stay_in_their_heads():
     assert out[1, 2].eq(0).all() and out[2, 0].isnan().all() and out[3, 1].isnan().any()
 
 
+def test_rotation_captured_and_replayed_at_other_positions():
+    g = torch.Generator().manual_seed(33)
+    q, k, freq = heads(g, 5, 4, 128), heads(g, 5, 2, 128), plain.frequencies(128)
+    dq, dk, table = q.cuda(), k.cuda(), pkv.rope_table(128)
+    pos, qo, ko = torch.zeros(5, dtype=torch.int32, device="cuda"), torch.empty_like(dq), torch.empty_like(dk)
+
+    def call():
+        pkv.qk_norm_rope(dq, dk, None, None, 0.0, pos, table, 1.0, False, qo, ko)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call()
+    torch.cuda.synchronize()
+    for at in ([0, 1, 2, 3, 4], [(1 << 31) - 1, 70000, 5, 0, 123456789]):
+        pos.copy_(torch.tensor(at, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, x in ((qo, q), (ko, k)):
+            close(got, *plain.norm_rope(x, None, 0.0, pos.cpu(), freq, 1.0, False))
+
+
 def test_given_frequencies():
     g = torch.Generator().manual_seed(9)
     freq = torch.rand(16, generator=g, dtype=torch.float64) * 7 - 1  # also more than a turn, negative
