@@ -35,8 +35,8 @@
 //    of a bf16 cache.
 //
 // Measured (GB300, whole calls in a graph, 64 query and 8 kv heads of 128; the cuBLAS rate is 1929
-// TFLOP/s, 1759 for seconds on end): 128 requests behind 131072 tokens 406 us = 1.35 PFLOP/s; on inputs
-// that change from call to call, for seconds, 459 us = 1.20, at 1.4 kW and 1.5 to 1.8 GHz.  64
+// TFLOP/s, 1759 for seconds on end): 128 requests behind 131072 tokens 390 us = 1.41 PFLOP/s; on inputs
+// that change from call to call, for seconds, 430 us = 1.28, at 1.4 kW and 1.5 to 1.8 GHz.  64
 // requests behind 8192 tokens and up to 2048 of their own 45.5 us, of which this grid has 25: a
 // start of 6 us (three dependent reads), 1 us a step, parts written in 2.  58 forked e4m3 samples
 // behind 500 to 32768 tokens (438 MB) 157 us; the same of bf16 (876 MB) 155 us = 84 % of the copy
@@ -58,6 +58,11 @@ constexpr int kTile = kPrefixTileKeys, kTileBoxes = kTile / 16;
 constexpr int kSlotWarp0 = 4;  // softmax warps: 4..7 slot 0, 8..11 slot 1
 constexpr int kSlotThreads = 128;
 constexpr int kScaleTiles = 8;  // tiles whose scales are kept: more than keys are ahead of the weights
+// Shares of at least so many tiles are read in turned order, see part_at.  128 requests behind
+// 131072 tokens (shares of 216 tiles, 537 MB) take 390 us instead of 406 and, where power limits
+// them, 430 instead of 459; behind 32768 (54 tiles) 127 and 128.  Shares of 8 to 16 tiles, whose
+// keys L2 holds in any order, lose: e4m3 heads of 64 35.4 us instead of 34.0.
+constexpr int kTurnTiles = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;   // log2 units
 constexpr float kTiny = 1e-37f;  // times any score that is finite: no change of its weight
@@ -142,6 +147,7 @@ struct Part {
   int row0;             // of the block within the group
   int kvh;
   int boxes, t0, t1;    // shared boxes; tiles of this part
+  int turn;             // its first step's tile is t0 + turn
   bool whole_start;     // it holds the first tile
   int next;             // place of the next unit
   __device__ __forceinline__ int tiles() const { return t1 - t0; }
@@ -149,6 +155,11 @@ struct Part {
   // steps of the two slots together: step j is slot j & 1's
   __device__ __forceinline__ int steps() const { return dual() ? 2 * tiles() : tiles(); }
   __device__ __forceinline__ int tile(int j) const { return dual() ? j >> 1 : j; }
+  // The tile of the unit that comes t-th: from t0 + turn on, then those before it.
+  __device__ __forceinline__ int at(int t) const {
+    t += turn;
+    return t0 + (t < tiles() ? t : t - tiles());
+  }
   // Operands come in the order in which the steps use them: K0 V0 K1 V1 .. for two query tiles,
   // K0 K1 V0 K2 V1 .. for one, whose steps j and j + 1 are at work together.  (Of an e4m3 cache
   // always as for two, which has less to work out.)
@@ -171,7 +182,7 @@ struct Part {
 // The unit that holds place f < the CTA's end `to`.
 template <bool kFp8>
 __device__ __forceinline__ Part<kFp8> part_at(const PagedParams& p, const PrefixParams& x,
-                                              const int* places, int f, int to) {
+                                              const int* places, int f, int to, int share) {
   Part<kFp8> r;
   const int* at = places + x.groups + 1;
   int lo = 0, hi = x.groups - 1;
@@ -197,6 +208,10 @@ __device__ __forceinline__ Part<kFp8> part_at(const PagedParams& p, const Prefix
   r.t0 = cut(f);
   r.t1 = cut(to);
   r.whole_start = r.t0 == 0;
+  // CTAs begin with tiles a share apart, so that those with other rows of the same keys, whose
+  // cuts fall elsewhere, read a tile at about the same time: once from DRAM, then from L2.
+  const int period = share / kTileBoxes, start = (r.t0 + period - 1) / period * period;
+  r.turn = period >= kTurnTiles && start < r.t1 ? start - r.t0 : 0;
   return r;
 }
 
@@ -321,15 +336,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     int op = 0, tiles = 0;                 // operands and tiles of units before
     OpRing<C> ring;
     for (int f = from; f < to;) {
-      const auto u = part_at<kFp8>(p, x, places, f, to);
+      const auto u = part_at<kFp8>(p, x, places, f, to, share);
       f = u.next;
       if (u.tiles() <= 0) continue;
       const int32_t* table = p.bt + (int64_t)u.lead * p.bt_sb;
       const int end = min(u.boxes, u.t1 * kTileBoxes) * 16;  // tokens
       ring.begin(u.dual());
       auto page_of = [&](int t) {  // this lane's page of tiles t ..
-        const int page = ((u.t0 + t) << in_tile) + lane;
-        return page << p.page_shift < end ? __ldg(table + min(page, p.max_blocks - 1)) : INT_MAX;
+        t += lane >> in_tile;
+        const int page = (u.at(t) << in_tile) + sub;
+        return t < u.tiles() && page << p.page_shift < end ? __ldg(table + min(page, p.max_blocks - 1)) : INT_MAX;
       };
       auto scale_of = [&](int page) {
         float2 s = make_float2(0.f, 0.f);
@@ -404,7 +420,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint32_t ready = 0, turns = 0;  // phases of P; of this slot's turns
     OpRing<C> ring;
     for (int f = from; f < to;) {
-      const auto u = part_at<kFp8>(p, x, places, f, to);
+      const auto u = part_at<kFp8>(p, x, places, f, to, share);
       f = u.next;
       if (u.tiles() <= 0) continue;
       const int steps = u.steps();
@@ -495,7 +511,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     int units = 0, tiles = 0;
     uint32_t got = 0, done[2] = {0, 0};  // phases of S; of O
     for (int f = from; f < to;) {
-      const auto u = part_at<kFp8>(p, x, places, f, to);
+      const auto u = part_at<kFp8>(p, x, places, f, to, share);
       f = u.next;
       if (u.tiles() <= 0) continue;
       const int steps = u.steps();
@@ -565,7 +581,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         __syncwarp();
         tc::fence_after_sync();
         if (live) {
-          const int valid = min(u.boxes - (u.t0 + t) * kTileBoxes, kTileBoxes);  // boxes
+          const int valid = min(u.boxes - u.at(t) * kTileBoxes, kTileBoxes);  // boxes
           const float2* sc = reinterpret_cast<const float2*>(base + C::kOffScale) +
                              (at % kScaleTiles) * kTileBoxes;
           // log2 units of a score of box h (never 0: no infinity times 0)
@@ -740,7 +756,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     int op = 0;
     OpRing<C> ring;
     for (int f = from; f < to;) {
-      const auto u = part_at<kFp8>(p, x, places, f, to);
+      const auto u = part_at<kFp8>(p, x, places, f, to, share);
       f = u.next;
       if (u.tiles() <= 0) continue;
       ring.begin(u.dual());
