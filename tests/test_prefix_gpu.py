@@ -112,6 +112,16 @@ def test_long_prefixes_cut_among_many_blocks(fp8, D, Hkv, S):
     check(pr, *run(pr))
 
 
+@BOTH
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 32), (64, 128)])
+def test_long_shares_of_many_blocks_of_rows(fp8, D, P):
+    """Shares of more than 32 tiles, cut elsewhere for each block of rows: their tiles come in
+    turned order, with the unit's last tile, which is cut short, among them."""
+    pr = plain.problem(P, [(11237, [11238 + 3 * i for i in range(100)]), (6100, [6101 + i for i in range(70)])],
+                       8, 16, D, P, fp8)
+    check(pr, *run(pr))
+
+
 GROUPS = [(500, [0, 510, 501, 700]), (0, [40, 30]), (1000, [1300]), (64, [0, 0]), (300, []),
           (256, [257] * 9), (90, [20, 95, 200]), (48, [48, 48, 48]), (5, [6, 9]), (33, [0, 35, 0])]
 
