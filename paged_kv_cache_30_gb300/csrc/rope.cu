@@ -33,13 +33,13 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 // Rows a lane has under way, and CTAs of an SM.  16384 tokens of 36 heads of 128 with norms:
-// 54.2 us, 59.4 without the limit of registers, 61.5 with 2 rows and without it; 5001 of 27
-// heads of 64 with norms: 9.0 us, 9.9 with 4 rows, 10.6 with the limit; 8191 of 48 heads of 64
-// without norms into the cache: 15.7 us, 16.4 with 2 rows.
+// 54.2 us, 59.4 without the limit of registers, 61.5 with 2 rows and without it.  On data that
+// L2 does not hold: 5001 of 27 heads of 64 with norms 12.1 us, 14.3 with 4 rows (with or without
+// the limit 12.1, 12.4 with 8 CTAs); 8191 of 48 heads of 64 without norms into the cache 19.1
+// us, 20.3 with 2 rows, 21.3 without the limit.
 template <int D, bool kNorm>
 constexpr int kBatch = D == 128 || !kNorm ? 4 : 2;
-template <int D>
-constexpr int kCtas = D == 128 ? 6 : 1;
+constexpr int kCtas = 6;
 
 enum : int { kNone, kHalf, kInterleaved };
 
@@ -113,7 +113,7 @@ __device__ __forceinline__ void load_weights(const void* w, bool f32, int d, flo
 }
 
 template <int D, bool kAppend, int kPairs, bool kNorm>
-__global__ void __launch_bounds__(kThreads, kCtas<D>)
+__global__ void __launch_bounds__(kThreads, kCtas)
     rope_kernel(const __grid_constant__ RopeParams p, int groups) {
   constexpr int kBatch = pkv::kBatch<D, kNorm>;
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a warp
