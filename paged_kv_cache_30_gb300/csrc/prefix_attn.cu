@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc + 16);
   const int from = min((long long)blockIdx.x * share, (long long)total);
-  const int to = min(from + share, total);
+  const int to = min((long long)from + share, (long long)total);
 
   // Registers: the softmax warpgroups take what the others give back (at launch 512 x 128, or
   // 384 x 168).
