@@ -60,8 +60,9 @@ constexpr int kSlotThreads = 128;
 constexpr int kScaleTiles = 8;  // tiles whose scales are kept: more than keys are ahead of the weights
 // Shares of at least so many tiles are read in turned order, see part_at.  128 requests behind
 // 131072 tokens (shares of 216 tiles, 537 MB) take 390 us instead of 406 and, where power limits
-// them, 430 instead of 459 (DRAM reads 0.80 GB instead of 2.15); behind 32768 (54 tiles) 127 and 128.  Shares of 8 to 16 tiles, whose
-// keys L2 holds in any order, lose: e4m3 heads of 64 35.4 us instead of 34.0.
+// them, 430 instead of 459 (DRAM reads 0.80 GB instead of 2.15); behind 32768 (54 tiles) 127 and
+// 128.  Shares of 8 to 16 tiles, whose keys L2 holds in any order, lose: e4m3 heads of 64 35.4 us
+// instead of 34.0.
 constexpr int kTurnTiles = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;   // log2 units
