@@ -570,6 +570,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if (kFp8) {  // each row's scale is another thread's
         named_bar_sync(1, 2 * kSlotThreads);
         c2 = fmaxf(scale2 * row_scale[(dual ? 128 * slot : 0) + row], kTiny);
+        // All have read before anyone writes there again: slot 1 its m and l, at once if the unit
+        // has one step, or the next unit's scales (a place of their own does not fit beside 2048
+        // groups).
+        named_bar_sync(1, 2 * kSlotThreads);
       }
       const int mine = dual ? min(u.rows - 128 * slot, 128) : u.rows;  // rows of this slot
       const bool live = 32 * (warp & 3) < mine;  // of the warp: else it only keeps step

@@ -277,6 +277,28 @@ def test_agrees_with_the_calls_that_share_nothing(fp8):
     check(pr, got, lse)
 
 
+@pytest.mark.parametrize("D,rows", [(128, 8), (64, 8), (128, 48), (64, 136)])
+def test_units_of_one_tile_with_queries_of_every_size(D, rows):
+    """An e4m3 query row's power of two lies where the second slot leaves its m and l, which comes
+    right behind in a unit of one step; the next unit's scales come there too.  Units of up to 128
+    rows and of more, one tile each, several a block; rows of sizes 2^-20 to 2^6, whose weights go
+    wrong with another row's power of two."""
+    G = 8
+    n = max(2, rows // G)
+    groups = [(16 * (1 + i % 8), [16 * (1 + i % 8) + 1 + (i + j) % 5 for j in range(n)])
+              for i in range(min(2000 // n, 300))]
+    pr = plain.problem(45, groups, 4, G, D, 16, True, sinks=True)
+    size = torch.arange(len(pr["sl"]) * 4 * G).view(len(pr["sl"]), 4 * G, 1) * 7 % 27 - 20
+    pr["q"] = (pr["q"].float() * torch.exp2(size.float())).bfloat16()
+    d = upload(pr)
+    outs = [torch.empty_like(d["q"]) for _ in range(40)]
+    for out in outs:
+        call(d, out, None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, outs[0]) for out in outs)
+    check(pr, outs[0], None)
+
+
 def test_captured_graphs_share_the_workspace_and_see_new_lengths():
     a = plain.problem(17, [(700, [701, 730, 900, 710]), (90, [95, 99])], 2, 8, 128, 16, True)
     b = plain.problem(18, [(1500, [1501 + i for i in range(40)])], 2, 8, 64, 32, False)
