@@ -584,7 +584,8 @@ PKV_API int pkv_rope_table(const double* inv_freq, int rot_dim, double base, dou
  * for pair p = (i, j) of the first rot_dim elements, (p, p + rot_dim / 2) or, if
  * interleaved, (2p, 2p + 1); the others are normed alone.  In 32 bits, the angle
  * reduced exactly for any position, rounded once to bf16.  (The squares are in 32 bits
- * too: a head with elements beyond 2^60 or so is infinitely long, and normed to 0.)
+ * too: a head with elements beyond 2^60 or so is infinitely long, and normed to 0; one
+ * whose elements are all below 2^-63 or so has the length that eps gives it.)
  *
  *   q            bf16 [T, Hq, D], D 64 or 128; last dim contiguous; strides multiples
  *                of 8; 16-byte aligned.  A view of part of a wider row will do: the

@@ -236,7 +236,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           b[0] = make_float2(lo_f32(now[u].z), hi_f32(now[u].z));
           b[1] = make_float2(lo_f32(now[u].w), hi_f32(now[u].w));
         }
-        float2 inv = make_float2(1.f, 1.f);
         if (norm) {
           float2 ss = mul2(a[0], a[0]);
           ss = fma2(a[1], a[1], ss);
@@ -245,7 +244,15 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           float s = ss.x + ss.y;
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          inv.x = inv.y = rsqrtf(__fmaf_rn(s, 1.f / D, p.eps));
+          const float r = rsqrtf(__fmaf_rn(s, 1.f / D, p.eps));
+          const float2 inv = make_float2(r, r);
+          // Before the weights: an element near the end of the range times its weight would be
+          // an infinity, which times the 0 of a head whose squares overflow is no 0.
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            a[i] = mul2(a[i], inv);
+            b[i] = mul2(b[i], inv);
+          }
         }
         float2 ya[2], yb[2];
 #pragma unroll
@@ -255,10 +262,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           if (rotates) {  // other elements stay apart: an infinity times 0 is none of theirs
             ya[i] = fma2(b[i], bs[i], ya[i]);
             yb[i] = fma2(a[i], as[i], yb[i]);
-          }
-          if (norm) {
-            ya[i] = mul2(ya[i], inv);
-            yb[i] = mul2(yb[i], inv);
           }
         }
         if (h >= rows.heads || !rows.dst) continue;

@@ -155,6 +155,28 @@ def test_zeros_infinities_and_nan_stay_in_their_heads():
     assert out[1, 2].eq(0).all() and out[2, 0].isnan().all() and out[3, 1].isnan().any()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_heads_whose_squares_overflow_are_normed_to_zero(D, interleaved):
+    g = torch.Generator().manual_seed(34)
+    q, k = heads(g, 8, 5, D), heads(g, 8, 2, D)
+    big = torch.tensor([2.0 ** 66, 2.0 ** 100, 2.0 ** 127, -3.3e38])
+    q[2, 1, ::7], q[3, 4] = big[3], big[0]
+    q[5, 0, :4], k[6, 1, D - 4:] = big, big
+    w = 1 + 3 * torch.rand(D, generator=g)  # weights above 1
+    pos, freq = torch.arange(8).int() * 1000, plain.frequencies(D // 2)
+    qo, ko = torch.empty_like(q).cuda(), torch.empty_like(k).cuda()
+    pkv.qk_norm_rope(q.cuda(), k.cuda(), w.cuda(), w.cuda(), 1e-6, pos.cuda(), pkv.rope_table(D // 2), 1.5,
+                     interleaved, qo, ko)
+    for got, x, zero in ((qo, q, [(2, 1), (3, 4), (5, 0)]), (ko, k, [(6, 1)])):
+        fine = torch.ones(x.shape[:2], dtype=torch.bool)
+        for t, h in zero:
+            assert got[t, h].eq(0).all()
+            fine[t, h] = False
+        want, tol = plain.norm_rope(x, w, 1e-6, pos, freq, 1.5, interleaved)
+        close(got[fine.cuda()], want[fine], tol[fine])
+
+
 def test_rotation_captured_and_replayed_at_other_positions():
     g = torch.Generator().manual_seed(33)
     q, k, freq = heads(g, 5, 4, 128), heads(g, 5, 2, 128), plain.frequencies(128)
