@@ -296,7 +296,13 @@ def test_units_of_one_tile_with_queries_of_every_size(D, rows):
         call(d, out, None)
     torch.cuda.synchronize()
     assert all(torch.equal(out, outs[0]) for out in outs)
-    check(pr, outs[0], None)
+    # Where a sink passes a row's largest score by 128 (log2), 2^(sink - m) is an infinity in 32 bits
+    # and the output 0, where it is sum_j 2^(x_j - sink) v_j <= 133 keys 2^-128 60 < 2^-115: values
+    # are below 448 2^3 / 60 < 60.  (Outputs below 2^-126 lose bits as well.)
+    want, _, tol, _ = plain.decode(pr, "cuda")
+    far = (outs[0].double() - want).abs() - tol - 2.0 ** -115
+    assert (far <= 0).all(), f"{int((far > 0).sum())} of {far.numel()}, {far.max():.3e} past the bound"
+    assert pkv.check_errors(0) == 0 and pkv.check_counters(0) == 0
 
 
 def test_captured_graphs_share_the_workspace_and_see_new_lengths():
