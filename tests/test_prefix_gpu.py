@@ -179,6 +179,30 @@ def test_scales_of_any_sign(fp8, scale):
     check(pr, *run(pr))
 
 
+@BOTH
+@pytest.mark.parametrize("scale", [0.0, -0.0, 0.75 * 2.0 ** -126, 2.0 ** -120])
+def test_small_scales_of_large_products(fp8, scale):
+    """Products of up to 2^125: a scale of 0 makes equal weights of them, one below the smallest
+    normal value the weights that it should."""
+    pr = plain.problem(46, [(500, [501, 520, 700]), (130, [131] * 20)], 2, 8, 128, 16, fp8)
+    pr["scale"] = scale
+    if fp8:
+        pr["q"] *= 2.0 ** 100
+        pr["sc"][..., 0] *= 2.0 ** 15
+    else:
+        pr["q"] *= 2.0 ** 59
+        pr["kv"][..., :128] *= 2.0 ** 59
+    out, lse = run(pr)
+    check(pr, out, lse)
+    d = upload(pr)
+    d["q"][1, 3, 7] = math.inf  # times 0 is no number
+    bad, _ = run(pr, d=d)
+    if scale == 0:
+        assert bad[1, 3].isnan().all()
+    bad[1, 3] = out[1, 3]
+    assert torch.equal(bad, out)
+
+
 def test_scales_far_apart_between_pages():
     """One page's keys outweigh the others', or its values do, by factors up to 2^40."""
     for seed in range(4):
