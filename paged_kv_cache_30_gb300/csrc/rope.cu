@@ -74,15 +74,16 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, long long t) {
     int b, left;  // request; its new tokens from this one on
     if (p.cu) {
       b = request_of(p.cu, p.B, t);
-      left = b < 0 ? 0 : (int)min(__ldg(p.cu + b + 1) - t, 1ll << 30);
+      left = b < 0 ? 0 : (int)max(__ldg(p.cu + b + 1) - t, 0ll);
     } else {
       const long long each = p.T / p.B;
       b = (int)(t / each);
       left = (int)(each - t % each);
     }
     if (left <= 0) return {-1, -1};  // behind the last request
-    const int pos = __ldg(p.seq_lens + b) - left;
-    if (pos < 0) return {-1, -1};
+    const int len = __ldg(p.seq_lens + b);
+    if (len < left) return {-1, -1};  // (their difference need not be an int)
+    const int pos = len - left;
     if (!p.positions) r.pos = pos;
     const int page = pos / p.page_size;
     if (r.pos < 0) return r;

@@ -289,6 +289,13 @@ def test_ragged_prompts_between_padding_rows(D, P, interleaved):
     verify(pr, *run(pr))
 
 
+def test_lengths_of_any_size_below_the_new_tokens():
+    for one in (True, False):
+        new = [1, 1, 1, 1] if one else [3, 1, 0, 5]
+        pr = problem(23, [-(1 << 31), 0, -(1 << 31) + 5, 7], new, 4, 2, 64, 16, 64, one_each=one)
+        verify(pr, *run(pr))
+
+
 def test_many_requests_and_long_prompts():
     pr = problem(11, [3 + b % 7 for b in range(1500)], [b % 3 for b in range(1500)], 4, 2, 64, 16, 64)
     verify(pr, *run(pr))
