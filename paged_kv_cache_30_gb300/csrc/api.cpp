@@ -232,21 +232,29 @@ int check_no_overlap(std::initializer_list<std::pair<const pkv_tensor*, const ch
   return PKV_OK;
 }
 
-// Whether two views of tokens (dim 0) share no byte although their spans may cross, as
-// queries, keys and values that lie side by side in a projection's output do: with one
-// stride, tokens of one fit between those of the other.
+// Whether two views of tokens (dim 0) and heads (dim 1) share no byte although their spans may
+// cross, as queries, keys and values that lie side by side in a projection's output do: with
+// one stride of the tokens, or of the heads in rows of whole such strides, what one has between
+// two of its steps fits beside what the other has.
 bool apart(const pkv_tensor* a, const pkv_tensor* b) {
   if (!overlaps(a, b)) return true;
-  const int64_t step = a->stride[0] * elem_bytes(a->dtype);
-  if (step != b->stride[0] * elem_bytes(b->dtype) || step <= 0) return false;
-  auto extent = [](const pkv_tensor* t) {
-    int64_t last = 0;
-    for (int i = 1; i < t->ndim; ++i) last += (t->shape[i] - 1) * t->stride[i];
-    return (last + 1) * elem_bytes(t->dtype);
-  };
   const intptr_t off = reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data);
-  const int64_t d = (off % step + step) % step;
-  return d >= extent(a) && d + extent(b) <= step;
+  for (int dim = 0; dim < 2; ++dim) {
+    const int64_t step = a->stride[dim] * elem_bytes(a->dtype);
+    if (step <= 0 || step != b->stride[dim] * elem_bytes(b->dtype)) continue;
+    auto extent = [&](const pkv_tensor* t) {  // -1: other rows do not begin at whole steps
+      int64_t last = 0;
+      for (int i = 0; i < t->ndim; ++i)
+        if (i > dim)
+          last += (t->shape[i] - 1) * t->stride[i];
+        else if (i < dim && t->shape[i] > 1 && t->stride[i] % t->stride[dim])
+          return int64_t(-1);
+      return (last + 1) * elem_bytes(t->dtype);
+    };
+    const int64_t ea = extent(a), eb = extent(b), d = (off % step + step) % step;
+    if (ea >= 0 && eb >= 0 && d >= ea && d + eb <= step) return true;
+  }
+  return false;
 }
 
 bool same_view(const pkv_tensor* a, const pkv_tensor* b) {

@@ -116,6 +116,25 @@ def test_append_refusals(lib, change, code):
     assert call(lib, {**args(), **change}, True) == code
 
 
+def test_views_side_by_side_are_told_from_views_that_cross(lib):
+    """Queries and keys in place inside the rows of a projection, next to one another in each token
+    or in each head."""
+    def refused(cache, heads, q, k, v):
+        views = {n: tensor(n, [4, heads, 128], BF16, s, PTR["q"] + 2 * at)
+                 for n, (s, at) in (("q", q), ("k", k), ("v", v))}
+        a = {**args(Hq=heads, Hkv=heads), **views, "qo": views["q"], "ko": views["k"]}
+        return call(lib, a, cache) == -1 and "overlaps" in pkv.last_error()
+    for cache in (False, True):
+        token, head = [6 * 128, 128, 1], [6 * 128, 3 * 128, 1]
+        assert not refused(cache, 2, (token, 0), (token, 256), (token, 512))
+        assert not refused(cache, 2, (head, 0), (head, 128), (head, 256))
+        assert not refused(cache, 2, (head, 256), (head, 0), (head, 128))
+        assert refused(cache, 2, (head, 0), (head, 64), (head, 256))  # half a head further
+        assert refused(cache, 2, (token, 0), (head, 128), (token, 512))
+        odd = [5 * 128, 2 * 128, 1]  # a token's row is no whole number of heads
+        assert refused(cache, 2, (odd, 0), (odd, 128), (odd, 8192))
+
+
 def test_no_tokens_are_no_ops(lib):
     for cache in (False, True):
         a = args(T=0)

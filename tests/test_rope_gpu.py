@@ -338,6 +338,25 @@ def test_strided_views_of_one_projection_and_an_nhd_cache():
     assert torch.equal(k.cpu(), pr["k"]) and torch.equal(v.cpu(), pr["v"])
 
 
+def test_queries_and_keys_in_place_side_by_side_in_each_head():
+    pr = problem(24, [30, 40], [30, 10], 3, 3, 64, 16, 64)
+    base = torch.stack([pr["q"], pr["k"], pr["v"]], dim=2).cuda()  # [T, H, 3, D]
+    q, k, v = base.unbind(2)
+    kv, table = pr["kv"].cuda(), pkv.rope_table(64)
+    pkv.gqa_rope_append(q, k, v, up(pr["qw"]), up(pr["kw"]), 1e-5, None, table, 1.0, False, kv,
+                        up(pr["bt"]), up(pr["sl"]), up(pr["cu"]), 16, q)
+    torch.cuda.synchronize()
+    verify(pr, q, kv)
+    assert torch.equal(k.cpu(), pr["k"]) and torch.equal(v.cpu(), pr["v"])
+    base = torch.stack([pr["q"], pr["k"], pr["v"]], dim=2).cuda()
+    q, k, v = base.unbind(2)
+    pos = torch.arange(40).int() * 77
+    pkv.qk_norm_rope(q, k, up(pr["qw"]), up(pr["kw"]), 1e-5, pos.cuda(), table, 1.0, False, q, k)
+    for got, x, w in ((q, pr["q"], pr["qw"]), (k, pr["k"], pr["kw"])):
+        close(got, *plain.norm_rope(x, w, 1e-5, pos, plain.frequencies(64), 1.0, False))
+    assert torch.equal(v.cpu(), pr["v"])
+
+
 def test_captured_and_replayed_with_other_lengths():
     pr = problem(18, [17, 30, 16], [1, 1, 1], 4, 2, 64, 16, 64, one_each=True)
     d = {n: up(pr[n]) for n in ("q", "k", "v", "qw", "kw", "bt", "sl")}
