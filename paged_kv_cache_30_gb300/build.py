@@ -21,7 +21,7 @@ SOURCES = ["api.cpp", "gqa_decode.cu", "gqa_noalloc.cu", "mla_verify.cu", "mla_v
            "rope.cu", "prefix_attn.cu", "prefix_own.cu",
            "prefix_combine.cu"]
 HEADERS = ["pkv_internal.h", "page_order.h", "ptx.cuh", "tcgen05.cuh", "mla_common.cuh",
-           "paged_attn.cuh", "prefix_common.cuh"]
+           "paged_attn.cuh", "prefix_common.cuh", "prefix_ring.h"]
 PYCALL = os.path.join(BUILD, "_pkvcall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",

@@ -46,6 +46,7 @@
 
 #include "pkv_internal.h"
 #include "prefix_common.cuh"
+#include "prefix_ring.h"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 
@@ -105,33 +106,11 @@ struct PrefixCfg {
   static_assert(4 * (plan_ints(kPagedMaxBatch) + kPagedMaxBatch + 1) <= kOffScale, "room for the plan of the groups");
 };
 
-// Operands of a unit in the ring, for one of the roles that go through them: operand n's
-// place, and the phase of its barriers.
+// A place of the ring in shared memory.
 template <class C>
-struct OpRing {
-  uint32_t base = 0;  // phases of the places at the unit's start
-  int mod = C::kOps;
-
-  __device__ __forceinline__ void begin(bool dual) {
-    if (C::kExtraOp) mod = dual ? C::kOps : C::kOps + 1;
-  }
-  __device__ __forceinline__ int uses(int n) const {  // n / mod
-    return !C::kExtraOp ? n / C::kOps : mod == C::kOps ? n / C::kOps : n / (C::kOps + 1);
-  }
-  __device__ __forceinline__ int place(int n) const { return n - uses(n) * mod; }
-  __device__ __forceinline__ uint32_t phase(int n) const {
-    return ((base >> place(n)) ^ (uint32_t)uses(n)) & 1u;
-  }
-  __device__ __forceinline__ void end(int n) {  // of a unit of n operands
-    const int all = uses(n), left = place(n);
-    // places below `left` were used once more
-    const uint32_t low = (1u << left) - 1u, places = (1u << mod) - 1u;
-    base ^= all & 1 ? places & ~low : low;
-  }
-  static __device__ __forceinline__ uint32_t offset(int place) {  // in shared memory
-    return C::kExtraOp && place == C::kOps ? C::kOpBytes : C::kOffOps + place * C::kOpBytes;
-  }
-};
+__device__ __forceinline__ uint32_t op_offset(int place) {
+  return C::kExtraOp && place == C::kOps ? C::kOpBytes : C::kOffOps + place * C::kOpBytes;
+}
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {  // RNE, lo in bits 0..15
   uint32_t r;
@@ -165,23 +144,7 @@ struct Part {
     t += turn;
     return t0 + (t < tiles() ? t : t - tiles());
   }
-  // Operands come in the order in which the steps use them: K0 V0 K1 V1 .. for two query tiles,
-  // K0 K1 V0 K2 V1 .. for one, whose steps j and j + 1 are at work together.  (Of an e4m3 cache
-  // always as for two, which has less to work out.)
-  __device__ __forceinline__ bool by_tile() const { return kFp8 || dual(); }
-  __device__ __forceinline__ int keys(int t) const { return by_tile() ? 2 * t : max(2 * t - 1, 0); }
-  __device__ __forceinline__ int values(int t) const {
-    return by_tile() || t == tiles() - 1 ? 2 * t + 1 : 2 * t + 2;
-  }
-  __device__ __forceinline__ bool are_values(int n) const {  // operand n
-    return by_tile() ? n & 1 : n == 2 * tiles() - 1 || (n > 0 && !(n & 1));
-  }
-  __device__ __forceinline__ int tile_of(int n) const {
-    return by_tile()                ? n >> 1
-           : n == 2 * tiles() - 1 ? tiles() - 1
-           : n & 1                ? (n + 1) >> 1
-                                  : max((n >> 1) - 1, 0);
-  }
+  __device__ __forceinline__ OperandOrder order() const { return {kFp8 || dual(), tiles()}; }
 };
 
 // The unit that holds place f < the CTA's end `to`.
@@ -339,7 +302,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const bool asks = kFp8 || (in_tile == 0 ? half == 0 : sub >> (in_tile - 1) == half);
     const uint32_t bytes = kFp8 ? C::kRawBytes : C::kOpBytes >> (in_tile == 0 ? (half ? 31 : 0) : 1);
     int op = 0, tiles = 0;                 // operands and tiles of units before
-    OpRing<C> ring;
+    OpRing<C::kOps, C::kExtraOp> ring;
     for (int f = from; f < to;) {
       const auto u = part_at<kFp8>(p, x, places, f, to, share);
       f = u.next;
@@ -364,8 +327,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       int pages[2] = {page_of(0), 0};
       float2 scale = scale_of(pages[0]), next_scale = scale;
       for (int n = 0; n < 2 * u.tiles(); ++n, ++op) {
-        const int t = u.tile_of(n), at = t & (batch - 1);
-        const bool values = u.are_values(n), odd = t & batch;
+        const int t = u.order().tile_of(n), at = t & (batch - 1);
+        const bool values = u.order().are_values(n), odd = t & batch;
         if (!values) {
           if (at == 0) {
             scale = next_scale;
@@ -405,7 +368,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           } else {
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
-              tma_load_5d(base_u32 + ring.offset(e) + c * C::kChunkBytes + (sub << p.page_shift) * 128,
+              tma_load_5d(base_u32 + op_offset<C>(e) + c * C::kChunkBytes + (sub << p.page_shift) * 128,
                           &kv_map, bar(full), 0, 0, (values ? C::kChunks : 0) + c, u.kvh, page);
           }
         }
@@ -423,7 +386,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     // fall into step, and the tensor cores stand still while both are at their exponentials.
     int units = 0, before = 0;      // the slot whose turn was the last
     uint32_t ready = 0, turns = 0;  // phases of P; of this slot's turns
-    OpRing<C> ring;
+    OpRing<C::kOps, C::kExtraOp> ring;
     for (int f = from; f < to;) {
       const auto u = part_at<kFp8>(p, x, places, f, to, share);
       f = u.next;
@@ -445,9 +408,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       for (int j = slot - 2; j < steps; j += 2) {
         const bool first = j < 0, more = j + 2 < steps;
         if (first && !more) continue;
-        const int kn = more ? u.keys(u.tile(j + 2)) : 0, vn = first ? 0 : u.values(u.tile(j));
+        const int kn = more ? u.order().keys(u.tile(j + 2)) : 0, vn = first ? 0 : u.order().values(u.tile(j));
         // All that can be waited for is, before the turn.  (The next e4m3 keys of a unit of one
-        // query tile may take the place of these values.)
+        // query tile are rewritten behind the other slot\'s values, and so come late.)
         if (more && (!kFp8 || dual || first)) wait_op(kn);
         if (!first) {
           wait_op(vn);
@@ -459,7 +422,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
         tc::fence_after_sync();
         if (!first) {
-          const uint32_t b = base_u32 + ring.offset(ring.place(vn));
+          const uint32_t b = base_u32 + op_offset<C>(ring.place(vn));
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks) {
             if (ks == kTile / 32) {
@@ -477,7 +440,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (kFp8 && !dual && more) wait_op(kn);
         }
         if (more) {
-          const uint32_t b = base_u32 + ring.offset(ring.place(kn));
+          const uint32_t b = base_u32 + op_offset<C>(ring.place(kn));
           tc::fence_after_sync();
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
@@ -767,7 +730,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     // ============= e4m3 operand -> bf16 operand, swizzled for the MMA =============
     const int ct = tid - 32 * (kSlotWarp0 + 8);
     int op = 0;
-    OpRing<C> ring;
+    OpRing<C::kOps, C::kExtraOp> ring;
     for (int f = from; f < to;) {
       const auto u = part_at<kFp8>(p, x, places, f, to, share);
       f = u.next;
@@ -777,7 +740,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int er = op % C::kRaws, eo = ring.place(i);
         mbar_wait(bar(kRawFull + er), (op / C::kRaws) & 1, p.err);
         const uint8_t* src = base + C::kOffRaw + er * C::kRawBytes;
-        uint8_t* dst = base + ring.offset(eo);
+        uint8_t* dst = base + op_offset<C>(eo);
         // 8 codes each, a 16-byte unit of the operand; a thread's are kStep rows apart, which keeps
         // the unit and the swizzle
         constexpr int kUnits = D / 8, kStep = C::kConverters / kUnits, kMine = kTile / kStep;
