@@ -497,7 +497,7 @@ PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
  * 64 of the device error word, and all requests are then attended to on their own.
  * The workspace holds 16 B + B Hq (8 D + 24) + 256 SMs (4 D + 8) bytes of it next to what
  * pkv_paged_window_attn needs (PKV_ERR_WORKSPACE).
- * The weights are rounded to bf16 (2^-9 of themselves).  Three launches; nothing is read
+ * The weights are rounded to bf16 (2^-8 of themselves).  Three launches; nothing is read
  * before the dependency wait.  Errors as pkv_paged_decode_attn_fp8.
  */
 PKV_API int pkv_paged_prefix_attn(const pkv_tensor* q, const pkv_tensor* kv_cache,

@@ -31,8 +31,8 @@
 //  * The reference m of a row moves when a score passes it by more than 2^8, and O is
 //    rescaled in tensor memory then; the scores of a step are there only after O of the
 //    steps before is, so that needs no wait.  P, times its value's scale, is rounded once to
-//    bf16, whose exponents are those of 32-bit values: 2^-9 of each weight, as in the decode
-//    of a bf16 cache.
+//    bf16, whose exponents are those of 32-bit values: up to 2^-8 of each weight, as in the
+//    decode of a bf16 cache.
 //
 // Measured (GB300, whole calls in a graph, 64 query and 8 kv heads of 128; the cuBLAS rate is 1929
 // TFLOP/s, 1759 for seconds on end): 128 requests behind 131072 tokens 390 us = 1.41 PFLOP/s; on inputs
