@@ -1112,7 +1112,6 @@ PKV_API int pkv_mla_kv_append(const pkv_tensor* latent, const pkv_tensor* latent
 }
 
 // ------------------------------------- decode with a window and first tokens --
-// Both entry points: kv_scale == nullptr is the bf16 cache.
 // The cache as a tensor map of `pieces` pieces of `elems` elements a row, in boxes of some
 // tokens by some pieces.
 static int encode_paged_map(EncodeTiledFn encode, const pkv_tensor* kv_cache, bool fp8, int page_size,
@@ -1136,7 +1135,9 @@ static int encode_paged_map(EncodeTiledFn encode, const pkv_tensor* kv_cache, bo
   return PKV_OK;
 }
 
-// cu_groups (with shared_lens): the calls for groups of requests with shared tokens.
+// The four entry points below: fp8 tells the cache's type (with kv_scale, else without), grouped
+// the calls for groups of requests with shared tokens (with cu_groups and shared_lens, without a
+// window).
 static int paged_attn_impl(const pkv_tensor* q, const pkv_tensor* kv_cache, bool fp8,
                            const pkv_tensor* kv_scale, const pkv_tensor* block_table,
                            const pkv_tensor* seq_lens, const pkv_tensor* sinks, int window,
