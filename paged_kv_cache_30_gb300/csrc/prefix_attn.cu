@@ -67,6 +67,9 @@ constexpr int kScaleTiles = 8;  // tiles whose scales are kept: more than keys a
 constexpr int kTurnTiles = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;   // log2 units
+// Instead of a unit of 0, which a masked score of -inf must not meet: it takes scores below 2^128 to
+// less than 2^-21, and leaves units of normal size as they are.
+constexpr float kLeast = 0x1p-149f;
 
 // barriers
 enum {
@@ -116,11 +119,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {  // RNE, lo i
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// Two bf16 elements times 0: NaN for those that are not finite.
-__device__ __forceinline__ uint32_t zero_times(uint32_t w) {
-  return ((w & 0x7f80u) == 0x7f80u ? 0x7fffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0x7fff0000u : 0u);
 }
 
 // A CTA's part of a unit.
@@ -472,9 +470,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + slot * kTile, tO = tmem + lanes + 2 * kTile + slot * D;
     const float scale2 = fabsf(p.scale) * kLog2e;
-    // A scale of 0 takes the queries to 0 instead of their scores, as a masked score is -inf.
-    const bool no_scale = p.scale == 0.f;
-    float c2 = no_scale ? 1.f : scale2;  // log2 units of a score
+    float c2 = fmaxf(scale2, kLeast);  // log2 units of a score
     const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;  // of the query's signs
     float2* other_ml = reinterpret_cast<float2*>(base + C::kOffMl);  // at a unit's end
     float* row_scale = reinterpret_cast<float*>(other_ml);           // at its start
@@ -529,8 +525,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               w[e] = pack_f16(__uint_as_float(w[e] << 16) * mul, __uint_as_float(w[e] & 0xffff0000u) * mul);
             v[i] = make_uint4(w[0], w[1], w[2], w[3]);
             if (k == 0) row_scale[128 * tile + r0 + i * kStep] = __uint_as_float((uint32_t)(127 - up) << 23);
-          } else if (no_scale) {
-            v[i] = make_uint4(zero_times(v[i].x), zero_times(v[i].y), zero_times(v[i].z), zero_times(v[i].w));
           }
           *reinterpret_cast<uint4*>(dst + i * kStep * 128) =
               make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
@@ -560,8 +554,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int valid = min(u.boxes - u.at(t) * kTileBoxes, kTileBoxes);  // boxes
           const float2* sc = reinterpret_cast<const float2*>(base + C::kOffScale) +
                              (at % kScaleTiles) * kTileBoxes;
-          // log2 units of a score of box h (not 0 for a masked one: no infinity times 0)
-          auto unit = [&](int h) { return !kFp8 ? c2 : h < valid ? c2 * sc[h].x : 1.f; };
+          // log2 units of a score of box h, never 0
+          auto unit = [&](int h) { return kFp8 ? __fmaf_rn(c2, sc[h].x, kLeast) : c2; };
           // Half of the row at a time in registers: two pieces of 32 keys, from piece c on.
           uint32_t s[2][32];
           auto load = [&](int c) {
