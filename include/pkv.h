@@ -499,6 +499,10 @@ PKV_API int pkv_paged_window_attn(const pkv_tensor* q, const pkv_tensor* kv_cach
  * pkv_paged_window_attn needs (PKV_ERR_WORKSPACE).
  * The weights are rounded to bf16 (2^-8 of themselves).  Three launches; nothing is read
  * before the dependency wait.  Errors as pkv_paged_decode_attn_fp8.
+ * Sharing pays where it saves many reads: for groups of n live requests, from about
+ * sum (n - 1) shared_lens[g] Hkv D = 64 million elements of keys on (8 kv heads of 128: 32
+ * requests behind 2048 tokens, or 8 behind 8192).  Below, pkv_paged_window_attn (_decode_attn_fp8)
+ * on the same rows is faster: 4 requests behind 512 tokens 7 us instead of 13.
  */
 PKV_API int pkv_paged_prefix_attn(const pkv_tensor* q, const pkv_tensor* kv_cache,
                                   const pkv_tensor* block_table, const pkv_tensor* seq_lens,

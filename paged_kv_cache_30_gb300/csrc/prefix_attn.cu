@@ -10,8 +10,10 @@
 // O, m and l go to the workspace in 32 bits; the grid after this one (paged_attn.cuh)
 // attends to each request's own keys, the third (prefix_combine.cu) adds up all parts.
 //
-// Bound by the tensor cores, and under them by power, with many rows (a key of 512 bytes is
-// multiplied with 1024 rows, say), by memory with few.
+// With many rows (a key of 512 bytes is multiplied with 1024 rows, say) a step takes its slots 1770
+// cycles, of which 1024 are products: bound by a slot's chain of scores, exponentials and weights,
+// which two slots cover in part, and by power, which takes a tenth of the clock.  With few rows:
+// latency, see below.
 //
 //  * A unit is (group, kv head, block of 256 rows); units are laid end to end, counted in
 //    16-key boxes plus a cost for each, and CTA c takes an equal share of the whole, whose
@@ -32,16 +34,20 @@
 //    rescaled in tensor memory then; the scores of a step are there only after O of the
 //    steps before is, so that needs no wait.  P, times its value's scale, is rounded once to
 //    bf16, whose exponents are those of 32-bit values: up to 2^-8 of each weight, as in the
-//    decode of a bf16 cache.
+//    decode of a bf16 cache.  Also for e4m3, whose decode has tf32 weights: as two bf16 terms
+//    (2^-16) they take half as many products again, and the samples below 202 us instead of
+//    156, 33 requests with heads of 64 44.2 instead of 35.6.
 //
 // Measured (GB300, whole calls in a graph, 64 query and 8 kv heads of 128; the cuBLAS rate is 1929
-// TFLOP/s, 1759 for seconds on end): 128 requests behind 131072 tokens 390 us = 1.41 PFLOP/s; on inputs
-// that change from call to call, for seconds, 430 us = 1.28, at 1.4 kW and 1.5 to 1.8 GHz.  64
-// requests behind 8192 tokens and up to 2048 of their own 45.5 us, of which this grid has 25: a
+// TFLOP/s, 1759 for seconds on end): 128 requests behind 131072 tokens 390 to 398 us = 1.4 PFLOP/s; on
+// inputs that change from call to call, for seconds, 420 us = 1.31, at 1.37 kW and 1.88 GHz (of 2.07).
+// 64 requests behind 8192 tokens and up to 2048 of their own 45.6 us, of which this grid has 25: a
 // start of 6 us (three dependent reads), 1 us a step, parts written in 2.  58 forked e4m3 samples
-// behind 500 to 32768 tokens (438 MB) 157 us; the same of bf16 (876 MB) 155 us = 84 % of the copy
-// bandwidth.  e4m3 tiles of few rows are bound by their rewriting, which is latency (8 codes a
-// thread at a time, 8 reads under way; 16 codes and 4 reads: 164 us; none at all: 149).
+// behind 500 to 32768 tokens (438 MB) 154 us; the same of bf16 (876 MB) 155 us = 84 % of the copy
+// bandwidth.  e4m3 tiles of few rows wait for one another along the chain of copy, rewriting,
+// products and exponentials; the rewriting's own work is 5 % (with 8 codes a thread at a time and 8
+// reads under way 157 us then, with 16 and 4 164, with nothing rewritten 149), memory and the
+// tensor pipe are each busy for a third of the time.
 #include <algorithm>
 
 #include "pkv_internal.h"
