@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (first && !more) continue;
         const int kn = more ? u.order().keys(u.tile(j + 2)) : 0, vn = first ? 0 : u.order().values(u.tile(j));
         // All that can be waited for is, before the turn.  (The next e4m3 keys of a unit of one
-        // query tile are rewritten behind the other slot\'s values, and so come late.)
+        // query tile are rewritten behind the other slot's values, and so come late.)
         if (more && (!kFp8 || dual || first)) wait_op(kn);
         if (!first) {
           wait_op(vn);
